@@ -400,6 +400,117 @@ upipe_status_t upipe_attn_ring_bwd(const upipe_ring_desc_t* desc, const uint16_t
                                    const int32_t* seg, void* tables, float* D, float* dq_acc, float* dk_acc,
                                    float* dv_acc, uint16_t* dq, uint16_t* dk, uint16_t* dv, void* stream);
 
+/* ------------------------------------------------------------------------------------------
+ * Operators around the two blocks: what a transformer block needs between the attention layer, the
+ * MLP and the optimizer.  The pages describe none of them; they are this library's own, for users
+ * who run its layer, attention core or MLP inside a whole block.  Conventions as above (every device
+ * pointer 16-byte aligned, stream-ordered, nothing allocated).  Zero rows or tokens are valid.
+ *
+ * Root-mean-square norm with the residual's addition.  Per row of d elements:
+ *   h = bf16(x + residual)  (without a residual h is x itself and is not written)
+ *   rstd = (mean(h^2) + eps)^(-1/2)  (fp32 sum),   y = h * rstd * w
+ * rows 0 .. 2^31 - 1; d a multiple of 8 (of 16 with q), at most 32768.
+ *   x, residual  device bf16 [rows, d]; residual NULL exactly when h is
+ *   w            device bf16 [d]
+ *   h            device bf16 [rows, d] (written): the residual stream; may be x or residual itself
+ *   y            device bf16 [rows, d] (written), or NULL with q; may be x or residual itself
+ *   q, scales    both NULL, or y in 8 bits for upipe_attn_gemm_fp8_nt's A: q device e4m3 [rows, d],
+ *                scales device fp32 [ceil(d / 128)][rows], for each row and 128 columns
+ *                s = max|y| / 448 (1 where max|y| < 2^-100) and q = e4m3(y / s), rounded to nearest
+ *                even from the fp32 y.  A NaN or infinity makes its block's scale NaN or infinity.
+ *   rstd         NULL, or device fp32 [rows] (written) for the backward pass
+ * Buffers that overlap in any other way are rejected with UPIPE_ERR_INVALID_ARG. */
+upipe_status_t upipe_attn_rms_norm_fwd(int64_t rows, int64_t d, float eps, const uint16_t* x, const uint16_t* residual,
+                                       const uint16_t* w, uint16_t* h, uint16_t* y, uint8_t* q, float* scales,
+                                       float* rstd, void* stream);
+
+/* Backward of the norm, from the h that the forward wrote (or x, without a residual) and its rstd; with
+ * t = dy * w:
+ *   dx = rstd * (t - h * rstd^2 * mean(t * h)) [+ dres]    the gradient of x and of residual alike
+ *   dw = sum over rows of dy * h * rstd
+ *   dy, h  device bf16 [rows, d];  rstd device fp32 [rows]
+ *   dres   NULL, or device bf16 [rows, d]: the gradient that reaches h along the residual stream
+ *   dx     device bf16 [rows, d] (written); may be dy, dres or h itself
+ *   dw     device fp32 [d] (written, not accumulated; zeros for no rows), summed in an order that
+ *          depends on rows and d alone
+ *   ws     device workspace of upipe_attn_rms_norm_workspace_size(rows, d) bytes */
+upipe_status_t upipe_attn_rms_norm_workspace_size(int64_t rows, int64_t d, size_t* bytes);
+upipe_status_t upipe_attn_rms_norm_bwd(int64_t rows, int64_t d, const uint16_t* dy, const uint16_t* h, const uint16_t* w,
+                                       const float* rstd, const uint16_t* dres, uint16_t* dx, float* dw, void* ws,
+                                       size_t ws_bytes, void* stream);
+
+/* bf16 to e4m3 with a scale for each block, as upipe_attn_gemm_fp8_nt reads its operands.
+ *   x       device bf16 [rows, cols], cols a multiple of 16
+ *   q       device e4m3 [rows, cols] (written)
+ *   scales  device fp32 (written): block_rows 1 (activations, A): [ceil(cols / 128)][rows], one for
+ *           each row and 128 columns; block_rows 128 (weights, B): [ceil(rows / 128)][ceil(cols / 128)]
+ * s and q as in upipe_attn_rms_norm_fwd. */
+upipe_status_t upipe_attn_fp8_quantize(int64_t rows, int64_t cols, int32_t block_rows, const uint16_t* x, uint8_t* q,
+                                       float* scales, void* stream);
+
+/* 8-bit matrix product with a scale for each block of 128:
+ *   C[m, n] = sum_kb a_scale[kb][m] * b_scale[n / 128][kb] * sum_{k in block kb} A[m, k] * B[n, k]
+ * e4m3 products, fp32 sums, C rounded once.
+ *   A        device e4m3 [M, K], rows of lda bytes;  B device e4m3 [N, K], rows of ldb bytes
+ *   a_scale  device fp32 [ceil(K / 128)] rows of a_scale_ld >= M
+ *   b_scale  device fp32 [ceil(N / 128)][ceil(K / 128)]
+ *   C        device [M, N], rows of ldc elements; c_dtype 0: fp32, 1: bf16
+ * M >= 0; K, lda, ldb multiples of 16; N, ldc multiples of 8; M, N, K <= 2^31 - 1. */
+upipe_status_t upipe_attn_gemm_fp8_nt(int64_t M, int64_t N, int64_t K, const uint8_t* A, int64_t lda,
+                                      const float* a_scale, int64_t a_scale_ld, const uint8_t* B, int64_t ldb,
+                                      const float* b_scale, void* C, int64_t ldc, int32_t c_dtype, void* stream);
+
+/* Rotary positions with several axes, between the projection and the attention core.  Rotary pair j of
+ * every head's row turns by  t = position[axis[j]][token] * inv_freq[j]:
+ *   (a, b) -> (a cos t - b sin t, b cos t + a sin t)
+ * The angle is reduced exactly, so positions up to +-2^31 lose nothing.  `inverse` turns by -t, which is
+ * the backward pass (dQ, dK back to the gradient of the projection).
+ *   head_dim    multiple of 16, at most 256
+ *   rotary_dim  R, a multiple of 16, at most head_dim: the row's first R elements; the rest is copied
+ *   n_axes      1 .. 4 rows of positions (1: text; 2: height, width; 3: time, height, width)
+ *   adjacent    0: pair j is elements (j, j + R/2); 1: elements (2j, 2j + 1)
+ *   inv_freq    radians per unit of position, for each of the R/2 pairs (host memory, read at the call)
+ *   axis        the row of positions that each pair reads */
+typedef struct {
+  int32_t head_dim, rotary_dim, n_axes, adjacent, inverse;
+  uint8_t axis[128];
+  double inv_freq[128];
+} upipe_rope_desc_t;
+/* Heads of one tensor, read and written through their own strides (in elements, multiples of 8; a row's
+ * elements are contiguous): head-major as the attention core takes them, or a part of the projection's
+ * token-major output.  out may be in itself with the same strides; otherwise the two must not overlap.
+ * No two rows of out may overlap, nor may the outputs of q and k. */
+typedef struct {
+  const uint16_t* in;
+  uint16_t* out;
+  int64_t in_head_stride, in_token_stride, out_head_stride, out_token_stride;
+  int32_t n_heads;
+} upipe_rope_tensor_t;
+/* positions: device int32 [n_axes][tokens].  k: NULL, or turned in the same launch. */
+upipe_status_t upipe_attn_rope(const upipe_rope_desc_t* desc, int64_t tokens, const int32_t* positions,
+                               const upipe_rope_tensor_t* q, const upipe_rope_tensor_t* k, void* stream);
+
+/* Global norm of many gradient tensors and clipping by it:
+ *   norm = sqrt(sum over all tensors of g^2),   out = g * min(1, max_norm / (norm + 1e-6))
+ * A norm that is not finite (an infinity or NaN among the gradients) scales nothing: read it and skip
+ * the step.  max_norm may be infinity (the norm alone).  The norm depends on the tensors and their order
+ * alone (no atomics); values whose squares leave fp32's range count in full.
+ *   grad   device, n elements of grad_dtype (0: fp32, 1: bf16); NULL only where n is 0
+ *   out    NULL: grad is scaled in place (not written where the factor is 1); else device, n elements of
+ *          out_dtype, and grad is left as it is
+ *   norm   device fp32 [1] (written)
+ *   ws     device workspace of upipe_attn_grad_clip_workspace_size(count) bytes
+ * A list whose buffers overlap (a tensor listed twice) is rejected with UPIPE_ERR_INVALID_ARG. */
+typedef struct {
+  const void* grad;
+  void* out;
+  int64_t n;
+  int32_t grad_dtype, out_dtype;
+} upipe_grad_tensor_t;
+upipe_status_t upipe_attn_grad_clip_workspace_size(int32_t count, size_t* bytes);
+upipe_status_t upipe_attn_grad_clip(const upipe_grad_tensor_t* tensors, int32_t count, float max_norm, float* norm,
+                                    void* ws, size_t ws_bytes, void* stream);
+
 /* Reads the device error word of a workspace (after fwd/bwd) or of a table (after
  * build_tile_table) into *code (a upipe_status_t value; UPIPE_OK when none).  Synchronises
  * `stream`.  `buf` is the workspace or the table.  No counterpart on the pages. */

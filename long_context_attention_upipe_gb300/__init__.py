@@ -28,7 +28,9 @@ EXPORTS = ["upipe_attn_status_string", "upipe_attn_last_error_string", "upipe_at
            "upipe_attn_workspace_size_offload", "upipe_attn_fwd_offload", "upipe_attn_bwd_offload",
            "upipe_attn_set_wait_limit_ns", "upipe_attn_set_dkdv_window", "upipe_attn_wait_probe", "upipe_mlp_workspace_size", "upipe_mlp_fwd",
            "upipe_mlp_bwd", "upipe_attn_ring_tables_size", "upipe_attn_ring_build_tables", "upipe_attn_ring_fwd_step",
-           "upipe_attn_ring_bwd_step", "upipe_attn_ring_fwd", "upipe_attn_ring_bwd"]
+           "upipe_attn_ring_bwd_step", "upipe_attn_ring_fwd", "upipe_attn_ring_bwd", "upipe_attn_rms_norm_fwd",
+           "upipe_attn_rms_norm_workspace_size", "upipe_attn_rms_norm_bwd", "upipe_attn_fp8_quantize",
+           "upipe_attn_gemm_fp8_nt", "upipe_attn_rope", "upipe_attn_grad_clip_workspace_size", "upipe_attn_grad_clip"]
 
 # kinds of the per-launch timing records (upipe_attn_timing_collect)
 KERNEL_KINDS = {0: "tile_table", 1: "qkv_proj", 2: "attn_fwd", 3: "o_proj", 4: "convert", 5: "do_proj",
@@ -78,6 +80,40 @@ class TimingRec(ctypes.Structure):
     _fields_ = [("kind", ctypes.c_int32), ("epilogue", ctypes.c_int32), ("split_k", ctypes.c_int32),
                 ("chunk", ctypes.c_int32), ("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64),
                 ("ms", ctypes.c_float), ("start_ms", ctypes.c_float)]
+
+
+ROPE_MAX_PAIRS = 128
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("adjacent", ctypes.c_int32), ("inverse", ctypes.c_int32), ("axis", ctypes.c_uint8 * ROPE_MAX_PAIRS),
+                ("inv_freq", ctypes.c_double * ROPE_MAX_PAIRS)]
+
+
+class RopeTensor(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("in_head_stride", ctypes.c_int64),
+                ("in_token_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("out_token_stride", ctypes.c_int64), ("n_heads", ctypes.c_int32)]
+
+
+def make_rope_desc(head_dim, inv_freq, axis=None, adjacent=False) -> RopeDesc:
+    """Rotary description of a model: inv_freq[j] is pair j's angle per unit of position (rotary_dim =
+    2 * len(inv_freq)), axis[j] the row of positions that it reads (None: one row).  adjacent: pairs
+    (2j, 2j + 1) instead of (j, j + rotary_dim / 2)."""
+    n = len(inv_freq)
+    axis = [0] * n if axis is None else list(axis)
+    if n > ROPE_MAX_PAIRS or len(axis) != n or any(not 0 <= a < 4 for a in axis):
+        raise UpipeError(1, "make_rope_desc")
+    d = RopeDesc(int(head_dim), 2 * n, max(axis, default=0) + 1, int(bool(adjacent)), 0)
+    for j in range(n):
+        d.axis[j], d.inv_freq[j] = int(axis[j]), float(inv_freq[j])
+    return d
+
+
+class GradTensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("grad_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
 
 class UpipeError(RuntimeError):
@@ -138,6 +174,16 @@ def lib():
                                          ctypes.c_int),
             "upipe_attn_ring_bwd_step": ([ctypes.POINTER(RingDesc), ctypes.c_int32, P, P, P, P, P, P, P, P, P, P, P,
                                           P, P, P], ctypes.c_int),
+            "upipe_attn_rms_norm_fwd": ([I64, I64, ctypes.c_float, P, P, P, P, P, P, P, P, P], ctypes.c_int),
+            "upipe_attn_rms_norm_workspace_size": ([I64, I64, ctypes.POINTER(SZ)], ctypes.c_int),
+            "upipe_attn_rms_norm_bwd": ([I64, I64, P, P, P, P, P, P, P, P, SZ, P], ctypes.c_int),
+            "upipe_attn_fp8_quantize": ([I64, I64, ctypes.c_int32, P, P, P, P], ctypes.c_int),
+            "upipe_attn_gemm_fp8_nt": ([I64, I64, I64, P, I64, P, I64, P, I64, P, P, I64, ctypes.c_int32, P], ctypes.c_int),
+            "upipe_attn_rope": ([ctypes.POINTER(RopeDesc), I64, P, ctypes.POINTER(RopeTensor), ctypes.POINTER(RopeTensor),
+                                 P], ctypes.c_int),
+            "upipe_attn_grad_clip_workspace_size": ([ctypes.c_int32, ctypes.POINTER(SZ)], ctypes.c_int),
+            "upipe_attn_grad_clip": ([ctypes.POINTER(GradTensor), ctypes.c_int32, ctypes.c_float, P, P, SZ, P],
+                                     ctypes.c_int),
             "upipe_attn_ring_fwd": ([ctypes.POINTER(RingDesc), P, P, P, P, P, P, P, P, P], ctypes.c_int),
             "upipe_attn_ring_bwd": ([ctypes.POINTER(RingDesc), P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P],
                                     ctypes.c_int),
@@ -363,6 +409,166 @@ def lse_merge(O_b, lse_b, O_acc, lse_acc, O_out=None, stream=None):
     rows = lse_b.numel()
     _check(lib().upipe_attn_lse_merge(rows, Dh, _bf16(O_b), _ptr(lse_b), _ptr(O_acc), _ptr(lse_acc),
                                       _bf16(O_out) if O_out is not None else None, _stream(stream)), "lse_merge")
+
+
+# ------------------------------------------------------------------------------------------------
+# Operators around the two blocks
+# ------------------------------------------------------------------------------------------------
+
+def _refuse(what):
+    raise ValueError(what)
+
+
+def _dev(t, dtype, shape, what):
+    """Address of a contiguous tensor of the given type and shape on the current device."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        _refuse(f"{what}: a tensor on the current CUDA device expected, got {t.device}")
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        _refuse(f"{what}: contiguous {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _opt(t, dtype, shape, what):
+    return None if t is None else _dev(t, dtype, shape, what)
+
+
+def _rms_norm(x, w, y, q, scales, rstd, residual, h, eps, stream):
+    if x.dim() != 2:
+        _refuse(f"rms_norm: x of [rows, d] expected, got {tuple(x.shape)}")
+    n, d = shape = x.shape
+    b = torch.bfloat16
+    _check(lib().upipe_attn_rms_norm_fwd(
+        n, d, eps, _dev(x, b, shape, "x"), _opt(residual, b, shape, "residual"), _dev(w, b, (d,), "w"),
+        _opt(h, b, shape, "h"), _opt(y, b, shape, "y"), _opt(q, torch.float8_e4m3fn, shape, "q"),
+        _opt(scales, torch.float32, (-(-d // 128), n), "scales"), _opt(rstd, torch.float32, (n,), "rstd"),
+        _stream(stream)), "rms_norm_fwd")
+
+
+def rms_norm_fwd(x, w, y, rstd=None, residual=None, h=None, eps=1e-5, stream=None):
+    """y = h * rstd * w with h = x + residual (written to h), rstd = 1 / sqrt(mean(h^2) + eps); bf16 [rows, d],
+    rstd fp32 [rows] (upipe_attn_rms_norm_fwd)."""
+    _rms_norm(x, w, y, None, None, rstd, residual, h, eps, stream)
+
+
+def rms_norm_fwd_fp8(x, w, q, scales, rstd=None, residual=None, h=None, eps=1e-5, y=None, stream=None):
+    """rms_norm_fwd into q, e4m3 [rows, d], with scales, fp32 [ceil(d / 128), rows]: the A operand of
+    gemm_fp8_nt.  y, optional, receives the bf16 output as well."""
+    if q is None or scales is None:
+        _refuse("rms_norm_fwd_fp8: q and scales expected")
+    _rms_norm(x, w, y, q, scales, rstd, residual, h, eps, stream)
+
+
+def rms_norm_workspace_bytes(rows, d) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().upipe_attn_rms_norm_workspace_size(rows, d, ctypes.byref(n)), "rms_norm_workspace_size")
+    return n.value
+
+
+def rms_norm_bwd(dy, h, w, rstd, dx, dw, ws, dres=None, stream=None):
+    """Gradients of rms_norm_fwd: dx bf16 [rows, d] (of x and residual alike, dres added), dw fp32 [d] (written)."""
+    if dy.dim() != 2:
+        _refuse(f"rms_norm_bwd: dy of [rows, d] expected, got {tuple(dy.shape)}")
+    n, d = shape = dy.shape
+    b, f = torch.bfloat16, torch.float32
+    _check(lib().upipe_attn_rms_norm_bwd(
+        n, d, _dev(dy, b, shape, "dy"), _dev(h, b, shape, "h"), _dev(w, b, (d,), "w"), _dev(rstd, f, (n,), "rstd"),
+        _opt(dres, b, shape, "dres"), _dev(dx, b, shape, "dx"), _dev(dw, f, (d,), "dw"), _dev(ws, torch.uint8, ws.shape, "ws"),
+        ws.numel(), _stream(stream)), "rms_norm_bwd")
+
+
+def fp8_quantize(x, q, scales, block_rows=1, stream=None):
+    """bf16 x [rows, cols] to e4m3 q with fp32 scales: block_rows 1 (activations) [ceil(cols / 128), rows],
+    128 (weights) [ceil(rows / 128), ceil(cols / 128)]."""
+    if x.dim() != 2 or block_rows not in (1, 128):
+        _refuse(f"fp8_quantize: x of [rows, cols] and block_rows 1 or 128 expected, got {tuple(x.shape)}, {block_rows}")
+    rows, cols = x.shape
+    nb = -(-cols // 128)
+    _check(lib().upipe_attn_fp8_quantize(
+        rows, cols, block_rows, _dev(x, torch.bfloat16, x.shape, "x"), _dev(q, torch.float8_e4m3fn, x.shape, "q"),
+        _dev(scales, torch.float32, (nb, rows) if block_rows == 1 else (-(-rows // 128), nb), "scales"), _stream(stream)),
+        "fp8_quantize")
+
+
+def _rows(t, dtype, shape, what):
+    """Address and row stride of a matrix whose rows are contiguous, on the current device."""
+    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+        _refuse(f"{what}: a tensor on the current CUDA device expected, got {t.device}")
+    if t.dtype not in dtype or tuple(t.shape) != tuple(shape) or (t.shape[1] > 1 and t.stride(1) != 1):
+        _refuse(f"{what}: {dtype} {tuple(shape)} with contiguous rows expected, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def gemm_fp8_nt(A, a_scale, B, b_scale, C, stream=None):
+    """C [M, N] (bf16 or fp32) = A [M, K] B [N, K]^T, e4m3 with a_scale fp32 [ceil(K / 128), M] and b_scale
+    fp32 [ceil(N / 128), ceil(K / 128)] (upipe_attn_gemm_fp8_nt).  A, B, C and a_scale may be row slices."""
+    if A.dim() != 2 or B.dim() != 2:
+        _refuse("gemm_fp8_nt: matrices expected")
+    (M, K), N = A.shape, B.shape[0]
+    e4m3, f = (torch.float8_e4m3fn,), torch.float32
+    nkb = -(-K // 128)
+    a, lda = _rows(A, e4m3, (M, K), "A")
+    b, ldb = _rows(B, e4m3, (N, K), "B")
+    c, ldc = _rows(C, (torch.bfloat16, f), (M, N), "C")
+    s, lds = _rows(a_scale, (f,), (nkb, M), "a_scale")
+    _check(lib().upipe_attn_gemm_fp8_nt(M, N, K, a, max(lda, K), s, max(lds, M), b, max(ldb, K),
+                                        _dev(b_scale, f, (-(-N // 128), nkb), "b_scale"), c, max(ldc, N),
+                                        int(C.dtype == torch.bfloat16), _stream(stream)), "gemm_fp8_nt")
+
+
+def _rope_tensor(x, out, head_dim, tokens, what):
+    for t in (x, out):
+        if not t.is_cuda or t.device.index != torch.cuda.current_device():
+            _refuse(f"rope: {what} on the current CUDA device expected, got {t.device}")
+        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape != x.shape or t.shape[1:] != (tokens, head_dim) or t.stride(2) != 1:
+            _refuse(f"rope: {what} of bf16 [heads, {tokens}, {head_dim}] with contiguous rows expected, got {t.dtype} "
+                    f"{tuple(t.shape)}")
+    return RopeTensor(x.data_ptr(), out.data_ptr(), x.stride(0), x.stride(1), out.stride(0), out.stride(1), x.shape[0])
+
+
+def rope(desc: RopeDesc, q, k, positions, q_out, k_out, inverse=False, stream=None):
+    """Rotary positions: q [Hq, tokens, head_dim] and k (or None) turned into q_out, k_out (which may be q, k),
+    any head and token strides; positions int32 [n_axes, tokens].  inverse: the backward pass."""
+    tokens = q.shape[1] if q.dim() == 3 else -1
+    qt = _rope_tensor(q, q_out, desc.head_dim, tokens, "q")
+    kt = None if k is None else _rope_tensor(k, k_out, desc.head_dim, tokens, "k")
+    pos = _dev(positions, torch.int32, (desc.n_axes, tokens), "positions")
+    if desc.inverse != int(inverse):
+        desc = RopeDesc.from_buffer_copy(desc)
+        desc.inverse = int(inverse)
+    _check(lib().upipe_attn_rope(ctypes.byref(desc), tokens, pos, ctypes.byref(qt),
+                                 None if kt is None else ctypes.byref(kt), _stream(stream)), "rope")
+
+
+class GradClip:
+    """Global gradient norm and clipping of a list of tensors (fp32 or bf16, contiguous), in place or into
+    `outs`; owns the workspace and the norm (upipe_attn_grad_clip).  The list is fixed: gradients are
+    buffers that every step writes again."""
+
+    def __init__(self, grads, outs=None):
+        self.grads = list(grads)
+        self.outs = None if outs is None else list(outs)
+        if self.outs is not None and len(self.outs) != len(self.grads):
+            _refuse(f"GradClip: {len(self.grads)} outputs expected, got {len(self.outs)}")
+        kinds = {torch.float32: 0, torch.bfloat16: 1}
+        self._list = (GradTensor * max(1, len(self.grads)))()
+        for i, g in enumerate(self.grads):
+            o = None if self.outs is None else self.outs[i]
+            for t in (g,) if o is None else (g, o):
+                if t.dtype not in kinds:
+                    _refuse(f"GradClip: fp32 or bf16 expected, got {t.dtype}")
+                _dev(t, t.dtype, g.shape, "GradClip")
+            self._list[i] = GradTensor(g.data_ptr(), None if o is None else o.data_ptr(), g.numel(), kinds[g.dtype],
+                                       0 if o is None else kinds[o.dtype])
+        n = ctypes.c_size_t(0)
+        _check(lib().upipe_attn_grad_clip_workspace_size(len(self.grads), ctypes.byref(n)), "grad_clip_workspace_size")
+        self.ws = torch.empty(n.value, dtype=torch.uint8, device="cuda")
+        self.norm = torch.zeros(1, dtype=torch.float32, device="cuda")
+
+    def __call__(self, max_norm, stream=None):
+        """Clips to max_norm (math.inf: the norm alone); returns the norm, fp32 [1] on the device."""
+        _check(lib().upipe_attn_grad_clip(self._list, len(self.grads), max_norm, self.norm.data_ptr(), self.ws.data_ptr(),
+                                          self.ws.numel(), _stream(stream)), "grad_clip")
+        return self.norm
 
 
 # ------------------------------------------------------------------------------------------------

@@ -1,0 +1,239 @@
+// C-ABI entry points of the operators around the attention layer and the MLP: argument checks on the
+// host, then one or two launches.  Nothing throws: the only allocation is the sort of grad_clip's
+// ranges, and its failure becomes a status.
+#include <cmath>
+#include <new>
+#include <algorithm>
+#include <vector>
+
+#include "common.cuh"
+#include "internal.h"
+
+using namespace upipe;
+
+namespace {
+
+constexpr int64_t kMaxNormCols = 32768;
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// Two buffers that share some bytes without being the same buffer.
+bool overlaps(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+}
+bool partly_overlaps(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
+  return a != b && overlaps(a, a_bytes, b, b_bytes);
+}
+
+upipe_status_t check_norm(int64_t rows, int64_t d) {
+  if (rows < 0 || rows > INT32_MAX || d <= 0) return UPIPE_ERR_INVALID_ARG;
+  if (d % 8 || d > kMaxNormCols) return UPIPE_ERR_UNSUPPORTED;
+  return UPIPE_OK;
+}
+
+// Rows of `elems` elements of a [heads][tokens] tensor with the given strides: whether no two rows
+// share an element.
+bool rows_disjoint(int64_t heads, int64_t tokens, int64_t hs, int64_t ts, int64_t elems) {
+  if (heads <= 1 && tokens <= 1) return true;
+  if (heads <= 1) return ts >= elems;
+  if (tokens <= 1) return hs >= elems;
+  const bool head_outer = hs >= ts;
+  const int64_t in = head_outer ? ts : hs, n_in = head_outer ? tokens : heads, outer = head_outer ? hs : ts;
+  return in >= elems && outer >= in * (n_in - 1) + elems;
+}
+
+int64_t span_bytes(int64_t heads, int64_t tokens, int64_t hs, int64_t ts, int64_t elems) {
+  return 2 * ((heads - 1) * hs + (tokens - 1) * ts + elems);
+}
+
+upipe_status_t check_rope_side(const upipe_rope_tensor_t* t, int64_t tokens, int head_dim) {
+  if (t->n_heads < 0) return UPIPE_ERR_INVALID_ARG;
+  if (t->n_heads == 0) return UPIPE_OK;
+  if (!t->in || !t->out) return UPIPE_ERR_INVALID_ARG;
+  if (t->in_head_stride < 0 || t->in_token_stride < 0 || t->out_head_stride < 0 || t->out_token_stride < 0)
+    return UPIPE_ERR_INVALID_ARG;
+  if (!rows_disjoint(t->n_heads, tokens, t->out_head_stride, t->out_token_stride, head_dim)) return UPIPE_ERR_INVALID_ARG;
+  if (t->in_head_stride % 8 || t->in_token_stride % 8 || t->out_head_stride % 8 || t->out_token_stride % 8)
+    return UPIPE_ERR_UNSUPPORTED;
+  if (!aligned16(t->in) || !aligned16(t->out)) return UPIPE_ERR_ALIGNMENT;
+  const bool same = t->in == t->out && (t->n_heads == 1 || t->in_head_stride == t->out_head_stride) &&
+                    (tokens == 1 || t->in_token_stride == t->out_token_stride);
+  if (!same &&
+      overlaps(t->in, span_bytes(t->n_heads, tokens, t->in_head_stride, t->in_token_stride, head_dim), t->out,
+               span_bytes(t->n_heads, tokens, t->out_head_stride, t->out_token_stride, head_dim)))
+    return UPIPE_ERR_INVALID_ARG;
+  return UPIPE_OK;
+}
+
+RopeTensor rope_side(const upipe_rope_tensor_t* t) {
+  if (!t || t->n_heads == 0) return RopeTensor{};
+  return RopeTensor{reinterpret_cast<const bf16*>(t->in), reinterpret_cast<bf16*>(t->out), t->in_head_stride,
+                    t->in_token_stride, t->out_head_stride, t->out_token_stride, t->n_heads};
+}
+
+}  // namespace
+
+extern "C" {
+
+upipe_status_t upipe_attn_rms_norm_fwd(int64_t rows, int64_t d, float eps, const uint16_t* x, const uint16_t* residual,
+                                       const uint16_t* w, uint16_t* h, uint16_t* y, uint8_t* q, float* scales,
+                                       float* rstd, void* stream) {
+  upipe_status_t s = check_norm(rows, d);
+  if (s != UPIPE_OK) return s;
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return UPIPE_ERR_INVALID_ARG;
+  if (rows == 0) return UPIPE_OK;  // buffers of no elements may be NULL
+  if (!x || !w || (!y && !q) || (!q != !scales) || (!residual != !h)) return UPIPE_ERR_INVALID_ARG;
+  if (q && d % 16) return UPIPE_ERR_UNSUPPORTED;
+  if (!aligned16(x) || !aligned16(residual) || !aligned16(w) || !aligned16(h) || !aligned16(y) || !aligned16(q) ||
+      !aligned16(scales) || !aligned16(rstd))
+    return UPIPE_ERR_ALIGNMENT;
+  const int64_t n = rows * d * 2;
+  const int64_t sb = (d + 127) / 128 * rows * 4;
+  // an output may take the place of an input of its own size; nothing else may share memory
+  if (partly_overlaps(h, n, x, n) || partly_overlaps(h, n, residual, n) || partly_overlaps(y, n, x, n) ||
+      partly_overlaps(y, n, residual, n) || overlaps(y, n, h, n) || overlaps(q, n / 2, x, n) ||
+      overlaps(q, n / 2, residual, n) || overlaps(q, n / 2, h, n) || overlaps(q, n / 2, y, n) ||
+      overlaps(scales, sb, q, n / 2))
+    return UPIPE_ERR_INVALID_ARG;
+  RmsNormArgs a{rows, (int)d, eps, reinterpret_cast<const bf16*>(x), reinterpret_cast<const bf16*>(residual),
+                reinterpret_cast<const bf16*>(w), reinterpret_cast<bf16*>(h), reinterpret_cast<bf16*>(y), q, scales, rstd};
+  return cuda_status(launch_rms_fwd(a, (cudaStream_t)stream));
+}
+
+upipe_status_t upipe_attn_rms_norm_workspace_size(int64_t rows, int64_t d, size_t* bytes) {
+  upipe_status_t s = check_norm(rows, d);
+  if (s != UPIPE_OK) return s;
+  if (!bytes) return UPIPE_ERR_INVALID_ARG;
+  *bytes = rms_bwd_workspace(rows, (int)d);
+  return UPIPE_OK;
+}
+
+upipe_status_t upipe_attn_rms_norm_bwd(int64_t rows, int64_t d, const uint16_t* dy, const uint16_t* h, const uint16_t* w,
+                                       const float* rstd, const uint16_t* dres, uint16_t* dx, float* dw, void* ws,
+                                       size_t ws_bytes, void* stream) {
+  upipe_status_t s = check_norm(rows, d);
+  if (s != UPIPE_OK) return s;
+  if (!w || !dw || !ws || (rows && (!dy || !h || !rstd || !dx))) return UPIPE_ERR_INVALID_ARG;
+  if (!aligned16(dy) || !aligned16(h) || !aligned16(w) || !aligned16(rstd) || !aligned16(dres) || !aligned16(dx) ||
+      !aligned16(dw) || !aligned16(ws))
+    return UPIPE_ERR_ALIGNMENT;
+  if (ws_bytes < rms_bwd_workspace(rows, (int)d)) return UPIPE_ERR_WORKSPACE_TOO_SMALL;
+  const int64_t n = rows * d * 2;
+  if (partly_overlaps(dx, n, dy, n) || partly_overlaps(dx, n, h, n) || partly_overlaps(dx, n, dres, n))
+    return UPIPE_ERR_INVALID_ARG;
+  RmsNormBwdArgs a{rows, (int)d, reinterpret_cast<const bf16*>(dy), reinterpret_cast<const bf16*>(h),
+                   reinterpret_cast<const bf16*>(w), rstd, reinterpret_cast<const bf16*>(dres),
+                   reinterpret_cast<bf16*>(dx), dw};
+  return cuda_status(launch_rms_bwd(a, reinterpret_cast<float*>(ws), (cudaStream_t)stream));
+}
+
+upipe_status_t upipe_attn_fp8_quantize(int64_t rows, int64_t cols, int32_t block_rows, const uint16_t* x, uint8_t* q,
+                                       float* scales, void* stream) {
+  if (rows < 0 || rows > INT32_MAX || cols <= 0 || cols > INT32_MAX - 128) return UPIPE_ERR_INVALID_ARG;
+  if (block_rows != 1 && block_rows != 128) return UPIPE_ERR_INVALID_ARG;
+  if (cols % 16) return UPIPE_ERR_UNSUPPORTED;
+  if (rows == 0) return UPIPE_OK;
+  if (!x || !q || !scales) return UPIPE_ERR_INVALID_ARG;
+  if (ceil_div(rows, 128) * ceil_div(cols, 128) > INT32_MAX) return UPIPE_ERR_UNSUPPORTED;
+  if (!aligned16(x) || !aligned16(q) || !aligned16(scales)) return UPIPE_ERR_ALIGNMENT;
+  if (overlaps(q, rows * cols, x, 2 * rows * cols)) return UPIPE_ERR_INVALID_ARG;
+  return cuda_status(launch_quantize(rows, (int)cols, block_rows, reinterpret_cast<const bf16*>(x), q, scales,
+                                     (cudaStream_t)stream));
+}
+
+upipe_status_t upipe_attn_rope(const upipe_rope_desc_t* desc, int64_t tokens, const int32_t* positions,
+                               const upipe_rope_tensor_t* q, const upipe_rope_tensor_t* k, void* stream) {
+  if (!desc || !q || tokens < 0 || tokens > INT32_MAX) return UPIPE_ERR_INVALID_ARG;
+  const int R = desc->rotary_dim;
+  if (desc->head_dim <= 0 || R <= 0 || R > desc->head_dim || desc->n_axes < 1 || desc->n_axes > 4 ||
+      (desc->adjacent != 0 && desc->adjacent != 1) || (desc->inverse != 0 && desc->inverse != 1))
+    return UPIPE_ERR_INVALID_ARG;
+  if (desc->head_dim % 16 || R % 16 || desc->head_dim > 2 * kRopeMaxPairs) return UPIPE_ERR_UNSUPPORTED;
+  for (int j = 0; j < R / 2; ++j)
+    if (!std::isfinite(desc->inv_freq[j]) || desc->axis[j] >= desc->n_axes) return UPIPE_ERR_INVALID_ARG;
+  if (tokens == 0) return UPIPE_OK;
+  if (!positions) return UPIPE_ERR_INVALID_ARG;
+  upipe_status_t s = check_rope_side(q, tokens, desc->head_dim);
+  if (s == UPIPE_OK && k) s = check_rope_side(k, tokens, desc->head_dim);
+  if (s != UPIPE_OK) return s;
+  if (q->n_heads > 65535 - (k ? k->n_heads : 0)) return UPIPE_ERR_UNSUPPORTED;
+  if (!aligned16(positions)) return UPIPE_ERR_ALIGNMENT;
+  RopeArgs a{};
+  a.head_dim = desc->head_dim;
+  a.rotary_dim = R;
+  a.n_axes = desc->n_axes;
+  a.adjacent = desc->adjacent;
+  a.inverse = desc->inverse;
+  a.inv_freq = desc->inv_freq;
+  a.axis = desc->axis;
+  a.tokens = tokens;
+  a.pos = positions;
+  a.side[0] = rope_side(q);
+  a.side[1] = rope_side(k);
+  return cuda_status(launch_rope(a, (cudaStream_t)stream));
+}
+
+upipe_status_t upipe_attn_grad_clip_workspace_size(int32_t count, size_t* bytes) {
+  if (count < 0 || !bytes) return UPIPE_ERR_INVALID_ARG;
+  *bytes = grad_clip_workspace(count);
+  return UPIPE_OK;
+}
+
+upipe_status_t upipe_attn_grad_clip(const upipe_grad_tensor_t* tensors, int32_t count, float max_norm, float* norm,
+                                    void* ws, size_t ws_bytes, void* stream) {
+  if (count < 0 || (count > 0 && !tensors) || !norm || !ws || !(max_norm > 0.f)) return UPIPE_ERR_INVALID_ARG;
+  if (!aligned16(norm) || !aligned16(ws)) return UPIPE_ERR_ALIGNMENT;
+  if (ws_bytes < grad_clip_workspace(count)) return UPIPE_ERR_WORKSPACE_TOO_SMALL;
+  try {
+    struct Range { uintptr_t lo, hi; int tensor; };
+    std::vector<GradTensor> t((size_t)count);
+    std::vector<int> idx;
+    std::vector<Range> r;
+    idx.reserve((size_t)count);
+    r.reserve(2 * (size_t)count);
+    for (int i = 0; i < count; ++i) {
+      const upipe_grad_tensor_t& e = tensors[i];
+      if (e.n < 0 || e.n > (int64_t)1 << 42 || e.grad_dtype < 0 || e.grad_dtype > 1 || e.out_dtype < 0 || e.out_dtype > 1)
+        return UPIPE_ERR_INVALID_ARG;
+      if (e.n == 0) continue;
+      void* out = e.out ? e.out : const_cast<void*>(e.grad);
+      const int out_dtype = e.out ? e.out_dtype : e.grad_dtype;
+      if (!e.grad || (out == e.grad && out_dtype != e.grad_dtype)) return UPIPE_ERR_INVALID_ARG;
+      if (!aligned16(e.grad) || !aligned16(out)) return UPIPE_ERR_ALIGNMENT;
+      t[i] = GradTensor{e.grad, out, e.n, e.grad_dtype, out_dtype};
+      idx.push_back(i);
+      const uintptr_t g = reinterpret_cast<uintptr_t>(e.grad), o = reinterpret_cast<uintptr_t>(out);
+      r.push_back(Range{g, g + (uintptr_t)(e.n * (e.grad_dtype ? 2 : 4)), i});
+      if (o != g) r.push_back(Range{o, o + (uintptr_t)(e.n * (out_dtype ? 2 : 4)), i});
+    }
+    // a tensor listed twice would be scaled twice, by blocks that race
+    std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
+    for (size_t i = 1; i < r.size(); ++i)
+      if (r[i].lo < r[i - 1].hi) return UPIPE_ERR_INVALID_ARG;
+    return cuda_status(launch_grad_clip(t.data(), idx.data(), (int)idx.size(), max_norm, norm,
+                                        reinterpret_cast<double*>(ws), (cudaStream_t)stream));
+  } catch (const std::bad_alloc&) {
+    return cuda_status(cudaErrorMemoryAllocation);
+  }
+}
+
+upipe_status_t upipe_attn_gemm_fp8_nt(int64_t M, int64_t N, int64_t K, const uint8_t* A, int64_t lda,
+                                      const float* a_scale, int64_t a_scale_ld, const uint8_t* B, int64_t ldb,
+                                      const float* b_scale, void* C, int64_t ldc, int32_t c_dtype, void* stream) {
+  if (M < 0 || N <= 0 || K <= 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX || lda < K || ldb < K || ldc < N ||
+      a_scale_ld < M || (c_dtype != 0 && c_dtype != 1))
+    return UPIPE_ERR_INVALID_ARG;
+  if (K % 16 || N % 8 || lda % 16 || ldb % 16 || ldc % 8) return UPIPE_ERR_UNSUPPORTED;
+  if (M == 0) return UPIPE_OK;
+  if (!A || !a_scale || !B || !b_scale || !C) return UPIPE_ERR_INVALID_ARG;
+  if (!aligned16(A) || !aligned16(B) || !aligned16(C) || !aligned16(a_scale) || !aligned16(b_scale))
+    return UPIPE_ERR_ALIGNMENT;
+  const int64_t c_bytes = ((M - 1) * ldc + N) * (c_dtype ? 2 : 4);
+  if (overlaps(C, c_bytes, A, (M - 1) * lda + K) || overlaps(C, c_bytes, B, (N - 1) * ldb + K))
+    return UPIPE_ERR_INVALID_ARG;
+  const Fp8GemmArgs g{M, N, K, A, lda, a_scale, a_scale_ld, B, ldb, b_scale, C, ldc, c_dtype};
+  return cuda_status(launch_gemm_fp8(g, (cudaStream_t)stream));
+}
+
+}  // extern "C"

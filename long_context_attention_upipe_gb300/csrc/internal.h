@@ -217,4 +217,82 @@ cudaError_t launch_swiglu_fwd(const bf16* H, bf16* A, int64_t rows, int64_t F, c
 cudaError_t launch_swiglu_bwd(const bf16* H, const bf16* dA, bf16* A, bf16* dH, int64_t rows, int64_t F,
                               cudaStream_t st);
 
+// ---------------------------------------------------------------- operators around the two blocks
+// SMs of the device that was current at the first call (every launch sizes its grid with it).
+int sm_count();
+// Status of a CUDA runtime call; keeps the error's name for upipe_attn_last_error_string.
+upipe_status_t cuda_status(cudaError_t e);
+
+struct RmsNormArgs {
+  int64_t rows;
+  int d;
+  float eps;
+  const bf16 *x, *res, *w;  // res: NULL, or added to x
+  bf16* h;                  // x + res (with res)
+  bf16* y;                  // NULL with q: no bf16 output
+  uint8_t* q;               // e4m3 output, or NULL
+  float* scales;            // [ceil(d / 128)][rows], with q
+  float* rstd;              // NULL: not written
+};
+cudaError_t launch_rms_fwd(const RmsNormArgs& a, cudaStream_t st);
+
+struct RmsNormBwdArgs {
+  int64_t rows;
+  int d;
+  const bf16 *dy, *h, *w;
+  const float* rstd;
+  const bf16* dres;  // NULL, or added to dx
+  bf16* dx;
+  float* dw;
+};
+size_t rms_bwd_workspace(int64_t rows, int d);
+cudaError_t launch_rms_bwd(const RmsNormBwdArgs& a, float* part, cudaStream_t st);
+
+cudaError_t launch_quantize(int64_t rows, int d, int block_rows, const bf16* x, uint8_t* q, float* scales,
+                            cudaStream_t st);
+
+// C = sum over 128-column blocks of K of a_scale[kb][m] b_scale[n / 128][kb] (A_kb B_kb^T), e4m3 operands.
+struct Fp8GemmArgs {
+  int64_t M, N, K;
+  const uint8_t* A;      // [M, K], rows of lda bytes
+  int64_t lda;
+  const float* sa;       // [ceil(K / 128)] rows of lds >= M
+  int64_t lds;
+  const uint8_t* B;      // [N, K], rows of ldb bytes
+  int64_t ldb;
+  const float* sb;       // [ceil(N / 128)][ceil(K / 128)]
+  void* C;               // [M, N], rows of ldc elements
+  int64_t ldc;
+  int c_bf16;            // bf16 output, else fp32
+};
+cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t st);
+
+constexpr int kRopeMaxPairs = 128;
+struct RopeTensor {
+  const bf16* in;
+  bf16* out;
+  int64_t in_head, in_tok, out_head, out_tok;  // strides in elements
+  int heads;
+};
+struct RopeArgs {
+  int head_dim, rotary_dim, n_axes, adjacent, inverse;
+  const double* inv_freq;  // host, rotary_dim / 2
+  const uint8_t* axis;     // host, rotary_dim / 2
+  int64_t tokens;
+  const int32_t* pos;      // device [n_axes][tokens]
+  RopeTensor side[2];      // queries, keys (heads 0: absent)
+};
+cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st);
+
+struct GradTensor {
+  const void* grad;
+  void* out;
+  int64_t n;
+  int grad_bf16, out_bf16;
+};
+size_t grad_clip_workspace(int count);
+// The tensors t[idx[0 .. count)] (those with elements).
+cudaError_t launch_grad_clip(const GradTensor* t, const int* idx, int count, float max_norm, float* norm, double* part,
+                             cudaStream_t st);
+
 }  // namespace upipe

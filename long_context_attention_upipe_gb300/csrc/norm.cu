@@ -1,0 +1,400 @@
+// Root-mean-square norm with the residual's addition (forward in bf16 or e4m3, backward), and the
+// e4m3 block quantiser.
+//
+// Forward, per row of d elements:
+//   h = bf16(x + r)                        (without a residual h = x, nothing written)
+//   rstd = (mean(h^2) + eps)^(-1/2),  y = h * rstd * w
+//   y rounded to bf16, or per block of 128 columns  s = max|y| / 448,  q = e4m3(y / s)
+// h is normalised as it is stored, so the backward pass, which reads the stored h, differentiates
+// exactly the function that ran.  Backward, with t = dy * w:
+//   dx = rstd * (t - h * rstd^2 * mean(t * h)) [+ dres],   dw = sum over rows of dy * h * rstd
+// All sums are fp32 (h and dy are bf16, so each product is exact to fp32's last bit); each output is
+// rounded once.
+//
+// A row belongs to a group of `tpr` threads, 8 elements (one 16-byte vector) per thread and step, V
+// steps, kept in registers between the statistics and the output: one read and one write of each
+// tensor, which is what bounds these kernels (HBM).  A 128-column block is 16 neighbouring lanes, so
+// its maximum is four shuffles; maxima are compared as the bits of |y|, which orders NaN above every
+// number, so a NaN reaches its block's scale.
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace upipe {
+
+namespace {
+
+constexpr int kMaxNormThreads = 1024;
+
+struct V8 {
+  float v[8];
+};
+
+__device__ __forceinline__ V8 unpack8(const uint4& q) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&q);
+  V8 f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = __bfloat1622float2(h[i]);
+    f.v[2 * i] = t.x;
+    f.v[2 * i + 1] = t.y;
+  }
+  return f;
+}
+
+__device__ __forceinline__ uint4 pack8(const V8& f) {
+  return make_uint4(pack_bf16(f.v[0], f.v[1]), pack_bf16(f.v[2], f.v[3]), pack_bf16(f.v[4], f.v[5]),
+                    pack_bf16(f.v[6], f.v[7]));
+}
+
+// Bits of the largest magnitude of 8 values (as unsigned integers: NaN > infinity > numbers).
+__device__ __forceinline__ uint32_t amax_bits(const V8& f) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f.v[i]) & 0x7fffffffu);
+  return m;
+}
+
+// Scale of a block whose largest magnitude has the given bits: amax / 448 (as a product with the
+// rounded 1/448), or 1 for a block below 2^-100, whose e4m3 codes are all zero then.
+__device__ __forceinline__ float block_scale(uint32_t bits) {
+  const float amax = __uint_as_float(bits);
+  return amax < 7.888609052210118e-31f ? 1.f : amax * (1.f / 448.f);
+}
+
+// 8 values times the scale's reciprocal, to e4m3 (nearest even, saturating; NaN stays NaN).
+__device__ __forceinline__ uint2 quant8(const V8& f, float inv) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(f.v[2 * i] * inv, f.v[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+// Maximum over the 16 lanes that hold a 128-column block.
+__device__ __forceinline__ uint32_t max16(uint32_t m) {
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+  return m;
+}
+
+// Sum over a group of tpr threads (16, or a multiple of 32), the same for every thread of it.  `red`
+// holds a float per warp of the block; callers alternate between two of them, so one barrier is enough.
+__device__ __forceinline__ float group_sum(float v, int tpr, float* red) {
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  if (tpr == 16) return v;
+  v += __shfl_xor_sync(0xffffffffu, v, 16);
+  if (tpr == 32) return v;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nw = tpr >> 5;
+  const int first = warp / nw * nw;
+  if (lane == 0) red[warp] = v;
+  __syncthreads();
+  v = lane < nw ? red[first + lane] : 0.f;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+struct NormShape {
+  int64_t rows;
+  int d, tpr, rpb;  // columns; threads per row; rows per block
+};
+
+template <int V, bool FP8>
+__global__ void __launch_bounds__(kMaxNormThreads) k_rms_fwd(NormShape n, float eps, const bf16* x, const bf16* res,
+                                                             const bf16* __restrict__ w, bf16* h, bf16* y, uint8_t* q,
+                                                             float* scales, float* rstd_out) {
+  __shared__ float red[2][32];
+  const int g = threadIdx.x / n.tpr, t = threadIdx.x - g * n.tpr;
+  const int nvec = n.d >> 3;
+  uint4 wv[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = t + i * n.tpr;
+    wv[i] = c < nvec ? *reinterpret_cast<const uint4*>(w + c * 8) : make_uint4(0, 0, 0, 0);
+  }
+  int par = 0;
+  // every group of the block makes the same number of turns (group_sum holds a barrier)
+  for (int64_t r0 = (int64_t)blockIdx.x * n.rpb; r0 < n.rows; r0 += (int64_t)gridDim.x * n.rpb, par ^= 1) {
+    const int64_t row = r0 + g;
+    const bool row_ok = row < n.rows;
+    V8 f[V];
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = t + i * n.tpr;
+      const bool ok = row_ok && c < nvec;
+      const int64_t at = row * n.d + c * 8;
+      f[i] = unpack8(ok ? *reinterpret_cast<const uint4*>(x + at) : make_uint4(0, 0, 0, 0));
+      if (res) {
+        const V8 b = unpack8(ok ? *reinterpret_cast<const uint4*>(res + at) : make_uint4(0, 0, 0, 0));
+#pragma unroll
+        for (int k = 0; k < 8; ++k) f[i].v[k] += b.v[k];
+        const uint4 hv = pack8(f[i]);
+        if (ok) *reinterpret_cast<uint4*>(h + at) = hv;
+        f[i] = unpack8(hv);
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) ss += f[i].v[k] * f[i].v[k];
+    }
+    ss = group_sum(ss, n.tpr, red[par]);
+    const float rstd = rsqrtf(ss / (float)n.d + eps);
+    if (rstd_out && row_ok && t == 0) rstd_out[row] = rstd;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = t + i * n.tpr;
+      const bool ok = row_ok && c < nvec;
+      const int64_t at = row * n.d + c * 8;
+      const V8 wf = unpack8(wv[i]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) f[i].v[k] = f[i].v[k] * rstd * wf.v[k];
+      if (!FP8 || y) {
+        if (ok) *reinterpret_cast<uint4*>(y + at) = pack8(f[i]);
+      }
+      if (FP8) {
+        // columns past d of the last block hold zeros (x and w were read as zeros there), unless
+        // rstd is not finite; they must not reach the block's maximum then either
+        const float s = block_scale(max16(ok ? amax_bits(f[i]) : 0u));
+        if (ok) *reinterpret_cast<uint2*>(q + at) = quant8(f[i], __fdividef(1.f, s));
+        if (ok && (t & 15) == 0) scales[(int64_t)(c >> 4) * n.rows + row] = s;
+      }
+    }
+  }
+}
+
+template <int V>
+__global__ void __launch_bounds__(kMaxNormThreads) k_rms_bwd(NormShape n, const bf16* dy, const bf16* h,
+                                                             const bf16* __restrict__ w, const float* __restrict__ rstd_in,
+                                                             const bf16* dres, bf16* dx, float* part) {
+  __shared__ float red[2][32];
+  const int g = threadIdx.x / n.tpr, t = threadIdx.x - g * n.tpr;
+  const int nvec = n.d >> 3;
+  uint4 wv[V];
+  V8 dw[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = t + i * n.tpr;
+    wv[i] = c < nvec ? *reinterpret_cast<const uint4*>(w + c * 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dw[i].v[k] = 0.f;
+  }
+  int par = 0;
+  for (int64_t r0 = (int64_t)blockIdx.x * n.rpb; r0 < n.rows; r0 += (int64_t)gridDim.x * n.rpb, par ^= 1) {
+    const int64_t row = r0 + g;
+    const bool row_ok = row < n.rows;
+    const float rstd = row_ok ? rstd_in[row] : 0.f;
+    uint4 dyv[V], hv[V], rv[V];
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = t + i * n.tpr;
+      const bool ok = row_ok && c < nvec;
+      const int64_t at = row * n.d + c * 8;
+      dyv[i] = ok ? *reinterpret_cast<const uint4*>(dy + at) : make_uint4(0, 0, 0, 0);
+      hv[i] = ok ? *reinterpret_cast<const uint4*>(h + at) : make_uint4(0, 0, 0, 0);
+      rv[i] = ok && dres ? *reinterpret_cast<const uint4*>(dres + at) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const V8 a = unpack8(dyv[i]), b = unpack8(hv[i]), wf = unpack8(wv[i]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        dot += a.v[k] * wf.v[k] * b.v[k];
+        dw[i].v[k] += a.v[k] * (b.v[k] * rstd);
+      }
+    }
+    dot = group_sum(dot, n.tpr, red[par]);
+    const float m = dot / (float)n.d * rstd * rstd;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = t + i * n.tpr;
+      if (!row_ok || c >= nvec) continue;
+      const V8 a = unpack8(dyv[i]), b = unpack8(hv[i]), wf = unpack8(wv[i]), r = unpack8(rv[i]);
+      V8 o;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o.v[k] = r.v[k] + rstd * (a.v[k] * wf.v[k] - b.v[k] * m);
+      *reinterpret_cast<uint4*>(dx + row * n.d + c * 8) = pack8(o);
+    }
+  }
+  // this group's share of dw: row `group` of the partial sums
+  float* dst = part + ((int64_t)blockIdx.x * n.rpb + g) * n.d;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = t + i * n.tpr;
+    if (c >= nvec) continue;
+    *reinterpret_cast<float4*>(dst + c * 8) = make_float4(dw[i].v[0], dw[i].v[1], dw[i].v[2], dw[i].v[3]);
+    *reinterpret_cast<float4*>(dst + c * 8 + 4) = make_float4(dw[i].v[4], dw[i].v[5], dw[i].v[6], dw[i].v[7]);
+  }
+}
+
+// dw[c] = sum over p of part[p][c], in an order that depends on the shape alone: 32 columns per
+// block, 8 warps that each take every 8th partial row, then the warps in turn.
+__global__ void __launch_bounds__(256) k_dw_reduce(const float* __restrict__ part, int p_rows, int d, float* dw) {
+  __shared__ float s[8][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float v = 0.f;
+  if (c < d)
+    for (int p = warp; p < p_rows; p += 8) v += part[(int64_t)p * d + c];
+  s[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && c < d) {
+    for (int i = 1; i < 8; ++i) v += s[i][lane];
+    dw[c] = v;
+  }
+}
+
+// One scale per row and 128 columns: 16 lanes per block, blocks of a row side by side.
+__global__ void __launch_bounds__(256) k_quant_rows(int64_t rows, int d, int nb, const bf16* __restrict__ x, uint8_t* q,
+                                                    float* scales) {
+  const int64_t total = rows * nb;  // (row, block) pairs
+  const int64_t stride = (int64_t)gridDim.x * 16;
+  const int lane16 = threadIdx.x & 15;
+  const int64_t first = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+  const int64_t turns = ceil_div(total, stride);  // the same for every lane: the shuffles need them all
+  for (int64_t k = 0; k < turns; ++k) {
+    const int64_t i = first + k * stride;
+    const int64_t row = i / nb;
+    const int b = (int)(i - row * nb), c = b * 128 + lane16 * 8;
+    const bool ok = i < total && c < d;
+    const V8 f = unpack8(ok ? *reinterpret_cast<const uint4*>(x + row * d + c) : make_uint4(0, 0, 0, 0));
+    const float s = block_scale(max16(amax_bits(f)));
+    if (ok) *reinterpret_cast<uint2*>(q + row * d + c) = quant8(f, __fdividef(1.f, s));
+    if (i < total && lane16 == 0) scales[(int64_t)b * rows + row] = s;
+  }
+}
+
+// One scale per 128 x 128 block: a block of threads per tile, 8 vectors per thread in registers.
+__global__ void __launch_bounds__(256) k_quant_tiles(int64_t rows, int d, int nb, const bf16* __restrict__ x, uint8_t* q,
+                                                     float* scales) {
+  __shared__ uint32_t red[8];
+  const int64_t tile = blockIdx.x;
+  const int64_t tr = tile / nb;
+  const int b = (int)(tile - tr * nb);
+  uint4 v[8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int id = threadIdx.x + 256 * i;
+    const int64_t row = tr * 128 + (id >> 4);
+    const int c = b * 128 + (id & 15) * 8;
+    v[i] = row < rows && c < d ? *reinterpret_cast<const uint4*>(x + row * d + c) : make_uint4(0, 0, 0, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, amax_bits(unpack8(v[i])));
+  m = __reduce_max_sync(0xffffffffu, m);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, red[i]);
+  const float s = block_scale(m), inv = __fdividef(1.f, s);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int id = threadIdx.x + 256 * i;
+    const int64_t row = tr * 128 + (id >> 4);
+    const int c = b * 128 + (id & 15) * 8;
+    if (row < rows && c < d) *reinterpret_cast<uint2*>(q + row * d + c) = quant8(unpack8(v[i]), inv);
+  }
+  if (threadIdx.x == 0) scales[tr * nb + b] = s;
+}
+
+// Threads per row and vectors per thread.  Rows of up to 32 vectors take half a warp or a warp with
+// one vector per thread; longer rows two vectors per thread (four past 2 x 1024 threads).
+NormShape norm_shape(int64_t rows, int d, int& V) {
+  const int nvec = d / 8;
+  NormShape n{rows, d, 0, 1};
+  if (nvec <= 32) {
+    V = 1;
+    n.tpr = nvec <= 16 ? 16 : 32;
+  } else {
+    V = nvec <= 2 * kMaxNormThreads ? 2 : 4;
+    n.tpr = (int)ceil_div(ceil_div(nvec, V), 32) * 32;
+  }
+  n.rpb = std::max(1, 256 / n.tpr);
+  return n;
+}
+
+int64_t norm_blocks(const NormShape& n, int per_sm_threads) {
+  const int threads = n.tpr * n.rpb;
+  const int64_t most = (int64_t)sm_count() * std::max(1, per_sm_threads / threads);
+  return std::max<int64_t>(1, std::min<int64_t>(ceil_div(n.rows, n.rpb), most));
+}
+
+constexpr int kBwdThreadsPerSm = 768;
+
+}  // namespace
+
+int sm_count() {
+  static int sms = 0;
+  if (sms == 0) {
+    int dev = 0, v = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || v <= 0)
+      v = 152;
+    sms = v;
+  }
+  return sms;
+}
+
+cudaError_t launch_rms_fwd(const RmsNormArgs& a, cudaStream_t st) {
+  if (a.rows <= 0) return cudaSuccess;
+  int V = 1;
+  const NormShape n = norm_shape(a.rows, a.d, V);
+  const unsigned blocks = (unsigned)norm_blocks(n, 2048), threads = n.tpr * n.rpb;
+#define UPIPE_RMS_FWD(VV, F8) \
+  k_rms_fwd<VV, F8><<<blocks, threads, 0, st>>>(n, a.eps, a.x, a.res, a.w, a.h, a.y, a.q, a.scales, a.rstd)
+  if (a.q) {
+    if (V == 1) UPIPE_RMS_FWD(1, true);
+    else if (V == 2) UPIPE_RMS_FWD(2, true);
+    else UPIPE_RMS_FWD(4, true);
+  } else {
+    if (V == 1) UPIPE_RMS_FWD(1, false);
+    else if (V == 2) UPIPE_RMS_FWD(2, false);
+    else UPIPE_RMS_FWD(4, false);
+  }
+#undef UPIPE_RMS_FWD
+  note_launch();
+  return cudaGetLastError();
+}
+
+size_t rms_bwd_workspace(int64_t rows, int d) {
+  int V = 1;
+  const NormShape n = norm_shape(std::max<int64_t>(rows, 1), d, V);
+  return (size_t)norm_blocks(n, kBwdThreadsPerSm) * n.rpb * d * sizeof(float);
+}
+
+cudaError_t launch_rms_bwd(const RmsNormBwdArgs& a, float* part, cudaStream_t st) {
+  int p_rows = 0;
+  if (a.rows > 0) {
+    int V = 1;
+    const NormShape n = norm_shape(a.rows, a.d, V);
+    const unsigned blocks = (unsigned)norm_blocks(n, kBwdThreadsPerSm), threads = n.tpr * n.rpb;
+    p_rows = (int)blocks * n.rpb;
+    if (V == 1) k_rms_bwd<1><<<blocks, threads, 0, st>>>(n, a.dy, a.h, a.w, a.rstd, a.dres, a.dx, part);
+    else if (V == 2) k_rms_bwd<2><<<blocks, threads, 0, st>>>(n, a.dy, a.h, a.w, a.rstd, a.dres, a.dx, part);
+    else k_rms_bwd<4><<<blocks, threads, 0, st>>>(n, a.dy, a.h, a.w, a.rstd, a.dres, a.dx, part);
+    note_launch();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  k_dw_reduce<<<(unsigned)ceil_div(a.d, 32), 256, 0, st>>>(part, p_rows, a.d, a.dw);
+  note_launch();
+  return cudaGetLastError();
+}
+
+cudaError_t launch_quantize(int64_t rows, int d, int block_rows, const bf16* x, uint8_t* q, float* scales,
+                            cudaStream_t st) {
+  if (rows <= 0) return cudaSuccess;
+  const int nb = (int)ceil_div(d, 128);
+  if (block_rows == 1) {
+    const int64_t blocks = std::min<int64_t>(ceil_div(rows * nb, 16), (int64_t)sm_count() * 8);
+    k_quant_rows<<<(unsigned)blocks, 256, 0, st>>>(rows, d, nb, x, q, scales);
+  } else {
+    k_quant_tiles<<<(unsigned)(ceil_div(rows, 128) * nb), 256, 0, st>>>(rows, d, nb, x, q, scales);
+  }
+  note_launch();
+  return cudaGetLastError();
+}
+
+}  // namespace upipe
