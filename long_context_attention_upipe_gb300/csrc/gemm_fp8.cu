@@ -152,8 +152,7 @@ __global__ void __launch_bounds__(kSwapThreads) k_gemm_fp8_swap(const __grid_con
 #pragma unroll
         for (int ch = 0; ch < TN / 16; ++ch) {
           uint32_t v[16];
-          tc::tmem_ld16(lane_addr + buf * TN + ch * 16, v);
-          tc::tmem_ld_wait();
+          tc::tmem_ld16_wait(lane_addr + buf * TN + ch * 16, v);
 #pragma unroll
           for (int i = 0; i < 16; i += 4) {
             const float4 s4 = *reinterpret_cast<const float4*>(&sc[buf * TN + ch * 16 + i]);
@@ -202,6 +201,343 @@ cudaError_t run_swap(const Fp8GemmArgs& a, const Fp8Params& p, cudaStream_t st) 
   return cudaGetLastError();
 }
 
+// ------------------------------------------------------------------------------------------------
+// 128 rows of A x BN = 32 NCH columns per CTA, clusters of two CTAs that share the columns
+// ------------------------------------------------------------------------------------------------
+// 12 warps, persistent, one CTA per SM:
+//   warp 0      TMA producer: its CTA's 128 rows of A, and half of the cluster's B tile, multicast to both
+//               CTAs, over a ring of 4 stages
+//   warp 1      MMA issuer: 4 MMAs (M128 BN K32) per block of K into one of two TMEM accumulators
+//   warps 2-3   the blocks' scales, four blocks of K at a time, into a ring in shared memory
+//   warps 4-11  scaling: TMEM lanes 32 * (warp % 4), one half of the columns each, the sums in registers
+// What bounds it is the chain MMA -> accumulator ready -> scaled -> free -> MMA: two accumulators hide it
+// only where one pass through the chain, less the MMA itself, fits into the other accumulator's MMA (512
+// clocks at BN 256).  Hence the CTA's own MMA with its own barriers (cta_group::1; a CTA pair's MMA frees
+// its accumulators across two CTAs, 950 clocks per block instead of 810), the accumulator released as soon
+// as its last columns are in registers, the scales fetched by warps of their own, and issuing loops that a
+// whole warp walks (elect_one: 923 -> 807 clocks).  At 8192 x 28672 x 4096: 746 us, 2579 TFLOP/s (2550 us for the
+// weights-on-rows kernel above, 2014 us for a CTA-pair version with one-lane issuing loops and direct stores).
+constexpr int kTileThreads = 384;
+constexpr int kScSlots = 4, kScGroup = 4;  // ring of scales: groups of four blocks of K
+
+template <int NCH>
+struct TileLayout {
+  static constexpr int BN = 32 * NCH, CW = BN / 2;  // CW: columns of a scaling warp
+  static constexpr uint32_t A = 128 * 128, B = BN * 128, STAGE = A + B;
+  static constexpr int STAGES = 4;
+  static constexpr uint32_t SC = STAGES * STAGE;         // per group: float4 of each of 128 rows, then of 2 x 2 column blocks
+  static constexpr uint32_t SCSLOT = (128 + 4) * 16;
+  static constexpr uint32_t OUT = SC + kScSlots * SCSLOT;  // per scaling warp: 32 rows x 64 bytes of C
+  static constexpr uint32_t OUTBOX = 32 * 64;
+  static constexpr uint32_t BAR = OUT + 8 * OUTBOX;
+  static constexpr uint32_t BYTES = BAR + 256;
+};
+
+struct TileSched {
+  int tiles_mp, tiles_n, m_fast;  // pairs of 128-row tiles, column tiles, and which of the two is the fast index
+};
+
+template <int NCH>
+__global__ void __launch_bounds__(kTileThreads, 1)
+    k_gemm_fp8_tile(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, Fp8Params p, TileSched sch) {
+  using L = TileLayout<NCH>;
+  constexpr int ST = L::STAGES, BN = L::BN, CW = L::CW;
+  constexpr bool kStraddle = CW % 64 != 0;  // a warp's columns may lie in two weight blocks
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR);
+  uint64_t* full = bars;               // [ST]
+  uint64_t* empty = bars + ST;         // [ST]
+  uint64_t* acc_full = bars + 2 * ST;  // [2]
+  uint64_t* acc_empty = acc_full + 2;  // [2]
+  uint64_t* sc_full = acc_empty + 2;          // [kScSlots]
+  uint64_t* sc_empty = sc_full + kScSlots;    // [kScSlots]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sc_empty + kScSlots);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sc_empty + kScSlots + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int crank = (int)tc::cluster_ctarank();
+  const int cid = blockIdx.x >> 1, n_clusters = gridDim.x >> 1;
+  const int n_tiles = sch.tiles_mp * sch.tiles_n;
+  const int nkb = p.nkb;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) {
+      tc::mbar_init(&full[i], 1);
+      tc::mbar_init(&empty[i], 2);  // both CTAs' MMAs have read their copy of the stage
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(&acc_full[i], 1);
+      tc::mbar_init(&acc_empty[i], 8);
+    }
+    for (int i = 0; i < kScSlots; ++i) {
+      tc::mbar_init(&sc_full[i], 64);
+      tc::mbar_init(&sc_empty[i], 8);
+    }
+    *abort_flag = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 1) {
+    tc::tmem_alloc(tmem_slot, 512);
+    tc::tmem_relinquish();
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();
+  tc::fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+
+  auto decode = [&](int t, int& tm, int& tn) {
+    if (sch.m_fast) {
+      tm = 2 * (t % sch.tiles_mp) + crank;
+      tn = t / sch.tiles_mp;
+    } else {
+      tm = 2 * (t / sch.tiles_n) + crank;
+      tn = t % sch.tiles_n;
+    }
+  };
+
+  // Launched with 168 registers per thread; the scaling warps rise to 216 (128 of them sums), the others
+  // drop to 72: 4 x 72 + 8 x 216 = 12 x 168.
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n" ::: "memory");
+    if (warp == 0) {
+      tc::prefetch_tmap(&ta);
+      tc::prefetch_tmap(&tb);
+      const bool leader = tc::elect_one();
+      const uint32_t emptya = smem_u32(empty);
+      int s = 0;
+      uint32_t ph = 1;  // parity of the stage's previous release: the first turn needs none
+      bool ok = true;
+      for (int t = cid; t < n_tiles; t += n_clusters) {
+        int tm, tn;
+        decode(t, tm, tn);
+#pragma unroll 1
+        for (int kb = 0; kb < nkb; ++kb) {
+          ok = tc::mbar_wait_addr(emptya + s * 8, ph, abort_flag, p.wait_ns) && ok;
+          uint8_t* sa = smem + s * L::STAGE;
+          if (leader && ok) {
+            tc::mbar_arrive_expect_tx(&full[s], L::STAGE);
+            tc::tma_load_2d(sa, &ta, &full[s], kb * kBlk, tm * 128);
+            tc::tma_load_2d_multicast(sa + L::A + crank * (CW * 128), &tb, &full[s], kb * kBlk, tn * BN + crank * CW, 0x3);
+          }
+          __syncwarp();
+          if (++s == ST) { s = 0; ph ^= 1; }
+        }
+      }
+    } else if (warp == 1) {
+      constexpr uint32_t idesc = tc::idesc_e4m3(128, BN);
+      const uint64_t a0 = tc::sdesc_sw128(smem_u32(smem), 16, 1024), b0 = tc::sdesc_add(a0, L::A);
+      const uint32_t fulla = smem_u32(full), acce = smem_u32(acc_empty);
+      const bool leader = tc::elect_one();
+      int s = 0, buf = 0;
+      uint32_t ph = 0, eph = 1;
+      bool ok = true;
+      for (int t = cid; t < n_tiles; t += n_clusters) {
+#pragma unroll 1
+        for (int kb = 0; kb < nkb; ++kb) {
+          ok = tc::mbar_wait_addr(fulla + s * 8, ph, abort_flag, p.wait_ns) && ok;
+          ok = tc::mbar_wait_addr(acce + buf * 8, eph, abort_flag, p.wait_ns) && ok;
+          tc::fence_after_sync();
+          const uint64_t ad = tc::sdesc_add(a0, s * L::STAGE), bd = tc::sdesc_add(b0, s * L::STAGE);
+          const uint32_t d = tmem + buf * 256;
+          if (leader && ok) {
+#pragma unroll
+            for (int k = 0; k < kBlk / 32; ++k)
+              tc::mma_ss_f8(d, tc::sdesc_add(ad, k * 32), tc::sdesc_add(bd, k * 32), idesc, k > 0);
+            tc::mma_commit(&acc_full[buf]);
+            tc::mma_commit_multicast(&empty[s], 0x3);
+          }
+          __syncwarp();
+          if (++s == ST) { s = 0; ph ^= 1; }
+          eph ^= buf;
+          buf ^= 1;
+        }
+      }
+    } else {
+      // rows j and j + 64 of this CTA's 128, and (4 threads) the weight blocks under both column halves
+      const int j = threadIdx.x - 64;
+      const int nblocks = (int)ceil_div(p.N, kBlk);
+      int slot = 0;
+      uint32_t ph = 1;
+      bool ok = true;
+      for (int t = cid; t < n_tiles; t += n_clusters) {
+        int tm, tn;
+        decode(t, tm, tn);
+        const int64_t ma = (int64_t)tm * 128 + j, mb = ma + 64;
+        const float* pa = p.sa + (ma < p.M ? ma : 0);
+        const float* pb = p.sa + (mb < p.M ? mb : 0);
+        const int blk = (int)(((int64_t)tn * BN + (j >> 1 & 1) * CW) / kBlk) + (j & 1);
+        const float* ps = p.sb + (int64_t)min(blk, nblocks - 1) * nkb;
+        float va[kScGroup], vb[kScGroup], vs[kScGroup];
+        auto fetch = [&](int kb0) {
+#pragma unroll
+          for (int u = 0; u < kScGroup; ++u) {
+            const bool in = kb0 + u < nkb;
+            va[u] = in && ma < p.M ? pa[(int64_t)(kb0 + u) * p.lds] : 0.f;
+            vb[u] = in && mb < p.M ? pb[(int64_t)(kb0 + u) * p.lds] : 0.f;
+            vs[u] = in && j < 4 ? ps[kb0 + u] : 0.f;
+          }
+        };
+        fetch(0);
+        for (int kb0 = 0; kb0 < nkb; kb0 += kScGroup) {
+          ok = tc::mbar_wait(&sc_empty[slot], ph, abort_flag, nullptr, p.wait_ns) && ok;
+          if (ok) {
+            float4* dst = reinterpret_cast<float4*>(smem + L::SC + slot * L::SCSLOT);
+            dst[j] = make_float4(va[0], va[1], va[2], va[3]);
+            dst[j + 64] = make_float4(vb[0], vb[1], vb[2], vb[3]);
+            if (j < 4) dst[128 + j] = make_float4(vs[0], vs[1], vs[2], vs[3]);
+          }
+          tc::mbar_arrive(&sc_full[slot]);
+          fetch(kb0 + kScGroup);
+          if (++slot == kScSlots) { slot = 0; ph ^= 1; }
+        }
+      }
+    }
+    __syncwarp();
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n" ::: "memory");
+    const int half = (warp - 4) >> 2;
+    const int r = 32 * (warp & 3) + lane;
+    const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + half * CW;
+    int slot = 0, buf = 0;
+    uint32_t sph = 0, aph = 0;
+    const uint32_t scf = smem_u32(sc_full), sce = smem_u32(sc_empty), accf = smem_u32(acc_full), acce = smem_u32(acc_empty);
+    bool ok = true;
+    for (int t = cid; t < n_tiles; t += n_clusters) {
+      int tm, tn;
+      decode(t, tm, tn);
+      const int64_t n0 = (int64_t)tn * BN + half * CW;
+      // the warp's columns lie in one weight block up to chunk `cut` (16 columns each), then in the next
+      const int cut = (int)((kBlk - n0 % kBlk) / 16);
+      float2 acc[CW / 2];
+#pragma unroll
+      for (int i = 0; i < CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+#pragma unroll 1
+      for (int kb0 = 0; kb0 < nkb; kb0 += kScGroup) {
+        ok = tc::mbar_wait_addr(scf + slot * 8, sph, abort_flag, p.wait_ns) && ok;
+        const float4* sc = reinterpret_cast<const float4*>(smem + L::SC + slot * L::SCSLOT);
+        const float4 a4 = sc[r], b4 = sc[128 + 2 * half], c4 = kStraddle ? sc[129 + 2 * half] : b4;
+        const float f0[4] = {a4.x * b4.x, a4.y * b4.y, a4.z * b4.z, a4.w * b4.w};
+        const float f1[4] = {a4.x * c4.x, a4.y * c4.y, a4.z * c4.z, a4.w * c4.w};
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_addr(sce + slot * 8);
+        if (++slot == kScSlots) { slot = 0; sph ^= 1; }
+#pragma unroll
+        for (int u = 0; u < kScGroup; ++u) {
+          if (kb0 + u < nkb) {
+            ok = tc::mbar_wait_addr(accf + buf * 8, aph, abort_flag, p.wait_ns) && ok;
+            __syncwarp();
+            tc::fence_after_sync();
+            const uint32_t src = lane_addr + buf * 256;
+#pragma unroll
+            for (int g = 0; g < NCH; ++g) {
+              uint32_t v[16];
+              tc::tmem_ld16_wait(src + g * 16, v);
+              if (g == NCH - 1) {
+                // everything is in registers: the accumulator may be written again while these are scaled
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive_addr(acce + buf * 8);
+              }
+              const float f = kStraddle && g >= cut ? f1[u] : f0[u];
+              const float2 f2 = make_float2(f, f);
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                acc[g * 8 + i] = __ffma2_rn(make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])), f2, acc[g * 8 + i]);
+            }
+            aph ^= buf;
+            buf ^= 1;
+          }
+        }
+      }
+      // C leaves through shared memory, 64 bytes of 32 rows at a time, so that a warp's stores fill whole
+      // sectors of 8 rows (a thread's own 16-byte stores to 32 rows took 8% of the kernel's time); 16-byte chunk j
+      // of row r lies at chunk j ^ (r / 2 % 4), which keeps both sides free of bank conflicts
+      uint8_t* box = smem + L::OUT + (warp - 4) * L::OUTBOX;
+      const int64_t mw = (int64_t)tm * 128 + 32 * (warp & 3);
+      const int e = p.c_bf16 ? 8 : 4;  // columns of a 16-byte chunk
+      auto flush = [&](int64_t n_at, int chunks) {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = i * 8 + (lane >> 2), j = lane & 3;
+          const int64_t m = mw + rr, n = n_at + j * e;
+          if (ok && j < chunks && m < p.M && n < p.N) {  // N is a multiple of 8: a chunk is inside or outside
+            const uint4 q = *reinterpret_cast<const uint4*>(box + rr * 64 + ((j ^ ((rr >> 1) & 3)) << 4));
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.c) + (m * p.ldc + n) * (p.c_bf16 ? 2 : 4)) = q;
+          }
+        }
+        __syncwarp();
+      };
+      uint8_t* mine = box + lane * 64;
+      const int sw = (lane >> 1) & 3;
+      if (p.c_bf16) {
+#pragma unroll
+        for (int c = 0; c < CW; c += 32) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (c + 8 * j < CW) {
+              const float2* v = &acc[(c + 8 * j) / 2];
+              *reinterpret_cast<uint4*>(mine + ((j ^ sw) << 4)) =
+                  make_uint4(tc::pack_bf16x2(v[0].x, v[0].y), tc::pack_bf16x2(v[1].x, v[1].y), tc::pack_bf16x2(v[2].x, v[2].y),
+                             tc::pack_bf16x2(v[3].x, v[3].y));
+            }
+          flush(n0 + c, CW - c >= 32 ? 4 : (CW - c) / 8);
+        }
+      } else {
+#pragma unroll
+        for (int c = 0; c < CW; c += 16) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2* v = &acc[(c + 4 * j) / 2];
+            *reinterpret_cast<float4*>(mine + ((j ^ sw) << 4)) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+          }
+          flush(n0 + c, 4);
+        }
+      }
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::cluster_sync();  // the peer's loads and commits reach into this CTA until it is done too
+  if (warp == 1) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int NCH>
+cudaError_t run_tile(const Fp8GemmArgs& a, const Fp8Params& p, cudaStream_t st) {
+  using L = TileLayout<NCH>;
+  CUtensorMap ta, tb;
+  if (!make_tmap_2d_u8(&ta, a.A, a.K, a.M, a.lda, kBlk, 128) || !make_tmap_2d_u8(&tb, a.B, a.K, a.N, a.ldb, kBlk, L::CW))
+    return cudaErrorInvalidValue;
+  auto kfn = k_gemm_fp8_tile<NCH>;
+  const size_t smem = L::BYTES + 1024;
+  cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  // the fast index sweeps the smaller operand, so the larger one is read from DRAM about once
+  const TileSched sch{(int)ceil_div(a.M, 256), (int)ceil_div(a.N, L::BN), a.N > a.M};
+  const int64_t units = (int64_t)sch.tiles_mp * sch.tiles_n;
+  if (units > INT32_MAX / 2) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(2 * std::max<int64_t>(1, std::min<int64_t>(units, sm_count() / 2))));
+  cfg.blockDim = dim3(kTileThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  e = cudaLaunchKernelEx(&cfg, kfn, ta, tb, p, sch);
+  note_launch();
+  return e;
+}
+
 }  // namespace
 
 cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t st) {
@@ -210,7 +546,24 @@ cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t st) {
   if (a.M <= 16) return run_swap<16>(a, p, st);
   if (a.M <= 32) return run_swap<32>(a, p, st);
   if (a.M <= 64) return run_swap<64>(a, p, st);
-  return run_swap<128>(a, p, st);
+  if (a.M <= 128) return run_swap<128>(a, p, st);
+  // Columns per tile: the width whose rounds over all clusters take the least time.  A block of K takes
+  // about 370 + 55 NCH clocks (590 measured at 128 columns, 810 at 256), a tile's output about 2800.
+  const int64_t clusters = sm_count() / 2, tm = ceil_div(a.M, 256);
+  int best = 8;
+  int64_t cost = INT64_MAX;
+  for (int c = 8; c >= 4; --c) {
+    const int64_t rounds = ceil_div(tm * ceil_div(a.N, 32 * c), clusters);
+    const int64_t k = rounds * ((int64_t)p.nkb * (370 + 55 * c) + 350 * c);
+    if (k < cost) { cost = k; best = c; }
+  }
+  switch (best) {
+    case 4: return run_tile<4>(a, p, st);
+    case 5: return run_tile<5>(a, p, st);
+    case 6: return run_tile<6>(a, p, st);
+    case 7: return run_tile<7>(a, p, st);
+    default: return run_tile<8>(a, p, st);
+  }
 }
 
 }  // namespace upipe
