@@ -34,48 +34,71 @@ struct Fp8Params {
 };
 
 // ------------------------------------------------------------------------------------------------
-// weights on the MMA's rows, TN tokens on its columns
+// few rows of A: weights on the MMA's rows, TN tokens on its columns, K split over a cluster
 // ------------------------------------------------------------------------------------------------
+// One CTA per 128 weight rows, TN tokens and share of K:
+//   warp 0      TMA producer over a ring of ST stages (128 x 128 weights, TN x 128 tokens)
+//   warp 1      MMA issuer: 4 MMAs (M128 N TN K32) per block of K into one of NBUF TMEM accumulators
+//   warps 2-3   the blocks' scales (token's times weight block's), four blocks of K at a time
+//   warps 4..   scaling: one weight row (TMEM lane) per thread, its tokens' sums in registers
+// Bound by the weights' bytes: enough CTAs have to stream at once, so K is split over a cluster of up to 8
+// CTAs while that fits on the SMs at once.  Each CTA then sends its sums to the CTAs that own the tokens
+// (token i belongs to CTA i % splits) through distributed shared memory, and the owners add them in the order
+// of the shares.  The accumulators are narrow here, so there are 4 to 8 of them: the chain from an MMA to its
+// accumulator's release (about 900 clocks) is long against the block's MMA (2 TN clocks), and its bytes
+// arrive every 800.
 template <int TN>
 struct SwapLayout {
-  static constexpr int STAGES = TN <= 32 ? 6 : 5;
+  static constexpr int STAGES = TN == 16 ? 5 : TN == 64 ? 3 : 4;
+  static constexpr int NBUF = TN <= 32 ? 8 : 4;
+  static constexpr int WARPS = TN <= 32 ? 4 : 8;   // scaling warps
+  static constexpr int CT = TN * 4 / WARPS;        // tokens of a scaling thread
+  static constexpr int THREADS = 128 + 32 * WARPS;
   static constexpr uint32_t W = 128 * 128, T = TN * 128, STAGE = W + T;
-  static constexpr uint32_t SC = STAGES * STAGE;               // two rows of TN scales
-  static constexpr uint32_t BAR = SC + 2 * TN * 4;
-  static constexpr uint32_t BYTES = BAR + 256;
-  static constexpr uint32_t TMEM = 2 * TN < 32 ? 32 : 2 * TN;  // power of two
+  static constexpr uint32_t SC = STAGES * STAGE;   // per group: 4 rows of TN scales
+  static constexpr uint32_t SCSLOT = 4 * TN * 4;
+  static constexpr uint32_t RED = SC + 4 * SCSLOT;  // [splits][ceil(TN / splits)][128] sums for the owned tokens
+  static constexpr uint32_t BAR = RED + (TN + 6) * 128 * 4;
+  static constexpr uint32_t BYTES = BAR + 512;
+  static constexpr uint32_t TMEM = NBUF * TN;       // 128 ... 512, a power of two
 };
 
-constexpr int kSwapThreads = 192;
-
 template <int TN>
-__global__ void __launch_bounds__(kSwapThreads) k_gemm_fp8_swap(const __grid_constant__ CUtensorMap tw,
-                                                                const __grid_constant__ CUtensorMap tt, Fp8Params p) {
+__global__ void __launch_bounds__(SwapLayout<TN>::THREADS)
+    k_gemm_fp8_swap(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tt, Fp8Params p, int splits) {
   using L = SwapLayout<TN>;
-  constexpr int ST = L::STAGES;
+  constexpr int ST = L::STAGES, NB = L::NBUF, CT = L::CT;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* sc = reinterpret_cast<float*>(smem + L::SC);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR);
-  uint64_t* full = bars;               // [ST]
-  uint64_t* empty = bars + ST;         // [ST]
-  uint64_t* acc_full = bars + 2 * ST;  // [2]
-  uint64_t* acc_empty = acc_full + 2;  // [2]
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 2);
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(acc_empty + 3);
+  uint64_t* full = bars;                // [ST]
+  uint64_t* empty = bars + ST;          // [ST]
+  uint64_t* acc_full = bars + 2 * ST;   // [NB]
+  uint64_t* acc_empty = acc_full + NB;  // [NB]
+  uint64_t* sc_full = acc_empty + NB;   // [4]
+  uint64_t* sc_empty = sc_full + 4;     // [4]
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sc_empty + 4);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(sc_empty + 5);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t n0 = (int64_t)blockIdx.x * 128, m0 = (int64_t)blockIdx.y * TN;
-  const int nkb = p.nkb;
+  const int rank = splits > 1 ? (int)tc::cluster_ctarank() : 0;
+  const int tile = blockIdx.x / splits;
+  const int64_t n0 = (int64_t)tile * 128, m0 = (int64_t)blockIdx.y * TN;
+  // this CTA's blocks of K: [kb0, kb0 + nkb), shares that differ by one block at most
+  const int kb0 = (int)((int64_t)p.nkb * rank / splits), nkb = (int)((int64_t)p.nkb * (rank + 1) / splits) - kb0;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
       tc::mbar_init(&full[i], 1);
       tc::mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < NB; ++i) {
       tc::mbar_init(&acc_full[i], 1);
-      tc::mbar_init(&acc_empty[i], 128);
+      tc::mbar_init(&acc_empty[i], L::WARPS);
+    }
+    for (int i = 0; i < 4; ++i) {
+      tc::mbar_init(&sc_full[i], 64);
+      tc::mbar_init(&sc_empty[i], L::WARPS);
     }
     *abort_flag = 0;
     tc::fence_mbar_init();
@@ -88,93 +111,170 @@ __global__ void __launch_bounds__(kSwapThreads) k_gemm_fp8_swap(const __grid_con
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  if (splits > 1) tc::cluster_arrive();  // (A) this CTA runs: its shared memory may be written
+  grid_dep_wait();
 
+  float acc[CT];
+  bool ok = true;
+  const int t0 = warp >= 4 ? ((warp - 4) >> 2) * CT : 0;  // first token of a scaling thread
+  const int wrow = 32 * (warp & 3) + lane;                // its weight row
   if (warp == 0) {
-    if (lane == 0) {
-      tc::prefetch_tmap(&tw);
-      tc::prefetch_tmap(&tt);
-      for (int kb = 0; kb < nkb; ++kb) {
-        const int s = kb % ST;
-        if (kb >= ST && !tc::mbar_wait(&empty[s], ((kb / ST) - 1) & 1, abort_flag, nullptr, p.wait_ns)) break;
+    tc::prefetch_tmap(&tw);
+    tc::prefetch_tmap(&tt);
+    const bool leader = tc::elect_one();
+    const uint32_t emptya = smem_u32(empty);
+    int s = 0;
+    uint32_t ph = 1;  // parity of the stage's previous release: the first turn needs none
+#pragma unroll 1
+    for (int kb = 0; kb < nkb; ++kb) {
+      ok = tc::mbar_wait_addr(emptya + s * 8, ph, abort_flag, p.wait_ns) && ok;
+      if (leader && ok) {
+        uint8_t* st = smem + s * L::STAGE;
         tc::mbar_arrive_expect_tx(&full[s], L::STAGE);
-        tc::tma_load_2d(smem + s * L::STAGE, &tw, &full[s], kb * kBlk, (int)n0);
-        tc::tma_load_2d(smem + s * L::STAGE + L::W, &tt, &full[s], kb * kBlk, (int)m0);
+        tc::tma_load_2d(st, &tw, &full[s], (kb0 + kb) * kBlk, (int)n0);
+        tc::tma_load_2d(st + L::W, &tt, &full[s], (kb0 + kb) * kBlk, (int)m0);
       }
+      __syncwarp();
+      if (++s == ST) { s = 0; ph ^= 1; }
     }
-    __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      constexpr uint32_t idesc = tc::idesc_e4m3(128, TN);
-      const uint64_t w0 = tc::sdesc_sw128(smem_u32(smem), 16, 1024), t0 = tc::sdesc_add(w0, L::W);
-      for (int kb = 0; kb < nkb; ++kb) {
-        const int s = kb % ST, buf = kb & 1;
-        if (kb >= 2 && !tc::mbar_wait(&acc_empty[buf], ((kb >> 1) - 1) & 1, abort_flag, nullptr, p.wait_ns)) break;
-        if (!tc::mbar_wait(&full[s], (kb / ST) & 1, abort_flag, nullptr, p.wait_ns)) break;
-        tc::fence_after_sync();
-        const uint64_t wd = tc::opaque(tc::sdesc_add(w0, s * L::STAGE)), td = tc::opaque(tc::sdesc_add(t0, s * L::STAGE));
+    constexpr uint32_t idesc = tc::idesc_e4m3(128, TN);
+    const uint64_t w0 = tc::sdesc_sw128(smem_u32(smem), 16, 1024), x0 = tc::sdesc_add(w0, L::W);
+    const uint32_t fulla = smem_u32(full), acce = smem_u32(acc_empty);
+    const bool leader = tc::elect_one();
+    int s = 0, buf = 0;
+    uint32_t ph = 0, eph = 1;
+#pragma unroll 1
+    for (int kb = 0; kb < nkb; ++kb) {
+      ok = tc::mbar_wait_addr(acce + buf * 8, eph, abort_flag, p.wait_ns) && ok;
+      ok = tc::mbar_wait_addr(fulla + s * 8, ph, abort_flag, p.wait_ns) && ok;
+      tc::fence_after_sync();
+      const uint64_t wd = tc::sdesc_add(w0, s * L::STAGE), xd = tc::sdesc_add(x0, s * L::STAGE);
+      const uint32_t d = tmem + buf * TN;
+      if (leader && ok) {
 #pragma unroll
         for (int k = 0; k < kBlk / 32; ++k)
-          tc::mma_ss_f8(tmem + buf * TN, tc::sdesc_add(wd, k * 32), tc::sdesc_add(td, k * 32), idesc, k > 0);
-        tc::mma_commit(&empty[s]);
+          tc::mma_ss_f8(d, tc::sdesc_add(wd, k * 32), tc::sdesc_add(xd, k * 32), idesc, k > 0);
         tc::mma_commit(&acc_full[buf]);
+        tc::mma_commit(&empty[s]);
       }
+      __syncwarp();
+      if (++s == ST) { s = 0; ph ^= 1; }
+      if (++buf == NB) { buf = 0; eph ^= 1; }
     }
-    __syncwarp();
+  } else if (warp < 4) {
+    // tokens j and j + 64
+    const int j = threadIdx.x - 64;
+    const float* sb = p.sb + (int64_t)tile * p.nkb + kb0;
+    const bool in0 = j < TN && m0 + j < p.M, in1 = j + 64 < TN && m0 + j + 64 < p.M;
+    const float* sa = p.sa + (int64_t)kb0 * p.lds + m0 + j;
+    float v0[4], v1[4];
+    auto fetch = [&](int kb) {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool in = kb + u < nkb;
+        const float w = in ? sb[kb + u] : 0.f;
+        v0[u] = in && in0 ? sa[(int64_t)(kb + u) * p.lds] * w : 0.f;
+        v1[u] = in && in1 ? sa[(int64_t)(kb + u) * p.lds + 64] * w : 0.f;
+      }
+    };
+    fetch(0);
+    int slot = 0;
+    uint32_t ph = 1;
+    for (int kb = 0; kb < nkb; kb += 4) {
+      ok = tc::mbar_wait(&sc_empty[slot], ph, abort_flag, nullptr, p.wait_ns) && ok;
+      if (ok) {
+        float* dst = reinterpret_cast<float*>(smem + L::SC + slot * L::SCSLOT);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          if (j < TN) dst[u * TN + j] = v0[u];
+          if (j + 64 < TN) dst[u * TN + j + 64] = v1[u];
+        }
+      }
+      tc::mbar_arrive(&sc_full[slot]);
+      fetch(kb + 4);
+      if (++slot == 4) { slot = 0; ph ^= 1; }
+    }
   } else {
-    // scaling warps: one weight row (TMEM lane) per thread, TN token columns
-    const int t = threadIdx.x - 64;
-    const int64_t n = n0 + 32 * (warp & 3) + lane;
-    const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
-    // token t's scale times the weight block's, loaded PF blocks ahead
-    constexpr int PF = 4;
-    const float* sb = p.sb + (int64_t)blockIdx.x * nkb;
-    const bool has = t < TN && m0 + t < p.M;
-    auto scale_of = [&](int kb) { return has && kb < nkb ? p.sa[(int64_t)kb * p.lds + m0 + t] * sb[kb] : 0.f; };
-    float ahead[PF];
 #pragma unroll
-    for (int i = 0; i < PF; ++i) ahead[i] = scale_of(i);
-    float acc[TN];
+    for (int i = 0; i < CT; ++i) acc[i] = 0.f;
+    const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + t0;
+    const uint32_t scf = smem_u32(sc_full), sce = smem_u32(sc_empty), accf = smem_u32(acc_full), acce = smem_u32(acc_empty);
+    int slot = 0, buf = 0;
+    uint32_t sph = 0, aph = 0;
+#pragma unroll 1
+    for (int kb = 0; kb < nkb; ++kb) {
+      const int u = kb & 3;
+      if (u == 0) ok = tc::mbar_wait_addr(scf + slot * 8, sph, abort_flag, p.wait_ns) && ok;
+      const float4* sc = reinterpret_cast<const float4*>(smem + L::SC + slot * L::SCSLOT + (u * TN + t0) * 4);
+      ok = tc::mbar_wait_addr(accf + buf * 8, aph, abort_flag, p.wait_ns) && ok;
+      __syncwarp();
+      tc::fence_after_sync();
 #pragma unroll
-    for (int i = 0; i < TN; ++i) acc[i] = 0.f;
-    bool ok = true;
-    for (int kb0 = 0; kb0 < nkb; kb0 += PF) {
-#pragma unroll
-      for (int u = 0; u < PF; ++u) {
-        const int kb = kb0 + u;
-        if (kb >= nkb) break;
-        const int buf = kb & 1;
-        if (t < TN) sc[buf * TN + t] = ahead[u];
-        ahead[u] = scale_of(kb + PF);
-        tc::named_bar_sync(1, 128);  // never skipped, so that a thread that gave up holds nobody up
-        if (ok) ok = tc::mbar_wait(&acc_full[buf], (kb >> 1) & 1, abort_flag, nullptr, p.wait_ns);
-        __syncwarp();
-        tc::fence_after_sync();
-#pragma unroll
-        for (int ch = 0; ch < TN / 16; ++ch) {
-          uint32_t v[16];
-          tc::tmem_ld16_wait(lane_addr + buf * TN + ch * 16, v);
-#pragma unroll
-          for (int i = 0; i < 16; i += 4) {
-            const float4 s4 = *reinterpret_cast<const float4*>(&sc[buf * TN + ch * 16 + i]);
-            acc[ch * 16 + i] += __uint_as_float(v[i]) * s4.x;
-            acc[ch * 16 + i + 1] += __uint_as_float(v[i + 1]) * s4.y;
-            acc[ch * 16 + i + 2] += __uint_as_float(v[i + 2]) * s4.z;
-            acc[ch * 16 + i + 3] += __uint_as_float(v[i + 3]) * s4.w;
-          }
+      for (int g = 0; g < CT / 16; ++g) {
+        uint32_t v[16];
+        tc::tmem_ld16_wait(lane_addr + buf * TN + g * 16, v);
+        if (g == CT / 16 - 1) {
+          tc::fence_before_sync();
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive_addr(acce + buf * 8);
         }
-        tc::fence_before_sync();
-        tc::mbar_arrive(&acc_empty[buf]);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+          const float4 s4 = sc[(g * 16 + i) / 4];
+          acc[g * 16 + i] += __uint_as_float(v[i]) * s4.x;
+          acc[g * 16 + i + 1] += __uint_as_float(v[i + 1]) * s4.y;
+          acc[g * 16 + i + 2] += __uint_as_float(v[i + 2]) * s4.z;
+          acc[g * 16 + i + 3] += __uint_as_float(v[i + 3]) * s4.w;
+        }
+      }
+      if (++buf == NB) { buf = 0; aph ^= 1; }
+      if (u == 3) {
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive_addr(sce + slot * 8);
+        if (++slot == 4) { slot = 0; sph ^= 1; }
       }
     }
-    // neighbouring lanes hold neighbouring columns of C
-    if (ok && n < p.N) {
+  }
+  __syncwarp();
+  grid_dep_trigger();
+
+  auto store = [&](int token, int64_t n, float v) {  // neighbouring lanes hold neighbouring columns of C
+    const int64_t at = (m0 + token) * p.ldc + n;
+    if (p.c_bf16) reinterpret_cast<bf16*>(p.c)[at] = __float2bfloat16_rn(v);
+    else reinterpret_cast<float*>(p.c)[at] = v;
+  };
+  if (splits == 1) {
+    if (warp >= 4 && ok && n0 + wrow < p.N) {
 #pragma unroll
-      for (int i = 0; i < TN; ++i) {
-        if (m0 + i < p.M) {
-          const int64_t at = (m0 + i) * p.ldc + n;
-          if (p.c_bf16) reinterpret_cast<bf16*>(p.c)[at] = __float2bfloat16_rn(acc[i]);
-          else reinterpret_cast<float*>(p.c)[at] = acc[i];
-        }
+      for (int i = 0; i < CT; ++i)
+        if (m0 + t0 + i < p.M) store(t0 + i, n0 + wrow, acc[i]);
+    }
+  } else {
+    const int per = (TN + splits - 1) / splits;  // tokens of an owner
+    tc::cluster_wait();                          // (A)
+    if (warp >= 4) {
+      const uint32_t red = smem_u32(smem + L::RED) + (rank * per * 128 + wrow) * 4;
+      int owner = t0 % splits, slot = t0 / splits;
+#pragma unroll
+      for (int i = 0; i < CT; ++i) {
+        // NaN marks the sums of a CTA that gave up
+        asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(tc::mapa_cluster(red + slot * 512, owner)),
+                     "f"(ok ? acc[i] : __int_as_float(0x7fc00000))
+                     : "memory");
+        if (++owner == splits) { owner = 0; ++slot; }
+      }
+    }
+    tc::cluster_sync();  // all sums have arrived; no CTA touches another's shared memory after this
+    const float* red = reinterpret_cast<const float*>(smem + L::RED) + (threadIdx.x & 127);
+    const int64_t n = n0 + (threadIdx.x & 127);
+    if (n < p.N) {
+      for (int slot = threadIdx.x >> 7; slot < per; slot += L::THREADS >> 7) {
+        const int token = slot * splits + rank;
+        if (token >= TN || m0 + token >= p.M) break;
+        float v = 0.f;
+        for (int r = 0; r < splits; ++r) v += red[(r * per + slot) * 128];
+        store(token, n, v);
       }
     }
   }
@@ -184,6 +284,13 @@ __global__ void __launch_bounds__(kSwapThreads) k_gemm_fp8_swap(const __grid_con
     tc::fence_after_sync();
     tc::tmem_dealloc(tmem, L::TMEM);
   }
+}
+
+// Shares of K: as many as let every CTA run at once, one per SM, with at least two blocks of K each.  TN 128
+// fills an SM's shared memory, and clusters do not pack all SMs of a GPC then: seven eighths of the SMs.
+int swap_splits(int64_t ctas, int nkb, int tn) {
+  const int64_t room = tn == 128 ? sm_count() * 7 / 8 : sm_count();
+  return (int)std::max<int64_t>(1, std::min<int64_t>({8, room / ctas, nkb / 2}));
 }
 
 template <int TN>
@@ -196,9 +303,11 @@ cudaError_t run_swap(const Fp8GemmArgs& a, const Fp8Params& p, cudaStream_t st) 
   const size_t smem = L::BYTES + 1024;
   cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
-  kfn<<<dim3((unsigned)ceil_div(a.N, 128), (unsigned)ceil_div(a.M, TN)), kSwapThreads, smem, st>>>(tw, tt, p);
+  const int64_t tiles = ceil_div(a.N, 128), mt = ceil_div(a.M, TN);
+  const int splits = swap_splits(tiles * mt, p.nkb, TN);
+  e = launch_pdl_cluster(kfn, dim3((unsigned)(tiles * splits), (unsigned)mt), dim3(L::THREADS), smem, st, splits, tw, tt, p, splits);
   note_launch();
-  return cudaGetLastError();
+  return e;
 }
 
 // ------------------------------------------------------------------------------------------------
@@ -286,6 +395,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc::cluster_sync();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
+  grid_dep_wait();
 
   auto decode = [&](int t, int& tm, int& tn) {
     if (sch.m_fast) {
@@ -521,19 +631,8 @@ cudaError_t run_tile(const Fp8GemmArgs& a, const Fp8Params& p, cudaStream_t st) 
   const TileSched sch{(int)ceil_div(a.M, 256), (int)ceil_div(a.N, L::BN), a.N > a.M};
   const int64_t units = (int64_t)sch.tiles_mp * sch.tiles_n;
   if (units > INT32_MAX / 2) return cudaErrorInvalidValue;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)(2 * std::max<int64_t>(1, std::min<int64_t>(units, sm_count() / 2))));
-  cfg.blockDim = dim3(kTileThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = cudaLaunchKernelEx(&cfg, kfn, ta, tb, p, sch);
+  const unsigned grid = (unsigned)(2 * std::max<int64_t>(1, std::min<int64_t>(units, sm_count() / 2)));
+  e = launch_pdl_cluster(kfn, dim3(grid), dim3(kTileThreads), smem, st, 2, ta, tb, p, sch);
   note_launch();
   return e;
 }
@@ -546,9 +645,11 @@ cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t st) {
   if (a.M <= 16) return run_swap<16>(a, p, st);
   if (a.M <= 32) return run_swap<32>(a, p, st);
   if (a.M <= 64) return run_swap<64>(a, p, st);
-  if (a.M <= 128) return run_swap<128>(a, p, st);
-  // Columns per tile: the width whose rounds over all clusters take the least time.  A block of K takes
-  // about 370 + 55 NCH clocks (590 measured at 128 columns, 810 at 256), a tile's output about 2800.
+  // The modelled clocks of both kernels.  Tile kernel: the column width whose rounds over all clusters take the
+  // least; a block of K takes about 370 + 55 NCH (590 measured at 128 columns, 810 at 256), a tile's output about
+  // 2800 at 256 columns.  Tokens on the columns: about 1000 for a block of K.  Measured on both sides (us, tile
+  // kernel / tokens on the columns): 128 x 5120 x 8192 25.2 / 19.0, 128 x 4096 x 4096 15.1 / 12.0, 100 x 1024 x
+  // 4096 14.1 / 8.7; 128 x 28672 x 4096 33.6 / 41.2, 200 x 6144 x 4096 15.4 / 20.4, 256 x 5120 x 8192 25.4 / 38.8.
   const int64_t clusters = sm_count() / 2, tm = ceil_div(a.M, 256);
   int best = 8;
   int64_t cost = INT64_MAX;
@@ -557,6 +658,10 @@ cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t st) {
     const int64_t k = rounds * ((int64_t)p.nkb * (370 + 55 * c) + 350 * c);
     if (k < cost) { cost = k; best = c; }
   }
+  const int64_t ctas = ceil_div(a.N, 128) * ceil_div(a.M, 128);
+  const int splits = swap_splits(ctas, p.nkb, 128);
+  if (ceil_div(a.M, 128) <= 65535 && 12500 + ceil_div(ctas * splits, sm_count()) * ceil_div(p.nkb, splits) * 1000 < 8000 + cost)
+    return run_swap<128>(a, p, st);
   switch (best) {
     case 4: return run_tile<4>(a, p, st);
     case 5: return run_tile<5>(a, p, st);

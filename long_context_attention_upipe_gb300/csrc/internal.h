@@ -171,6 +171,26 @@ cudaError_t launch_pdl(K kfn, dim3 grid, dim3 block, size_t smem, cudaStream_t s
   return cudaLaunchKernelEx(&cfg, kfn, args...);
 }
 
+// The same with clusters of `cluster` CTAs along x.
+template <typename K, typename... Args>
+cudaError_t launch_pdl_cluster(K kfn, dim3 grid, dim3 block, size_t smem, cudaStream_t st, int cluster, const Args&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kfn, args...);
+}
+
 // Plain launches leave the plane fields zero: one device, one key shard, all heads of the launch.
 inline void fill_planes(AttnArgs& a) {
   if (a.hq == 0) a.hq = a.nh;
