@@ -419,29 +419,44 @@ def _refuse(what):
     raise ValueError(what)
 
 
-def _dev(t, dtype, shape, what):
-    """Address of a contiguous tensor of the given type and shape on the current device."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
+def _on(t, what):
+    """Index of the current CUDA device, which has to be the tensor's."""
+    dev = t.get_device()
+    if dev < 0 or dev != torch._C._cuda_getDevice():
         _refuse(f"{what}: a tensor on the current CUDA device expected, got {t.device}")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        _refuse(f"{what}: contiguous {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+    return dev
+
+
+def _dev(t, dev, dtype, shape, what):
+    """Address of a contiguous tensor of the given type and shape on device `dev`."""
+    if t.get_device() != dev or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        _refuse(f"{what}: contiguous {dtype} {tuple(shape)} on device {dev} expected, got {t.dtype} {tuple(t.shape)} on "
+                f"{t.device}")
     return t.data_ptr()
 
 
-def _opt(t, dtype, shape, what):
-    return None if t is None else _dev(t, dtype, shape, what)
+def _raw_stream(stream, dev):
+    # the handle itself: building a Stream object costs more than the launch
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
+
+
+_BF16, _F32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
 
 
 def _rms_norm(x, w, y, q, scales, rstd, residual, h, eps, stream):
     if x.dim() != 2:
         _refuse(f"rms_norm: x of [rows, d] expected, got {tuple(x.shape)}")
-    n, d = shape = x.shape
-    b = torch.bfloat16
-    _check(lib().upipe_attn_rms_norm_fwd(
-        n, d, eps, _dev(x, b, shape, "x"), _opt(residual, b, shape, "residual"), _dev(w, b, (d,), "w"),
-        _opt(h, b, shape, "h"), _opt(y, b, shape, "y"), _opt(q, torch.float8_e4m3fn, shape, "q"),
-        _opt(scales, torch.float32, (-(-d // 128), n), "scales"), _opt(rstd, torch.float32, (n,), "rstd"),
-        _stream(stream)), "rms_norm_fwd")
+    dev = _on(x, "x")
+    shape = x.shape
+    n, d = shape
+    rc = lib().upipe_attn_rms_norm_fwd(
+        n, d, eps, _dev(x, dev, _BF16, shape, "x"), None if residual is None else _dev(residual, dev, _BF16, shape, "residual"),
+        _dev(w, dev, _BF16, (d,), "w"), None if h is None else _dev(h, dev, _BF16, shape, "h"),
+        None if y is None else _dev(y, dev, _BF16, shape, "y"), None if q is None else _dev(q, dev, _E4M3, shape, "q"),
+        None if scales is None else _dev(scales, dev, _F32, (-(-d // 128), n), "scales"),
+        None if rstd is None else _dev(rstd, dev, _F32, (n,), "rstd"), _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "rms_norm_fwd")
 
 
 def rms_norm_fwd(x, w, y, rstd=None, residual=None, h=None, eps=1e-5, stream=None):
@@ -468,12 +483,16 @@ def rms_norm_bwd(dy, h, w, rstd, dx, dw, ws, dres=None, stream=None):
     """Gradients of rms_norm_fwd: dx bf16 [rows, d] (of x and residual alike, dres added), dw fp32 [d] (written)."""
     if dy.dim() != 2:
         _refuse(f"rms_norm_bwd: dy of [rows, d] expected, got {tuple(dy.shape)}")
-    n, d = shape = dy.shape
-    b, f = torch.bfloat16, torch.float32
-    _check(lib().upipe_attn_rms_norm_bwd(
-        n, d, _dev(dy, b, shape, "dy"), _dev(h, b, shape, "h"), _dev(w, b, (d,), "w"), _dev(rstd, f, (n,), "rstd"),
-        _opt(dres, b, shape, "dres"), _dev(dx, b, shape, "dx"), _dev(dw, f, (d,), "dw"), _dev(ws, torch.uint8, ws.shape, "ws"),
-        ws.numel(), _stream(stream)), "rms_norm_bwd")
+    dev = _on(dy, "dy")
+    shape = dy.shape
+    n, d = shape
+    rc = lib().upipe_attn_rms_norm_bwd(
+        n, d, _dev(dy, dev, _BF16, shape, "dy"), _dev(h, dev, _BF16, shape, "h"), _dev(w, dev, _BF16, (d,), "w"),
+        _dev(rstd, dev, _F32, (n,), "rstd"), None if dres is None else _dev(dres, dev, _BF16, shape, "dres"),
+        _dev(dx, dev, _BF16, shape, "dx"), _dev(dw, dev, _F32, (d,), "dw"), _dev(ws, dev, torch.uint8, ws.shape, "ws"),
+        ws.numel(), _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "rms_norm_bwd")
 
 
 def fp8_quantize(x, q, scales, block_rows=1, stream=None):
@@ -481,62 +500,74 @@ def fp8_quantize(x, q, scales, block_rows=1, stream=None):
     128 (weights) [ceil(rows / 128), ceil(cols / 128)]."""
     if x.dim() != 2 or block_rows not in (1, 128):
         _refuse(f"fp8_quantize: x of [rows, cols] and block_rows 1 or 128 expected, got {tuple(x.shape)}, {block_rows}")
-    rows, cols = x.shape
+    dev = _on(x, "x")
+    shape = x.shape
+    rows, cols = shape
     nb = -(-cols // 128)
-    _check(lib().upipe_attn_fp8_quantize(
-        rows, cols, block_rows, _dev(x, torch.bfloat16, x.shape, "x"), _dev(q, torch.float8_e4m3fn, x.shape, "q"),
-        _dev(scales, torch.float32, (nb, rows) if block_rows == 1 else (-(-rows // 128), nb), "scales"), _stream(stream)),
-        "fp8_quantize")
+    rc = lib().upipe_attn_fp8_quantize(
+        rows, cols, block_rows, _dev(x, dev, _BF16, shape, "x"), _dev(q, dev, _E4M3, shape, "q"),
+        _dev(scales, dev, _F32, (nb, rows) if block_rows == 1 else (-(-rows // 128), nb), "scales"), _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "fp8_quantize")
 
 
-def _rows(t, dtype, shape, what):
-    """Address and row stride of a matrix whose rows are contiguous, on the current device."""
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        _refuse(f"{what}: a tensor on the current CUDA device expected, got {t.device}")
-    if t.dtype not in dtype or tuple(t.shape) != tuple(shape) or (t.shape[1] > 1 and t.stride(1) != 1):
-        _refuse(f"{what}: {dtype} {tuple(shape)} with contiguous rows expected, got {t.dtype} {tuple(t.shape)}")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _rows(t, dev, shape, what):
+    """Address and row stride of a matrix whose rows are contiguous, on device `dev`."""
+    if t.get_device() != dev or t.shape != shape:
+        _refuse(f"{what}: {tuple(shape)} on device {dev} expected, got {tuple(t.shape)} on {t.device}")
+    ld, inner = t.stride()
+    if inner != 1 and shape[1] > 1:
+        _refuse(f"{what}: contiguous rows expected, got strides {t.stride()}")
+    return t.data_ptr(), ld if shape[0] > 1 and ld > shape[1] else shape[1]
 
 
 def gemm_fp8_nt(A, a_scale, B, b_scale, C, stream=None):
     """C [M, N] (bf16 or fp32) = A [M, K] B [N, K]^T, e4m3 with a_scale fp32 [ceil(K / 128), M] and b_scale
     fp32 [ceil(N / 128), ceil(K / 128)] (upipe_attn_gemm_fp8_nt).  A, B, C and a_scale may be row slices."""
-    if A.dim() != 2 or B.dim() != 2:
-        _refuse("gemm_fp8_nt: matrices expected")
-    (M, K), N = A.shape, B.shape[0]
-    e4m3, f = (torch.float8_e4m3fn,), torch.float32
+    if A.dim() != 2 or B.dim() != 2 or A.dtype != _E4M3 or B.dtype != _E4M3 or a_scale.dtype != _F32:
+        _refuse(f"gemm_fp8_nt: e4m3 matrices with fp32 scales expected, got {A.dtype}, {B.dtype}, {a_scale.dtype}")
+    if C.dtype != _BF16 and C.dtype != _F32:
+        _refuse(f"gemm_fp8_nt: C of bf16 or fp32 expected, got {C.dtype}")
+    dev = _on(A, "A")
+    M, K = A.shape
+    N = B.shape[0]
     nkb = -(-K // 128)
-    a, lda = _rows(A, e4m3, (M, K), "A")
-    b, ldb = _rows(B, e4m3, (N, K), "B")
-    c, ldc = _rows(C, (torch.bfloat16, f), (M, N), "C")
-    s, lds = _rows(a_scale, (f,), (nkb, M), "a_scale")
-    _check(lib().upipe_attn_gemm_fp8_nt(M, N, K, a, max(lda, K), s, max(lds, M), b, max(ldb, K),
-                                        _dev(b_scale, f, (-(-N // 128), nkb), "b_scale"), c, max(ldc, N),
-                                        int(C.dtype == torch.bfloat16), _stream(stream)), "gemm_fp8_nt")
+    a, lda = _rows(A, dev, (M, K), "A")
+    b, ldb = _rows(B, dev, (N, K), "B")
+    c, ldc = _rows(C, dev, (M, N), "C")
+    s, lds = _rows(a_scale, dev, (nkb, M), "a_scale")
+    rc = lib().upipe_attn_gemm_fp8_nt(M, N, K, a, lda, s, lds, b, ldb, _dev(b_scale, dev, _F32, (-(-N // 128), nkb), "b_scale"),
+                                      c, ldc, int(C.dtype == _BF16), _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "gemm_fp8_nt")
 
 
-def _rope_tensor(x, out, head_dim, tokens, what):
-    for t in (x, out):
-        if not t.is_cuda or t.device.index != torch.cuda.current_device():
-            _refuse(f"rope: {what} on the current CUDA device expected, got {t.device}")
-        if t.dtype != torch.bfloat16 or t.dim() != 3 or t.shape != x.shape or t.shape[1:] != (tokens, head_dim) or t.stride(2) != 1:
-            _refuse(f"rope: {what} of bf16 [heads, {tokens}, {head_dim}] with contiguous rows expected, got {t.dtype} "
-                    f"{tuple(t.shape)}")
-    return RopeTensor(x.data_ptr(), out.data_ptr(), x.stride(0), x.stride(1), out.stride(0), out.stride(1), x.shape[0])
+def _rope_tensor(x, out, dev, head_dim, tokens, what):
+    shape = x.shape
+    xs, os = x.stride(), out.stride()
+    if (x.get_device() != dev or out.get_device() != dev or x.dtype != _BF16 or out.dtype != _BF16 or out.shape != shape
+            or len(shape) != 3 or shape[1] != tokens or shape[2] != head_dim or xs[2] != 1 or os[2] != 1):
+        _refuse(f"rope: {what} and its output of bf16 [heads, {tokens}, {head_dim}] with contiguous rows on device {dev} "
+                f"expected, got {x.dtype} {tuple(shape)} and {out.dtype} {tuple(out.shape)} on {x.device} and {out.device}")
+    return RopeTensor(x.data_ptr(), out.data_ptr(), xs[0], xs[1], os[0], os[1], shape[0])
 
 
 def rope(desc: RopeDesc, q, k, positions, q_out, k_out, inverse=False, stream=None):
     """Rotary positions: q [Hq, tokens, head_dim] and k (or None) turned into q_out, k_out (which may be q, k),
     any head and token strides; positions int32 [n_axes, tokens].  inverse: the backward pass."""
-    tokens = q.shape[1] if q.dim() == 3 else -1
-    qt = _rope_tensor(q, q_out, desc.head_dim, tokens, "q")
-    kt = None if k is None else _rope_tensor(k, k_out, desc.head_dim, tokens, "k")
-    pos = _dev(positions, torch.int32, (desc.n_axes, tokens), "positions")
-    if desc.inverse != int(inverse):
+    if q.dim() != 3:
+        _refuse(f"rope: q of [heads, tokens, head_dim] expected, got {tuple(q.shape)}")
+    dev = _on(q, "q")
+    tokens, head_dim = q.shape[1], desc.head_dim
+    qt = _rope_tensor(q, q_out, dev, head_dim, tokens, "q")
+    kt = None if k is None else _rope_tensor(k, k_out, dev, head_dim, tokens, "k")
+    if desc.inverse != inverse:
         desc = RopeDesc.from_buffer_copy(desc)
         desc.inverse = int(inverse)
-    _check(lib().upipe_attn_rope(ctypes.byref(desc), tokens, pos, ctypes.byref(qt),
-                                 None if kt is None else ctypes.byref(kt), _stream(stream)), "rope")
+    rc = lib().upipe_attn_rope(desc, tokens, _dev(positions, dev, torch.int32, (desc.n_axes, tokens), "positions"), qt, kt,
+                               _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "rope")
 
 
 class GradClip:
@@ -556,7 +587,7 @@ class GradClip:
             for t in (g,) if o is None else (g, o):
                 if t.dtype not in kinds:
                     _refuse(f"GradClip: fp32 or bf16 expected, got {t.dtype}")
-                _dev(t, t.dtype, g.shape, "GradClip")
+                _dev(t, _on(t, "GradClip"), t.dtype, g.shape, "GradClip")
             self._list[i] = GradTensor(g.data_ptr(), None if o is None else o.data_ptr(), g.numel(), kinds[g.dtype],
                                        0 if o is None else kinds[o.dtype])
         n = ctypes.c_size_t(0)
@@ -566,8 +597,11 @@ class GradClip:
 
     def __call__(self, max_norm, stream=None):
         """Clips to max_norm (math.inf: the norm alone); returns the norm, fp32 [1] on the device."""
-        _check(lib().upipe_attn_grad_clip(self._list, len(self.grads), max_norm, self.norm.data_ptr(), self.ws.data_ptr(),
-                                          self.ws.numel(), _stream(stream)), "grad_clip")
+        dev = _on(self.norm, "GradClip")
+        rc = lib().upipe_attn_grad_clip(self._list, len(self.grads), max_norm, self.norm.data_ptr(), self.ws.data_ptr(),
+                                        self.ws.numel(), _raw_stream(stream, dev))
+        if rc:
+            _check(rc, "grad_clip")
         return self.norm
 
 
