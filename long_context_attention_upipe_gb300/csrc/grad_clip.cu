@@ -108,6 +108,7 @@ __device__ __forceinline__ double block_sum(double v) {
 template <int CAP>
 __global__ void __launch_bounds__(kClipThreads) k_clip_norm(const __grid_constant__ ClipList<CAP> l, double* part) {
   double total = 0.0;
+  grid_dep_wait();
   for (uint32_t c = blockIdx.x; c < l.chunks; c += gridDim.x) {
     const ClipEntry& e = l.t[find_tensor(l, c)];
     const int64_t base = (int64_t)(c - e.chunk0) * kChunk;
@@ -202,8 +203,7 @@ cudaError_t run_clip(const GradTensor* t, const int* idx, int count, float max_n
       const int blocks = clip_blocks(l.chunks);
       cudaError_t e;
       if (pass == 0) {
-        k_clip_norm<CAP><<<blocks, kClipThreads, 0, st>>>(l, part + slot);
-        e = cudaGetLastError();
+        e = launch_pdl(k_clip_norm<CAP>, dim3(blocks), dim3(kClipThreads), 0, st, l, part + slot);
       } else {
         e = launch_pdl(k_clip_scale<CAP>, dim3(blocks), dim3(kClipThreads), 0, st, l, (const double*)part, n_part,
                        max_norm, first ? norm : (float*)nullptr);

@@ -102,14 +102,29 @@ struct NormShape {
   int d, tpr, rpb;  // columns; threads per row; rows per block
 };
 
-template <int V, bool FP8>
-__global__ void __launch_bounds__(kMaxNormThreads) k_rms_fwd(NormShape n, float eps, const bf16* x, const bf16* res,
-                                                             const bf16* __restrict__ w, bf16* h, bf16* y, uint8_t* q,
-                                                             float* scales, float* rstd_out) {
+// PF: the next row's loads are issued as soon as the current row's registers are free, before the row's
+// reduction, so every block always has a row in flight.
+template <int V, bool FP8, int MAXT, int MINB, bool PF>
+__global__ void __launch_bounds__(MAXT, MINB) k_rms_fwd(NormShape n, float eps, const bf16* x, const bf16* res,
+                                                        const bf16* __restrict__ w, bf16* h, bf16* y, uint8_t* q,
+                                                        float* scales, float* rstd_out) {
   __shared__ float red[2][32];
   const int g = threadIdx.x / n.tpr, t = threadIdx.x - g * n.tpr;
   const int nvec = n.d >> 3;
-  uint4 wv[V];
+  grid_dep_wait();
+  uint4 wv[V], xv[V], rv[V];
+  auto load = [&](int64_t row) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = t + i * n.tpr;
+      const bool ok = row < n.rows && c < nvec;
+      xv[i] = ok ? *reinterpret_cast<const uint4*>(x + row * n.d + c * 8) : make_uint4(0, 0, 0, 0);
+      if (res) rv[i] = ok ? *reinterpret_cast<const uint4*>(res + row * n.d + c * 8) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * n.rpb;
+  int64_t row = (int64_t)blockIdx.x * n.rpb + g;
+  if (PF) load(row);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = t + i * n.tpr;
@@ -117,28 +132,27 @@ __global__ void __launch_bounds__(kMaxNormThreads) k_rms_fwd(NormShape n, float 
   }
   int par = 0;
   // every group of the block makes the same number of turns (group_sum holds a barrier)
-  for (int64_t r0 = (int64_t)blockIdx.x * n.rpb; r0 < n.rows; r0 += (int64_t)gridDim.x * n.rpb, par ^= 1) {
-    const int64_t row = r0 + g;
+  for (int64_t r0 = (int64_t)blockIdx.x * n.rpb; r0 < n.rows; r0 += step, row += step, par ^= 1) {
     const bool row_ok = row < n.rows;
+    if (!PF) load(row);
     V8 f[V];
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = t + i * n.tpr;
-      const bool ok = row_ok && c < nvec;
-      const int64_t at = row * n.d + c * 8;
-      f[i] = unpack8(ok ? *reinterpret_cast<const uint4*>(x + at) : make_uint4(0, 0, 0, 0));
+      f[i] = unpack8(xv[i]);
       if (res) {
-        const V8 b = unpack8(ok ? *reinterpret_cast<const uint4*>(res + at) : make_uint4(0, 0, 0, 0));
+        const V8 b = unpack8(rv[i]);
 #pragma unroll
         for (int k = 0; k < 8; ++k) f[i].v[k] += b.v[k];
         const uint4 hv = pack8(f[i]);
-        if (ok) *reinterpret_cast<uint4*>(h + at) = hv;
+        if (row_ok && c < nvec) *reinterpret_cast<uint4*>(h + row * n.d + c * 8) = hv;
         f[i] = unpack8(hv);
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k) ss += f[i].v[k] * f[i].v[k];
     }
+    if (PF) load(row + step);
     ss = group_sum(ss, n.tpr, red[par]);
     const float rstd = rsqrtf(ss / (float)n.d + eps);
     if (rstd_out && row_ok && t == 0) rstd_out[row] = rstd;
@@ -164,41 +178,59 @@ __global__ void __launch_bounds__(kMaxNormThreads) k_rms_fwd(NormShape n, float 
   }
 }
 
-template <int V>
-__global__ void __launch_bounds__(kMaxNormThreads) k_rms_bwd(NormShape n, const bf16* dy, const bf16* h,
-                                                             const bf16* __restrict__ w, const float* __restrict__ rstd_in,
-                                                             const bf16* dres, bf16* dx, float* part) {
+template <int V, int MAXT, int MINB, bool PF>
+__global__ void __launch_bounds__(MAXT, MINB) k_rms_bwd(NormShape n, const bf16* dy, const bf16* h,
+                                                        const bf16* __restrict__ w, const float* __restrict__ rstd_in,
+                                                        const bf16* dres, bf16* dx, float* part) {
   __shared__ float red[2][32];
   const int g = threadIdx.x / n.tpr, t = threadIdx.x - g * n.tpr;
   const int nvec = n.d >> 3;
-  uint4 wv[V];
+  grid_dep_wait();
+  constexpr bool kHoldW = V <= 2;  // longer rows read w again (from L1): their registers hold the sums of dw
+  uint4 wv[V], nd[V], nh[V], nr[V];
+  float rstd_next = 0.f;
+  auto load = [&](int64_t row) {
+    rstd_next = row < n.rows ? rstd_in[row] : 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = t + i * n.tpr;
+      const bool ok = row < n.rows && c < nvec;
+      const int64_t at = row * n.d + c * 8;
+      nd[i] = ok ? *reinterpret_cast<const uint4*>(dy + at) : make_uint4(0, 0, 0, 0);
+      nh[i] = ok ? *reinterpret_cast<const uint4*>(h + at) : make_uint4(0, 0, 0, 0);
+      nr[i] = ok && dres ? *reinterpret_cast<const uint4*>(dres + at) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  const int64_t step = (int64_t)gridDim.x * n.rpb;
+  int64_t row = (int64_t)blockIdx.x * n.rpb + g;
+  if (PF) load(row);
   V8 dw[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = t + i * n.tpr;
-    wv[i] = c < nvec ? *reinterpret_cast<const uint4*>(w + c * 8) : make_uint4(0, 0, 0, 0);
+    if (kHoldW) wv[i] = c < nvec ? *reinterpret_cast<const uint4*>(w + c * 8) : make_uint4(0, 0, 0, 0);
 #pragma unroll
     for (int k = 0; k < 8; ++k) dw[i].v[k] = 0.f;
   }
   int par = 0;
-  for (int64_t r0 = (int64_t)blockIdx.x * n.rpb; r0 < n.rows; r0 += (int64_t)gridDim.x * n.rpb, par ^= 1) {
-    const int64_t row = r0 + g;
+  for (int64_t r0 = (int64_t)blockIdx.x * n.rpb; r0 < n.rows; r0 += step, row += step, par ^= 1) {
     const bool row_ok = row < n.rows;
-    const float rstd = row_ok ? rstd_in[row] : 0.f;
-    uint4 dyv[V], hv[V], rv[V];
+    if (!PF) load(row);
+    uint4 dv[V], hv[V], rv[V];
+    const float rstd = rstd_next;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      dv[i] = nd[i];
+      hv[i] = nh[i];
+      rv[i] = nr[i];
+    }
+    if (PF) load(row + step);
     float dot = 0.f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = t + i * n.tpr;
-      const bool ok = row_ok && c < nvec;
-      const int64_t at = row * n.d + c * 8;
-      dyv[i] = ok ? *reinterpret_cast<const uint4*>(dy + at) : make_uint4(0, 0, 0, 0);
-      hv[i] = ok ? *reinterpret_cast<const uint4*>(h + at) : make_uint4(0, 0, 0, 0);
-      rv[i] = ok && dres ? *reinterpret_cast<const uint4*>(dres + at) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const V8 a = unpack8(dyv[i]), b = unpack8(hv[i]), wf = unpack8(wv[i]);
+      if (!kHoldW) wv[i] = c < nvec ? *reinterpret_cast<const uint4*>(w + c * 8) : make_uint4(0, 0, 0, 0);
+      const V8 a = unpack8(dv[i]), b = unpack8(hv[i]), wf = unpack8(wv[i]);
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         dot += a.v[k] * wf.v[k] * b.v[k];
@@ -211,7 +243,8 @@ __global__ void __launch_bounds__(kMaxNormThreads) k_rms_bwd(NormShape n, const 
     for (int i = 0; i < V; ++i) {
       const int c = t + i * n.tpr;
       if (!row_ok || c >= nvec) continue;
-      const V8 a = unpack8(dyv[i]), b = unpack8(hv[i]), wf = unpack8(wv[i]), r = unpack8(rv[i]);
+      if (!kHoldW) wv[i] = *reinterpret_cast<const uint4*>(w + c * 8);
+      const V8 a = unpack8(dv[i]), b = unpack8(hv[i]), wf = unpack8(wv[i]), r = unpack8(rv[i]);
       V8 o;
 #pragma unroll
       for (int k = 0; k < 8; ++k) o.v[k] = r.v[k] + rstd * (a.v[k] * wf.v[k] - b.v[k] * m);
@@ -229,45 +262,75 @@ __global__ void __launch_bounds__(kMaxNormThreads) k_rms_bwd(NormShape n, const 
   }
 }
 
-// dw[c] = sum over p of part[p][c], in an order that depends on the shape alone: 32 columns per
-// block, 8 warps that each take every 8th partial row, then the warps in turn.
-__global__ void __launch_bounds__(256) k_dw_reduce(const float* __restrict__ part, int p_rows, int d, float* dw) {
-  __shared__ float s[8][32];
+// dw[c] = sum over p of part[p][c], in an order that depends on the shape alone: 32 columns per block, 32
+// warps that each take every 32nd partial row (4 loads in flight), then the warps in turn.
+__global__ void __launch_bounds__(1024) k_dw_reduce(const float* __restrict__ part, int p_rows, int d, float* dw) {
+  __shared__ float s[32][33];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
+  grid_dep_wait();
   float v = 0.f;
-  if (c < d)
-    for (int p = warp; p < p_rows; p += 8) v += part[(int64_t)p * d + c];
+  if (c < d) {
+    int p = warp;
+    for (; p + 96 < p_rows; p += 128) {
+      const float a0 = part[(int64_t)p * d + c], a1 = part[(int64_t)(p + 32) * d + c];
+      const float a2 = part[(int64_t)(p + 64) * d + c], a3 = part[(int64_t)(p + 96) * d + c];
+      v += (a0 + a1) + (a2 + a3);
+    }
+    for (; p < p_rows; p += 32) v += part[(int64_t)p * d + c];
+  }
   s[warp][lane] = v;
   __syncthreads();
-  if (warp == 0 && c < d) {
-    for (int i = 1; i < 8; ++i) v += s[i][lane];
-    dw[c] = v;
-  }
+  v = s[lane][warp];  // column `warp` of the block, warp `lane`'s share
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  const int cw = blockIdx.x * 32 + warp;
+  if (lane == 0 && cw < d) dw[cw] = v;
 }
 
-// One scale per row and 128 columns: 16 lanes per block, blocks of a row side by side.
-__global__ void __launch_bounds__(256) k_quant_rows(int64_t rows, int d, int nb, const bf16* __restrict__ x, uint8_t* q,
+// One scale per row and 128 columns: 16 lanes per block, blocks of a row side by side, four blocks of a
+// 16-lane group in flight at once.
+__global__ void __launch_bounds__(256, 4) k_quant_rows(int64_t rows, int d, int nb, const bf16* __restrict__ x, uint8_t* q,
                                                     float* scales) {
+  constexpr int U = 4;
   const int64_t total = rows * nb;  // (row, block) pairs
-  const int64_t stride = (int64_t)gridDim.x * 16;
+  const int64_t step = (int64_t)gridDim.x * 16;
   const int lane16 = threadIdx.x & 15;
   const int64_t first = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
-  const int64_t turns = ceil_div(total, stride);  // the same for every lane: the shuffles need them all
+  const int64_t turns = ceil_div(total, step * U);  // the same for every lane: the shuffles need them all
+  // the pair `step` further on, without a division per pair
+  const int64_t step_row = step / nb;
+  const int step_b = (int)(step - step_row * nb);
+  int64_t row = first / nb;
+  int b = (int)(first - row * nb);
+  grid_dep_wait();
   for (int64_t k = 0; k < turns; ++k) {
-    const int64_t i = first + k * stride;
-    const int64_t row = i / nb;
-    const int b = (int)(i - row * nb), c = b * 128 + lane16 * 8;
-    const bool ok = i < total && c < d;
-    const V8 f = unpack8(ok ? *reinterpret_cast<const uint4*>(x + row * d + c) : make_uint4(0, 0, 0, 0));
-    const float s = block_scale(max16(amax_bits(f)));
-    if (ok) *reinterpret_cast<uint2*>(q + row * d + c) = quant8(f, __fdividef(1.f, s));
-    if (i < total && lane16 == 0) scales[(int64_t)b * rows + row] = s;
+    uint4 v[U];
+    int64_t rw[U];
+    int bl[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      rw[u] = row;
+      bl[u] = b;
+      const int c = b * 128 + lane16 * 8;
+      v[u] = row < rows && c < d ? *reinterpret_cast<const uint4*>(x + row * d + c) : make_uint4(0, 0, 0, 0);
+      row += step_row;
+      b += step_b;
+      if (b >= nb) { b -= nb; ++row; }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const V8 f = unpack8(v[u]);
+      const float s = block_scale(max16(amax_bits(f)));
+      const int c = bl[u] * 128 + lane16 * 8;
+      if (rw[u] < rows && c < d) *reinterpret_cast<uint2*>(q + rw[u] * d + c) = quant8(f, __fdividef(1.f, s));
+      if (rw[u] < rows && lane16 == 0) scales[(int64_t)bl[u] * rows + rw[u]] = s;
+    }
   }
 }
 
 // One scale per 128 x 128 block: a block of threads per tile, 8 vectors per thread in registers.
-__global__ void __launch_bounds__(256) k_quant_tiles(int64_t rows, int d, int nb, const bf16* __restrict__ x, uint8_t* q,
+__global__ void __launch_bounds__(256, 4) k_quant_tiles(int64_t rows, int d, int nb, const bf16* __restrict__ x, uint8_t* q,
                                                      float* scales) {
   __shared__ uint32_t red[8];
   const int64_t tile = blockIdx.x;
@@ -275,6 +338,7 @@ __global__ void __launch_bounds__(256) k_quant_tiles(int64_t rows, int d, int nb
   const int b = (int)(tile - tr * nb);
   uint4 v[8];
   uint32_t m = 0;
+  grid_dep_wait();
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int id = threadIdx.x + 256 * i;
@@ -300,8 +364,8 @@ __global__ void __launch_bounds__(256) k_quant_tiles(int64_t rows, int d, int nb
   if (threadIdx.x == 0) scales[tr * nb + b] = s;
 }
 
-// Threads per row and vectors per thread.  Rows of up to 32 vectors take half a warp or a warp with
-// one vector per thread; longer rows two vectors per thread (four past 2 x 1024 threads).
+// Threads per row and vectors per thread.  Rows of up to 32 vectors take half a warp or a warp with one
+// vector per thread; longer rows two vectors per thread, up to 512 threads (d 8192), then four.
 NormShape norm_shape(int64_t rows, int d, int& V) {
   const int nvec = d / 8;
   NormShape n{rows, d, 0, 1};
@@ -309,10 +373,23 @@ NormShape norm_shape(int64_t rows, int d, int& V) {
     V = 1;
     n.tpr = nvec <= 16 ? 16 : 32;
   } else {
-    V = nvec <= 2 * kMaxNormThreads ? 2 : 4;
+    V = nvec <= 1024 ? 2 : 4;
     n.tpr = (int)ceil_div(ceil_div(nvec, V), 32) * 32;
   }
   n.rpb = std::max(1, 256 / n.tpr);
+  return n;
+}
+
+// The backward pass holds a row's vectors twice (the next row's are in flight) and the sums of dw: at two
+// vectors per thread it takes 128 registers (at 96 it spills and runs at half the speed), so an SM holds 512
+// threads.  Rows of 257 to 320 such threads would leave a third of them unused: they take one vector per
+// thread (d 5120: 123 us, two vectors 130 us at 16381 rows).
+NormShape bwd_shape(int64_t rows, int d, int& V) {
+  NormShape n = norm_shape(rows, d, V);
+  if (n.tpr > 256 && n.tpr <= 320) {
+    V = 1;
+    n.tpr = (int)ceil_div(d / 8, 32) * 32;
+  }
   return n;
 }
 
@@ -322,7 +399,10 @@ int64_t norm_blocks(const NormShape& n, int per_sm_threads) {
   return std::max<int64_t>(1, std::min<int64_t>(ceil_div(n.rows, n.rpb), most));
 }
 
-constexpr int kBwdThreadsPerSm = 768;
+// resident threads per SM that the launch bounds below leave room for
+constexpr int kFwdThreadsPerSm = 1024, kBwdThreadsPerSm = 512, kBwdThreadsPerSmNarrow = 768;
+
+int bwd_threads(int V) { return V == 1 ? kBwdThreadsPerSmNarrow : kBwdThreadsPerSm; }
 
 }  // namespace
 
@@ -337,64 +417,74 @@ int sm_count() {
   return sms;
 }
 
+template <int V, int MAXT, int MINB, bool PF>
+static cudaError_t run_rms_fwd(const NormShape& n, const RmsNormArgs& a, cudaStream_t st) {
+  const dim3 grid((unsigned)norm_blocks(n, kFwdThreadsPerSm)), block(n.tpr * n.rpb);
+  const cudaError_t e = launch_pdl(a.q ? k_rms_fwd<V, true, MAXT, MINB, PF> : k_rms_fwd<V, false, MAXT, MINB, PF>, grid, block, 0,
+                                   st, n, a.eps, a.x, a.res, a.w, a.h, a.y, a.q, a.scales, a.rstd);
+  note_launch();
+  return e;
+}
+
 cudaError_t launch_rms_fwd(const RmsNormArgs& a, cudaStream_t st) {
   if (a.rows <= 0) return cudaSuccess;
   int V = 1;
   const NormShape n = norm_shape(a.rows, a.d, V);
-  const unsigned blocks = (unsigned)norm_blocks(n, 2048), threads = n.tpr * n.rpb;
-#define UPIPE_RMS_FWD(VV, F8) \
-  k_rms_fwd<VV, F8><<<blocks, threads, 0, st>>>(n, a.eps, a.x, a.res, a.w, a.h, a.y, a.q, a.scales, a.rstd)
-  if (a.q) {
-    if (V == 1) UPIPE_RMS_FWD(1, true);
-    else if (V == 2) UPIPE_RMS_FWD(2, true);
-    else UPIPE_RMS_FWD(4, true);
-  } else {
-    if (V == 1) UPIPE_RMS_FWD(1, false);
-    else if (V == 2) UPIPE_RMS_FWD(2, false);
-    else UPIPE_RMS_FWD(4, false);
-  }
-#undef UPIPE_RMS_FWD
-  note_launch();
-  return cudaGetLastError();
+  if (V == 1) return run_rms_fwd<1, 320, 3, true>(n, a, st);
+  if (n.tpr <= 320) return run_rms_fwd<2, 320, 3, true>(n, a, st);
+  if (V == 2) return run_rms_fwd<2, 512, 2, true>(n, a, st);
+  if (n.tpr <= 512) return run_rms_fwd<4, 512, 1, true>(n, a, st);
+  return run_rms_fwd<4, kMaxNormThreads, 1, false>(n, a, st);
 }
 
 size_t rms_bwd_workspace(int64_t rows, int d) {
   int V = 1;
-  const NormShape n = norm_shape(std::max<int64_t>(rows, 1), d, V);
-  return (size_t)norm_blocks(n, kBwdThreadsPerSm) * n.rpb * d * sizeof(float);
+  const NormShape n = bwd_shape(std::max<int64_t>(rows, 1), d, V);
+  return (size_t)norm_blocks(n, bwd_threads(V)) * n.rpb * d * sizeof(float);
+}
+
+template <int V, int MAXT, int MINB, bool PF>
+static cudaError_t run_rms_bwd(const NormShape& n, const RmsNormBwdArgs& a, float* part, cudaStream_t st) {
+  const dim3 grid((unsigned)norm_blocks(n, bwd_threads(V))), block(n.tpr * n.rpb);
+  const cudaError_t e = launch_pdl(k_rms_bwd<V, MAXT, MINB, PF>, grid, block, 0, st, n, a.dy, a.h, a.w, a.rstd, a.dres, a.dx, part);
+  note_launch();
+  return e;
 }
 
 cudaError_t launch_rms_bwd(const RmsNormBwdArgs& a, float* part, cudaStream_t st) {
   int p_rows = 0;
   if (a.rows > 0) {
     int V = 1;
-    const NormShape n = norm_shape(a.rows, a.d, V);
-    const unsigned blocks = (unsigned)norm_blocks(n, kBwdThreadsPerSm), threads = n.tpr * n.rpb;
-    p_rows = (int)blocks * n.rpb;
-    if (V == 1) k_rms_bwd<1><<<blocks, threads, 0, st>>>(n, a.dy, a.h, a.w, a.rstd, a.dres, a.dx, part);
-    else if (V == 2) k_rms_bwd<2><<<blocks, threads, 0, st>>>(n, a.dy, a.h, a.w, a.rstd, a.dres, a.dx, part);
-    else k_rms_bwd<4><<<blocks, threads, 0, st>>>(n, a.dy, a.h, a.w, a.rstd, a.dres, a.dx, part);
-    note_launch();
-    const cudaError_t e = cudaGetLastError();
+    const NormShape n = bwd_shape(a.rows, a.d, V);
+    p_rows = (int)norm_blocks(n, bwd_threads(V)) * n.rpb;
+    cudaError_t e;
+    if (n.tpr > 512 && V == 1) e = run_rms_bwd<1, 640, 1, true>(n, a, part, st);
+    else if (V == 1) e = run_rms_bwd<1, 256, 3, true>(n, a, part, st);
+    else if (n.tpr <= 256) e = run_rms_bwd<2, 256, 2, true>(n, a, part, st);
+    else if (V == 2) e = run_rms_bwd<2, 512, 1, true>(n, a, part, st);
+    else if (n.tpr <= 512) e = run_rms_bwd<4, 512, 1, false>(n, a, part, st);
+    else e = run_rms_bwd<4, kMaxNormThreads, 1, false>(n, a, part, st);
     if (e != cudaSuccess) return e;
   }
-  k_dw_reduce<<<(unsigned)ceil_div(a.d, 32), 256, 0, st>>>(part, p_rows, a.d, a.dw);
+  const cudaError_t e = launch_pdl(k_dw_reduce, dim3((unsigned)ceil_div(a.d, 32)), dim3(1024), 0, st, (const float*)part, p_rows,
+                                   a.d, a.dw);
   note_launch();
-  return cudaGetLastError();
+  return e;
 }
 
 cudaError_t launch_quantize(int64_t rows, int d, int block_rows, const bf16* x, uint8_t* q, float* scales,
                             cudaStream_t st) {
   if (rows <= 0) return cudaSuccess;
   const int nb = (int)ceil_div(d, 128);
+  cudaError_t e;
   if (block_rows == 1) {
-    const int64_t blocks = std::min<int64_t>(ceil_div(rows * nb, 16), (int64_t)sm_count() * 8);
-    k_quant_rows<<<(unsigned)blocks, 256, 0, st>>>(rows, d, nb, x, q, scales);
+    const int64_t blocks = std::min<int64_t>(ceil_div(rows * nb, 16), (int64_t)sm_count() * 4);
+    e = launch_pdl(k_quant_rows, dim3((unsigned)blocks), dim3(256), 0, st, rows, d, nb, x, q, scales);
   } else {
-    k_quant_tiles<<<(unsigned)(ceil_div(rows, 128) * nb), 256, 0, st>>>(rows, d, nb, x, q, scales);
+    e = launch_pdl(k_quant_tiles, dim3((unsigned)(ceil_div(rows, 128) * nb)), dim3(256), 0, st, rows, d, nb, x, q, scales);
   }
   note_launch();
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace upipe

@@ -66,6 +66,7 @@ __global__ void __launch_bounds__(256) k_rope(const __grid_constant__ RopeParams
   const int per_block = blockDim.x / p.units;  // tokens
   const int tl = threadIdx.x / p.units, u = threadIdx.x - tl * p.units;
   const int64_t tok = (int64_t)blockIdx.x * per_block + tl;
+  grid_dep_wait();  // before any thread leaves: this grid must not complete before the one that it follows
   if (tl >= per_block || tok >= p.tokens) return;
   const bool rot = u < p.rot_units;
   // the unit's two vectors: (j.., j + R/2..) of a split row, 16 neighbours otherwise
@@ -158,9 +159,9 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
   const int64_t want = ceil_div((int64_t)sm_count() * 8, bx);
   p.heads_per_block = (int)ceil_div(p.n_all, std::min<int64_t>(want, p.n_all));
   const dim3 grid((unsigned)bx, (unsigned)ceil_div(p.n_all, p.heads_per_block));
-  k_rope<<<grid, per_block * p.units, 0, st>>>(p);
+  const cudaError_t e = launch_pdl(k_rope, grid, dim3(per_block * p.units), 0, st, p);
   note_launch();
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace upipe
