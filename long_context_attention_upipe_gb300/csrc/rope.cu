@@ -83,39 +83,54 @@ __global__ void __launch_bounds__(256) k_rope(const __grid_constant__ RopeParams
     }
   }
   const int h0 = blockIdx.y * p.heads_per_block, h1 = min(p.n_all, h0 + p.heads_per_block);
-  for (int h = h0; h < h1; ++h) {
-    const RopeSide& s = p.s[h >= p.n_q];
-    const int hl = h >= p.n_q ? h - p.n_q : h;
-    const bf16* src = s.in + hl * s.in_head + tok * s.in_tok;
-    bf16* dst = s.out + hl * s.out_head + tok * s.out_tok;
-    uint4 v0 = *reinterpret_cast<const uint4*>(src + e0), v1 = *reinterpret_cast<const uint4*>(src + e1);
-    if (rot) {
-      float a[8], b[8];
-      unpack(v0, a);
-      unpack(v1, b);
-      if (split) {
+  // two heads at a time, their loads in flight together (110 -> 106.7 us at 32768 tokens of 32 + 8 heads, 6.3 TB/s)
+  for (int hb = h0; hb < h1; hb += 2) {
+    uint4 v0[2], v1[2];
+    bf16* dst[2];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float x = a[i], y = b[i];
-          a[i] = x * cs[i] - y * sn[i];
-          b[i] = y * cs[i] + x * sn[i];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = a[2 * i], y = a[2 * i + 1];
-          a[2 * i] = x * cs[i] - y * sn[i];
-          a[2 * i + 1] = y * cs[i] + x * sn[i];
-          const float z = b[2 * i], t = b[2 * i + 1];
-          b[2 * i] = z * cs[4 + i] - t * sn[4 + i];
-          b[2 * i + 1] = t * cs[4 + i] + z * sn[4 + i];
-        }
+    for (int k = 0; k < 2; ++k) {
+      const int h = hb + k;
+      if (h < h1) {
+        const RopeSide& s = p.s[h >= p.n_q];
+        const int hl = h >= p.n_q ? h - p.n_q : h;
+        const bf16* src = s.in + hl * s.in_head + tok * s.in_tok;
+        dst[k] = s.out + hl * s.out_head + tok * s.out_tok;
+        v0[k] = *reinterpret_cast<const uint4*>(src + e0);
+        v1[k] = *reinterpret_cast<const uint4*>(src + e1);
       }
-      v0 = pack(a);
-      v1 = pack(b);
     }
-    *reinterpret_cast<uint4*>(dst + e0) = v0;
-    *reinterpret_cast<uint4*>(dst + e1) = v1;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (hb + k < h1) {
+        if (rot) {
+          float a[8], b[8];
+          unpack(v0[k], a);
+          unpack(v1[k], b);
+          if (split) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float x = a[i], y = b[i];
+              a[i] = x * cs[i] - y * sn[i];
+              b[i] = y * cs[i] + x * sn[i];
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float x = a[2 * i], y = a[2 * i + 1];
+              a[2 * i] = x * cs[i] - y * sn[i];
+              a[2 * i + 1] = y * cs[i] + x * sn[i];
+              const float z = b[2 * i], t = b[2 * i + 1];
+              b[2 * i] = z * cs[4 + i] - t * sn[4 + i];
+              b[2 * i + 1] = t * cs[4 + i] + z * sn[4 + i];
+            }
+          }
+          v0[k] = pack(a);
+          v1[k] = pack(b);
+        }
+        *reinterpret_cast<uint4*>(dst[k] + e0) = v0[k];
+        *reinterpret_cast<uint4*>(dst[k] + e1) = v1[k];
+      }
+    }
   }
 }
 
