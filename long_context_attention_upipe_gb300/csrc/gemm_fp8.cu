@@ -311,29 +311,31 @@ cudaError_t run_swap(const Fp8GemmArgs& a, const Fp8Params& p, cudaStream_t st) 
 }
 
 // ------------------------------------------------------------------------------------------------
-// 128 rows of A x BN = 32 NCH columns per CTA, clusters of two CTAs that share the columns
+// CTA pairs: 256 rows of A x BN = 32 NCH columns
 // ------------------------------------------------------------------------------------------------
-// 12 warps, persistent, one CTA per SM:
-//   warp 0      TMA producer: its CTA's 128 rows of A, and half of the cluster's B tile, multicast to both
-//               CTAs, over a ring of 4 stages
-//   warp 1      MMA issuer: 4 MMAs (M128 BN K32) per block of K into one of two TMEM accumulators
+// 12 warps per CTA, persistent, one CTA per SM, a pair (cluster of two) per tile:
+//   warp 0      TMA producer: this CTA's 128 rows of A and its half of B's BN columns, ring of 6 stages
+//   warp 1      in the even CTA the MMA issuer: 4 MMAs (M256 BN K32, cta_group::2) per block of K into one of two
+//               TMEM accumulators, which both CTAs hold for their rows
 //   warps 2-3   the blocks' scales, four blocks of K at a time, into a ring in shared memory
 //   warps 4-11  scaling: TMEM lanes 32 * (warp % 4), one half of the columns each, the sums in registers
-// What bounds it is the chain MMA -> accumulator ready -> scaled -> free -> MMA: two accumulators hide it
-// only where one pass through the chain, less the MMA itself, fits into the other accumulator's MMA (512
-// clocks at BN 256).  Hence the CTA's own MMA with its own barriers (cta_group::1; a CTA pair's MMA frees
-// its accumulators across two CTAs, 950 clocks per block instead of 810), the accumulator released as soon
-// as its last columns are in registers, the scales fetched by warps of their own, and issuing loops that a
-// whole warp walks (elect_one: 923 -> 807 clocks).  At 8192 x 28672 x 4096: 746 us, 2579 TFLOP/s (2550 us for the
-// weights-on-rows kernel above, 2014 us for a CTA-pair version with one-lane issuing loops and direct stores).
+// What bounds it is the chain MMA -> accumulator ready -> scaled -> free -> MMA, about 830 clocks per block of K
+// at BN 256 where its MMAs take 512.  What the chain was made of, and what it cost (clocks per block): an
+// arrive.release.cluster waits for every load in flight, so the accumulator is released by a relaxed arrive
+// (tcgen05.fence orders the reads of TMEM before it) and the scales are fetched by warps of their own; a
+// one-lane issuing loop moves every descriptor into uniform registers, 930, so the whole warp walks it
+// (elect_one); the accumulator is released as soon as its last columns are in registers; four blocks are
+// unrolled, 900 otherwise.  An MMA per CTA with the columns multicast to both frees its accumulators without
+// the other CTA, but writes half as many bytes again to shared memory: 750 us at 8192 x 28672 x 4096, the
+// pair 710 us (2710 TFLOP/s); tokens on the columns, the kernel above: 2550 us.
 constexpr int kTileThreads = 384;
 constexpr int kScSlots = 4, kScGroup = 4;  // ring of scales: groups of four blocks of K
 
 template <int NCH>
 struct TileLayout {
   static constexpr int BN = 32 * NCH, CW = BN / 2;  // CW: columns of a scaling warp
-  static constexpr uint32_t A = 128 * 128, B = BN * 128, STAGE = A + B;
-  static constexpr int STAGES = 4;
+  static constexpr uint32_t A = 128 * 128, B = CW * 128, STAGE = A + B;
+  static constexpr int STAGES = 6;
   static constexpr uint32_t SC = STAGES * STAGE;         // per group: float4 of each of 128 rows, then of 2 x 2 column blocks
   static constexpr uint32_t SCSLOT = (128 + 4) * 16;
   static constexpr uint32_t OUT = SC + kScSlots * SCSLOT;  // per scaling warp: 32 rows x 64 bytes of C
@@ -373,11 +375,11 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) {
       tc::mbar_init(&full[i], 1);
-      tc::mbar_init(&empty[i], 2);  // both CTAs' MMAs have read their copy of the stage
+      tc::mbar_init(&empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       tc::mbar_init(&acc_full[i], 1);
-      tc::mbar_init(&acc_empty[i], 8);
+      tc::mbar_init(&acc_empty[i], 16);  // even CTA: both CTAs' 8 scaling warps
     }
     for (int i = 0; i < kScSlots; ++i) {
       tc::mbar_init(&sc_full[i], 64);
@@ -387,8 +389,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     tc::fence_mbar_init();
   }
   if (warp == 1) {
-    tc::tmem_alloc(tmem_slot, 512);
-    tc::tmem_relinquish();
+    tc::tmem_alloc_pair(tmem_slot, 512);
+    tc::tmem_relinquish_pair();
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -415,7 +417,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tc::prefetch_tmap(&ta);
       tc::prefetch_tmap(&tb);
       const bool leader = tc::elect_one();
-      const uint32_t emptya = smem_u32(empty);
+      const uint32_t emptya = smem_u32(empty), full0 = tc::mapa_cluster(smem_u32(full), 0);
       int s = 0;
       uint32_t ph = 1;  // parity of the stage's previous release: the first turn needs none
       bool ok = true;
@@ -427,16 +429,16 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = tc::mbar_wait_addr(emptya + s * 8, ph, abort_flag, p.wait_ns) && ok;
           uint8_t* sa = smem + s * L::STAGE;
           if (leader && ok) {
-            tc::mbar_arrive_expect_tx(&full[s], L::STAGE);
-            tc::tma_load_2d(sa, &ta, &full[s], kb * kBlk, tm * 128);
-            tc::tma_load_2d_multicast(sa + L::A + crank * (CW * 128), &tb, &full[s], kb * kBlk, tn * BN + crank * CW, 0x3);
+            if (crank == 0) tc::mbar_arrive_expect_tx(&full[s], 2 * L::STAGE);  // both CTAs' halves
+            tc::tma_load_2d_pair(sa, &ta, full0 + s * 8, kb * kBlk, tm * 128);
+            tc::tma_load_2d_pair(sa + L::A, &tb, full0 + s * 8, kb * kBlk, tn * BN + crank * CW);
           }
           __syncwarp();
           if (++s == ST) { s = 0; ph ^= 1; }
         }
       }
-    } else if (warp == 1) {
-      constexpr uint32_t idesc = tc::idesc_e4m3(128, BN);
+    } else if (warp == 1 && crank == 0) {
+      constexpr uint32_t idesc = tc::idesc_e4m3(256, BN);
       const uint64_t a0 = tc::sdesc_sw128(smem_u32(smem), 16, 1024), b0 = tc::sdesc_add(a0, L::A);
       const uint32_t fulla = smem_u32(full), acce = smem_u32(acc_empty);
       const bool leader = tc::elect_one();
@@ -454,9 +456,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (leader && ok) {
 #pragma unroll
             for (int k = 0; k < kBlk / 32; ++k)
-              tc::mma_ss_f8(d, tc::sdesc_add(ad, k * 32), tc::sdesc_add(bd, k * 32), idesc, k > 0);
-            tc::mma_commit(&acc_full[buf]);
-            tc::mma_commit_multicast(&empty[s], 0x3);
+              tc::mma_ss_pair_f8(d, tc::sdesc_add(ad, k * 32), tc::sdesc_add(bd, k * 32), idesc, k > 0);
+            tc::mma_commit_pair(&acc_full[buf]);
+            tc::mma_commit_pair(&empty[s]);
           }
           __syncwarp();
           if (++s == ST) { s = 0; ph ^= 1; }
@@ -464,7 +466,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           buf ^= 1;
         }
       }
-    } else {
+    } else if (warp >= 2) {
       // rows j and j + 64 of this CTA's 128, and (4 threads) the weight blocks under both column halves
       const int j = threadIdx.x - 64;
       const int nblocks = (int)ceil_div(p.N, kBlk);
@@ -512,7 +514,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + half * CW;
     int slot = 0, buf = 0;
     uint32_t sph = 0, aph = 0;
-    const uint32_t scf = smem_u32(sc_full), sce = smem_u32(sc_empty), accf = smem_u32(acc_full), acce = smem_u32(acc_empty);
+    const uint32_t scf = smem_u32(sc_full), sce = smem_u32(sc_empty), accf = smem_u32(acc_full);
+    const uint32_t acc0 = tc::mapa_cluster(smem_u32(acc_empty), 0);  // the even CTA's
     bool ok = true;
     for (int t = cid; t < n_tiles; t += n_clusters) {
       int tm, tn;
@@ -548,7 +551,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
                 // everything is in registers: the accumulator may be written again while these are scaled
                 tc::fence_before_sync();
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive_addr(acce + buf * 8);
+                if (lane == 0) tc::mbar_arrive_cluster_relaxed(acc0 + buf * 8);
               }
               const float f = kStraddle && g >= cut ? f1[u] : f0[u];
               const float2 f2 = make_float2(f, f);
@@ -613,7 +616,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   tc::cluster_sync();  // the peer's loads and commits reach into this CTA until it is done too
   if (warp == 1) {
     tc::fence_after_sync();
-    tc::tmem_dealloc(tmem, 512);
+    tc::tmem_dealloc_pair(tmem, 512);
   }
 }
 
@@ -646,16 +649,16 @@ cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t st) {
   if (a.M <= 32) return run_swap<32>(a, p, st);
   if (a.M <= 64) return run_swap<64>(a, p, st);
   // The modelled clocks of both kernels.  Tile kernel: the column width whose rounds over all clusters take the
-  // least; a block of K takes about 370 + 55 NCH (590 measured at 128 columns, 810 at 256), a tile's output about
-  // 2800 at 256 columns.  Tokens on the columns: about 1000 for a block of K.  Measured on both sides (us, tile
-  // kernel / tokens on the columns): 128 x 5120 x 8192 25.2 / 19.0, 128 x 4096 x 4096 15.1 / 12.0, 100 x 1024 x
-  // 4096 14.1 / 8.7; 128 x 28672 x 4096 33.6 / 41.2, 200 x 6144 x 4096 15.4 / 20.4, 256 x 5120 x 8192 25.4 / 38.8.
+  // least; a block of K takes about 300 + 66 NCH (565 measured at 128 columns, 830 at 256), a tile's output about
+  // 2000 at 256 columns.  Tokens on the columns: about 1000 for a block of K.  Measured on both sides (us, tile
+  // kernel / tokens on the columns): 128 x 5120 x 8192 21.6 / 18.9, 128 x 4096 x 4096 13.4 / 12.0, 100 x 1024 x
+  // 4096 12.3 / 8.5; 128 x 28672 x 4096 31.5 / 41.8, 200 x 6144 x 4096 13.7 / 20.3, 256 x 5120 x 8192 21.7 / 38.9.
   const int64_t clusters = sm_count() / 2, tm = ceil_div(a.M, 256);
   int best = 8;
   int64_t cost = INT64_MAX;
   for (int c = 8; c >= 4; --c) {
     const int64_t rounds = ceil_div(tm * ceil_div(a.N, 32 * c), clusters);
-    const int64_t k = rounds * ((int64_t)p.nkb * (370 + 55 * c) + 350 * c);
+    const int64_t k = rounds * ((int64_t)p.nkb * (300 + 66 * c) + 250 * c);
     if (k < cost) { cost = k; best = c; }
   }
   const int64_t ctas = ceil_div(a.N, 128) * ceil_div(a.M, 128);
