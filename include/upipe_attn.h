@@ -409,7 +409,8 @@ upipe_status_t upipe_attn_ring_bwd(const upipe_ring_desc_t* desc, const uint16_t
  * Root-mean-square norm with the residual's addition.  Per row of d elements:
  *   h = bf16(x + residual)  (without a residual h is x itself and is not written)
  *   rstd = (mean(h^2) + eps)^(-1/2)  (fp32 sum),   y = h * rstd * w
- * rows 0 .. 2^31 - 1; d a multiple of 8 (of 16 with q), at most 32768.
+ * rows 0 .. 2^31 - 1; d a multiple of 8 (of 16 with q), at most 32768.  The sum of h^2 has fp32's range: a
+ * row's magnitudes stay below 1e18 or so.
  *   x, residual  device bf16 [rows, d]; residual NULL exactly when h is
  *   w            device bf16 [d]
  *   h            device bf16 [rows, d] (written): the residual stream; may be x or residual itself
@@ -455,7 +456,7 @@ upipe_status_t upipe_attn_fp8_quantize(int64_t rows, int64_t cols, int32_t block
  *   a_scale  device fp32 [ceil(K / 128)] rows of a_scale_ld >= M
  *   b_scale  device fp32 [ceil(N / 128)][ceil(K / 128)]
  *   C        device [M, N], rows of ldc elements; c_dtype 0: fp32, 1: bf16
- * M >= 0; K, lda, ldb multiples of 16; N, ldc multiples of 8; M, N, K <= 2^31 - 1. */
+ * M >= 0; K, lda, ldb multiples of 16; N, ldc multiples of 8; M, N, K <= 2^31 - 1.  C overlaps no operand. */
 upipe_status_t upipe_attn_gemm_fp8_nt(int64_t M, int64_t N, int64_t K, const uint8_t* A, int64_t lda,
                                       const float* a_scale, int64_t a_scale_ld, const uint8_t* B, int64_t ldb,
                                       const float* b_scale, void* C, int64_t ldc, int32_t c_dtype, void* stream);
@@ -478,8 +479,10 @@ typedef struct {
 } upipe_rope_desc_t;
 /* Heads of one tensor, read and written through their own strides (in elements, multiples of 8; a row's
  * elements are contiguous): head-major as the attention core takes them, or a part of the projection's
- * token-major output.  out may be in itself with the same strides; otherwise the two must not overlap.
- * No two rows of out may overlap, nor may the outputs of q and k. */
+ * token-major output.  Strides of a single head or token do not count.  out may be in itself with the same
+ * strides; no output may otherwise share an element with an input or with the other output, nor two rows of
+ * an output with each other (UPIPE_ERR_INVALID_ARG, also where the strides do not show that they are apart:
+ * only separate ranges and parts of one token-major or head-major tensor are told apart). */
 typedef struct {
   const uint16_t* in;
   uint16_t* out;

@@ -516,9 +516,11 @@ def _rows(t, dev, shape, what):
     if t.get_device() != dev or t.shape != shape:
         _refuse(f"{what}: {tuple(shape)} on device {dev} expected, got {tuple(t.shape)} on {t.device}")
     ld, inner = t.stride()
-    if inner != 1 and shape[1] > 1:
-        _refuse(f"{what}: contiguous rows expected, got strides {t.stride()}")
-    return t.data_ptr(), ld if shape[0] > 1 and ld > shape[1] else shape[1]
+    if shape[0] <= 1:
+        ld = shape[1]
+    if (inner != 1 and shape[1] > 1) or ld < shape[1]:
+        _refuse(f"{what}: rows that are contiguous and do not overlap expected, got strides {t.stride()}")
+    return t.data_ptr(), ld
 
 
 def gemm_fp8_nt(A, a_scale, B, b_scale, C, stream=None):

@@ -47,22 +47,43 @@ int64_t span_bytes(int64_t heads, int64_t tokens, int64_t hs, int64_t ts, int64_
   return 2 * ((heads - 1) * hs + (tokens - 1) * ts + elems);
 }
 
-upipe_status_t check_rope_side(const upipe_rope_tensor_t* t, int64_t tokens, int head_dim) {
+// Rows of one tensor: [heads][tokens] of `elems` elements; strides of single heads or tokens do not count.
+struct RopeRows {
+  const void* base;
+  int64_t heads, tokens, hs, ts, elems;
+  int64_t bytes() const { return span_bytes(heads, tokens, hs, ts, elems); }
+  bool same(const RopeRows& o) const { return base == o.base && hs == o.hs && ts == o.ts; }
+};
+RopeRows rows_of(const void* base, int64_t heads, int64_t tokens, int64_t hs, int64_t ts, int64_t elems) {
+  return RopeRows{base, heads, tokens, heads > 1 ? hs : 0, tokens > 1 ? ts : 0, elems};
+}
+
+// Whether two tensors share elements, as far as it can be told from their strides: not if their address ranges
+// are apart, nor if they are parts of one token-major (or head-major) tensor, the heads (tokens) of the one in
+// the gaps of the other.
+bool rows_may_meet(const RopeRows& a, const RopeRows& b) {
+  if (!overlaps(a.base, a.bytes(), b.base, b.bytes())) return false;
+  auto in_gaps = [&](int64_t period_a, int64_t period_b, int64_t inner_a, int64_t inner_b) {
+    if (period_a != period_b || period_a <= 0) return false;
+    const int64_t d = (reinterpret_cast<intptr_t>(b.base) - reinterpret_cast<intptr_t>(a.base)) / 2;
+    const int64_t off = ((d % period_a) + period_a) % period_a;  // b's place in a's period
+    return off >= inner_a && off + inner_b <= period_a;
+  };
+  return !in_gaps(a.ts, b.ts, (a.heads - 1) * a.hs + a.elems, (b.heads - 1) * b.hs + b.elems) &&
+         !in_gaps(a.hs, b.hs, (a.tokens - 1) * a.ts + a.elems, (b.tokens - 1) * b.ts + b.elems);
+}
+
+upipe_status_t check_rope_side(const upipe_rope_tensor_t* t, int64_t tokens, int head_dim, RopeRows& in, RopeRows& out) {
   if (t->n_heads < 0) return UPIPE_ERR_INVALID_ARG;
   if (t->n_heads == 0) return UPIPE_OK;
   if (!t->in || !t->out) return UPIPE_ERR_INVALID_ARG;
-  if (t->in_head_stride < 0 || t->in_token_stride < 0 || t->out_head_stride < 0 || t->out_token_stride < 0)
-    return UPIPE_ERR_INVALID_ARG;
-  if (!rows_disjoint(t->n_heads, tokens, t->out_head_stride, t->out_token_stride, head_dim)) return UPIPE_ERR_INVALID_ARG;
-  if (t->in_head_stride % 8 || t->in_token_stride % 8 || t->out_head_stride % 8 || t->out_token_stride % 8)
-    return UPIPE_ERR_UNSUPPORTED;
+  in = rows_of(t->in, t->n_heads, tokens, t->in_head_stride, t->in_token_stride, head_dim);
+  out = rows_of(t->out, t->n_heads, tokens, t->out_head_stride, t->out_token_stride, head_dim);
+  if (in.hs < 0 || in.ts < 0 || out.hs < 0 || out.ts < 0) return UPIPE_ERR_INVALID_ARG;
+  if (!rows_disjoint(out.heads, tokens, out.hs, out.ts, head_dim)) return UPIPE_ERR_INVALID_ARG;
+  if (in.hs % 8 || in.ts % 8 || out.hs % 8 || out.ts % 8) return UPIPE_ERR_UNSUPPORTED;
   if (!aligned16(t->in) || !aligned16(t->out)) return UPIPE_ERR_ALIGNMENT;
-  const bool same = t->in == t->out && (t->n_heads == 1 || t->in_head_stride == t->out_head_stride) &&
-                    (tokens == 1 || t->in_token_stride == t->out_token_stride);
-  if (!same &&
-      overlaps(t->in, span_bytes(t->n_heads, tokens, t->in_head_stride, t->in_token_stride, head_dim), t->out,
-               span_bytes(t->n_heads, tokens, t->out_head_stride, t->out_token_stride, head_dim)))
-    return UPIPE_ERR_INVALID_ARG;
+  if (!in.same(out) && rows_may_meet(in, out)) return UPIPE_ERR_INVALID_ARG;
   return UPIPE_OK;
 }
 
@@ -154,9 +175,14 @@ upipe_status_t upipe_attn_rope(const upipe_rope_desc_t* desc, int64_t tokens, co
     if (!std::isfinite(desc->inv_freq[j]) || desc->axis[j] >= desc->n_axes) return UPIPE_ERR_INVALID_ARG;
   if (tokens == 0) return UPIPE_OK;
   if (!positions) return UPIPE_ERR_INVALID_ARG;
-  upipe_status_t s = check_rope_side(q, tokens, desc->head_dim);
-  if (s == UPIPE_OK && k) s = check_rope_side(k, tokens, desc->head_dim);
+  RopeRows rows[4] = {};
+  upipe_status_t s = check_rope_side(q, tokens, desc->head_dim, rows[0], rows[1]);
+  if (s == UPIPE_OK && k) s = check_rope_side(k, tokens, desc->head_dim, rows[2], rows[3]);
   if (s != UPIPE_OK) return s;
+  // one launch: neither output may touch the other tensor
+  if (k && q->n_heads && k->n_heads &&
+      (rows_may_meet(rows[1], rows[2]) || rows_may_meet(rows[1], rows[3]) || rows_may_meet(rows[0], rows[3])))
+    return UPIPE_ERR_INVALID_ARG;
   if (q->n_heads > 65535 - (k ? k->n_heads : 0)) return UPIPE_ERR_UNSUPPORTED;
   if (!aligned16(positions)) return UPIPE_ERR_ALIGNMENT;
   RopeArgs a{};
@@ -225,12 +251,15 @@ upipe_status_t upipe_attn_gemm_fp8_nt(int64_t M, int64_t N, int64_t K, const uin
       a_scale_ld < M || (c_dtype != 0 && c_dtype != 1))
     return UPIPE_ERR_INVALID_ARG;
   if (K % 16 || N % 8 || lda % 16 || ldb % 16 || ldc % 8) return UPIPE_ERR_UNSUPPORTED;
+  if (ceil_div(M, 256) * ceil_div(N, 128) > INT32_MAX / 2) return UPIPE_ERR_UNSUPPORTED;  // tiles are counted in 32 bits
   if (M == 0) return UPIPE_OK;
   if (!A || !a_scale || !B || !b_scale || !C) return UPIPE_ERR_INVALID_ARG;
   if (!aligned16(A) || !aligned16(B) || !aligned16(C) || !aligned16(a_scale) || !aligned16(b_scale))
     return UPIPE_ERR_ALIGNMENT;
   const int64_t c_bytes = ((M - 1) * ldc + N) * (c_dtype ? 2 : 4);
-  if (overlaps(C, c_bytes, A, (M - 1) * lda + K) || overlaps(C, c_bytes, B, (N - 1) * ldb + K))
+  const int64_t nkb = ceil_div(K, 128);
+  if (overlaps(C, c_bytes, A, (M - 1) * lda + K) || overlaps(C, c_bytes, B, (N - 1) * ldb + K) ||
+      overlaps(C, c_bytes, a_scale, ((nkb - 1) * a_scale_ld + M) * 4) || overlaps(C, c_bytes, b_scale, ceil_div(N, 128) * nkb * 4))
     return UPIPE_ERR_INVALID_ARG;
   const Fp8GemmArgs g{M, N, K, A, lda, a_scale, a_scale_ld, B, ldb, b_scale, C, ldc, c_dtype};
   return cuda_status(launch_gemm_fp8(g, (cudaStream_t)stream));

@@ -633,7 +633,6 @@ cudaError_t run_tile(const Fp8GemmArgs& a, const Fp8Params& p, cudaStream_t st) 
   // the fast index sweeps the smaller operand, so the larger one is read from DRAM about once
   const TileSched sch{(int)ceil_div(a.M, 256), (int)ceil_div(a.N, L::BN), a.N > a.M};
   const int64_t units = (int64_t)sch.tiles_mp * sch.tiles_n;
-  if (units > INT32_MAX / 2) return cudaErrorInvalidValue;
   const unsigned grid = (unsigned)(2 * std::max<int64_t>(1, std::min<int64_t>(units, sm_count() / 2)));
   e = launch_pdl_cluster(kfn, dim3(grid), dim3(kTileThreads), smem, st, 2, ta, tb, p, sch);
   note_launch();

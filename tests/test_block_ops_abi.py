@@ -85,6 +85,8 @@ def test_fp8_quantize_refusals(kw, code):
     (dict(lda=128), 1), (dict(ldb=264), 2), (dict(ldc=100), 1), (dict(ldc=516), 2), (dict(lds=63), 1), (dict(ct=2), 1), (dict(A=None), 1),
     (dict(sb=None), 1), (dict(A=ODD), 3), (dict(C=ODD), 3), (dict(sa=ODD), 3),
     (dict(C=fake(0)), 1), (dict(C=fake(2) + 4096), 1),  # C over A, inside B
+    (dict(C=fake(1)), 1), (dict(C=fake(3)), 1),         # over the scales
+    (dict(M=1 << 30, N=1 << 30, ldc=1 << 30, lds=1 << 30), 2),
     (dict(M=0, A=None, sa=None, C=None), 0)])
 def test_gemm_fp8_refusals(kw, code):
     a = dict(M=64, N=512, K=256, A=fake(0), lda=256, sa=fake(1), lds=64, B=fake(2), ldb=256, sb=fake(3), C=fake(4), ldc=512,
@@ -117,6 +119,27 @@ def test_rope_refuses_layouts(kw, code):
     good = rope_side(in_=fake(2), out=fake(3))
     if kw.get("n_heads", 1) < 65536:
         assert rope(good, k=rope_side(**kw)) == code
+
+
+def test_rope_tells_parts_of_one_tensor_from_tensors_that_meet():
+    """Only refusals are called here: what is accepted would launch."""
+    tok = 12 * 128                                                     # token-major: 8 + 2 + 2 heads of 128
+    side = lambda base, out, heads, hs=128, ts=tok, oh=128, ot=tok: up.RopeTensor(base, out, hs, ts, oh, ot, heads)
+    a, b = fake(0), fake(5)
+    kb = 8 * 128 * 2                                                   # bytes to the first key head
+    bad = [
+        (side(a, b, 8), side(a + kb, b, 2)),                           # the same output twice
+        (side(a, b, 8), side(a + kb, b + kb - 256, 2)),                # outputs that share a head
+        (side(a, a + 256, 2), None),                                   # moved by one head, over its neighbour
+        (side(a, a, 8), side(a + kb - 256, b, 2)),                     # q in place over a head that k reads
+        (side(a + kb, b, 2), side(a, a, 9)),                           # k in place over heads that q reads
+        (side(a, b, 8), side(a + kb, b + kb, 2, oh=128, ot=tok * 2)),  # outputs of different strides, ranges that overlap
+        (side(a, b, 8, oh=64 * 128, ot=128), side(a + kb, b + 2 * 7 * 64 * 128, 2, oh=64 * 128, ot=128)),
+    ]
+    for q, k in bad:
+        assert rope(q, k=k) == 1
+    one = up.RopeTensor(a, ODD, 3, 5, 3, 5, 1)                         # one head, one token: strides do not count
+    assert rope(one, tokens=1) == 3
 
 
 def test_rope_refuses_descriptors():

@@ -478,13 +478,20 @@ def test_binding_refuses_wrong_tensors():
            lambda: up.rms_norm_fwd(torch.zeros(256, 4, dtype=torch.bfloat16, device="cuda").t(), w, y), lambda: up.rms_norm_fwd(x[0], w, y),
            lambda: up.rms_norm_fwd_fp8(x, w, q, s.t()), lambda: up.rms_norm_fwd_fp8(x, w, q.view(torch.uint8), s),
            lambda: up.fp8_quantize(x, q, s.t()), lambda: up.fp8_quantize(x, q, s, block_rows=64), lambda: up.gemm_fp8_nt(q, s, q, s, y),
-           lambda: up.gemm_fp8_nt(q, s, q, s[:1], y.half()), lambda: up.rope(up.make_rope_desc(64, [0.1] * 32), y[None], None, s, y[None], None)]
+           lambda: up.gemm_fp8_nt(q, s, q, s[:1], y.half()),
+           lambda: up.gemm_fp8_nt(q[:1].expand(4, 256), s, q, s[:1, :2].contiguous(), y[:, :4]),   # rows that overlap
+           lambda: up.gemm_fp8_nt(q, s[:, :1].expand(2, 4), q, s[:1, :2].contiguous(), y[:, :4]),
+           lambda: up.gemm_fp8_nt(q, s, q, s[:1, :2].contiguous(), y[:1, :4].expand(4, 4)), lambda: up.rope(up.make_rope_desc(64, [0.1] * 32), y[None], None, s, y[None], None)]
     n = up.launch_count()
     for call in bad:
         with pytest.raises(ValueError):
             call()
     with pytest.raises(up.UpipeError):
         up.rms_norm_fwd(x, w, y, residual=x)              # a residual without h
+    d, pos, z = up.make_rope_desc(64, [0.1] * 32), torch.zeros(1, 4, dtype=torch.int32, device="cuda"), y.view(4, 4, 64)
+    for q_out, k_out in ((y.view(4, 4, 64), y.view(4, 4, 64)), (z[:1].expand(4, 4, 64), x.view(4, 4, 64))):
+        with pytest.raises(up.UpipeError):
+            up.rope(d, x.view(4, 4, 64), x.view(4, 4, 64), pos, q_out, k_out)
     with pytest.raises(up.UpipeError):
         up.rms_norm_bwd(x, x, w, s.view(-1)[:4].contiguous(), y, s.new_empty(256), torch.empty(16, dtype=torch.uint8, device="cuda"))
     assert up.launch_count() == n
