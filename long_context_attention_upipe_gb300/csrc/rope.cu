@@ -140,9 +140,8 @@ uint64_t turn_fraction(double inv_freq) {
   const double turns = inv_freq / 6.283185307179586476925;
   double f = turns - std::floor(turns);
   if (!(f < 1.0)) f = 0.0;
-  const double hi = std::floor(std::ldexp(f, 32));
-  const double lo = std::ldexp(std::ldexp(f, 32) - hi, 32);
-  return ((uint64_t)hi << 32) | (uint64_t)lo;
+  const double scaled = f * 4294967296.0, hi = std::floor(scaled);  // powers of two and their differences are exact
+  return ((uint64_t)hi << 32) | (uint64_t)((scaled - hi) * 4294967296.0);
 }
 
 }  // namespace
