@@ -386,7 +386,7 @@ NormShape norm_shape(int64_t rows, int d, int& V) {
 // thread (d 5120: 123 us, two vectors 130 us at 16381 rows).
 NormShape bwd_shape(int64_t rows, int d, int& V) {
   NormShape n = norm_shape(rows, d, V);
-  if (n.tpr > 256 && n.tpr <= 320) {
+  if (V == 2 && n.tpr > 256 && n.tpr <= 320) {
     V = 1;
     n.tpr = (int)ceil_div(d / 8, 32) * 32;
   }
@@ -431,7 +431,7 @@ cudaError_t launch_rms_fwd(const RmsNormArgs& a, cudaStream_t st) {
   int V = 1;
   const NormShape n = norm_shape(a.rows, a.d, V);
   if (V == 1) return run_rms_fwd<1, 320, 3, true>(n, a, st);
-  if (n.tpr <= 320) return run_rms_fwd<2, 320, 3, true>(n, a, st);
+  if (V == 2 && n.tpr <= 320) return run_rms_fwd<2, 320, 3, true>(n, a, st);
   if (V == 2) return run_rms_fwd<2, 512, 2, true>(n, a, st);
   if (n.tpr <= 512) return run_rms_fwd<4, 512, 1, true>(n, a, st);
   return run_rms_fwd<4, kMaxNormThreads, 1, false>(n, a, st);
@@ -460,7 +460,7 @@ cudaError_t launch_rms_bwd(const RmsNormBwdArgs& a, float* part, cudaStream_t st
     cudaError_t e;
     if (n.tpr > 512 && V == 1) e = run_rms_bwd<1, 640, 1, true>(n, a, part, st);
     else if (V == 1) e = run_rms_bwd<1, 256, 3, true>(n, a, part, st);
-    else if (n.tpr <= 256) e = run_rms_bwd<2, 256, 2, true>(n, a, part, st);
+    else if (V == 2 && n.tpr <= 256) e = run_rms_bwd<2, 256, 2, true>(n, a, part, st);
     else if (V == 2) e = run_rms_bwd<2, 512, 1, true>(n, a, part, st);
     else if (n.tpr <= 512) e = run_rms_bwd<4, 512, 1, false>(n, a, part, st);
     else e = run_rms_bwd<4, kMaxNormThreads, 1, false>(n, a, part, st);

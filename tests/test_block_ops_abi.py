@@ -67,6 +67,8 @@ def test_rms_norm_workspace():
     assert up.rms_norm_workspace_bytes(1, 64) >= 64 * 4
     a, b = (up.rms_norm_workspace_bytes(n, 4096) for n in (1 << 20, 1 << 24))
     assert a == b                                     # a share per resident group of threads, not per row
+    for d in (8, 4096, 5120, 8192, 8208, 10240, 16384, 32768):         # a share per group, at most a row's threads each
+        assert up.rms_norm_workspace_bytes(1, d) <= 16 * 4 * d
     with pytest.raises(up.UpipeError):
         up.rms_norm_workspace_bytes(4, 20)
 

@@ -83,8 +83,9 @@ def check_q(q, s, y, br, rel):
     within(q, v, torch.maximum((v.abs() + off) * 2.0 ** -4, torch.full_like(v, 2.0 ** -10)) + off)
 
 
-SHAPES = [(1, 8), (3, 64), (17, 128), (33, 136), (5, 256), (2, 264), (7, 1040), (130, 4096), (3, 5120), (2, 8192), (1, 16384),
-          (2, 16400), (1, 32768), (0, 256)]
+# rows that end within each step of the threads per row and vectors per thread
+SHAPES = [(1, 8), (3, 64), (17, 128), (33, 136), (5, 256), (2, 264), (7, 1040), (130, 4096), (3, 4112), (3, 5120), (3, 5136), (2, 8192),
+          (3, 8208), (2, 10240), (2, 10256), (1, 16384), (2, 16400), (1, 32768), (0, 256)]
 
 
 @pytest.mark.parametrize("rows,d", SHAPES)
@@ -143,7 +144,8 @@ def test_norm_keeps_nan_and_infinity_in_their_rows():
 
 
 @pytest.mark.parametrize("rows,d", [(1, 8), (3, 64), (300, 128), (33, 136), (5, 256), (2, 264), (7, 1040), (1000, 4096),
-                                    (3, 5120), (1, 16384), (2, 16400), (1, 32768), (0, 256)])
+                                    (3, 4112), (3, 5120), (3, 5136), (2, 8192), (3, 8208), (2, 10240), (2, 10256), (1, 16384),
+                                    (2, 16400), (1, 32768), (0, 256)])
 @pytest.mark.parametrize("dres", [False, True])
 def test_norm_backward(rows, d, dres):
     g = gen(rows + 3 * d)
