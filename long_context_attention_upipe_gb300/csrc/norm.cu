@@ -262,6 +262,65 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rms_bwd(NormShape n, const bf16*
   }
 }
 
+// The same for rows of more than 16384 columns (1024 threads at 64 registers), whose vectors do not fit into
+// registers beside the sums of dw: the row is read twice, the second time from L1 or L2 (3.9 TB/s at d 32768,
+// where spilled registers left 1.5; at d 16384 the kernel above runs at 4.8, this one at 4.3).
+template <int V>
+__global__ void __launch_bounds__(kMaxNormThreads, 1) k_rms_bwd_long(NormShape n, const bf16* dy, const bf16* h,
+                                                                     const bf16* __restrict__ w,
+                                                                     const float* __restrict__ rstd_in, const bf16* dres,
+                                                                     bf16* dx, float* part) {
+  __shared__ float red[2][32];
+  const int t = threadIdx.x, nvec = n.d >> 3;
+  grid_dep_wait();
+  V8 dw[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i)
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dw[i].v[k] = 0.f;
+  int par = 0;
+  for (int64_t row = blockIdx.x; row < n.rows; row += gridDim.x, par ^= 1) {
+    const float rstd = rstd_in[row];
+    const bf16 *dyr = dy + row * n.d, *hr = h + row * n.d, *rr = dres ? dres + row * n.d : nullptr;
+    bf16* dxr = dx + row * n.d;
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = t + i * n.tpr;
+      if (c >= nvec) continue;
+      const V8 a = unpack8(*reinterpret_cast<const uint4*>(dyr + c * 8)), b = unpack8(*reinterpret_cast<const uint4*>(hr + c * 8));
+      const V8 wf = unpack8(*reinterpret_cast<const uint4*>(w + c * 8));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        dot += a.v[k] * wf.v[k] * b.v[k];
+        dw[i].v[k] += a.v[k] * (b.v[k] * rstd);
+      }
+    }
+    dot = group_sum(dot, n.tpr, red[par]);
+    const float m = dot / (float)n.d * rstd * rstd;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = t + i * n.tpr;
+      if (c >= nvec) continue;
+      const V8 a = unpack8(*reinterpret_cast<const uint4*>(dyr + c * 8)), b = unpack8(*reinterpret_cast<const uint4*>(hr + c * 8));
+      const V8 wf = unpack8(*reinterpret_cast<const uint4*>(w + c * 8));
+      const V8 r = unpack8(rr ? *reinterpret_cast<const uint4*>(rr + c * 8) : make_uint4(0, 0, 0, 0));
+      V8 o;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o.v[k] = r.v[k] + rstd * (a.v[k] * wf.v[k] - b.v[k] * m);
+      *reinterpret_cast<uint4*>(dxr + c * 8) = pack8(o);
+    }
+  }
+  float* dst = part + (int64_t)blockIdx.x * n.d;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = t + i * n.tpr;
+    if (c >= nvec) continue;
+    *reinterpret_cast<float4*>(dst + c * 8) = make_float4(dw[i].v[0], dw[i].v[1], dw[i].v[2], dw[i].v[3]);
+    *reinterpret_cast<float4*>(dst + c * 8 + 4) = make_float4(dw[i].v[4], dw[i].v[5], dw[i].v[6], dw[i].v[7]);
+  }
+}
+
 // dw[c] = sum over p of part[p][c], in an order that depends on the shape alone: 32 columns per block, 32
 // warps that each take every 32nd partial row (4 loads in flight), then the warps in turn.
 __global__ void __launch_bounds__(1024) k_dw_reduce(const float* __restrict__ part, int p_rows, int d, float* dw) {
@@ -463,7 +522,11 @@ cudaError_t launch_rms_bwd(const RmsNormBwdArgs& a, float* part, cudaStream_t st
     else if (V == 2 && n.tpr <= 256) e = run_rms_bwd<2, 256, 2, true>(n, a, part, st);
     else if (V == 2) e = run_rms_bwd<2, 512, 1, true>(n, a, part, st);
     else if (n.tpr <= 512) e = run_rms_bwd<4, 512, 1, false>(n, a, part, st);
-    else e = run_rms_bwd<4, kMaxNormThreads, 1, false>(n, a, part, st);
+    else {
+      e = launch_pdl(k_rms_bwd_long<4>, dim3((unsigned)norm_blocks(n, bwd_threads(V))), dim3(n.tpr), 0, st, n, a.dy, a.h, a.w, a.rstd,
+                     a.dres, a.dx, part);
+      note_launch();
+    }
     if (e != cudaSuccess) return e;
   }
   const cudaError_t e = launch_pdl(k_dw_reduce, dim3((unsigned)ceil_div(a.d, 32)), dim3(1024), 0, st, (const float*)part, p_rows,
