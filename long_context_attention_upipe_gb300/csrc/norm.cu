@@ -18,14 +18,16 @@
 // number, so a NaN reaches its block's scale.
 #include <cuda_fp8.h>
 
-#include "common.cuh"
 #include "internal.h"
+#include "tc_common.cuh"
 
 namespace upipe {
 
 namespace {
 
 constexpr int kMaxNormThreads = 1024;
+constexpr int kRingBytes = 216 * 1024;
+constexpr int kMaxRing = 8;  // rows in flight of the ring kernel
 
 struct V8 {
   float v[8];
@@ -262,6 +264,131 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rms_bwd(NormShape n, const bf16*
   }
 }
 
+// The same for rows of 4104 to 16384 columns, whose next row would not fit into registers without leaving SMs
+// short of threads: a producer warp copies whole rows (dy, h, dres) ahead into a ring in shared memory, tpr
+// threads work on one row after the other.  One block per SM.
+template <int V>
+__global__ void __launch_bounds__(V == 2 ? 512 : 544, 1) k_rms_bwd_ring(NormShape n, const bf16* dy, const bf16* h, const bf16* __restrict__ w,
+                                                         const float* __restrict__ rstd_in, const bf16* dres, bf16* dx,
+                                                         float* part, int stages, uint64_t wait_ns) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ uint64_t full[kMaxRing], empty[kMaxRing];
+  __shared__ float red[2][32];
+  __shared__ int abort_word;
+  volatile int* abort_flag = &abort_word;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nvec = n.d >> 3, nw = n.tpr >> 5;
+  const uint32_t row_bytes = (uint32_t)n.d * 2, stage_bytes = row_bytes * (dres ? 3 : 2);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) {
+      tc::mbar_init(&full[i], 1);
+      tc::mbar_init(&empty[i], nw);
+    }
+    abort_word = 0;
+    tc::fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dep_wait();
+  int s = 0;
+  bool ok = true;
+  if (warp == 0) {
+    const bool leader = tc::elect_one();
+    uint32_t ph = 1;  // parity of the stage's previous release: the first turn needs none
+    for (int64_t row = blockIdx.x; row < n.rows; row += gridDim.x) {
+      ok = tc::mbar_wait_addr(smem_u32(&empty[s]), ph, abort_flag, wait_ns) && ok;
+      if (leader && ok) {
+        uint8_t* st = ring + s * stage_bytes;
+        tc::mbar_arrive_expect_tx(&full[s], stage_bytes);
+        tc::bulk_load(st, dy + row * n.d, row_bytes, &full[s]);
+        tc::bulk_load(st + row_bytes, h + row * n.d, row_bytes, &full[s]);
+        if (dres) tc::bulk_load(st + 2 * row_bytes, dres + row * n.d, row_bytes, &full[s]);
+      }
+      __syncwarp();
+      if (++s == stages) { s = 0; ph ^= 1; }
+    }
+    return;
+  }
+  const int t = threadIdx.x - 32;
+  // two vectors per thread stay in registers between the sum and the output; four are read from the ring again
+  constexpr bool kHold = V == 2;
+  uint4 wv[kHold ? V : 1];
+  V8 dw[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = t + i * n.tpr;
+    if (kHold) wv[i] = c < nvec ? *reinterpret_cast<const uint4*>(w + c * 8) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) dw[i].v[k] = 0.f;
+  }
+  uint32_t ph = 0;
+  int par = 0;
+  float rstd_next = blockIdx.x < n.rows ? rstd_in[blockIdx.x] : 0.f;
+  for (int64_t row = blockIdx.x; row < n.rows; row += gridDim.x, par ^= 1) {
+    const float rstd = rstd_next;
+    if (row + gridDim.x < n.rows) rstd_next = rstd_in[row + gridDim.x];
+    ok = tc::mbar_wait_addr(smem_u32(&full[s]), ph, abort_flag, wait_ns) && ok;
+    const uint8_t* st = ring + s * stage_bytes;
+    uint4 dv[V], hv[V], rv[V];
+    auto read = [&](int i, int c) {
+      dv[i] = hv[i] = rv[i] = make_uint4(0, 0, 0, 0);
+      if (c < nvec) {
+        dv[i] = *reinterpret_cast<const uint4*>(st + c * 16);
+        hv[i] = *reinterpret_cast<const uint4*>(st + row_bytes + c * 16);
+        if (dres) rv[i] = *reinterpret_cast<const uint4*>(st + 2 * row_bytes + c * 16);
+      }
+    };
+    auto weight = [&](int i, int c) {
+      return kHold ? wv[i] : c < nvec ? *reinterpret_cast<const uint4*>(w + c * 8) : make_uint4(0, 0, 0, 0);
+    };
+    auto release = [&]() {
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&empty[s]);
+      if (++s == stages) { s = 0; ph ^= 1; }
+    };
+    float dot = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = t + i * n.tpr;
+      read(i, c);
+      const V8 a = unpack8(dv[i]), b = unpack8(hv[i]), wf = unpack8(weight(i, c));
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        dot += a.v[k] * wf.v[k] * b.v[k];
+        dw[i].v[k] += a.v[k] * (b.v[k] * rstd);
+      }
+    }
+    if (kHold) release();
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+    if (lane == 0) red[par][warp - 1] = dot;
+    tc::named_bar_sync(1, n.tpr);
+    dot = lane < nw ? red[par][lane] : 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
+    const float m = dot / (float)n.d * rstd * rstd;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = t + i * n.tpr;
+      if (c >= nvec || !ok) continue;
+      if (!kHold) read(i, c);
+      const V8 a = unpack8(dv[i]), b = unpack8(hv[i]), wf = unpack8(weight(i, c)), r = unpack8(rv[i]);
+      V8 o;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) o.v[k] = r.v[k] + rstd * (a.v[k] * wf.v[k] - b.v[k] * m);
+      *reinterpret_cast<uint4*>(dx + row * n.d + c * 8) = pack8(o);
+    }
+    if (!kHold) release();
+  }
+  float* dst = part + (int64_t)blockIdx.x * n.d;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = t + i * n.tpr;
+    if (c >= nvec) continue;
+    const float bad = ok ? 0.f : __int_as_float(0x7fc00000);  // a wait that ran out leaves NaN
+    *reinterpret_cast<float4*>(dst + c * 8) = make_float4(dw[i].v[0] + bad, dw[i].v[1] + bad, dw[i].v[2] + bad, dw[i].v[3] + bad);
+    *reinterpret_cast<float4*>(dst + c * 8 + 4) = make_float4(dw[i].v[4] + bad, dw[i].v[5] + bad, dw[i].v[6] + bad, dw[i].v[7] + bad);
+  }
+}
+
 // The same for rows of more than 16384 columns (1024 threads at 64 registers), whose vectors do not fit into
 // registers beside the sums of dw: the row is read twice, the second time from L1 or L2 (3.9 TB/s at d 32768,
 // where spilled registers left 1.5; at d 16384 the kernel above runs at 4.8, this one at 4.3).
@@ -441,13 +568,14 @@ NormShape norm_shape(int64_t rows, int d, int& V) {
 
 // The backward pass holds a row's vectors twice (the next row's are in flight) and the sums of dw: at two
 // vectors per thread it takes 128 registers (at 96 it spills and runs at half the speed), so an SM holds 512
-// threads.  Rows of 257 to 320 such threads would leave a third of them unused: they take one vector per
-// thread (d 5120: 123 us, two vectors 130 us at 16381 rows).
+// threads.  Between 4096 and 16384 columns the rows in flight lie in shared memory instead.
+bool bwd_ring(int d) { return d > 4096 && d <= 16384; }
 NormShape bwd_shape(int64_t rows, int d, int& V) {
   NormShape n = norm_shape(rows, d, V);
-  if (V == 2 && n.tpr > 256 && n.tpr <= 320) {
-    V = 1;
-    n.tpr = (int)ceil_div(d / 8, 32) * 32;
+  if (bwd_ring(d)) {  // with its producer warp at most 16 warps at two vectors per thread: 128 registers
+    V = d <= 7680 ? 2 : 4;
+    n.tpr = (int)ceil_div(d / 8, 32 * V) * 32;
+    n.rpb = 1;
   }
   return n;
 }
@@ -461,7 +589,7 @@ int64_t norm_blocks(const NormShape& n, int per_sm_threads) {
 // resident threads per SM that the launch bounds below leave room for
 constexpr int kFwdThreadsPerSm = 1024, kBwdThreadsPerSm = 512, kBwdThreadsPerSmNarrow = 768;
 
-int bwd_threads(int V) { return V == 1 ? kBwdThreadsPerSmNarrow : kBwdThreadsPerSm; }
+int bwd_threads(int d, int V) { return bwd_ring(d) ? 0 : V == 1 ? kBwdThreadsPerSmNarrow : kBwdThreadsPerSm; }
 
 }  // namespace
 
@@ -499,13 +627,25 @@ cudaError_t launch_rms_fwd(const RmsNormArgs& a, cudaStream_t st) {
 size_t rms_bwd_workspace(int64_t rows, int d) {
   int V = 1;
   const NormShape n = bwd_shape(std::max<int64_t>(rows, 1), d, V);
-  return (size_t)norm_blocks(n, bwd_threads(V)) * n.rpb * d * sizeof(float);
+  return (size_t)norm_blocks(n, bwd_threads(n.d, V)) * n.rpb * d * sizeof(float);
 }
 
 template <int V, int MAXT, int MINB, bool PF>
 static cudaError_t run_rms_bwd(const NormShape& n, const RmsNormBwdArgs& a, float* part, cudaStream_t st) {
-  const dim3 grid((unsigned)norm_blocks(n, bwd_threads(V))), block(n.tpr * n.rpb);
+  const dim3 grid((unsigned)norm_blocks(n, bwd_threads(n.d, V))), block(n.tpr * n.rpb);
   const cudaError_t e = launch_pdl(k_rms_bwd<V, MAXT, MINB, PF>, grid, block, 0, st, n, a.dy, a.h, a.w, a.rstd, a.dres, a.dx, part);
+  note_launch();
+  return e;
+}
+
+template <int V>
+static cudaError_t run_rms_bwd_ring(const NormShape& n, const RmsNormBwdArgs& a, float* part, cudaStream_t st) {
+  const int stage = n.d * 2 * (a.dres ? 3 : 2);
+  const int stages = std::min(kMaxRing, kRingBytes / stage);
+  cudaError_t e = cudaFuncSetAttribute(k_rms_bwd_ring<V>, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(k_rms_bwd_ring<V>, dim3((unsigned)norm_blocks(n, 0)), dim3(32 + n.tpr), (size_t)stages * stage, st, n,
+                 a.dy, a.h, a.w, a.rstd, a.dres, a.dx, part, stages, wait_limit_ns());
   note_launch();
   return e;
 }
@@ -515,18 +655,15 @@ cudaError_t launch_rms_bwd(const RmsNormBwdArgs& a, float* part, cudaStream_t st
   if (a.rows > 0) {
     int V = 1;
     const NormShape n = bwd_shape(a.rows, a.d, V);
-    p_rows = (int)norm_blocks(n, bwd_threads(V)) * n.rpb;
+    p_rows = (int)norm_blocks(n, bwd_threads(n.d, V)) * n.rpb;
     cudaError_t e;
-    if (n.tpr > 512 && V == 1) e = run_rms_bwd<1, 640, 1, true>(n, a, part, st);
-    else if (V == 1) e = run_rms_bwd<1, 256, 3, true>(n, a, part, st);
-    else if (V == 2 && n.tpr <= 256) e = run_rms_bwd<2, 256, 2, true>(n, a, part, st);
-    else if (V == 2) e = run_rms_bwd<2, 512, 1, true>(n, a, part, st);
-    else if (n.tpr <= 512) e = run_rms_bwd<4, 512, 1, false>(n, a, part, st);
-    else {
-      e = launch_pdl(k_rms_bwd_long<4>, dim3((unsigned)norm_blocks(n, bwd_threads(V))), dim3(n.tpr), 0, st, n, a.dy, a.h, a.w, a.rstd,
+    if (bwd_ring(a.d)) e = V == 2 ? run_rms_bwd_ring<2>(n, a, part, st) : run_rms_bwd_ring<4>(n, a, part, st);
+    else if (V == 4) {
+      e = launch_pdl(k_rms_bwd_long<4>, dim3((unsigned)norm_blocks(n, bwd_threads(n.d, V))), dim3(n.tpr), 0, st, n, a.dy, a.h, a.w, a.rstd,
                      a.dres, a.dx, part);
       note_launch();
-    }
+    } else if (V == 1) e = run_rms_bwd<1, 256, 3, true>(n, a, part, st);
+    else e = run_rms_bwd<2, 256, 2, true>(n, a, part, st);
     if (e != cudaSuccess) return e;
   }
   const cudaError_t e = launch_pdl(k_dw_reduce, dim3((unsigned)ceil_div(a.d, 32)), dim3(1024), 0, st, (const float*)part, p_rows,
