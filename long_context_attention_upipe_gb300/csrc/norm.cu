@@ -264,8 +264,8 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rms_bwd(NormShape n, const bf16*
   }
 }
 
-// The same for rows of 4104 to 16384 columns, whose next row would not fit into registers without leaving SMs
-// short of threads: a producer warp copies whole rows (dy, h, dres) ahead into a ring in shared memory, tpr
+// The same for longer rows, whose next row would not fit into registers without leaving SMs short of threads
+// (see bwd_ring): a producer warp copies whole rows (dy, h, dres) ahead into a ring in shared memory, tpr
 // threads work on one row after the other.  One block per SM.
 template <int V>
 __global__ void __launch_bounds__(V == 2 ? 512 : 544, 1) k_rms_bwd_ring(NormShape n, const bf16* dy, const bf16* h, const bf16* __restrict__ w,
@@ -568,8 +568,9 @@ NormShape norm_shape(int64_t rows, int d, int& V) {
 
 // The backward pass holds a row's vectors twice (the next row's are in flight) and the sums of dw: at two
 // vectors per thread it takes 128 registers (at 96 it spills and runs at half the speed), so an SM holds 512
-// threads.  Between 4096 and 16384 columns the rows in flight lie in shared memory instead.
-bool bwd_ring(int d) { return d > 4096 && d <= 16384; }
+// threads.  Between 4096 and 16384 columns the rows in flight lie in shared memory instead (d 5120: 5.5 TB/s in
+// registers, 6.5 in shared memory; 16384: 4.8, 6.3), but for 7688 to 8192, which fill 512 threads (8192: 6.1, 5.8).
+bool bwd_ring(int d) { return (d > 4096 && d <= 7680) || (d > 8192 && d <= 16384); }
 NormShape bwd_shape(int64_t rows, int d, int& V) {
   NormShape n = norm_shape(rows, d, V);
   if (bwd_ring(d)) {  // with its producer warp at most 16 warps at two vectors per thread: 128 registers
@@ -663,7 +664,8 @@ cudaError_t launch_rms_bwd(const RmsNormBwdArgs& a, float* part, cudaStream_t st
                      a.dres, a.dx, part);
       note_launch();
     } else if (V == 1) e = run_rms_bwd<1, 256, 3, true>(n, a, part, st);
-    else e = run_rms_bwd<2, 256, 2, true>(n, a, part, st);
+    else if (n.tpr <= 256) e = run_rms_bwd<2, 256, 2, true>(n, a, part, st);
+    else e = run_rms_bwd<2, 512, 1, true>(n, a, part, st);
     if (e != cudaSuccess) return e;
   }
   const cudaError_t e = launch_pdl(k_dw_reduce, dim3((unsigned)ceil_div(a.d, 32)), dim3(1024), 0, st, (const float*)part, p_rows,

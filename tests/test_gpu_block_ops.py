@@ -144,8 +144,9 @@ def test_norm_keeps_nan_and_infinity_in_their_rows():
 
 
 @pytest.mark.parametrize("rows,d", [(1, 8), (3, 64), (300, 128), (33, 136), (5, 256), (2, 264), (7, 1040), (1000, 4096),
-                                    (3, 4112), (3, 5120), (3, 5136), (2, 8192), (3, 8208), (2, 10240), (2, 10256), (1, 16384),
-                                    (2, 16400), (1, 32768), (0, 256)])
+                                    (3, 4112), (3, 5120), (3, 5136), (3, 7680), (3, 7688), (2, 8192), (3, 8208), (2, 10240), (2, 10256),
+                                    (1, 16384), (2, 16400), (1, 32768), (0, 256),
+                                    (2500, 4104), (700, 16384), (2000, 200)])   # more rows than are in flight
 @pytest.mark.parametrize("dres", [False, True])
 def test_norm_backward(rows, d, dres):
     g = gen(rows + 3 * d)
