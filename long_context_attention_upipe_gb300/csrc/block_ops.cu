@@ -17,6 +17,12 @@ constexpr int64_t kMaxNormCols = 32768;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+// Status of a launch; a failed one leaves no error behind for the next call's check to find.
+upipe_status_t finish(cudaError_t e) {
+  if (e != cudaSuccess) (void)cudaGetLastError();
+  return cuda_status(e);
+}
+
 // Two buffers that share some bytes without being the same buffer.
 bool overlaps(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -119,7 +125,7 @@ upipe_status_t upipe_attn_rms_norm_fwd(int64_t rows, int64_t d, float eps, const
     return UPIPE_ERR_INVALID_ARG;
   RmsNormArgs a{rows, (int)d, eps, reinterpret_cast<const bf16*>(x), reinterpret_cast<const bf16*>(residual),
                 reinterpret_cast<const bf16*>(w), reinterpret_cast<bf16*>(h), reinterpret_cast<bf16*>(y), q, scales, rstd};
-  return cuda_status(launch_rms_fwd(a, (cudaStream_t)stream));
+  return finish(launch_rms_fwd(a, (cudaStream_t)stream));
 }
 
 upipe_status_t upipe_attn_rms_norm_workspace_size(int64_t rows, int64_t d, size_t* bytes) {
@@ -146,7 +152,7 @@ upipe_status_t upipe_attn_rms_norm_bwd(int64_t rows, int64_t d, const uint16_t* 
   RmsNormBwdArgs a{rows, (int)d, reinterpret_cast<const bf16*>(dy), reinterpret_cast<const bf16*>(h),
                    reinterpret_cast<const bf16*>(w), rstd, reinterpret_cast<const bf16*>(dres),
                    reinterpret_cast<bf16*>(dx), dw};
-  return cuda_status(launch_rms_bwd(a, reinterpret_cast<float*>(ws), (cudaStream_t)stream));
+  return finish(launch_rms_bwd(a, reinterpret_cast<float*>(ws), (cudaStream_t)stream));
 }
 
 upipe_status_t upipe_attn_fp8_quantize(int64_t rows, int64_t cols, int32_t block_rows, const uint16_t* x, uint8_t* q,
@@ -159,7 +165,7 @@ upipe_status_t upipe_attn_fp8_quantize(int64_t rows, int64_t cols, int32_t block
   if (ceil_div(rows, 128) * ceil_div(cols, 128) > INT32_MAX) return UPIPE_ERR_UNSUPPORTED;
   if (!aligned16(x) || !aligned16(q) || !aligned16(scales)) return UPIPE_ERR_ALIGNMENT;
   if (overlaps(q, rows * cols, x, 2 * rows * cols)) return UPIPE_ERR_INVALID_ARG;
-  return cuda_status(launch_quantize(rows, (int)cols, block_rows, reinterpret_cast<const bf16*>(x), q, scales,
+  return finish(launch_quantize(rows, (int)cols, block_rows, reinterpret_cast<const bf16*>(x), q, scales,
                                      (cudaStream_t)stream));
 }
 
@@ -197,7 +203,7 @@ upipe_status_t upipe_attn_rope(const upipe_rope_desc_t* desc, int64_t tokens, co
   a.pos = positions;
   a.side[0] = rope_side(q);
   a.side[1] = rope_side(k);
-  return cuda_status(launch_rope(a, (cudaStream_t)stream));
+  return finish(launch_rope(a, (cudaStream_t)stream));
 }
 
 upipe_status_t upipe_attn_grad_clip_workspace_size(int32_t count, size_t* bytes) {
@@ -237,7 +243,7 @@ upipe_status_t upipe_attn_grad_clip(const upipe_grad_tensor_t* tensors, int32_t 
     std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
     for (size_t i = 1; i < r.size(); ++i)
       if (r[i].lo < r[i - 1].hi) return UPIPE_ERR_INVALID_ARG;
-    return cuda_status(launch_grad_clip(t.data(), idx.data(), (int)idx.size(), max_norm, norm,
+    return finish(launch_grad_clip(t.data(), idx.data(), (int)idx.size(), max_norm, norm,
                                         reinterpret_cast<double*>(ws), (cudaStream_t)stream));
   } catch (const std::bad_alloc&) {
     return cuda_status(cudaErrorMemoryAllocation);
@@ -262,7 +268,7 @@ upipe_status_t upipe_attn_gemm_fp8_nt(int64_t M, int64_t N, int64_t K, const uin
       overlaps(C, c_bytes, a_scale, ((nkb - 1) * a_scale_ld + M) * 4) || overlaps(C, c_bytes, b_scale, ceil_div(N, 128) * nkb * 4))
     return UPIPE_ERR_INVALID_ARG;
   const Fp8GemmArgs g{M, N, K, A, lda, a_scale, a_scale_ld, B, ldb, b_scale, C, ldc, c_dtype};
-  return cuda_status(launch_gemm_fp8(g, (cudaStream_t)stream));
+  return finish(launch_gemm_fp8(g, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -573,6 +573,34 @@ def test_operators_on_another_stream_and_in_graphs():
     assert same(graphs[0][1], want_b)
 
 
+def test_two_streams_at_once():
+    """Runs of every operator on two streams that overlap, products of every kernel among them, beside the attention
+    core: each result is the one of a run alone."""
+    states = [block_state(s, rows=r) for s, r in ((5, 9), (6, 700), (7, 40), (8, 257))]
+    core = up.make_desc(1024, 256, 4, 2, 128)
+    g = gen(9)
+    q, k, v = (randn(g, h, 1024, 128).bfloat16() for h in (4, 2, 2))
+    table = torch.empty(up.tile_table_bytes(core), dtype=torch.uint8, device="cuda")
+    up.build_tile_table(core, None, table)
+    o, lse = torch.empty_like(q), torch.empty(4, 1024, device="cuda")
+    up.core_fwd(core, q, k, v, None, table, o, lse)
+    want_o = o.clone()
+    want = [[t.clone() for t in block_pass(s)] for s in states]
+    for t in [o] + [x for s in states for x in (s["qkv"], s["dx"], s["q8"], s["q"])]:
+        t.view(torch.uint8).zero_()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, s in enumerate(states):
+            block_pass(s, stream=streams[i % 2])
+        up.core_fwd(core, q, k, v, None, table, o, lse, stream=streams[2])
+    torch.cuda.synchronize()
+    assert torch.equal(o, want_o) and up.device_status(table) == 0
+    for s, w in zip(states, want):
+        assert same([s[k] for k in ("h", "q8", "sx", "rstd", "W8", "sw", "qkv", "q", "k", "dqkv", "dx", "dw")] + s["clip"].outs
+                    + [s["clip"].norm], w)
+
+
 def test_norm_and_rope_offsets_past_32_bits():
     """Tensors of more than 2^31 elements: the last rows are right and the first were not overwritten."""
     rows, d = 530_000, 4096                               # 2.17e9 elements, 4.3 GB each
