@@ -434,7 +434,8 @@ upipe_status_t upipe_attn_rms_norm_fwd(int64_t rows, int64_t d, float eps, const
  *   dx     device bf16 [rows, d] (written); may be dy, dres or h itself
  *   dw     device fp32 [d] (written, not accumulated; zeros for no rows), summed in an order that
  *          depends on rows and d alone
- *   ws     device workspace of upipe_attn_rms_norm_workspace_size(rows, d) bytes */
+ *   ws     device workspace of upipe_attn_rms_norm_workspace_size(rows, d) bytes
+ * Buffers that overlap in any other way are rejected with UPIPE_ERR_INVALID_ARG. */
 upipe_status_t upipe_attn_rms_norm_workspace_size(int64_t rows, int64_t d, size_t* bytes);
 upipe_status_t upipe_attn_rms_norm_bwd(int64_t rows, int64_t d, const uint16_t* dy, const uint16_t* h, const uint16_t* w,
                                        const float* rstd, const uint16_t* dres, uint16_t* dx, float* dw, void* ws,
@@ -445,7 +446,7 @@ upipe_status_t upipe_attn_rms_norm_bwd(int64_t rows, int64_t d, const uint16_t* 
  *   q       device e4m3 [rows, cols] (written)
  *   scales  device fp32 (written): block_rows 1 (activations, A): [ceil(cols / 128)][rows], one for
  *           each row and 128 columns; block_rows 128 (weights, B): [ceil(rows / 128)][ceil(cols / 128)]
- * s and q as in upipe_attn_rms_norm_fwd. */
+ * s and q as in upipe_attn_rms_norm_fwd.  No two of the three overlap. */
 upipe_status_t upipe_attn_fp8_quantize(int64_t rows, int64_t cols, int32_t block_rows, const uint16_t* x, uint8_t* q,
                                        float* scales, void* stream);
 
@@ -489,7 +490,7 @@ typedef struct {
   int64_t in_head_stride, in_token_stride, out_head_stride, out_token_stride;
   int32_t n_heads;
 } upipe_rope_tensor_t;
-/* positions: device int32 [n_axes][tokens].  k: NULL, or turned in the same launch. */
+/* positions: device int32 [n_axes][tokens], apart from the outputs.  k: NULL, or turned in the same launch. */
 upipe_status_t upipe_attn_rope(const upipe_rope_desc_t* desc, int64_t tokens, const int32_t* positions,
                                const upipe_rope_tensor_t* q, const upipe_rope_tensor_t* k, void* stream);
 
@@ -503,7 +504,7 @@ upipe_status_t upipe_attn_rope(const upipe_rope_desc_t* desc, int64_t tokens, co
  *          out_dtype, and grad is left as it is
  *   norm   device fp32 [1] (written)
  *   ws     device workspace of upipe_attn_grad_clip_workspace_size(count) bytes
- * A list whose buffers overlap (a tensor listed twice) is rejected with UPIPE_ERR_INVALID_ARG. */
+ * Buffers that overlap (a tensor listed twice, one over ws or norm) are rejected with UPIPE_ERR_INVALID_ARG. */
 typedef struct {
   const void* grad;
   void* out;

@@ -575,7 +575,7 @@ def rope(desc: RopeDesc, q, k, positions, q_out, k_out, inverse=False, stream=No
 class GradClip:
     """Global gradient norm and clipping of a list of tensors (fp32 or bf16, contiguous), in place or into
     `outs`; owns the workspace and the norm (upipe_attn_grad_clip).  The list is fixed: gradients are
-    buffers that every step writes again."""
+    buffers that every step writes again.  Calls of one object follow one another, on one stream or in order."""
 
     def __init__(self, grads, outs=None):
         self.grads = list(grads)
@@ -595,7 +595,7 @@ class GradClip:
         n = ctypes.c_size_t(0)
         _check(lib().upipe_attn_grad_clip_workspace_size(len(self.grads), ctypes.byref(n)), "grad_clip_workspace_size")
         self.ws = torch.empty(n.value, dtype=torch.uint8, device="cuda")
-        self.norm = torch.zeros(1, dtype=torch.float32, device="cuda")
+        self.norm = torch.empty(1, dtype=torch.float32, device="cuda")  # not zeroed: the first call may be on another stream
 
     def __call__(self, max_norm, stream=None):
         """Clips to max_norm (math.inf: the norm alone); returns the norm, fp32 [1] on the device."""

@@ -2,6 +2,7 @@
 // host, then one or two launches.  Nothing throws: the only allocation is the sort of grad_clip's
 // ranges, and its failure becomes a status.
 #include <cmath>
+#include <initializer_list>
 #include <new>
 #include <algorithm>
 #include <vector>
@@ -23,13 +24,29 @@ upipe_status_t finish(cudaError_t e) {
   return cuda_status(e);
 }
 
-// Two buffers that share some bytes without being the same buffer.
+// Two buffers that share some bytes.
 bool overlaps(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
+  return a && b && a_bytes && b_bytes && x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
 }
-bool partly_overlaps(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
-  return a != b && overlaps(a, a_bytes, b, b_bytes);
+
+// A buffer of one call.  `rowwise`: every row is read, or written, by the threads that own it alone, so that an
+// output may take the very place of an input.
+struct Buf {
+  const void* p;
+  int64_t bytes;
+  bool rowwise = false;
+};
+
+// Whether every output is apart from every other buffer, but for row-wise ones in one place.
+bool outputs_apart(std::initializer_list<Buf> outs, std::initializer_list<Buf> ins) {
+  for (const Buf* o = outs.begin(); o != outs.end(); ++o) {
+    for (const Buf* p = outs.begin(); p != o; ++p)
+      if (overlaps(o->p, o->bytes, p->p, p->bytes)) return false;
+    for (const Buf& i : ins)
+      if (overlaps(o->p, o->bytes, i.p, i.bytes) && !(o->rowwise && i.rowwise && o->p == i.p)) return false;
+  }
+  return true;
 }
 
 upipe_status_t check_norm(int64_t rows, int64_t d) {
@@ -117,11 +134,8 @@ upipe_status_t upipe_attn_rms_norm_fwd(int64_t rows, int64_t d, float eps, const
     return UPIPE_ERR_ALIGNMENT;
   const int64_t n = rows * d * 2;
   const int64_t sb = (d + 127) / 128 * rows * 4;
-  // an output may take the place of an input of its own size; nothing else may share memory
-  if (partly_overlaps(h, n, x, n) || partly_overlaps(h, n, residual, n) || partly_overlaps(y, n, x, n) ||
-      partly_overlaps(y, n, residual, n) || overlaps(y, n, h, n) || overlaps(q, n / 2, x, n) ||
-      overlaps(q, n / 2, residual, n) || overlaps(q, n / 2, h, n) || overlaps(q, n / 2, y, n) ||
-      overlaps(scales, sb, q, n / 2))
+  if (!outputs_apart({{h, n, true}, {y, n, true}, {q, n / 2}, {scales, sb}, {rstd, rows * 4}},
+                     {{x, n, true}, {residual, n, true}, {w, d * 2}}))
     return UPIPE_ERR_INVALID_ARG;
   RmsNormArgs a{rows, (int)d, eps, reinterpret_cast<const bf16*>(x), reinterpret_cast<const bf16*>(residual),
                 reinterpret_cast<const bf16*>(w), reinterpret_cast<bf16*>(h), reinterpret_cast<bf16*>(y), q, scales, rstd};
@@ -145,9 +159,11 @@ upipe_status_t upipe_attn_rms_norm_bwd(int64_t rows, int64_t d, const uint16_t* 
   if (!aligned16(dy) || !aligned16(h) || !aligned16(w) || !aligned16(rstd) || !aligned16(dres) || !aligned16(dx) ||
       !aligned16(dw) || !aligned16(ws))
     return UPIPE_ERR_ALIGNMENT;
-  if (ws_bytes < rms_bwd_workspace(rows, (int)d)) return UPIPE_ERR_WORKSPACE_TOO_SMALL;
+  const size_t need = rms_bwd_workspace(rows, (int)d);
+  if (ws_bytes < need) return UPIPE_ERR_WORKSPACE_TOO_SMALL;
   const int64_t n = rows * d * 2;
-  if (partly_overlaps(dx, n, dy, n) || partly_overlaps(dx, n, h, n) || partly_overlaps(dx, n, dres, n))
+  if (!outputs_apart({{dx, n, true}, {dw, d * 4}, {ws, (int64_t)need}},
+                     {{dy, n, true}, {h, n, true}, {dres, n, true}, {w, d * 2}, {rstd, rows * 4}}))
     return UPIPE_ERR_INVALID_ARG;
   RmsNormBwdArgs a{rows, (int)d, reinterpret_cast<const bf16*>(dy), reinterpret_cast<const bf16*>(h),
                    reinterpret_cast<const bf16*>(w), rstd, reinterpret_cast<const bf16*>(dres),
@@ -164,7 +180,8 @@ upipe_status_t upipe_attn_fp8_quantize(int64_t rows, int64_t cols, int32_t block
   if (!x || !q || !scales) return UPIPE_ERR_INVALID_ARG;
   if (ceil_div(rows, 128) * ceil_div(cols, 128) > INT32_MAX) return UPIPE_ERR_UNSUPPORTED;
   if (!aligned16(x) || !aligned16(q) || !aligned16(scales)) return UPIPE_ERR_ALIGNMENT;
-  if (overlaps(q, rows * cols, x, 2 * rows * cols)) return UPIPE_ERR_INVALID_ARG;
+  const int64_t sb = ceil_div(rows, (int64_t)block_rows) * ceil_div(cols, 128) * 4;
+  if (!outputs_apart({{q, rows * cols}, {scales, sb}}, {{x, 2 * rows * cols}})) return UPIPE_ERR_INVALID_ARG;
   return finish(launch_quantize(rows, (int)cols, block_rows, reinterpret_cast<const bf16*>(x), q, scales,
                                      (cudaStream_t)stream));
 }
@@ -191,6 +208,9 @@ upipe_status_t upipe_attn_rope(const upipe_rope_desc_t* desc, int64_t tokens, co
     return UPIPE_ERR_INVALID_ARG;
   if (q->n_heads > 65535 - (k ? k->n_heads : 0)) return UPIPE_ERR_UNSUPPORTED;
   if (!aligned16(positions)) return UPIPE_ERR_ALIGNMENT;
+  for (int i = 1; i < 4; i += 2)
+    if (rows[i].base && overlaps(rows[i].base, rows[i].bytes(), positions, 4 * tokens * desc->n_axes))
+      return UPIPE_ERR_INVALID_ARG;
   RopeArgs a{};
   a.head_dim = desc->head_dim;
   a.rotary_dim = R;
@@ -218,12 +238,15 @@ upipe_status_t upipe_attn_grad_clip(const upipe_grad_tensor_t* tensors, int32_t 
   if (!aligned16(norm) || !aligned16(ws)) return UPIPE_ERR_ALIGNMENT;
   if (ws_bytes < grad_clip_workspace(count)) return UPIPE_ERR_WORKSPACE_TOO_SMALL;
   try {
-    struct Range { uintptr_t lo, hi; int tensor; };
+    struct Range { uintptr_t lo, hi; };
     std::vector<GradTensor> t((size_t)count);
     std::vector<int> idx;
     std::vector<Range> r;
     idx.reserve((size_t)count);
-    r.reserve(2 * (size_t)count);
+    r.reserve(2 * (size_t)count + 2);
+    const uintptr_t pn = reinterpret_cast<uintptr_t>(norm), pw = reinterpret_cast<uintptr_t>(ws);
+    r.push_back(Range{pn, pn + sizeof(float)});
+    r.push_back(Range{pw, pw + grad_clip_workspace(count)});
     for (int i = 0; i < count; ++i) {
       const upipe_grad_tensor_t& e = tensors[i];
       if (e.n < 0 || e.n > (int64_t)1 << 42 || e.grad_dtype < 0 || e.grad_dtype > 1 || e.out_dtype < 0 || e.out_dtype > 1)
@@ -236,10 +259,10 @@ upipe_status_t upipe_attn_grad_clip(const upipe_grad_tensor_t* tensors, int32_t 
       t[i] = GradTensor{e.grad, out, e.n, e.grad_dtype, out_dtype};
       idx.push_back(i);
       const uintptr_t g = reinterpret_cast<uintptr_t>(e.grad), o = reinterpret_cast<uintptr_t>(out);
-      r.push_back(Range{g, g + (uintptr_t)(e.n * (e.grad_dtype ? 2 : 4)), i});
-      if (o != g) r.push_back(Range{o, o + (uintptr_t)(e.n * (out_dtype ? 2 : 4)), i});
+      r.push_back(Range{g, g + (uintptr_t)(e.n * (e.grad_dtype ? 2 : 4))});
+      if (o != g) r.push_back(Range{o, o + (uintptr_t)(e.n * (out_dtype ? 2 : 4))});
     }
-    // a tensor listed twice would be scaled twice, by blocks that race
+    // a tensor listed twice would be scaled twice, by blocks that race; so would one over the workspace
     std::sort(r.begin(), r.end(), [](const Range& a, const Range& b) { return a.lo < b.lo; });
     for (size_t i = 1; i < r.size(); ++i)
       if (r[i].lo < r[i - 1].hi) return UPIPE_ERR_INVALID_ARG;

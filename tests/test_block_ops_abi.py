@@ -46,6 +46,10 @@ def norm_fwd(**kw):
     (dict(res=fake(4), h=fake(2)), 1),                # h is y
     (dict(res=fake(4), h=fake(4) - 512), 1),          # h ends inside the residual
     (dict(q=fake(0), scales=fake(5)), 1),             # q over x
+    (dict(y=fake(1)), 1), (dict(y=fake(1) - 1024), 1),  # y is w, y ends inside w
+    (dict(rstd=fake(0)), 1), (dict(rstd=fake(2) + 16), 1), (dict(rstd=fake(1)), 1),
+    (dict(q=fake(3), scales=fake(2)), 1), (dict(q=fake(3), scales=fake(0) + 16), 1), (dict(q=fake(1), scales=fake(4)), 1),
+    (dict(q=fake(3), scales=fake(4), rstd=fake(4) + 16), 1),
     (dict(rows=0, x=None, w=None, y=None), 0),
 ])
 def test_rms_norm_fwd_refusals(kw, code):
@@ -54,7 +58,10 @@ def test_rms_norm_fwd_refusals(kw, code):
 
 @pytest.mark.parametrize("kw,code", [
     (dict(rows=-1), 1), (dict(d=12), 2), (dict(dy=None), 1), (dict(rstd=None), 1), (dict(dw=None), 1), (dict(ws=None), 1),
-    (dict(dres=ODD), 3), (dict(bytes=16), 4), (dict(dx=fake(0) + 256), 1), (dict(dx=fake(1) + 256), 1)])
+    (dict(dres=ODD), 3), (dict(bytes=16), 4), (dict(dx=fake(0) + 256), 1), (dict(dx=fake(1) + 256), 1),
+    (dict(dw=fake(2)), 1), (dict(dw=fake(4)), 1), (dict(dw=fake(0) + 16), 1), (dict(ws=fake(5)), 1), (dict(ws=fake(1)), 1),
+    (dict(dx=fake(2)), 1), (dict(dx=fake(3)), 1), (dict(dres=fake(7), ws=fake(7) + 2032), 1),
+    (dict(rows=0, dw=fake(2)), 1)])
 def test_rms_norm_bwd_refusals(kw, code):
     a = dict(rows=4, d=256, dy=fake(0), h=fake(1), w=fake(2), rstd=fake(3), dres=None, dx=fake(4), dw=fake(5), ws=fake(6),
              bytes=1 << 40)
@@ -75,7 +82,8 @@ def test_rms_norm_workspace():
 
 @pytest.mark.parametrize("kw,code", [
     (dict(rows=-1), 1), (dict(cols=0), 1), (dict(cols=24), 2), (dict(block=64), 1), (dict(x=None), 1), (dict(q=ODD), 3),
-    (dict(q=fake(0) + 1024), 1), (dict(rows=0, x=None, q=None, scales=None), 0)])
+    (dict(q=fake(0) + 1024), 1), (dict(scales=fake(0)), 1), (dict(scales=fake(1) + 16), 1), (dict(block=128, scales=fake(1)), 1),
+    (dict(rows=0, x=None, q=None, scales=None), 0)])
 def test_fp8_quantize_refusals(kw, code):
     a = dict(rows=4, cols=256, block=1, x=fake(0), q=fake(1), scales=fake(2))
     a.update(kw)
@@ -158,6 +166,8 @@ def test_rope_refuses_descriptors():
     assert rope(rope_side(), up.make_rope_desc(128, [math.inf] + good[1:])) == 1
     assert rope(rope_side(), pos=None) == 1
     assert rope(rope_side(), pos=ODD) == 3
+    assert rope(rope_side(), pos=fake(1) + 64) == 1                   # positions inside the output
+    assert rope(rope_side(), pos=fake(4) - 16, k=rope_side(in_=fake(3), out=fake(4))) == 1
     assert rope(rope_side(), tokens=-1) == 1
     assert rope(rope_side(in_=None, out=None), tokens=0, pos=None) == 0
     for bad in (([0.1] * 129, None), (good, [0] * 63), (good, [4] * 64), (good, [-1] * 64)):
@@ -189,6 +199,10 @@ def test_grad_clip_refusals():
     assert clip([one, (fake(0) + 384, None, 100, 0, 0)]) == 1          # two that overlap
     assert clip([one, (fake(1), fake(0) + 16, 4, 0, 0)]) == 1          # an output inside another gradient
     assert clip([(fake(0), fake(0), 4, 0, 1)]) == 1                    # in place into another type
+    assert clip([one], norm=fake(0) + 16) == 1                        # the norm, the workspace over a tensor
+    assert clip([one], ws=fake(0) + 384) == 1
+    assert clip([(fake(0), fake(31) + 64, 100, 0, 0)]) == 1
+    assert clip([one], norm=fake(31)) == 1
     n = ctypes.c_size_t(0)
     assert up.lib().upipe_attn_grad_clip_workspace_size(-1, ctypes.byref(n)) == 1
     assert up.lib().upipe_attn_grad_clip_workspace_size(4, None) == 1
