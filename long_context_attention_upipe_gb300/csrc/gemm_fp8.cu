@@ -314,33 +314,55 @@ cudaError_t run_swap(const Fp8GemmArgs& a, const Fp8Params& p, cudaStream_t st) 
 // CTA pairs: 256 rows of A x BN = 32 NCH columns
 // ------------------------------------------------------------------------------------------------
 // 12 warps per CTA, persistent, one CTA per SM, a pair (cluster of two) per tile:
-//   warp 0      TMA producer: this CTA's 128 rows of A and its half of B's BN columns, ring of 6 stages
-//   warp 1      in the even CTA the MMA issuer: 4 MMAs (M256 BN K32, cta_group::2) per block of K into one of two
-//               TMEM accumulators, which both CTAs hold for their rows
-//   warps 2-3   the blocks' scales, eight blocks of K at a time, into a ring in shared memory
+//   warp 0      TMA producer: this CTA's 128 rows of A and its half of B's BN columns, ring of 5 or 6 stages
+//   warp 1      in the even CTA the MMA issuer: 4 MMAs (M256 BN K32, cta_group::2) per block of K into one of the
+//               512 / BN TMEM accumulators, which both CTAs hold for their rows
+//   warps 2-3   the blocks' scales, eight blocks of K at a time, into a ring in shared memory (cp.async)
 //   warps 4-11  scaling: TMEM lanes 32 * (warp % 4), one half of the columns each, the sums in registers
-// What bounds it is the chain MMA -> accumulator ready -> scaled -> free -> MMA, about 830 clocks per block of K
-// at BN 256 where its MMAs take 512.  What the chain was made of, and what it cost (clocks per block): an
+// One commit per block of K says both that its accumulator is ready and that its stage may be filled again:
+// the scaling warps wait on the stages' ring.  A stage completes again only after ACCS blocks were handed back,
+// and ACCS <= STAGES, so no waiter can miss a phase.
+//
+// What bounds it is the scaling warps' own path, about 720 clocks per block of K at BN 256 where its MMAs take 512:
+// the wait (120, though the block is ready), the loads and sums (385 until the accumulator is handed back, of which
+// 256 are the sums') and the rest.  With neither loads of operands nor MMAs the kernel took 85% of its time; a
+// free-running loop of the same loads and sums takes 320, with waits and arrivals 490.  On the way here: an
 // arrive.release.cluster waits for every load in flight, so the accumulator is released by a relaxed arrive
-// (tcgen05.fence orders the reads of TMEM before it) and the scales are fetched by warps of their own; a
-// one-lane issuing loop moves every descriptor into uniform registers, 930, so the whole warp walks it
-// (elect_one); the accumulator is released as soon as its last columns are in registers; eight blocks are
-// unrolled, 900 otherwise.  An MMA per CTA with the columns multicast to both frees its accumulators without
-// the other CTA, but writes half as many bytes again to shared memory: 750 us at 8192 x 28672 x 4096, the
-// pair 710 us; with 16 columns loaded ahead and scales for eight blocks at a time instead of four 700 us (2750
-// TFLOP/s); tokens on the columns, the kernel above: 2550 us.
+// (tcgen05.fence orders the reads of TMEM before it) and the scales are fetched by warps of their own; a one-lane
+// issuing loop moves every descriptor into uniform registers, so the whole warp walks it (elect_one); the
+// accumulator is released as soon as its last columns are in registers.  Loops are kept short, one block of K per
+// turn: the issuer's unrolled over the ring took 12% more, the scaling loop's unrolled by eight 4% (by two, with
+// spills, 30%).  An MMA per CTA with the columns multicast to both frees its accumulators without the other CTA,
+// but writes half as many bytes again to shared memory: 5% slower.  C leaves by TMA from small boxes: a tile's
+// output took 3300 clocks with 16-byte stores, of which 2300 were instructions, and cost 3 to 4% more in all.
+// us at 1000 x 5120 x 8192 / 8192 x 28672 x 4096: one commit and short loops 46.8 -> 42.7 / 735 -> 703, C by TMA ->
+// 40.4 / 684 (2810 TFLOP/s; more than one box of 32 columns in flight: with three of 16 and a sixth stage 3% slower).
+// Sixteen scaling warps of a quarter of the columns each: 763.  Tokens on the columns, the kernel above: 171 / 2550 us.
 constexpr int kTileThreads = 384;
 constexpr int kScSlots = 2, kScGroup = 8;  // ring of scales: groups of eight blocks of K
+constexpr int kScRow = 128 + 4;            // a block's scales: of each row, and of 2 x 2 column blocks
+
+// Four bytes (or, with `bytes` 0, a zero) to shared memory without a register in between.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const float* src, uint32_t bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+// One arrival of this thread's once its copies so far are there.
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 
 template <int NCH>
 struct TileLayout {
   static constexpr int BN = 32 * NCH, CW = BN / 2;  // CW: columns of a scaling warp
   static constexpr uint32_t A = 128 * 128, B = CW * 128, STAGE = A + B;
-  static constexpr int STAGES = 6;
-  static constexpr uint32_t SC = STAGES * STAGE;         // per group and four blocks: float4 of each of 128 rows, of 2 x 2 column blocks
-  static constexpr uint32_t SCSLOT = kScGroup / 4 * (128 + 4) * 16;
-  static constexpr uint32_t OUT = SC + kScSlots * SCSLOT;  // per scaling warp: 32 rows x 64 bytes of C
-  static constexpr uint32_t OUTBOX = 32 * 64;
+  static constexpr int STAGES = NCH == 8 ? 5 : 6;  // what fits
+  static constexpr int ACCS = 512 / BN;  // accumulators in TMEM
+  static constexpr uint32_t SC = STAGES * STAGE;
+  static constexpr uint32_t SCSLOT = kScGroup * kScRow * 4;
+  static constexpr uint32_t OUT = (SC + kScSlots * SCSLOT + 1023) / 1024 * 1024;
+  static constexpr int BC = NCH % 2 ? 16 : 32;      // columns of a box of C in bf16 (a warp's are a multiple); 16 in fp32
+  static constexpr uint32_t BOX = 32 * 64;          // 32 rows
+  static constexpr uint32_t OUTBOX = 2 * BOX;       // per scaling warp
   static constexpr uint32_t BAR = OUT + 8 * OUTBOX;
   static constexpr uint32_t BYTES = BAR + 256;
 };
@@ -351,7 +373,8 @@ struct TileSched {
 
 template <int NCH>
 __global__ void __launch_bounds__(kTileThreads, 1)
-    k_gemm_fp8_tile(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb, Fp8Params p, TileSched sch) {
+    k_gemm_fp8_tile(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tb,
+                    const __grid_constant__ CUtensorMap tcm, Fp8Params p, TileSched sch) {
   using L = TileLayout<NCH>;
   constexpr int ST = L::STAGES, BN = L::BN, CW = L::CW;
   constexpr bool kStraddle = CW % 64 != 0;  // a warp's columns may lie in two weight blocks
@@ -359,10 +382,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR);
   uint64_t* full = bars;               // [ST]
-  uint64_t* empty = bars + ST;         // [ST]
-  uint64_t* acc_full = bars + 2 * ST;  // [2]
-  uint64_t* acc_empty = acc_full + 2;  // [2]
-  uint64_t* sc_full = acc_empty + 2;          // [kScSlots]
+  uint64_t* empty = bars + ST;                 // [ST]: the stage's MMAs are done, in both CTAs
+  uint64_t* acc_empty = bars + 2 * ST;         // [ACCS]
+  uint64_t* sc_full = acc_empty + L::ACCS;     // [kScSlots]
   uint64_t* sc_empty = sc_full + kScSlots;    // [kScSlots]
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(sc_empty + kScSlots);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(sc_empty + kScSlots + 1);
@@ -378,10 +400,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       tc::mbar_init(&full[i], 1);
       tc::mbar_init(&empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      tc::mbar_init(&acc_full[i], 1);
-      tc::mbar_init(&acc_empty[i], 16);  // even CTA: both CTAs' 8 scaling warps
-    }
+    for (int i = 0; i < L::ACCS; ++i) tc::mbar_init(&acc_empty[i], 16);  // even CTA: both CTAs' 8 scaling warps
     for (int i = 0; i < kScSlots; ++i) {
       tc::mbar_init(&sc_full[i], 64);
       tc::mbar_init(&sc_empty[i], 8);
@@ -449,22 +468,21 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       for (int t = cid; t < n_tiles; t += n_clusters) {
 #pragma unroll 1
         for (int kb = 0; kb < nkb; ++kb) {
-          ok = tc::mbar_wait_addr(fulla + s * 8, ph, abort_flag, p.wait_ns) && ok;
-          ok = tc::mbar_wait_addr(acce + buf * 8, eph, abort_flag, p.wait_ns) && ok;
+          const bool f = tc::mbar_try_wait_addr(fulla + s * 8, ph), e = tc::mbar_try_wait_addr(acce + buf * 8, eph);
+          if (!f) ok = tc::mbar_wait_addr(fulla + s * 8, ph, abort_flag, p.wait_ns) && ok;
+          if (!e) ok = tc::mbar_wait_addr(acce + buf * 8, eph, abort_flag, p.wait_ns) && ok;
           tc::fence_after_sync();
           const uint64_t ad = tc::sdesc_add(a0, s * L::STAGE), bd = tc::sdesc_add(b0, s * L::STAGE);
-          const uint32_t d = tmem + buf * 256;
+          const uint32_t d = tmem + buf * BN;
           if (leader && ok) {
 #pragma unroll
             for (int k = 0; k < kBlk / 32; ++k)
               tc::mma_ss_pair_f8(d, tc::sdesc_add(ad, k * 32), tc::sdesc_add(bd, k * 32), idesc, k > 0);
-            tc::mma_commit_pair(&acc_full[buf]);
             tc::mma_commit_pair(&empty[s]);
           }
           __syncwarp();
           if (++s == ST) { s = 0; ph ^= 1; }
-          eph ^= buf;
-          buf ^= 1;
+          if (++buf == L::ACCS) { buf = 0; eph ^= 1; }
         }
       }
     } else if (warp >= 2) {
@@ -482,34 +500,29 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const float* pb = p.sa + (mb < p.M ? mb : 0);
         const int blk = (int)(((int64_t)tn * BN + (j >> 1 & 1) * CW) / kBlk) + (j & 1);
         const float* ps = p.sb + (int64_t)min(blk, nblocks - 1) * nkb;
-        float va[kScGroup], vb[kScGroup], vs[kScGroup];
-        auto fetch = [&](int kb0) {
-#pragma unroll
-          for (int u = 0; u < kScGroup; ++u) {
-            const bool in = kb0 + u < nkb;
-            va[u] = in && ma < p.M ? pa[(int64_t)(kb0 + u) * p.lds] : 0.f;
-            vb[u] = in && mb < p.M ? pb[(int64_t)(kb0 + u) * p.lds] : 0.f;
-            vs[u] = in && j < 4 ? ps[kb0 + u] : 0.f;
-          }
-        };
-        fetch(0);
+        const uint32_t na = ma < p.M ? 4 : 0, nb = mb < p.M ? 4 : 0, ns = j < 4 ? 4 : 0;  // bytes: 0 writes a zero
+#pragma unroll 1
         for (int kb0 = 0; kb0 < nkb; kb0 += kScGroup) {
-          ok = tc::mbar_wait(&sc_empty[slot], ph, abort_flag, nullptr, p.wait_ns) && ok;
+          ok = tc::mbar_wait_addr(smem_u32(&sc_empty[slot]), ph, abort_flag, p.wait_ns) && ok;
           if (ok) {
-            float4* dst = reinterpret_cast<float4*>(smem + L::SC + slot * L::SCSLOT);
-#pragma unroll
-            for (int q = 0; q < kScGroup / 4; ++q, dst += 132) {
-              dst[j] = make_float4(va[4 * q], va[4 * q + 1], va[4 * q + 2], va[4 * q + 3]);
-              dst[j + 64] = make_float4(vb[4 * q], vb[4 * q + 1], vb[4 * q + 2], vb[4 * q + 3]);
-              if (j < 4) dst[128 + j] = make_float4(vs[4 * q], vs[4 * q + 1], vs[4 * q + 2], vs[4 * q + 3]);
+            uint32_t dst = smem_u32(smem + L::SC + slot * L::SCSLOT) + j * 4;
+            const int n = min(kScGroup, nkb - kb0);
+#pragma unroll 1
+            for (int u = 0; u < n; ++u, dst += kScRow * 4) {
+              cp_async4(dst, pa, na);
+              cp_async4(dst + 256, pb, nb);
+              if (j < 4) cp_async4(dst + 512, ps, ns);
+              pa += p.lds;
+              pb += p.lds;
+              ++ps;
             }
           }
-          tc::mbar_arrive(&sc_full[slot]);
-          fetch(kb0 + kScGroup);
+          cp_async_arrive(smem_u32(&sc_full[slot]));
           if (++slot == kScSlots) { slot = 0; ph ^= 1; }
         }
       }
     }
+    asm volatile("cp.async.wait_all;" ::: "memory");
     __syncwarp();
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;\n" ::: "memory");
@@ -518,7 +531,8 @@ __global__ void __launch_bounds__(kTileThreads, 1)
     const uint32_t lane_addr = tmem + ((uint32_t)(32 * (warp & 3)) << 16) + half * CW;
     int slot = 0, buf = 0;
     uint32_t sph = 0, aph = 0;
-    const uint32_t scf = smem_u32(sc_full), sce = smem_u32(sc_empty), accf = smem_u32(acc_full);
+    const uint32_t scf = smem_u32(sc_full), sce = smem_u32(sc_empty), done = smem_u32(empty);
+    int st = 0, ob = 0;
     const uint32_t acc0 = tc::mapa_cluster(smem_u32(acc_empty), 0);  // the even CTA's
     bool ok = true;
     for (int t = cid; t < n_tiles; t += n_clusters) {
@@ -531,96 +545,93 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll
       for (int i = 0; i < CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
 #pragma unroll 1
-      for (int kb0 = 0; kb0 < nkb; kb0 += kScGroup) {
-        ok = tc::mbar_wait_addr(scf + slot * 8, sph, abort_flag, p.wait_ns) && ok;
-        const float4* sc = reinterpret_cast<const float4*>(smem + L::SC + slot * L::SCSLOT);
-        float f0[kScGroup], f1[kScGroup];
-#pragma unroll
-        for (int q = 0; q < kScGroup / 4; ++q, sc += 132) {
-          const float4 a4 = sc[r], b4 = sc[128 + 2 * half], c4 = kStraddle ? sc[129 + 2 * half] : b4;
-          f0[4 * q] = a4.x * b4.x; f0[4 * q + 1] = a4.y * b4.y; f0[4 * q + 2] = a4.z * b4.z; f0[4 * q + 3] = a4.w * b4.w;
-          f1[4 * q] = a4.x * c4.x; f1[4 * q + 1] = a4.y * c4.y; f1[4 * q + 2] = a4.z * c4.z; f1[4 * q + 3] = a4.w * c4.w;
-        }
+      for (int kb = 0; kb < nkb; ++kb) {
+        const int u = kb % kScGroup;
+        if (u == 0) ok = tc::mbar_wait_addr(scf + slot * 8, sph, abort_flag, p.wait_ns) && ok;
+        const float* sc = reinterpret_cast<const float*>(smem + L::SC + slot * L::SCSLOT) + u * kScRow;
+        const float sa = sc[r], sb0 = sc[128 + 2 * half], sb1 = kStraddle ? sc[129 + 2 * half] : 0.f;
+        ok = tc::mbar_wait_addr(done + st * 8, aph, abort_flag, p.wait_ns) && ok;
+        if (++st == ST) { st = 0; aph ^= 1; }
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive_addr(sce + slot * 8);
-        if (++slot == kScSlots) { slot = 0; sph ^= 1; }
+        tc::fence_after_sync();
+        const uint32_t src = lane_addr + buf * BN;
+        uint32_t v[2][16];  // the next 16 columns are loaded while these are scaled
+        tc::tmem_ld16(src, v[0]);
+        const float f0 = sa * sb0, f1 = kStraddle ? sa * sb1 : f0;
+        if (u == kScGroup - 1 || kb + 1 == nkb) {
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive_addr(sce + slot * 8);
+          if (++slot == kScSlots) { slot = 0; sph ^= 1; }
+        }
 #pragma unroll
-        for (int u = 0; u < kScGroup; ++u) {
-          if (kb0 + u < nkb) {
-            ok = tc::mbar_wait_addr(accf + buf * 8, aph, abort_flag, p.wait_ns) && ok;
+        for (int g = 0; g < NCH; ++g) {
+          tc::tmem_ld16_ready(v[g & 1]);
+          if (g + 1 < NCH) tc::tmem_ld16(src + (g + 1) * 16, v[(g + 1) & 1]);
+          else {
+            // everything is in registers: the accumulator may be written again while these are scaled
+            tc::fence_before_sync();
             __syncwarp();
-            tc::fence_after_sync();
-            const uint32_t src = lane_addr + buf * 256;
-            uint32_t v[2][16];  // the next 16 columns are loaded while these are scaled
-            tc::tmem_ld16(src, v[0]);
-#pragma unroll
-            for (int g = 0; g < NCH; ++g) {
-              tc::tmem_ld16_ready(v[g & 1]);
-              if (g + 1 < NCH) tc::tmem_ld16(src + (g + 1) * 16, v[(g + 1) & 1]);
-              else {
-                // everything is in registers: the accumulator may be written again while these are scaled
-                tc::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive_cluster_relaxed(acc0 + buf * 8);
-              }
-              const float f = kStraddle && g >= cut ? f1[u] : f0[u];
-              const float2 f2 = make_float2(f, f);
-#pragma unroll
-              for (int i = 0; i < 8; ++i)
-                acc[g * 8 + i] = __ffma2_rn(make_float2(__uint_as_float(v[g & 1][2 * i]), __uint_as_float(v[g & 1][2 * i + 1])), f2,
-                                            acc[g * 8 + i]);
-            }
-            aph ^= buf;
-            buf ^= 1;
+            if (lane == 0) tc::mbar_arrive_cluster_relaxed(acc0 + buf * 8);
           }
+          const float f = kStraddle && g >= cut ? f1 : f0;
+          const float2 f2 = make_float2(f, f);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            acc[g * 8 + i] = __ffma2_rn(make_float2(__uint_as_float(v[g & 1][2 * i]), __uint_as_float(v[g & 1][2 * i + 1])), f2,
+                                        acc[g * 8 + i]);
         }
+        if (++buf == L::ACCS) buf = 0;
       }
-      // C leaves through shared memory, 64 bytes of 32 rows at a time, so that a warp's stores fill whole
-      // sectors of 8 rows (a thread's own 16-byte stores to 32 rows took 8% of the kernel's time); 16-byte chunk j
-      // of row r lies at chunk j ^ (r / 2 % 4), which keeps both sides free of bank conflicts
+      // C leaves through shared memory by TMA, which drops what lies outside, two boxes per warp in turn; 16-byte chunk j
+      // of row r lies at chunk j ^ (r / 2 % 4) of a row of 64 bytes, j ^ (r / 4 % 2) of one of 32 (the map's swizzle,
+      // which keeps the writes free of bank conflicts)
       uint8_t* box = smem + L::OUT + (warp - 4) * L::OUTBOX;
-      const int64_t mw = (int64_t)tm * 128 + 32 * (warp & 3);
-      const int e = p.c_bf16 ? 8 : 4;  // columns of a 16-byte chunk
-      auto flush = [&](int64_t n_at, int chunks) {
+      const int mw = tm * 128 + 32 * (warp & 3);
+      auto room = [&]() {
+        if (lane == 0) tc::bulk_wait_read<1>();
         __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = i * 8 + (lane >> 2), j = lane & 3;
-          const int64_t m = mw + rr, n = n_at + j * e;
-          if (ok && j < chunks && m < p.M && n < p.N) {  // N is a multiple of 8: a chunk is inside or outside
-            const uint4 q = *reinterpret_cast<const uint4*>(box + rr * 64 + ((j ^ ((rr >> 1) & 3)) << 4));
-            *reinterpret_cast<uint4*>(reinterpret_cast<uint8_t*>(p.c) + (m * p.ldc + n) * (p.c_bf16 ? 2 : 4)) = q;
-          }
-        }
-        __syncwarp();
+        return box + ob * L::BOX;
       };
-      uint8_t* mine = box + lane * 64;
-      const int sw = (lane >> 1) & 3;
+      auto leave = [&](const uint8_t* from, int64_t n) {
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (ok && mw < p.M && n < p.N) tc::tma_store_2d(&tcm, from, (int)n, mw);
+          tc::bulk_commit();
+        }
+        ob ^= 1;
+      };
       if (p.c_bf16) {
+        constexpr int BC = L::BC;
+        const int sw = BC == 32 ? (lane >> 1) & 3 : (lane >> 2) & 1;
 #pragma unroll
-        for (int c = 0; c < CW; c += 32) {
+        for (int c = 0; c < CW; c += BC) {
+          uint8_t* to = room();
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (c + 8 * j < CW) {
-              const float2* v = &acc[(c + 8 * j) / 2];
-              *reinterpret_cast<uint4*>(mine + ((j ^ sw) << 4)) =
-                  make_uint4(tc::pack_bf16x2(v[0].x, v[0].y), tc::pack_bf16x2(v[1].x, v[1].y), tc::pack_bf16x2(v[2].x, v[2].y),
-                             tc::pack_bf16x2(v[3].x, v[3].y));
-            }
-          flush(n0 + c, CW - c >= 32 ? 4 : (CW - c) / 8);
+          for (int j = 0; j < BC / 8; ++j) {
+            const float2* v = &acc[(c + 8 * j) / 2];
+            *reinterpret_cast<uint4*>(to + lane * (BC * 2) + ((j ^ sw) << 4)) =
+                make_uint4(tc::pack_bf16x2(v[0].x, v[0].y), tc::pack_bf16x2(v[1].x, v[1].y), tc::pack_bf16x2(v[2].x, v[2].y),
+                           tc::pack_bf16x2(v[3].x, v[3].y));
+          }
+          leave(to, n0 + c);
         }
       } else {
+        const int sw = (lane >> 1) & 3;
 #pragma unroll
         for (int c = 0; c < CW; c += 16) {
+          uint8_t* to = room();
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const float2* v = &acc[(c + 4 * j) / 2];
-            *reinterpret_cast<float4*>(mine + ((j ^ sw) << 4)) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+            *reinterpret_cast<float4*>(to + lane * 64 + ((j ^ sw) << 4)) = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
           }
-          flush(n0 + c, 4);
+          leave(to, n0 + c);
         }
       }
     }
+    if (lane == 0) tc::bulk_wait_all();
+    __syncwarp();
   }
   tc::fence_before_sync();
   __syncthreads();
@@ -634,8 +645,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 template <int NCH>
 cudaError_t run_tile(const Fp8GemmArgs& a, const Fp8Params& p, cudaStream_t st) {
   using L = TileLayout<NCH>;
-  CUtensorMap ta, tb;
-  if (!make_tmap_2d_u8(&ta, a.A, a.K, a.M, a.lda, kBlk, 128) || !make_tmap_2d_u8(&tb, a.B, a.K, a.N, a.ldb, kBlk, L::CW))
+  CUtensorMap ta, tb, tcm;
+  if (!make_tmap_2d_u8(&ta, a.A, a.K, a.M, a.lda, kBlk, 128) || !make_tmap_2d_u8(&tb, a.B, a.K, a.N, a.ldb, kBlk, L::CW) ||
+      !make_tmap_2d_out(&tcm, a.C, a.c_bf16, a.N, a.M, a.ldc, a.c_bf16 ? L::BC : 16))
     return cudaErrorInvalidValue;
   auto kfn = k_gemm_fp8_tile<NCH>;
   const size_t smem = L::BYTES + 1024;
@@ -645,7 +657,7 @@ cudaError_t run_tile(const Fp8GemmArgs& a, const Fp8Params& p, cudaStream_t st) 
   const TileSched sch{(int)ceil_div(a.M, 256), (int)ceil_div(a.N, L::BN), a.N > a.M};
   const int64_t units = (int64_t)sch.tiles_mp * sch.tiles_n;
   const unsigned grid = (unsigned)(2 * std::max<int64_t>(1, std::min<int64_t>(units, sm_count() / 2)));
-  e = launch_pdl_cluster(kfn, dim3(grid), dim3(kTileThreads), smem, st, 2, ta, tb, p, sch);
+  e = launch_pdl_cluster(kfn, dim3(grid), dim3(kTileThreads), smem, st, 2, ta, tb, tcm, p, sch);
   note_launch();
   return e;
 }
@@ -659,16 +671,16 @@ cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t st) {
   if (a.M <= 32) return run_swap<32>(a, p, st);
   if (a.M <= 64) return run_swap<64>(a, p, st);
   // The modelled clocks of both kernels.  Tile kernel: the column width whose rounds over all clusters take the
-  // least; a block of K takes about 300 + 66 NCH (565 measured at 128 columns, 830 at 256), a tile's output about
-  // 2000 at 256 columns.  Tokens on the columns: about 1000 for a block of K.  Measured on both sides (us, tile
-  // kernel / tokens on the columns): 128 x 5120 x 8192 21.6 / 18.9, 128 x 4096 x 4096 13.4 / 12.0, 100 x 1024 x
-  // 4096 12.3 / 8.5; 128 x 28672 x 4096 31.5 / 41.8, 200 x 6144 x 4096 13.7 / 20.3, 256 x 5120 x 8192 21.7 / 38.9.
+  // least; a block of K takes about 130 + 90 NCH (510 measured at 128 columns, 570 at 160, 850 at 256, each with
+  // its share of a tile's ends), a tile's output about 200 NCH.  Tokens on the columns: about 1000 for a block of
+  // K.  Measured on both sides (us, tile kernel / tokens on the columns): 100 x 1024 x 4096 11.2 / 8.5, 128 x 4096 x
+  // 4096 12.2 / 12.1; 128 x 28672 x 4096 28 / 42, 200 x 6144 x 4096 12.3 / 20.3, 256 x 5120 x 8192 19.5 / 38.9.
   const int64_t clusters = sm_count() / 2, tm = ceil_div(a.M, 256);
   int best = 8;
   int64_t cost = INT64_MAX;
   for (int c = 8; c >= 4; --c) {
     const int64_t rounds = ceil_div(tm * ceil_div(a.N, 32 * c), clusters);
-    const int64_t k = rounds * ((int64_t)p.nkb * (300 + 66 * c) + 250 * c);
+    const int64_t k = rounds * ((int64_t)p.nkb * (130 + 90 * c) + 200 * c);
     if (k < cost) { cost = k; best = c; }
   }
   const int64_t ctas = ceil_div(a.N, 128) * ceil_div(a.M, 128);

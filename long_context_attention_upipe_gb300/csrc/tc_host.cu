@@ -63,6 +63,20 @@ bool make_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool make_tmap_2d_out(CUtensorMap* map, void* base, bool bf16_out, uint64_t cols, uint64_t rows, uint64_t ld, uint32_t box_cols) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const uint32_t size = bf16_out ? 2 : 4, row = box_cols * size;
+  if (row != 32 && row != 64) return false;
+  cuuint64_t dims[2] = {cols, rows};
+  cuuint64_t strides[1] = {ld * size};
+  cuuint32_t box[2] = {box_cols, 32};
+  cuuint32_t es[2] = {1, 1};
+  return fn(map, bf16_out ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, base, dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, row == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+            CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool make_tmap_f32_out(CUtensorMap* map, void* base, int rank, const uint64_t* dims, const uint64_t* strides_bytes) {
   auto fn = encode_fn();
   if (!fn || rank < 2 || rank > 3) return false;
