@@ -33,6 +33,11 @@ struct Fp8Params {
   uint64_t wait_ns;
 };
 
+// Shared memory from its next multiple of 1024.  An offset, not a rounded address: a pointer that comes from an integer
+// has lost its address space, and every access through it goes by the generic path (8192 x 28672 x 4096: 1 to 2%,
+// 1000 x 5120 x 8192 40.4 -> 38.0 us, 128 x 5120 x 8192 19.0 -> 16.4).
+__device__ __forceinline__ uint8_t* align_smem(uint8_t* p) { return p + ((0u - smem_u32(p)) & 1023); }
+
 // ------------------------------------------------------------------------------------------------
 // few rows of A: weights on the MMA's rows, TN tokens on its columns, K split over a cluster
 // ------------------------------------------------------------------------------------------------
@@ -69,7 +74,7 @@ __global__ void __launch_bounds__(SwapLayout<TN>::THREADS)
   using L = SwapLayout<TN>;
   constexpr int ST = L::STAGES, NB = L::NBUF, CT = L::CT;
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = align_smem(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR);
   uint64_t* full = bars;                // [ST]
   uint64_t* empty = bars + ST;          // [ST]
@@ -379,7 +384,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
   constexpr int ST = L::STAGES, BN = L::BN, CW = L::CW;
   constexpr bool kStraddle = CW % 64 != 0;  // a warp's columns may lie in two weight blocks
   extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* smem = align_smem(smem_raw);
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR);
   uint64_t* full = bars;               // [ST]
   uint64_t* empty = bars + ST;                 // [ST]: the stage's MMAs are done, in both CTAs
@@ -673,8 +678,9 @@ cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t st) {
   // The modelled clocks of both kernels.  Tile kernel: the column width whose rounds over all clusters take the
   // least; a block of K takes about 130 + 90 NCH (510 measured at 128 columns, 570 at 160, 850 at 256, each with
   // its share of a tile's ends), a tile's output about 200 NCH.  Tokens on the columns: about 1000 for a block of
-  // K.  Measured on both sides (us, tile kernel / tokens on the columns): 100 x 1024 x 4096 11.2 / 8.5, 128 x 4096 x
-  // 4096 12.2 / 12.1; 128 x 28672 x 4096 28 / 42, 200 x 6144 x 4096 12.3 / 20.3, 256 x 5120 x 8192 19.5 / 38.9.
+  // K.  Measured on both sides (us, tile kernel / tokens on the columns): 100 x 1024 x 4096 10.4 / 7.6, 128 x 4096 x
+  // 4096 11.4 / 10.6, 128 x 5120 x 8192 18.1 / 16.4; 128 x 28672 x 4096 27.7 / 36.8, 200 x 6144 x 4096 11.8 / 17.9,
+  // 256 x 5120 x 8192 18.2 / 34.7.
   const int64_t clusters = sm_count() / 2, tm = ceil_div(a.M, 256);
   int best = 8;
   int64_t cost = INT64_MAX;
