@@ -250,10 +250,10 @@ __global__ void __launch_bounds__(SwapLayout<TN>::THREADS)
     else reinterpret_cast<float*>(p.c)[at] = v;
   };
   if (splits == 1) {
-    if (warp >= 4 && ok && n0 + wrow < p.N) {
+    if (warp >= 4 && n0 + wrow < p.N) {
 #pragma unroll
       for (int i = 0; i < CT; ++i)
-        if (m0 + t0 + i < p.M) store(t0 + i, n0 + wrow, acc[i]);
+        if (m0 + t0 + i < p.M) store(t0 + i, n0 + wrow, ok ? acc[i] : __int_as_float(0x7fc00000));
     }
   } else {
     const int per = (TN + splits - 1) / splits;  // tokens of an owner
@@ -587,6 +587,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         }
         if (++buf == L::ACCS) buf = 0;
       }
+      if (!ok) {  // a wait that ran out leaves NaN
+#pragma unroll
+        for (int i = 0; i < CW / 2; ++i) acc[i] = make_float2(__int_as_float(0x7fc00000), __int_as_float(0x7fc00000));
+      }
       // C leaves through shared memory by TMA, which drops what lies outside, two boxes per warp in turn; 16-byte chunk j
       // of row r lies at chunk j ^ (r / 2 % 4) of a row of 64 bytes, j ^ (r / 4 % 2) of one of 32 (the map's swizzle,
       // which keeps the writes free of bank conflicts)
@@ -601,7 +605,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         tc::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
-          if (ok && mw < p.M && n < p.N) tc::tma_store_2d(&tcm, from, (int)n, mw);
+          if (mw < p.M && n < p.N) tc::tma_store_2d(&tcm, from, (int)n, mw);
           tc::bulk_commit();
         }
         ob ^= 1;
