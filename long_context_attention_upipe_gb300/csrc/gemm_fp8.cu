@@ -325,12 +325,13 @@ cudaError_t run_swap(const Fp8GemmArgs& a, const Fp8Params& p, cudaStream_t st) 
 //   warps 2-3   the blocks' scales, eight blocks of K at a time, into a ring in shared memory (cp.async)
 //   warps 4-11  scaling: TMEM lanes 32 * (warp % 4), one half of the columns each, the sums in registers
 // One commit per block of K says both that its accumulator is ready and that its stage may be filled again:
-// the scaling warps wait on the stages' ring.  A stage completes again only after ACCS blocks were handed back,
-// and ACCS <= STAGES, so no waiter can miss a phase.
+// the scaling warps wait on the stages' ring.  Block b's stage completes again with block b + STAGES, whose MMAs wait
+// for block b + STAGES - ACCS to be handed back, and ACCS <= STAGES: every scaling warp has seen b by then, so none
+// can miss a phase.
 //
 // What bounds it is the scaling warps' own path, about 720 clocks per block of K at BN 256 where its MMAs take 512:
 // the wait (120, though the block is ready), the loads and sums (385 until the accumulator is handed back, of which
-// 256 are the sums') and the rest.  With neither loads of operands nor MMAs the kernel took 85% of its time; a
+// 256 are the sums') and the rest.  With neither loads of operands nor MMAs the kernel took 75% of its time; a
 // free-running loop of the same loads and sums takes 320, with waits and arrivals 490.  On the way here: an
 // arrive.release.cluster waits for every load in flight, so the accumulator is released by a relaxed arrive
 // (tcgen05.fence orders the reads of TMEM before it) and the scales are fetched by warps of their own; a one-lane
@@ -341,7 +342,7 @@ cudaError_t run_swap(const Fp8GemmArgs& a, const Fp8Params& p, cudaStream_t st) 
 // but writes half as many bytes again to shared memory: 5% slower.  C leaves by TMA from small boxes: a tile's
 // output took 3300 clocks with 16-byte stores, of which 2300 were instructions, and cost 3 to 4% more in all.
 // us at 1000 x 5120 x 8192 / 8192 x 28672 x 4096: one commit and short loops 46.8 -> 42.7 / 735 -> 703, C by TMA ->
-// 40.4 / 684 (2810 TFLOP/s; more than one box of 32 columns in flight: with three of 16 and a sixth stage 3% slower).
+// 40.4 / 684 (with three boxes of 16 columns and a sixth stage 3% more), shared addressing -> 38 / 662 (2900 TFLOP/s).
 // Sixteen scaling warps of a quarter of the columns each: 763.  Tokens on the columns, the kernel above: 171 / 2550 us.
 constexpr int kTileThreads = 384;
 constexpr int kScSlots = 2, kScGroup = 8;  // ring of scales: groups of eight blocks of K
