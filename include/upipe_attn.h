@@ -418,8 +418,9 @@ upipe_status_t upipe_attn_ring_bwd(const upipe_ring_desc_t* desc, const uint16_t
  *   y            device bf16 [rows, d] (written), or NULL with q; may be x or residual itself
  *   q, scales    both NULL, or y in 8 bits for upipe_attn_gemm_fp8_nt's A: q device e4m3 [rows, d],
  *                scales device fp32 [ceil(d / 128)][rows], for each row and 128 columns
- *                s = max|y| / 448 (1 where max|y| < 2^-100) and q = e4m3(y / s), rounded to nearest
- *                even from the fp32 y.  A NaN or infinity makes its block's scale NaN or infinity.
+ *                s = max|y| * fp32(1 / 448), one fp32 product (1 where max|y| < 2^-100), and
+ *                q = e4m3(fp32(y / s)) of the fp32 y, every step rounded to nearest even.
+ *                A NaN or infinity makes its block's scale NaN or infinity.
  *   rstd         NULL, or device fp32 [rows] (written) for the backward pass
  * Buffers that overlap in any other way are rejected with UPIPE_ERR_INVALID_ARG. */
 upipe_status_t upipe_attn_rms_norm_fwd(int64_t rows, int64_t d, float eps, const uint16_t* x, const uint16_t* residual,
@@ -447,7 +448,7 @@ upipe_status_t upipe_attn_rms_norm_bwd(int64_t rows, int64_t d, const uint16_t* 
  *   q       device e4m3 [rows, cols] (written)
  *   scales  device fp32 (written): block_rows 1 (activations, A): [ceil(cols / 128)][rows], one for
  *           each row and 128 columns; block_rows 128 (weights, B): [ceil(rows / 128)][ceil(cols / 128)]
- * s and q as in upipe_attn_rms_norm_fwd.  No two of the three overlap. */
+ * s and q as in upipe_attn_rms_norm_fwd, bit for bit.  No two of the three overlap. */
 upipe_status_t upipe_attn_fp8_quantize(int64_t rows, int64_t cols, int32_t block_rows, const uint16_t* x, uint8_t* q,
                                        float* scales, void* stream);
 

@@ -4,7 +4,7 @@
 // Forward, per row of d elements:
 //   h = bf16(x + r)                        (without a residual h = x, nothing written)
 //   rstd = (mean(h^2) + eps)^(-1/2),  y = h * rstd * w
-//   y rounded to bf16, or per block of 128 columns  s = max|y| / 448,  q = e4m3(y / s)
+//   y rounded to bf16, or per block of 128 columns  s = max|y| fp32(1 / 448),  q = e4m3(fp32(y / s))
 // h is normalised as it is stored, so the backward pass, which reads the stored h, differentiates
 // exactly the function that ran.  Backward, with t = dy * w:
 //   dx = rstd * (t - h * rstd^2 * mean(t * h)) [+ dres],   dw = sum over rows of dy * h * rstd
@@ -12,7 +12,7 @@
 //
 // A row belongs to a group of `tpr` threads, 8 elements (one 16-byte vector) per thread and step, V
 // steps, kept in registers between the statistics and the output: one read and one write of each
-// tensor, which is what bounds these kernels (HBM: 32768 x 4096 into e4m3 151 us, 6.2 TB/s; 16381 x 5120
+// tensor, which is what bounds these kernels (HBM: 32768 x 4096 into e4m3 149 us, 6.3 TB/s; 16381 x 5120
 // backward 105 us, 6.4 TB/s).  A 128-column block is 16 neighbouring lanes, so
 // its maximum is four shuffles; maxima are compared as the bits of |y|, which orders NaN above every
 // number, so a NaN reaches its block's scale.
@@ -51,12 +51,24 @@ __device__ __forceinline__ uint4 pack8(const V8& f) {
 }
 
 // Bits of the largest magnitude of 8 values (as unsigned integers: NaN > infinity > numbers).
-__device__ __forceinline__ uint32_t amax_bits(const V8& f) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f.v[i]) & 0x7fffffffu);
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+  float m;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
   return m;
 }
+__device__ __forceinline__ uint32_t amax_bits(const V8& f) {
+  const float m = max3_abs(max3_abs(f.v[0], f.v[1], f.v[2]), f.v[3], f.v[4]);
+  return __float_as_uint(max3_abs(max3_abs(m, f.v[5], f.v[6]), f.v[7], 0.f));
+}
+// The same of bf16 pairs, which need not be unpacked for it: the larger magnitudes of two pairs (with any signs),
+// and the larger of a pair's as the bits of an fp32.
+__device__ __forceinline__ uint32_t amax2(uint32_t a, uint32_t b) {
+  uint32_t m;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+  return m;
+}
+__device__ __forceinline__ uint32_t amax2(const uint4& v) { return amax2(amax2(v.x, v.y), amax2(v.z, v.w)); }
+__device__ __forceinline__ uint32_t pair_bits(uint32_t m) { return max((m << 16) & 0x7fffffffu, m & 0x7fff0000u); }
 
 // Scale of a block whose largest magnitude has the given bits: amax / 448 (as a product with the
 // rounded 1/448), or 1 for a block below 2^-100, whose e4m3 codes are all zero then.
@@ -65,12 +77,65 @@ __device__ __forceinline__ float block_scale(uint32_t bits) {
   return amax < 7.888609052210118e-31f ? 1.f : amax * (1.f / 448.f);
 }
 
-// 8 values times the scale's reciprocal, to e4m3 (nearest even, saturating; NaN stays NaN).
-__device__ __forceinline__ uint2 quant8(const V8& f, float inv) {
+// Codes are e4m3(fp32(y / s)), every step exactly rounded: bf16 values over a shared scale meet e4m3's ties often
+// (17 m over a largest value of 7 m), and a quotient that is one unit off sends them to either side.  A division
+// per value takes 32% more time (norm of 32768 x 4096: 150 -> 199 us), so the quotient Q = y / s is the product
+// with 1 / s as the sum hi + lo of two fp32 numbers, fma(y, hi, y * lo): Q (1 + delta) rounded once, |delta| < 2^-43.
+// That differs from fp32(Q) only if a midpoint M of two fp32 numbers lies within 2^-43 of Q, and the code only if one
+// of the two is a tie t 2^p of e4m3 (t < 32 odd).  M is then m 2^j with m = t 2^k +- 1 < 2^25, k >= 20, and with the
+// 24-bit significands Y and S of y and s, |Q - M| / M = |N| / (m S) for the integer N = Y 2^i - m S, i >= 24.  Modulo
+// 2^20 N is S or -S, N is not zero (2^24 would divide S), and N < 2^-43 m S < 64.  So only scales whose low 20 bits
+// are within 64 of zero, but not zero, are in doubt: one in 8000, and some percent of those of bf16 blocks (largest
+// value 7 m).  These, and scales from 2^60 on, are divided by.
+struct Divisor {
+  float hi, lo;  // lo >= 0, so that a zero keeps its sign
+  bool doubt;
+};
+__device__ __forceinline__ Divisor divisor(float s) {
+  const uint32_t bits = __float_as_uint(s), low = bits & 0xfffffu;
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+  const float hi = __uint_as_float(__float_as_uint(r) - 3u);  // r is off by a unit at most: hi < 1 / s
+  const float e = __fmaf_rn(-hi, s, 1.f);
+  return Divisor{hi, __fmaf_rn(e, e, e) * hi, !(bits < 0x5d800000u && low - 1u >= 64u && low < 0x100000u - 64u)};
+}
+
+// 8 values over the scale, to e4m3 (nearest even, saturating; NaN stays NaN).
+__device__ __forceinline__ uint2 quant8(const V8& f, const Divisor& d) {
+  const float2 hi = make_float2(d.hi, d.hi), lo = make_float2(d.lo, d.lo);
   uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    w[i] = __nv_cvt_float2_to_fp8x2(make_float2(f.v[2 * i] * inv, f.v[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+  for (int i = 0; i < 4; ++i) {
+    const float2 y = make_float2(f.v[2 * i], f.v[2 * i + 1]);
+    w[i] = __nv_cvt_float2_to_fp8x2(__ffma2_rn(y, hi, __fmul2_rn(y, lo)), __NV_SATFINITE, __NV_E4M3);
+  }
+  return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+}
+
+// The same for a scale in doubt, by Markstein's scheme (IBM J. Res. Dev. 34, 1990): with r = fp32(1 / s) and a q
+// within a unit of Q (y r after one such step), q + (y - q s) r with both sums fused is fp32(Q).  y and s go to s in
+// [1, 2) by a power of two first, so that no difference is subnormal; an infinite scale makes zeros of the numbers, and NaN of the rest.  A
+// function of its own: inlined, it cost the callers registers (norm 149 -> 152 us).
+__device__ __noinline__ uint2 quant8_divided(V8 f, float s) {
+  float m;
+  if (s < 1.3e36f) {  // scales end at 2^128 / 448
+    m = __uint_as_float((254u - (__float_as_uint(s) >> 23)) << 23);
+    s *= m;
+  } else {
+    m = s != s ? s : 0.f;
+    s = 1.f;
+  }
+  const float r = -__frcp_rn(s);  // the quotients' negatives, with which zeros come out with the right sign
+  const float2 m2 = make_float2(m, m), s2 = make_float2(s, s), r2 = make_float2(r, r);
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 y = __fmul2_rn(make_float2(f.v[2 * i], f.v[2 * i + 1]), m2);
+    float2 q = __fmul2_rn(y, r2);
+    q = __ffma2_rn(__ffma2_rn(q, s2, y), r2, q);
+    q = __ffma2_rn(__ffma2_rn(q, s2, y), r2, q);
+    w[i] = __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3) ^ 0x8080u;
+  }
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
@@ -165,7 +230,12 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rms_fwd(NormShape n, float eps, 
       const int64_t at = row * n.d + c * 8;
       const V8 wf = unpack8(wv[i]);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) f[i].v[k] = f[i].v[k] * rstd * wf.v[k];
+      for (int k = 0; k < 8; k += 2) {
+        const float2 o = __fmul2_rn(__fmul2_rn(make_float2(f[i].v[k], f[i].v[k + 1]), make_float2(rstd, rstd)),
+                                    make_float2(wf.v[k], wf.v[k + 1]));
+        f[i].v[k] = o.x;
+        f[i].v[k + 1] = o.y;
+      }
       if (!FP8 || y) {
         if (ok) *reinterpret_cast<uint4*>(y + at) = pack8(f[i]);
       }
@@ -173,7 +243,8 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rms_fwd(NormShape n, float eps, 
         // columns past d of the last block hold zeros (x and w were read as zeros there), unless
         // rstd is not finite; they must not reach the block's maximum then either
         const float s = block_scale(max16(ok ? amax_bits(f[i]) : 0u));
-        if (ok) *reinterpret_cast<uint2*>(q + at) = quant8(f[i], __fdividef(1.f, s));
+        const Divisor by = divisor(s);
+        if (ok) *reinterpret_cast<uint2*>(q + at) = by.doubt ? quant8_divided(f[i], s) : quant8(f[i], by);
         if (ok && (t & 15) == 0) scales[(int64_t)(c >> 4) * n.rows + row] = s;
       }
     }
@@ -471,7 +542,7 @@ __global__ void __launch_bounds__(1024) k_dw_reduce(const float* __restrict__ pa
 }
 
 // One scale per row and 128 columns: 16 lanes per block, blocks of a row side by side, four blocks of a
-// 16-lane group in flight at once (32768 x 4096: 73 us, 5.5 TB/s; one block in flight 94 us).
+// 16-lane group in flight at once (32768 x 4096: 75 us, 5.4 TB/s; one block in flight 94 us).
 __global__ void __launch_bounds__(256, 4) k_quant_rows(int64_t rows, int d, int nb, const bf16* __restrict__ x, uint8_t* q,
                                                     float* scales) {
   constexpr int U = 4;
@@ -503,9 +574,10 @@ __global__ void __launch_bounds__(256, 4) k_quant_rows(int64_t rows, int d, int 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const V8 f = unpack8(v[u]);
-      const float s = block_scale(max16(amax_bits(f)));
+      const float s = block_scale(max16(pair_bits(amax2(v[u]))));
+      const Divisor by = divisor(s);
       const int c = bl[u] * 128 + lane16 * 8;
-      if (rw[u] < rows && c < d) *reinterpret_cast<uint2*>(q + rw[u] * d + c) = quant8(f, __fdividef(1.f, s));
+      if (rw[u] < rows && c < d) *reinterpret_cast<uint2*>(q + rw[u] * d + c) = by.doubt ? quant8_divided(f, s) : quant8(f, by);
       if (rw[u] < rows && lane16 == 0) scales[(int64_t)bl[u] * rows + rw[u]] = s;
     }
   }
@@ -530,19 +602,24 @@ __global__ void __launch_bounds__(256, 4) k_quant_tiles(int64_t rows, int d, int
     v[i] = row < rows && c < d ? *reinterpret_cast<const uint4*>(x + row * d + c) : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = max(m, amax_bits(unpack8(v[i])));
+  for (int i = 0; i < 8; ++i) m = amax2(m, amax2(v[i]));
+  m = pair_bits(m);
   m = __reduce_max_sync(0xffffffffu, m);
   if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = max(m, red[i]);
-  const float s = block_scale(m), inv = __fdividef(1.f, s);
+  const float s = block_scale(m);
+  const Divisor by = divisor(s);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int id = threadIdx.x + 256 * i;
     const int64_t row = tr * 128 + (id >> 4);
     const int c = b * 128 + (id & 15) * 8;
-    if (row < rows && c < d) *reinterpret_cast<uint2*>(q + row * d + c) = quant8(unpack8(v[i]), inv);
+    if (row < rows && c < d) {
+      const V8 f = unpack8(v[i]);
+      *reinterpret_cast<uint2*>(q + row * d + c) = by.doubt ? quant8_divided(f, s) : quant8(f, by);
+    }
   }
   if (threadIdx.x == 0) scales[tr * nb + b] = s;
 }
