@@ -8,8 +8,7 @@
 // one while the other is scaled.
 //
 // Few rows of A (decode): the weights take the 128 rows of the MMA and the tokens its N side (TN = 16
-// ... 128 of them), so the tensor core's rows are full whatever the batch.  One CTA per 128 weight rows
-// and TN tokens, 6 warps: 0 TMA producer, 1 MMA issuer, 2-5 scaling (one weight row per thread).
+// ... 128 of them), so the tensor core's rows are full whatever the batch.
 #include <cstring>
 
 #include "internal.h"
@@ -188,13 +187,12 @@ __global__ void __launch_bounds__(SwapLayout<TN>::THREADS)
     uint32_t ph = 1;
     for (int kb = 0; kb < nkb; kb += 4) {
       ok = tc::mbar_wait(&sc_empty[slot], ph, abort_flag, nullptr, p.wait_ns) && ok;
-      if (ok) {
-        float* dst = reinterpret_cast<float*>(smem + L::SC + slot * L::SCSLOT);
+      if (!ok) break;
+      float* dst = reinterpret_cast<float*>(smem + L::SC + slot * L::SCSLOT);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if (j < TN) dst[u * TN + j] = v0[u];
-          if (j + 64 < TN) dst[u * TN + j + 64] = v1[u];
-        }
+      for (int u = 0; u < 4; ++u) {
+        if (j < TN) dst[u * TN + j] = v0[u];
+        if (j + 64 < TN) dst[u * TN + j + 64] = v1[u];
       }
       tc::mbar_arrive(&sc_full[slot]);
       fetch(kb + 4);
@@ -222,7 +220,7 @@ __global__ void __launch_bounds__(SwapLayout<TN>::THREADS)
         if (g == CT / 16 - 1) {
           tc::fence_before_sync();
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive_addr(acce + buf * 8);
+          if (lane == 0 && ok) tc::mbar_arrive_addr(acce + buf * 8);
         }
 #pragma unroll
         for (int i = 0; i < 16; i += 4) {
@@ -236,7 +234,7 @@ __global__ void __launch_bounds__(SwapLayout<TN>::THREADS)
       if (++buf == NB) { buf = 0; aph ^= 1; }
       if (u == 3) {
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive_addr(sce + slot * 8);
+        if (lane == 0 && ok) tc::mbar_arrive_addr(sce + slot * 8);
         if (++slot == 4) { slot = 0; sph ^= 1; }
       }
     }
@@ -324,6 +322,9 @@ cudaError_t run_swap(const Fp8GemmArgs& a, const Fp8Params& p, cudaStream_t st) 
 //               512 / BN TMEM accumulators, which both CTAs hold for their rows
 //   warps 2-3   the blocks' scales, eight blocks of K at a time, into a ring in shared memory (cp.async)
 //   warps 4-11  scaling: TMEM lanes 32 * (warp % 4), one half of the columns each, the sums in registers
+// A wait that runs out (p.wait_ns) makes its thread give up for good: it loads, issues and arrives no more, so that
+// whoever depends on it gives up in turn, and a sum to which every wait came through is a right one; all others leave
+// as NaN.
 // One commit per block of K says both that its accumulator is ready and that its stage may be filled again:
 // the scaling warps wait on the stages' ring.  Block b's stage completes again with block b + STAGES, whose MMAs wait
 // for block b + STAGES - ACCS to be handed back, and ACCS <= STAGES: every scaling warp has seen b by then, so none
@@ -447,7 +448,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       int s = 0;
       uint32_t ph = 1;  // parity of the stage's previous release: the first turn needs none
       bool ok = true;
-      for (int t = cid; t < n_tiles; t += n_clusters) {
+      for (int t = cid; t < n_tiles && __all_sync(0xffffffffu, ok); t += n_clusters) {
         int tm, tn;
         decode(t, tm, tn);
 #pragma unroll 1
@@ -471,7 +472,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       int s = 0, buf = 0;
       uint32_t ph = 0, eph = 1;
       bool ok = true;
-      for (int t = cid; t < n_tiles; t += n_clusters) {
+      for (int t = cid; t < n_tiles && __all_sync(0xffffffffu, ok); t += n_clusters) {
 #pragma unroll 1
         for (int kb = 0; kb < nkb; ++kb) {
           const bool f = tc::mbar_try_wait_addr(fulla + s * 8, ph), e = tc::mbar_try_wait_addr(acce + buf * 8, eph);
@@ -498,7 +499,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       int slot = 0;
       uint32_t ph = 1;
       bool ok = true;
-      for (int t = cid; t < n_tiles; t += n_clusters) {
+      for (int t = cid; t < n_tiles && ok; t += n_clusters) {
         int tm, tn;
         decode(t, tm, tn);
         const int64_t ma = (int64_t)tm * 128 + j, mb = ma + 64;
@@ -510,18 +511,17 @@ __global__ void __launch_bounds__(kTileThreads, 1)
 #pragma unroll 1
         for (int kb0 = 0; kb0 < nkb; kb0 += kScGroup) {
           ok = tc::mbar_wait_addr(smem_u32(&sc_empty[slot]), ph, abort_flag, p.wait_ns) && ok;
-          if (ok) {
-            uint32_t dst = smem_u32(smem + L::SC + slot * L::SCSLOT) + j * 4;
-            const int n = min(kScGroup, nkb - kb0);
+          if (!ok) break;
+          uint32_t dst = smem_u32(smem + L::SC + slot * L::SCSLOT) + j * 4;
+          const int n = min(kScGroup, nkb - kb0);
 #pragma unroll 1
-            for (int u = 0; u < n; ++u, dst += kScRow * 4) {
-              cp_async4(dst, pa, na);
-              cp_async4(dst + 256, pb, nb);
-              if (j < 4) cp_async4(dst + 512, ps, ns);
-              pa += p.lds;
-              pb += p.lds;
-              ++ps;
-            }
+          for (int u = 0; u < n; ++u, dst += kScRow * 4) {
+            cp_async4(dst, pa, na);
+            cp_async4(dst + 256, pb, nb);
+            if (j < 4) cp_async4(dst + 512, ps, ns);
+            pa += p.lds;
+            pb += p.lds;
+            ++ps;
           }
           cp_async_arrive(smem_u32(&sc_full[slot]));
           if (++slot == kScSlots) { slot = 0; ph ^= 1; }
@@ -550,8 +550,10 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       float2 acc[CW / 2];
 #pragma unroll
       for (int i = 0; i < CW / 2; ++i) acc[i] = make_float2(0.f, 0.f);
+      ok = __all_sync(0xffffffffu, ok);  // a warp that gave up only fills the rest of its tiles
+      const int blocks = ok ? nkb : 0;
 #pragma unroll 1
-      for (int kb = 0; kb < nkb; ++kb) {
+      for (int kb = 0; kb < blocks; ++kb) {
         const int u = kb % kScGroup;
         if (u == 0) ok = tc::mbar_wait_addr(scf + slot * 8, sph, abort_flag, p.wait_ns) && ok;
         const float* sc = reinterpret_cast<const float*>(smem + L::SC + slot * L::SCSLOT) + u * kScRow;
@@ -566,7 +568,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
         const float f0 = sa * sb0, f1 = kStraddle ? sa * sb1 : f0;
         if (u == kScGroup - 1 || kb + 1 == nkb) {
           __syncwarp();
-          if (lane == 0) tc::mbar_arrive_addr(sce + slot * 8);
+          if (lane == 0 && ok) tc::mbar_arrive_addr(sce + slot * 8);
           if (++slot == kScSlots) { slot = 0; sph ^= 1; }
         }
 #pragma unroll
@@ -577,7 +579,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
             // everything is in registers: the accumulator may be written again while these are scaled
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive_cluster_relaxed(acc0 + buf * 8);
+            if (lane == 0 && ok) tc::mbar_arrive_cluster_relaxed(acc0 + buf * 8);
           }
           const float f = kStraddle && g >= cut ? f1 : f0;
           const float2 f2 = make_float2(f, f);
