@@ -37,6 +37,14 @@ struct Fp8Params {
 // 1000 x 5120 x 8192 40.4 -> 38.0 us, 128 x 5120 x 8192 19.0 -> 16.4).
 __device__ __forceinline__ uint8_t* align_smem(uint8_t* p) { return p + ((0u - smem_u32(p)) & 1023); }
 
+// Waits for the last `ring` of the `turns` that went through a ring of barriers, so that nothing is in flight towards
+// this CTA's shared memory or TMEM when it leaves.  Where every wait came through, the scaling warps need the same.
+__device__ __forceinline__ void drain_ring(uint32_t bars, uint32_t turns, uint32_t ring) {
+  const uint64_t until = tc::globaltimer() + tc::kDrainNs;
+#pragma unroll 1
+  for (uint32_t i = turns > ring ? turns - ring : 0; i < turns; ++i) tc::mbar_drain(bars + i % ring * 8, i / ring & 1, until);
+}
+
 // ------------------------------------------------------------------------------------------------
 // few rows of A: weights on the MMA's rows, TN tokens on its columns, K split over a cluster
 // ------------------------------------------------------------------------------------------------
@@ -128,11 +136,12 @@ __global__ void __launch_bounds__(SwapLayout<TN>::THREADS)
     const bool leader = tc::elect_one();
     const uint32_t emptya = smem_u32(empty);
     int s = 0;
-    uint32_t ph = 1;  // parity of the stage's previous release: the first turn needs none
+    uint32_t ph = 1, turns = 0;  // parity of the stage's previous release: the first turn needs none
 #pragma unroll 1
     for (int kb = 0; kb < nkb; ++kb) {
       ok = tc::mbar_wait_addr(emptya + s * 8, ph, abort_flag, p.wait_ns) && ok;
       if (leader && ok) {
+        ++turns;
         uint8_t* st = smem + s * L::STAGE;
         tc::mbar_arrive_expect_tx(&full[s], L::STAGE);
         tc::tma_load_2d(st, &tw, &full[s], (kb0 + kb) * kBlk, (int)n0);
@@ -141,13 +150,14 @@ __global__ void __launch_bounds__(SwapLayout<TN>::THREADS)
       __syncwarp();
       if (++s == ST) { s = 0; ph ^= 1; }
     }
+    if (leader) drain_ring(smem_u32(full), turns, ST);
   } else if (warp == 1) {
     constexpr uint32_t idesc = tc::idesc_e4m3(128, TN);
     const uint64_t w0 = tc::sdesc_sw128(smem_u32(smem), 16, 1024), x0 = tc::sdesc_add(w0, L::W);
     const uint32_t fulla = smem_u32(full), acce = smem_u32(acc_empty);
     const bool leader = tc::elect_one();
     int s = 0, buf = 0;
-    uint32_t ph = 0, eph = 1;
+    uint32_t ph = 0, eph = 1, turns = 0;
 #pragma unroll 1
     for (int kb = 0; kb < nkb; ++kb) {
       ok = tc::mbar_wait_addr(acce + buf * 8, eph, abort_flag, p.wait_ns) && ok;
@@ -156,6 +166,7 @@ __global__ void __launch_bounds__(SwapLayout<TN>::THREADS)
       const uint64_t wd = tc::sdesc_add(w0, s * L::STAGE), xd = tc::sdesc_add(x0, s * L::STAGE);
       const uint32_t d = tmem + buf * TN;
       if (leader && ok) {
+        ++turns;
 #pragma unroll
         for (int k = 0; k < kBlk / 32; ++k)
           tc::mma_ss_f8(d, tc::sdesc_add(wd, k * 32), tc::sdesc_add(xd, k * 32), idesc, k > 0);
@@ -165,6 +176,10 @@ __global__ void __launch_bounds__(SwapLayout<TN>::THREADS)
       __syncwarp();
       if (++s == ST) { s = 0; ph ^= 1; }
       if (++buf == NB) { buf = 0; eph ^= 1; }
+    }
+    if (leader) {
+      drain_ring(smem_u32(empty), turns, ST);
+      drain_ring(smem_u32(acc_full), turns, NB);
     }
   } else if (warp < 4) {
     // tokens j and j + 64
@@ -446,7 +461,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       const bool leader = tc::elect_one();
       const uint32_t emptya = smem_u32(empty), full0 = tc::mapa_cluster(smem_u32(full), 0);
       int s = 0;
-      uint32_t ph = 1;  // parity of the stage's previous release: the first turn needs none
+      uint32_t ph = 1, turns = 0;  // parity of the stage's previous release: the first turn needs none
       bool ok = true;
       for (int t = cid; t < n_tiles && __all_sync(0xffffffffu, ok); t += n_clusters) {
         int tm, tn;
@@ -456,6 +471,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           ok = tc::mbar_wait_addr(emptya + s * 8, ph, abort_flag, p.wait_ns) && ok;
           uint8_t* sa = smem + s * L::STAGE;
           if (leader && ok) {
+            ++turns;
             if (crank == 0) tc::mbar_arrive_expect_tx(&full[s], 2 * L::STAGE);  // both CTAs' halves
             tc::tma_load_2d_pair(sa, &ta, full0 + s * 8, kb * kBlk, tm * 128);
             tc::tma_load_2d_pair(sa + L::A, &tb, full0 + s * 8, kb * kBlk, tn * BN + crank * CW);
@@ -464,6 +480,9 @@ __global__ void __launch_bounds__(kTileThreads, 1)
           if (++s == ST) { s = 0; ph ^= 1; }
         }
       }
+      // a stage whose MMAs are done holds neither CTA's loads any more; one whose MMAs never come holds loads that
+      // land in microseconds, the limit's second later
+      if (leader) drain_ring(emptya, turns, ST);
     } else if (warp == 1 && crank == 0) {
       constexpr uint32_t idesc = tc::idesc_e4m3(256, BN);
       const uint64_t a0 = tc::sdesc_sw128(smem_u32(smem), 16, 1024), b0 = tc::sdesc_add(a0, L::A);

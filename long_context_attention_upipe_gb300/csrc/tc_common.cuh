@@ -89,6 +89,13 @@ __device__ __forceinline__ bool mbar_wait_addr(uint32_t bar, uint32_t parity, vo
   }
   return true;
 }
+// For copies and MMAs that a block has in flight when it leaves: waits for their barrier whatever the abort flag says,
+// until `until` (of globaltimer) at the latest.  A second is far more than any of them takes.
+constexpr uint64_t kDrainNs = 1000000000ull;
+__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, uint64_t until) {
+  while (!mbar_try_wait_addr(bar, parity))
+    if (globaltimer() > until) return;
+}
 __device__ __forceinline__ void mbar_arrive_addr(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }

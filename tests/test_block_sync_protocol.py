@@ -292,10 +292,15 @@ def with_waits_that_run_out(pair, rings, old, runs, seed):
 
 
 @pytest.mark.parametrize("pair,rings", [(True, r) for r in PAIR] + [(False, r) for r in FEW])
-def test_product_stores_nan_or_the_right_value(pair, rings):
-    wrong, nan, right, _ = with_waits_that_run_out(pair, rings, ("leave",), 300, 3)
+def test_product_stores_nan_or_the_right_value_and_leaves_nothing_in_flight(pair, rings):
+    wrong, nan, right, left = with_waits_that_run_out(pair, rings, (), 300, 3)
     assert nan > 0 and right > 0
-    assert wrong == 0
+    assert wrong == 0 and left == 0
+
+
+@pytest.mark.parametrize("rings", FEW)
+def test_a_producer_that_just_leaves_has_copies_in_flight(rings):
+    assert with_waits_that_run_out(False, rings, ("leave",), 300, 5)[3] > 0
 
 
 @pytest.mark.parametrize("pair,rings", [(True, PAIR[0]), (False, FEW[1])])
