@@ -405,7 +405,8 @@ upipe_status_t upipe_attn_ring_bwd(const upipe_ring_desc_t* desc, const uint16_t
  * MLP and the optimizer.  The pages describe none of them; they are this library's own, for users
  * who run its layer, attention core or MLP inside a whole block.  Conventions as above (every device
  * pointer 16-byte aligned, stream-ordered, nothing allocated).  Zero rows or tokens are valid.  They have no
- * error word: a bounded device wait that ran out leaves NaN in the product's C and in the norm's dw.
+ * error word: a bounded device wait that ran out leaves NaN in the product's C, or in dw and the rows of dx that it
+ * kept the norm's backward pass from.
  *
  * Root-mean-square norm with the residual's addition.  Per row of d elements:
  *   h = bf16(x + residual)  (without a residual h is x itself and is not written)

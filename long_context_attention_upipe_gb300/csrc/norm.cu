@@ -333,7 +333,8 @@ __global__ void __launch_bounds__(MAXT, MINB) k_rms_bwd(NormShape n, const bf16*
 
 // The same for longer rows, whose next row would not fit into registers without leaving SMs short of threads
 // (see bwd_ring): a producer warp copies whole rows (dy, h, dres) ahead into a ring in shared memory, tpr
-// threads work on one row after the other.  One block per SM.
+// threads work on one row after the other.  One block per SM.  A thread whose wait runs out (wait_ns) gives up for good
+// and hands no stage back; the rows of dx that its block has not finished, and dw, become NaN.
 template <int V>
 __global__ void __launch_bounds__(V == 2 ? 512 : 544, 1) k_rms_bwd_ring(NormShape n, const bf16* dy, const bf16* h, const bf16* __restrict__ w,
                                                          const float* __restrict__ rstd_in, const bf16* dres, bf16* dx,
@@ -360,7 +361,7 @@ __global__ void __launch_bounds__(V == 2 ? 512 : 544, 1) k_rms_bwd_ring(NormShap
   if (warp == 0) {
     const bool leader = tc::elect_one();
     uint32_t ph = 1;  // parity of the stage's previous release: the first turn needs none
-    for (int64_t row = blockIdx.x; row < n.rows; row += gridDim.x) {
+    for (int64_t row = blockIdx.x; row < n.rows && __all_sync(0xffffffffu, ok); row += gridDim.x) {
       ok = tc::mbar_wait_addr(smem_u32(&empty[s]), ph, abort_flag, wait_ns) && ok;
       if (leader && ok) {
         uint8_t* st = ring + s * stage_bytes;
@@ -392,7 +393,7 @@ __global__ void __launch_bounds__(V == 2 ? 512 : 544, 1) k_rms_bwd_ring(NormShap
   for (int64_t row = blockIdx.x; row < n.rows; row += gridDim.x, par ^= 1) {
     const float rstd = rstd_next;
     if (row + gridDim.x < n.rows) rstd_next = rstd_in[row + gridDim.x];
-    ok = tc::mbar_wait_addr(smem_u32(&full[s]), ph, abort_flag, wait_ns) && ok;
+    ok = ok && tc::mbar_wait_addr(smem_u32(&full[s]), ph, abort_flag, wait_ns);
     const uint8_t* st = ring + s * stage_bytes;
     uint4 dv[V], hv[V], rv[V];
     auto read = [&](int i, int c) {
@@ -408,7 +409,7 @@ __global__ void __launch_bounds__(V == 2 ? 512 : 544, 1) k_rms_bwd_ring(NormShap
     };
     auto release = [&]() {
       __syncwarp();
-      if (lane == 0) tc::mbar_arrive(&empty[s]);
+      if (lane == 0 && ok) tc::mbar_arrive(&empty[s]);
       if (++s == stages) { s = 0; ph ^= 1; }
     };
     float dot = 0.f;
@@ -424,6 +425,7 @@ __global__ void __launch_bounds__(V == 2 ? 512 : 544, 1) k_rms_bwd_ring(NormShap
       }
     }
     if (kHold) release();
+    if (!ok) dot = __int_as_float(0x7fc00000);  // through the sum, the whole row becomes NaN
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) dot += __shfl_xor_sync(0xffffffffu, dot, off);
     if (lane == 0) red[par][warp - 1] = dot;
@@ -435,7 +437,7 @@ __global__ void __launch_bounds__(V == 2 ? 512 : 544, 1) k_rms_bwd_ring(NormShap
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = t + i * n.tpr;
-      if (c >= nvec || !ok) continue;
+      if (c >= nvec) continue;
       if (!kHold) read(i, c);
       const V8 a = unpack8(dv[i]), b = unpack8(hv[i]), wf = unpack8(weight(i, c)), r = unpack8(rv[i]);
       V8 o;
@@ -446,11 +448,12 @@ __global__ void __launch_bounds__(V == 2 ? 512 : 544, 1) k_rms_bwd_ring(NormShap
     if (!kHold) release();
   }
   float* dst = part + (int64_t)blockIdx.x * n.d;
+  tc::named_bar_sync(1, n.tpr);
+  const float bad = *abort_flag ? __int_as_float(0x7fc00000) : 0.f;  // rows are missing from every column's sum
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = t + i * n.tpr;
     if (c >= nvec) continue;
-    const float bad = ok ? 0.f : __int_as_float(0x7fc00000);  // a wait that ran out leaves NaN
     *reinterpret_cast<float4*>(dst + c * 8) = make_float4(dw[i].v[0] + bad, dw[i].v[1] + bad, dw[i].v[2] + bad, dw[i].v[3] + bad);
     *reinterpret_cast<float4*>(dst + c * 8 + 4) = make_float4(dw[i].v[4] + bad, dw[i].v[5] + bad, dw[i].v[6] + bad, dw[i].v[7] + bad);
   }

@@ -88,6 +88,8 @@ class World:
             actor, (block, bar, parity) = todo[i]
             if bar.done(parity):
                 answer = True
+            elif block == "threads":                # a barrier of threads: nobody gives up on it
+                answer = None
             elif block == "drain":
                 answer = False if not self.flight and not self.queue and idle > 200 else None
             elif self.abort[block] and self.rng.random() < 0.02:
@@ -307,3 +309,94 @@ def test_a_producer_that_just_leaves_has_copies_in_flight(rings):
 def test_an_arrival_of_a_role_that_gave_up_lets_wrong_values_through(pair, rings):
     wrong, _, _, _ = with_waits_that_run_out(pair, rings, ("arrive", "leave"), 300, 4)
     assert wrong > 0
+
+
+# ------------------------------------------------------------------------------------------------
+# norm backward: rows ahead in a ring
+# ------------------------------------------------------------------------------------------------
+
+def norm_ring(w, rows, stages, warps=3):
+    full, empty = [Bar(1) for _ in range(stages)], [Bar(warps) for _ in range(stages)]
+    named = Bar(warps)
+    stage = [None] * stages
+    row_ok, row_right = [True] * rows, [True] * rows     # what the row's sum is made of
+    dw_ok = [True] * warps
+
+    def producer():
+        ring, ok, n = Ring(stages, 1), True, 0
+        for row in range(rows):
+            ok = (yield (0, empty[ring.at], ring.parity)) and ok
+            if not ok:
+                break
+            full[ring.at].arrive(tx=1)
+
+            def land(s=ring.at, row=row):
+                stage[s] = row
+                full[s].complete()
+            w.flight.append(land)
+            n += 1
+            ring.step()
+        if "leave" not in w.old:
+            for i in last_turns(n, stages):
+                yield ("drain", full[i % stages], i // stages & 1)
+
+    def worker(k):
+        ring, ok, turn = Ring(stages, 0), True, 0
+        for row in range(rows):
+            if ok or "stale" in w.old:
+                ok = (yield (0, full[ring.at], ring.parity)) and ok
+            row_right[row] &= stage[ring.at] == row
+            if ok or "stale" in w.old:
+                empty[ring.at].arrive()
+            else:
+                row_ok[row] = False                      # NaN in the sum
+            ring.step()
+            named.arrive()
+            yield ("threads", named, turn)
+            turn ^= 1
+            if "stale" in w.old and not ok:
+                w.wrong += 1                             # its part of the row keeps what was there
+            else:
+                w.store(row_ok[row], row_right[row])
+        named.arrive()
+        yield ("threads", named, turn)
+        dw_ok[k] = not w.abort[0]
+
+    w.run([producer()] + [worker(k) for k in range(warps)])
+    return warps * rows, dw_ok
+
+
+def norm_with_waits_that_run_out(stages, old, runs, seed):
+    rng = random.Random(seed)
+    wrong = nan = right = left = 0
+    for _ in range(runs):
+        w = World(rng, rng.choice([0.0005, 0.003, 0.02]), 1, old)
+        try:
+            n, dw_ok = norm_ring(w, rng.choice([1, 2, 5, 9, 20]), stages)
+            assert w.wrong + w.nan + w.right == n
+            assert len(set(dw_ok)) == 1 and (not w.nan or not dw_ok[0])    # NaN in a row: NaN in every column of dw
+        except AssertionError:
+            if not old:
+                raise
+            w.wrong += 1
+        wrong, nan, right, left = wrong + w.wrong, nan + w.nan, right + w.right, left + drain(w)
+    return wrong, nan, right, left
+
+
+@pytest.mark.parametrize("stages", [3, 5, 8])
+def test_norm_ring_ends_and_is_right(stages):
+    rng = random.Random(6)
+    for _ in range(200):
+        w = World(rng, 0.0, 1)
+        n, dw_ok = norm_ring(w, rng.choice([1, 2, 5, 9, 20]), stages)
+        assert w.right == n and all(dw_ok) and not drain(w)
+
+
+@pytest.mark.parametrize("stages", [3, 5, 8])
+def test_norm_ring_stores_nan_or_the_right_rows(stages):
+    wrong, nan, right, _ = norm_with_waits_that_run_out(stages, ("leave",), 300, 7)
+    assert nan > 0 and right > 0 and wrong == 0
+
+
+def test_norm_ring_that_skips_rows_leaves_old_values():
+    assert norm_with_waits_that_run_out(5, ("stale", "leave"), 300, 8)[0] > 0
