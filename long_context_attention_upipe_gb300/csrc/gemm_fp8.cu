@@ -37,14 +37,6 @@ struct Fp8Params {
 // 1000 x 5120 x 8192 40.4 -> 38.0 us, 128 x 5120 x 8192 19.0 -> 16.4).
 __device__ __forceinline__ uint8_t* align_smem(uint8_t* p) { return p + ((0u - smem_u32(p)) & 1023); }
 
-// Waits for the last `ring` of the `turns` that went through a ring of barriers, so that nothing is in flight towards
-// this CTA's shared memory or TMEM when it leaves.  Where every wait came through, the scaling warps need the same.
-__device__ __forceinline__ void drain_ring(uint32_t bars, uint32_t turns, uint32_t ring) {
-  const uint64_t until = tc::globaltimer() + tc::kDrainNs;
-#pragma unroll 1
-  for (uint32_t i = turns > ring ? turns - ring : 0; i < turns; ++i) tc::mbar_drain(bars + i % ring * 8, i / ring & 1, until);
-}
-
 // ------------------------------------------------------------------------------------------------
 // few rows of A: weights on the MMA's rows, TN tokens on its columns, K split over a cluster
 // ------------------------------------------------------------------------------------------------
@@ -150,7 +142,7 @@ __global__ void __launch_bounds__(SwapLayout<TN>::THREADS)
       __syncwarp();
       if (++s == ST) { s = 0; ph ^= 1; }
     }
-    if (leader) drain_ring(smem_u32(full), turns, ST);
+    if (leader) tc::drain_ring(smem_u32(full), turns, ST);
   } else if (warp == 1) {
     constexpr uint32_t idesc = tc::idesc_e4m3(128, TN);
     const uint64_t w0 = tc::sdesc_sw128(smem_u32(smem), 16, 1024), x0 = tc::sdesc_add(w0, L::W);
@@ -178,8 +170,8 @@ __global__ void __launch_bounds__(SwapLayout<TN>::THREADS)
       if (++buf == NB) { buf = 0; eph ^= 1; }
     }
     if (leader) {
-      drain_ring(smem_u32(empty), turns, ST);
-      drain_ring(smem_u32(acc_full), turns, NB);
+      tc::drain_ring(smem_u32(empty), turns, ST);
+      tc::drain_ring(smem_u32(acc_full), turns, NB);
     }
   } else if (warp < 4) {
     // tokens j and j + 64
@@ -482,7 +474,7 @@ __global__ void __launch_bounds__(kTileThreads, 1)
       }
       // a stage whose MMAs are done holds neither CTA's loads any more; one whose MMAs never come holds loads that
       // land in microseconds, the limit's second later
-      if (leader) drain_ring(emptya, turns, ST);
+      if (leader) tc::drain_ring(emptya, turns, ST);
     } else if (warp == 1 && crank == 0) {
       constexpr uint32_t idesc = tc::idesc_e4m3(256, BN);
       const uint64_t a0 = tc::sdesc_sw128(smem_u32(smem), 16, 1024), b0 = tc::sdesc_add(a0, L::A);

@@ -360,10 +360,11 @@ __global__ void __launch_bounds__(V == 2 ? 512 : 544, 1) k_rms_bwd_ring(NormShap
   bool ok = true;
   if (warp == 0) {
     const bool leader = tc::elect_one();
-    uint32_t ph = 1;  // parity of the stage's previous release: the first turn needs none
+    uint32_t ph = 1, turns = 0;  // parity of the stage's previous release: the first turn needs none
     for (int64_t row = blockIdx.x; row < n.rows && __all_sync(0xffffffffu, ok); row += gridDim.x) {
       ok = tc::mbar_wait_addr(smem_u32(&empty[s]), ph, abort_flag, wait_ns) && ok;
       if (leader && ok) {
+        ++turns;
         uint8_t* st = ring + s * stage_bytes;
         tc::mbar_arrive_expect_tx(&full[s], stage_bytes);
         tc::bulk_load(st, dy + row * n.d, row_bytes, &full[s]);
@@ -373,6 +374,7 @@ __global__ void __launch_bounds__(V == 2 ? 512 : 544, 1) k_rms_bwd_ring(NormShap
       __syncwarp();
       if (++s == stages) { s = 0; ph ^= 1; }
     }
+    if (leader) tc::drain_ring(smem_u32(full), turns, stages);
     return;
   }
   const int t = threadIdx.x - 32;
@@ -393,7 +395,7 @@ __global__ void __launch_bounds__(V == 2 ? 512 : 544, 1) k_rms_bwd_ring(NormShap
   for (int64_t row = blockIdx.x; row < n.rows; row += gridDim.x, par ^= 1) {
     const float rstd = rstd_next;
     if (row + gridDim.x < n.rows) rstd_next = rstd_in[row + gridDim.x];
-    ok = ok && tc::mbar_wait_addr(smem_u32(&full[s]), ph, abort_flag, wait_ns);
+    ok = tc::mbar_wait_addr(smem_u32(&full[s]), ph, abort_flag, wait_ns) && ok;
     const uint8_t* st = ring + s * stage_bytes;
     uint4 dv[V], hv[V], rv[V];
     auto read = [&](int i, int c) {

@@ -89,12 +89,16 @@ __device__ __forceinline__ bool mbar_wait_addr(uint32_t bar, uint32_t parity, vo
   }
   return true;
 }
-// For copies and MMAs that a block has in flight when it leaves: waits for their barrier whatever the abort flag says,
-// until `until` (of globaltimer) at the latest.  A second is far more than any of them takes.
+// Waits for the last `ring` of the `turns` that went through a ring of barriers, so that nothing is in flight towards
+// this CTA's shared memory or TMEM when it leaves, whatever its abort flag says; a second at most, far more than a copy
+// or an MMA takes.  Where every wait came through, the threads that use the data wait for the same.
 constexpr uint64_t kDrainNs = 1000000000ull;
-__device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity, uint64_t until) {
-  while (!mbar_try_wait_addr(bar, parity))
-    if (globaltimer() > until) return;
+__device__ __forceinline__ void drain_ring(uint32_t bars, uint32_t turns, uint32_t ring) {
+  const uint64_t t0 = globaltimer();
+#pragma unroll 1
+  for (uint32_t i = turns > ring ? turns - ring : 0; i < turns; ++i)
+    while (!mbar_try_wait_addr(bars + i % ring * 8, i / ring & 1))
+      if (globaltimer() - t0 > kDrainNs) return;
 }
 __device__ __forceinline__ void mbar_arrive_addr(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");

@@ -58,6 +58,7 @@ class World:
         self.abort = [False] * blocks      # the blocks' abort flags
         self.flight = []                   # loads on their way: functions that land them
         self.queue = []                    # MMAs and commits, in order
+        self.pace = rng.choice([0.01, 0.1, 0.25])   # how fast loads and MMAs are beside the actors
         self.wrong, self.nan, self.right = 0, 0, 0
 
     def store(self, ok, value_right):
@@ -76,11 +77,11 @@ class World:
         idle = 0
         while todo:
             r = self.rng.random()
-            if r < 0.25 and self.flight:
+            if r < self.pace and self.flight:
                 self.flight.pop(self.rng.randrange(len(self.flight)))()
                 idle = 0
                 continue
-            if r < 0.5 and self.queue:
+            if self.pace <= r < 2 * self.pace and self.queue:
                 self.queue.pop(0)()
                 idle = 0
                 continue
@@ -343,8 +344,7 @@ def norm_ring(w, rows, stages, warps=3):
     def worker(k):
         ring, ok, turn = Ring(stages, 0), True, 0
         for row in range(rows):
-            if ok or "stale" in w.old:
-                ok = (yield (0, full[ring.at], ring.parity)) and ok
+            ok = (yield (0, full[ring.at], ring.parity)) and ok
             row_right[row] &= stage[ring.at] == row
             if ok or "stale" in w.old:
                 empty[ring.at].arrive()
@@ -393,9 +393,13 @@ def test_norm_ring_ends_and_is_right(stages):
 
 
 @pytest.mark.parametrize("stages", [3, 5, 8])
-def test_norm_ring_stores_nan_or_the_right_rows(stages):
-    wrong, nan, right, _ = norm_with_waits_that_run_out(stages, ("leave",), 300, 7)
-    assert nan > 0 and right > 0 and wrong == 0
+def test_norm_ring_stores_nan_or_the_right_rows_and_leaves_nothing_in_flight(stages):
+    wrong, nan, right, left = norm_with_waits_that_run_out(stages, (), 300, 7)
+    assert nan > 0 and right > 0 and wrong == 0 and left == 0
+
+
+def test_a_norm_producer_that_just_leaves_has_copies_in_flight():
+    assert norm_with_waits_that_run_out(8, ("leave",), 600, 9)[3] > 0
 
 
 def test_norm_ring_that_skips_rows_leaves_old_values():
