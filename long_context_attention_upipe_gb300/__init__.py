@@ -559,6 +559,8 @@ def rope(desc: RopeDesc, q, k, positions, q_out, k_out, inverse=False, stream=No
     any head and token strides; positions int32 [n_axes, tokens].  inverse: the backward pass."""
     if q.dim() != 3:
         _refuse(f"rope: q of [heads, tokens, head_dim] expected, got {tuple(q.shape)}")
+    if q_out is None or (k is not None and k_out is None):
+        _refuse("rope: an output for q, and for k where it is given, expected")
     dev = _on(q, "q")
     tokens, head_dim = q.shape[1], desc.head_dim
     qt = _rope_tensor(q, q_out, dev, head_dim, tokens, "q")
