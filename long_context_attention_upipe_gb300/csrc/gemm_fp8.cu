@@ -696,9 +696,11 @@ cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t st) {
   // The modelled clocks of both kernels.  Tile kernel: the column width whose rounds over all clusters take the
   // least; a block of K takes about 130 + 90 NCH (510 measured at 128 columns, 570 at 160, 850 at 256, each with
   // its share of a tile's ends), a tile's output about 200 NCH.  Tokens on the columns: about 1000 for a block of
-  // K.  Measured on both sides (us, tile kernel / tokens on the columns): 100 x 1024 x 4096 10.4 / 7.6, 128 x 4096 x
-  // 4096 11.4 / 10.6, 128 x 5120 x 8192 18.1 / 16.4; 128 x 28672 x 4096 27.7 / 36.8, 200 x 6144 x 4096 11.8 / 17.9,
-  // 256 x 5120 x 8192 18.2 / 34.7.
+  // K, and about 12500 for the ends and the output of every round of CTAs, which is not persistent.  Measured on both
+  // sides (us, tile kernel / tokens on the columns): 100 x 1024 x 4096 10.4 / 7.6, 128 x 4096 x 4096 11.4 / 10.6,
+  // 128 x 5120 x 8192 18.1 / 16.4; 128 x 28672 x 4096 27.7 / 36.8, 200 x 6144 x 4096 11.8 / 17.9, 256 x 5120 x 8192
+  // 18.2 / 34.7; one or two blocks of K: 8192 x 28672 x 128 105 / 518, 4096 x 4096 x 128 11.8 / 39.3, 8192 x 28672 x 256
+  // 123 / 567, 128 x 28672 x 256 9.4 / 12.6, 1000 x 512 x 128 and 1024 x 1024 x 256 8.5 / 8.5.
   const int64_t clusters = sm_count() / 2, tm = ceil_div(a.M, 256);
   int best = 8;
   int64_t cost = INT64_MAX;
@@ -709,7 +711,7 @@ cudaError_t launch_gemm_fp8(const Fp8GemmArgs& a, cudaStream_t st) {
   }
   const int64_t ctas = ceil_div(a.N, 128) * ceil_div(a.M, 128);
   const int splits = swap_splits(ctas, p.nkb, 128);
-  if (ceil_div(a.M, 128) <= 65535 && 12500 + ceil_div(ctas * splits, sm_count()) * ceil_div(p.nkb, splits) * 1000 < 8000 + cost)
+  if (ceil_div(a.M, 128) <= 65535 && ceil_div(ctas * splits, sm_count()) * (12500 + ceil_div(p.nkb, splits) * 1000) < 8000 + cost)
     return run_swap<128>(a, p, st);
   switch (best) {
     case 4: return run_tile<4>(a, p, st);

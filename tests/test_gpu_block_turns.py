@@ -37,7 +37,7 @@ def kernel_of(M, N, K, sms):
     cost, best = min((cdiv(tm * cdiv(N, 32 * c), clusters) * (nkb * (130 + 90 * c) + 200 * c), -c) for c in range(4, 9))
     ctas = cdiv(N, 128) * cdiv(M, 128)
     s = splits(ctas, nkb, 128, sms)
-    if cdiv(M, 128) <= 65535 and 12500 + cdiv(ctas * s, sms) * cdiv(nkb, s) * 1000 < 8000 + cost:
+    if cdiv(M, 128) <= 65535 and cdiv(ctas * s, sms) * (12500 + cdiv(nkb, s) * 1000) < 8000 + cost:
         return "few", 128, s
     return "pair", -best, tm * cdiv(N, -32 * best) / clusters
 
@@ -76,6 +76,23 @@ def test_product_of_few_rows_reaches_every_number_of_shares():
         up.gemm_fp8_nt(A, sa, B, sb, C)
         check_gemm(C, A, sa, B, sb)
     assert seen >= {1, 2, 3, 4, 5, 6, 8}
+
+
+def test_product_of_one_block_of_k_takes_no_longer_than_of_two():
+    """By the kernel of few rows it took four times as long."""
+    def us(K):
+        A, sa, B, sb = fp8_operands(gen(K), 8192, 14336, K)
+        C = nan_like((8192, 14336), torch.bfloat16)
+        start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        for i in range(13):
+            if i == 3:
+                start.record()
+            up.gemm_fp8_nt(A, sa, B, sb, C)
+        end.record()
+        torch.cuda.synchronize()
+        check_gemm(C[-300:], A.view(torch.uint8)[-300:].view(A.dtype), sa[:, -300:], B, sb)
+        return start.elapsed_time(end)
+    assert us(128) < 2 * us(256)
 
 
 def test_tiled_product_offsets_past_32_bits():
