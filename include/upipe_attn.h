@@ -468,8 +468,9 @@ upipe_status_t upipe_attn_gemm_fp8_nt(int64_t M, int64_t N, int64_t K, const uin
 /* Rotary positions with several axes, between the projection and the attention core.  Rotary pair j of
  * every head's row turns by  t = position[axis[j]][token] * inv_freq[j]:
  *   (a, b) -> (a cos t - b sin t, b cos t + a sin t)
- * The angle is reduced exactly, so positions up to +-2^31 lose nothing.  `inverse` turns by -t, which is
- * the backward pass (dQ, dK back to the gradient of the projection).
+ * The angle is reduced in integers: it is off by at most 2^-26 of a turn, plus 2^-52 of the turns that it makes,
+ * for any int32 position.  `inverse` turns by -t, which is the backward pass (dQ, dK back to the gradient of the
+ * projection).
  *   head_dim    multiple of 16, at most 256
  *   rotary_dim  R, a multiple of 16, at most head_dim: the row's first R elements; the rest is copied
  *   n_axes      1 .. 4 rows of positions (1: text; 2: height, width; 3: time, height, width)
@@ -499,9 +500,11 @@ upipe_status_t upipe_attn_rope(const upipe_rope_desc_t* desc, int64_t tokens, co
 
 /* Global norm of many gradient tensors and clipping by it:
  *   norm = sqrt(sum over all tensors of g^2),   out = g * min(1, max_norm / (norm + 1e-6))
- * A norm that is not finite (an infinity or NaN among the gradients) scales nothing: read it and skip
- * the step.  max_norm may be infinity (the norm alone).  The norm depends on the tensors and their order
- * alone (no atomics); values whose squares leave fp32's range count in full.
+ * An infinity or NaN among the gradients makes the norm infinite or NaN and scales nothing: read the norm and
+ * skip the step.  Finite gradients whose norm is past fp32 are scaled by the right factor, although the norm
+ * reads as infinity then: a step that is skipped for it must not use gradients scaled in place.  max_norm may be
+ * infinity (the norm alone).  The norm depends on the tensors and their order alone (no atomics); values whose
+ * squares leave fp32's range count in full.
  *   grad   device, n elements of grad_dtype (0: fp32, 1: bf16); NULL only where n is 0
  *   out    NULL: grad is scaled in place (not written where the factor is 1); else device, n elements of
  *          out_dtype, and grad is left as it is
@@ -537,7 +540,8 @@ upipe_status_t upipe_attn_no_alloc_device_status(int32_t* code, void* stream);
 /* Per-launch timing of the layer's kernels, a diagnostic with no counterpart on the pages (the
  * pages point to a profiler to find where memory and time go: podcast summary, chapter
  * "PyTorch profiler").  While enabled, every kernel launch of upipe_attn_fwd / upipe_attn_bwd
- * (and their offloaded forms), upipe_mlp_fwd / upipe_mlp_bwd and the ring steps is
+ * (and their offloaded forms), upipe_mlp_fwd / upipe_mlp_bwd and the ring steps (not of the operators around
+ * the two blocks) is
  * bracketed by two CUDA events on the call's stream and logged with its kind and shape; do not
  * enable it while a stream is being captured into a CUDA graph.  Process-wide; off by default.
  *   kind      UPIPE_K_* below
@@ -589,7 +593,8 @@ upipe_status_t upipe_attn_set_dkdv_window(int32_t items);
 /* Limit of every bounded device-side wait of the library's kernels, in nanoseconds (0 restores the
  * default of 4 s; at most 60 s).  Each kernel receives the value in effect when it is launched.
  * When a wait runs out, the kernel raises UPIPE_ERR_DEVICE_TIMEOUT in the error word of its
- * workspace or table and returns instead of hanging.  A diagnostic with no counterpart on the
+ * workspace or table (the operators around the two blocks, which have none, leave NaN) and returns instead of
+ * hanging.  A diagnostic with no counterpart on the
  * pages: shorter limits are for testing the timeout path with upipe_attn_wait_probe. */
 upipe_status_t upipe_attn_set_wait_limit_ns(uint64_t ns);
 

@@ -525,7 +525,8 @@ def _rows(t, dev, shape, what):
 
 def gemm_fp8_nt(A, a_scale, B, b_scale, C, stream=None):
     """C [M, N] (bf16 or fp32) = A [M, K] B [N, K]^T, e4m3 with a_scale fp32 [ceil(K / 128), M] and b_scale
-    fp32 [ceil(N / 128), ceil(K / 128)] (upipe_attn_gemm_fp8_nt).  A, B, C and a_scale may be row slices."""
+    fp32 [ceil(N / 128), ceil(K / 128)] (upipe_attn_gemm_fp8_nt).  A, B, C and a_scale may be slices of rows and
+    columns that start on 16 bytes (a_scale: at a multiple of four rows of A)."""
     if A.dim() != 2 or B.dim() != 2 or A.dtype != _E4M3 or B.dtype != _E4M3 or a_scale.dtype != _F32:
         _refuse(f"gemm_fp8_nt: e4m3 matrices with fp32 scales expected, got {A.dtype}, {B.dtype}, {a_scale.dtype}")
     if C.dtype != _BF16 and C.dtype != _F32:

@@ -349,8 +349,10 @@ cudaError_t run_swap(const Fp8GemmArgs& a, const Fp8Params& p, cudaStream_t st) 
 // spills, 30%).  An MMA per CTA with the columns multicast to both frees its accumulators without the other CTA,
 // but writes half as many bytes again to shared memory: 5% slower.  C leaves by TMA from small boxes: a tile's
 // output took 3300 clocks with 16-byte stores, of which 2300 were instructions, and cost 3 to 4% more in all.
-// us at 1000 x 5120 x 8192 / 8192 x 28672 x 4096: one commit and short loops 46.8 -> 42.7 / 735 -> 703, C by TMA ->
-// 40.4 / 684 (with three boxes of 16 columns and a sixth stage 3% more), shared addressing -> 38 / 662 (2900 TFLOP/s).
+// us at 1000 x 5120 x 8192 / 8192 x 28672 x 4096, each step beside the last on a GPU that was not at its power limit:
+// one commit and short loops 46.8 -> 42.7 / 735 -> 703, C by TMA -> 40.4 / 684 (with three boxes of 16 columns and a
+// sixth stage 3% more), shared addressing -> 38 / 662.  The large size runs at the limit after some seconds (1760 of
+// 2070 MHz) and takes 730 to 750 then, 2560 to 2640 TFLOP/s; the other 40 to 41 with cold operands.
 // Sixteen scaling warps of a quarter of the columns each: 763.  Tokens on the columns, the kernel above: 171 / 2550 us.
 constexpr int kTileThreads = 384;
 constexpr int kScSlots = 2, kScGroup = 8;  // ring of scales: groups of eight blocks of K

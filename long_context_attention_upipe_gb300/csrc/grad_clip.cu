@@ -14,7 +14,9 @@
 // Bound by HBM: reading twice and writing once, less what the second launch still finds in L2; it walks
 // the chunks backwards, so that what was read last is read first.  Only the last 64 MB of the first launch are
 // left in L2; everything else is marked to leave it first, stores and second reads too (872 MB of fp32 gradients
-// into bf16: 332 us, all left to L2 340 us, nothing 330 us; 361 MB into fp32: 172, 181, 181 us).
+// into bf16: 332 us, all left to L2 340 us, nothing 330 us; 361 MB into fp32: 172, 181, 181 us).  The 64 MB are
+// counted as fp32 elements and for each list of tensors: 32 MB of bf16 gradients, and of many lists every one's last,
+// of which the second pass finds only the last list's.
 #include "common.cuh"
 #include "internal.h"
 
@@ -27,7 +29,7 @@ constexpr int kPer = 16;                     // elements of a thread and step
 constexpr int kStep = kClipThreads * kPer;   // 4096
 constexpr int kFewTensors = 24, kSomeTensors = 120, kManyTensors = 960;  // tensors of one launch (its parameters hold the list)
 constexpr int kClipBlocksPerSm = 4;
-constexpr int64_t kKeepBytes = 64 << 20;  // of gradients left in L2 (129 MB) for the second launch
+constexpr int64_t kKeepBytes = 64 << 20;  // of fp32 gradients left in L2 (129 MB) for the second launch
 
 struct ClipEntry {
   const void* g;
@@ -186,7 +188,8 @@ __global__ void __launch_bounds__(kClipThreads, kClipBlocksPerSm) k_clip_scale(c
   for (int i = threadIdx.x; i < n_part; i += kClipThreads) total += part[i];
   const double norm = sqrt(block_sum(total));
   if (norm_out && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
-  // a norm that is not finite scales nothing: the caller sees it and skips the step
+  // gradients that hold an infinity or NaN are not scaled: the caller sees it in the norm and skips the step.  Finite
+  // ones are, even where their norm is past fp32 and is returned as infinity.
   float coef = 1.f;
   if (norm <= 1.7976931348623157e308) coef = (float)fmin(1.0, (double)max_norm / (norm + 1e-6));
   if (coef == 1.f && l.in_place) return;

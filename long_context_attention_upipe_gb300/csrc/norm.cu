@@ -463,7 +463,7 @@ __global__ void __launch_bounds__(V == 2 ? 512 : 544, 1) k_rms_bwd_ring(NormShap
 
 // The same for rows of more than 16384 columns (1024 threads at 64 registers), whose vectors do not fit into
 // registers beside the sums of dw: the row is read twice, the second time from L1 or L2 (3.9 TB/s at d 32768,
-// where spilled registers left 1.5; at d 16384 the kernel above runs at 4.8, this one at 4.3).
+// where spilled registers left 1.5; at d 16384 the kernel above runs at 6.3, this one at 4.3).
 __global__ void __launch_bounds__(kMaxNormThreads, 1) k_rms_bwd_long(NormShape n, const bf16* dy, const bf16* h,
                                                                      const bf16* __restrict__ w,
                                                                      const float* __restrict__ rstd_in, const bf16* dres,

@@ -4,11 +4,12 @@
 //   (a, b) -> (a cos t - b sin t, b cos t + a sin t),   t = position[axis(j)] * inv_freq(j)
 // for the rotary pairs j of every head's row: elements (j, j + R/2), or (2j, 2j + 1).
 //
-// The angle is reduced exactly.  The host turns inv_freq / 2 pi into a 64-bit fraction of a turn, so
+// The angle is reduced in integers.  The host turns inv_freq / 2 pi into a 64-bit fraction of a turn, so
 // position * fraction modulo 2^64 is one integer product whose high half is the angle within its
-// turn, however far the position: the error is that of the 53-bit frequency (2^-33 of a turn at five
-// million), where an fp32 product of the same position would be off by whole radians.  The fraction's
-// high 32 bits become x in [-1, 1), the angle over pi, for sincospif.
+// turn, however far the position.  Its high 32 bits become x in [-1, 1), the angle over pi, for sincospif.  The
+// angle is off by at most 2^-26 of a turn (x in fp32) plus 2^-52 of the turns made (the 53-bit frequency: 2^-23 of a
+// turn at position 2^31 and a radian per position), where an fp32 product of a position of five million
+// would be off by whole radians.
 //
 // A thread owns 16 elements of a row (8 pairs, two 16-byte vectors) of one token and walks over heads:
 // the sines and cosines, which all heads of a token share, are computed once.  Rows are read and
@@ -36,7 +37,6 @@ struct RopeParams {
   int units, rot_units;  // 16-element units of a row, and those of them that are rotated
   int half;              // rotary pairs
   int adjacent;
-  int n_axes;
   int heads_per_block;
   int64_t tokens;
   const int32_t* pos;    // [n_axes][tokens]
@@ -159,7 +159,6 @@ cudaError_t launch_rope(const RopeArgs& a, cudaStream_t st) {
   p.rot_units = a.rotary_dim / 16;
   p.half = a.rotary_dim / 2;
   p.adjacent = a.adjacent;
-  p.n_axes = a.n_axes;
   p.tokens = a.tokens;
   p.pos = a.pos;
   for (int j = 0; j < p.half; ++j) {
