@@ -521,6 +521,77 @@ upipe_status_t upipe_attn_grad_clip_workspace_size(int32_t count, size_t* bytes)
 upipe_status_t upipe_attn_grad_clip(const upipe_grad_tensor_t* tensors, int32_t count, float max_norm, float* norm,
                                     void* ws, size_t ws_bytes, void* stream);
 
+/* Paged cache of keys and values: what a generated token attends to.  A row is the key, or the value, of one
+ * token and KV head: head_dim elements.  Pages hold page_size tokens of every head and are handed out by the
+ * caller; position p of sequence b is row p % page_size of page pages[b * stride + p / page_size] of its table.
+ *   k, v       device, rows of bf16 (dtype 0) or e4m3 codes (dtype 1), [n_pages][n_kv_heads][page_size] in any
+ *              order of strides (in elements, whole 16 bytes), the same for both; the two may interleave
+ *   k_scale, v_scale  device fp32 with e4m3, else NULL: one scale for each row (a row reads code * scale),
+ *              through strides of their own
+ *   page_size  a multiple of 16;  n_kv_heads  at most 1024;  head_dim  64 or 128
+ * Strides of a single page or head do not count.  Rows do not overlap, nor do the tensors
+ * (UPIPE_ERR_INVALID_ARG). */
+typedef struct {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  int64_t n_pages;
+  int64_t page_stride, head_stride, token_stride;
+  int64_t scale_page_stride, scale_head_stride, scale_token_stride;
+  int32_t page_size, n_kv_heads, head_dim, dtype;
+} upipe_kv_cache_t;
+/* Page numbers of n_seqs sequences (at most 65536), device int32, rows of max_pages entries `stride` apart.
+ * Entries of positions that are not used may hold anything.  Tables, lengths, seq and pos need an alignment of
+ * 4 bytes only. */
+typedef struct {
+  const int32_t* pages;
+  int64_t stride;
+  int32_t n_seqs, max_pages;
+} upipe_page_table_t;
+
+/* Writes the keys and values of `tokens` tokens into the cache, token i at position pos[i] of sequence seq[i].
+ * With e4m3, scales and codes are those of upipe_attn_fp8_quantize, bit for bit, with one block for each row; a
+ * row that holds an infinity or NaN reads back as NaN.
+ *   seq, pos  device int32 [tokens], apart from the cache, as is the table.  A token of a negative seq (padding),
+ *             or whose place does not exist (no such sequence, past the table, a page number outside the cache),
+ *             is not written.  Two tokens of one call must not have the same place.
+ *   k, v      device bf16, heads and tokens through their strides (in elements, multiples of 8), as
+ *             upipe_attn_rope writes them or as the projection does; apart from the cache */
+upipe_status_t upipe_attn_kv_write(const upipe_kv_cache_t* cache, const upipe_page_table_t* table, int64_t tokens,
+                                   const int32_t* seq, const int32_t* pos, const uint16_t* k, int64_t k_head_stride,
+                                   int64_t k_token_stride, const uint16_t* v, int64_t v_head_stride, int64_t v_token_stride,
+                                   void* stream);
+
+/* Reads cached rows back, head by head as the attention core takes them or through any other strides: code * scale,
+ * rounded once to bf16 (bf16 rows as they are).
+ *   seq, pos  as above.  A token of a negative seq is left as it was; one whose place does not exist becomes NaN.
+ *   k, v      device bf16 (written), rows that overlap neither each other nor any input (UPIPE_ERR_INVALID_ARG,
+ *             also where the strides do not show it, as in upipe_attn_rope) */
+upipe_status_t upipe_attn_kv_read(const upipe_kv_cache_t* cache, const upipe_page_table_t* table, int64_t tokens,
+                                  const int32_t* seq, const int32_t* pos, uint16_t* k, int64_t k_head_stride,
+                                  int64_t k_token_stride, uint16_t* v, int64_t v_head_stride, int64_t v_token_stride,
+                                  void* stream);
+
+/* Attention of the q_len newest tokens of every sequence over its cached keys (theirs among them: write first).
+ * Query t of sequence b sees the keys j < lens[b] - q_len + 1 + t:
+ *   s_j = scale q . k_j,  lse = log sum_j exp s_j,  o = sum_j exp(s_j - lse) v_j
+ * fp32 sums, o rounded once; a row that sees no key gets o = 0 and lse = -infinity (an empty sequence, or fewer
+ * keys than q_len).  What a query does not see does not reach it, infinities and NaN included.
+ *   lens    device int32 [n_seqs]; the result depends on the device's values alone, so a captured call may be
+ *           replayed with other lengths, tables and pages.  Negative lengths count as 0.  Where a page number that
+ *           is needed lies outside the cache, or a length past the table, the rows that depend on it are NaN.
+ *   n_q_heads  a multiple of n_kv_heads, up to 128 for each;  q_len 1 .. 16;  softmax_scale 0: 1/sqrt(head_dim)
+ *   q, o    device bf16, [n_q_heads][n_seqs * q_len] rows, a sequence's tokens in order, through their strides (in
+ *           elements, multiples of 8); o (written) may lie beside q in one tensor, but not over it
+ *   lse     NULL, or device fp32 [n_q_heads][n_seqs * q_len] (written)
+ *   ws      device workspace of upipe_attn_decode_workspace_size bytes
+ * The order of all sums depends on sizes and lengths alone: equal calls give equal bits. */
+upipe_status_t upipe_attn_decode_workspace_size(const upipe_kv_cache_t* cache, int32_t n_seqs, int32_t n_q_heads, int32_t q_len,
+                                                size_t* bytes);
+upipe_status_t upipe_attn_decode(const upipe_kv_cache_t* cache, const upipe_page_table_t* table, const int32_t* lens,
+                                 int32_t n_q_heads, int32_t q_len, float softmax_scale, const uint16_t* q,
+                                 int64_t q_head_stride, int64_t q_token_stride, uint16_t* o, int64_t o_head_stride,
+                                 int64_t o_token_stride, float* lse, void* ws, size_t ws_bytes, void* stream);
+
 /* Reads the device error word of a workspace (after fwd/bwd) or of a table (after
  * build_tile_table) into *code (a upipe_status_t value; UPIPE_OK when none).  Synchronises
  * `stream`.  `buf` is the workspace or the table.  No counterpart on the pages. */

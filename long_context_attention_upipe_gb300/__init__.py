@@ -30,7 +30,8 @@ EXPORTS = ["upipe_attn_status_string", "upipe_attn_last_error_string", "upipe_at
            "upipe_mlp_bwd", "upipe_attn_ring_tables_size", "upipe_attn_ring_build_tables", "upipe_attn_ring_fwd_step",
            "upipe_attn_ring_bwd_step", "upipe_attn_ring_fwd", "upipe_attn_ring_bwd", "upipe_attn_rms_norm_fwd",
            "upipe_attn_rms_norm_workspace_size", "upipe_attn_rms_norm_bwd", "upipe_attn_fp8_quantize",
-           "upipe_attn_gemm_fp8_nt", "upipe_attn_rope", "upipe_attn_grad_clip_workspace_size", "upipe_attn_grad_clip"]
+           "upipe_attn_gemm_fp8_nt", "upipe_attn_rope", "upipe_attn_grad_clip_workspace_size", "upipe_attn_grad_clip",
+           "upipe_attn_kv_write", "upipe_attn_kv_read", "upipe_attn_decode_workspace_size", "upipe_attn_decode"]
 
 # kinds of the per-launch timing records (upipe_attn_timing_collect)
 KERNEL_KINDS = {0: "tile_table", 1: "qkv_proj", 2: "attn_fwd", 3: "o_proj", 4: "convert", 5: "do_proj",
@@ -116,6 +117,20 @@ class GradTensor(ctypes.Structure):
                 ("grad_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
 
 
+class KVCacheDesc(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("n_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("token_stride", ctypes.c_int64), ("scale_page_stride", ctypes.c_int64),
+                ("scale_head_stride", ctypes.c_int64), ("scale_token_stride", ctypes.c_int64),
+                ("page_size", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class PageTable(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_void_p), ("stride", ctypes.c_int64), ("n_seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)]
+
+
 class UpipeError(RuntimeError):
     def __init__(self, code, where):
         super().__init__(f"{where}: {STATUS.get(code, code)}")
@@ -184,6 +199,14 @@ def lib():
             "upipe_attn_grad_clip_workspace_size": ([ctypes.c_int32, ctypes.POINTER(SZ)], ctypes.c_int),
             "upipe_attn_grad_clip": ([ctypes.POINTER(GradTensor), ctypes.c_int32, ctypes.c_float, P, P, SZ, P],
                                      ctypes.c_int),
+            "upipe_attn_kv_write": ([ctypes.POINTER(KVCacheDesc), ctypes.POINTER(PageTable), I64, P, P, P, I64, I64, P, I64, I64,
+                                     P], ctypes.c_int),
+            "upipe_attn_kv_read": ([ctypes.POINTER(KVCacheDesc), ctypes.POINTER(PageTable), I64, P, P, P, I64, I64, P, I64, I64,
+                                    P], ctypes.c_int),
+            "upipe_attn_decode_workspace_size": ([ctypes.POINTER(KVCacheDesc), ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                                  ctypes.POINTER(SZ)], ctypes.c_int),
+            "upipe_attn_decode": ([ctypes.POINTER(KVCacheDesc), ctypes.POINTER(PageTable), P, ctypes.c_int32, ctypes.c_int32,
+                                   ctypes.c_float, P, I64, I64, P, I64, I64, P, P, SZ, P], ctypes.c_int),
             "upipe_attn_ring_fwd": ([ctypes.POINTER(RingDesc), P, P, P, P, P, P, P, P, P], ctypes.c_int),
             "upipe_attn_ring_bwd": ([ctypes.POINTER(RingDesc), P, P, P, P, P, P, P, P, P, P, P, P, P, P, P, P],
                                     ctypes.c_int),
@@ -608,6 +631,112 @@ class GradClip:
         if rc:
             _check(rc, "grad_clip")
         return self.norm
+
+
+# ------------------------------------------------------------------------------------------------
+# Paged cache of keys and values, and the attention that reads it
+# ------------------------------------------------------------------------------------------------
+
+def _strides(t):
+    return tuple(s if n > 1 else 0 for n, s in zip(t.shape, t.stride()))
+
+
+class KVCache:
+    """A paged cache over the caller's tensors: k, v [pages, n_kv_heads, page_size, head_dim], bf16, or e4m3 with
+    k_scale, v_scale fp32 [pages, n_kv_heads, page_size] (upipe_kv_cache_t).  Any strides with contiguous rows, the
+    same for k and v (of one layer of a larger tensor, token by token, the two interleaved, ...)."""
+
+    def __init__(self, k, v, k_scale=None, v_scale=None):
+        if k.dim() != 4 or k.dtype not in (_BF16, _E4M3):
+            _refuse(f"KVCache: k of [pages, heads, page_size, head_dim] in bf16 or e4m3 expected, got {k.dtype} {tuple(k.shape)}")
+        if (k_scale is not None) != (k.dtype == _E4M3) or (v_scale is not None) != (k.dtype == _E4M3):
+            _refuse("KVCache: scales expected with e4m3 codes, and only with them")
+        dev, shape = _on(k, "KVCache"), k.shape
+        if v.get_device() != dev or v.dtype != k.dtype or v.shape != shape or _strides(v) != _strides(k) or k.stride(3) != 1 or v.stride(3) != 1:
+            _refuse(f"KVCache: k and v of one type, shape and device, with the same strides and contiguous rows, expected, got "
+                    f"{k.dtype} {tuple(k.shape)} {k.stride()} on {k.device} and {v.dtype} {tuple(v.shape)} {v.stride()} on {v.device}")
+        st, ss = _strides(k), (0, 0, 0)
+        if k_scale is not None:
+            ss = _strides(k_scale)
+            for t in (k_scale, v_scale):
+                if t.get_device() != dev or t.dtype != _F32 or t.shape != shape[:3] or _strides(t) != ss:
+                    _refuse(f"KVCache: scales of fp32 {tuple(shape[:3])} with the same strides on device {dev} expected, got "
+                            f"{t.dtype} {tuple(t.shape)} {t.stride()} on {t.device}")
+        self.k, self.v, self.k_scale, self.v_scale, self.device_index = k, v, k_scale, v_scale, dev
+        self.n_kv_heads, self.page_size, self.head_dim = shape[1:]
+        self.desc = KVCacheDesc(k.data_ptr(), v.data_ptr(), None if k_scale is None else k_scale.data_ptr(),
+                                None if v_scale is None else v_scale.data_ptr(), shape[0], *st[:3], *ss, shape[2], shape[1],
+                                shape[3], int(k.dtype == _E4M3))
+
+
+def _page_table(t, dev):
+    if t.get_device() != dev or t.dtype != torch.int32 or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+        _refuse(f"page_table: int32 [sequences, pages] with contiguous rows on device {dev} expected, got {t.dtype} "
+                f"{tuple(t.shape)} {t.stride()} on {t.device}")
+    n, m = t.shape
+    return PageTable(t.data_ptr(), t.stride(0) if n > 1 else m, n, m)
+
+
+def _heads(t, dev, shape, what):
+    """Address, head stride and token stride of bf16 rows [heads, tokens, head_dim]."""
+    if t.get_device() != dev or t.dtype != _BF16 or t.shape != shape or t.stride(2) != 1:
+        _refuse(f"{what}: bf16 {tuple(shape)} with contiguous rows on device {dev} expected, got {t.dtype} {tuple(t.shape)} "
+                f"{t.stride()} on {t.device}")
+    return t.data_ptr(), t.stride(0), t.stride(1)
+
+
+def _kv_copy(f, where, cache, k, v, seq, pos, page_table, stream):
+    dev = _on(k, "k")
+    if dev != cache.device_index or seq.dim() != 1:
+        _refuse(f"{where}: a cache on device {dev} and seq of [tokens] expected, got {cache.k.device} and {tuple(seq.shape)}")
+    n = seq.shape[0]
+    shape = (cache.n_kv_heads, n, cache.head_dim)
+    rc = f(cache.desc, _page_table(page_table, dev), n, _dev(seq, dev, torch.int32, (n,), "seq"),
+           _dev(pos, dev, torch.int32, (n,), "pos"), *_heads(k, dev, shape, "k"), *_heads(v, dev, shape, "v"),
+           _raw_stream(stream, dev))
+    if rc:
+        _check(rc, where)
+
+
+def kv_write(cache: KVCache, k, v, seq, pos, page_table, stream=None):
+    """Writes keys and values, bf16 [n_kv_heads, tokens, head_dim] of any head and token strides, into the cache: token i
+    at position pos[i] of sequence seq[i] (int32 [tokens]; negative seq: padding, not written), found through
+    page_table int32 [sequences, pages] (upipe_attn_kv_write)."""
+    _kv_copy(lib().upipe_attn_kv_write, "kv_write", cache, k, v, seq, pos, page_table, stream)
+
+
+def kv_read(cache: KVCache, seq, pos, page_table, k, v, stream=None):
+    """The cached rows of the tokens (seq[i], pos[i]) into k, v, bf16 [n_kv_heads, tokens, head_dim] of any head and token
+    strides (upipe_attn_kv_read): rows of a negative seq stay, rows that the cache does not hold become NaN."""
+    _kv_copy(lib().upipe_attn_kv_read, "kv_read", cache, k, v, seq, pos, page_table, stream)
+
+
+def decode_workspace_bytes(cache: KVCache, n_seqs, n_q_heads, q_len=1) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().upipe_attn_decode_workspace_size(cache.desc, n_seqs, n_q_heads, q_len, ctypes.byref(n)), "decode_workspace_size")
+    return n.value
+
+
+def decode(cache: KVCache, q, page_table, lens, o, ws, lse=None, scale=0.0, stream=None):
+    """Attention of every sequence's newest tokens over its lens[b] cached keys (upipe_attn_decode): q, o bf16
+    [n_q_heads, sequences * q_len, head_dim] of any head and token strides, q_len newest tokens of each sequence in
+    order (query t sees the keys before lens[b] - q_len + 1 + t); lens int32 [sequences]; lse, optional, fp32
+    [n_q_heads, sequences * q_len]; ws uint8 of decode_workspace_bytes."""
+    dev = _on(q, "q")
+    if dev != cache.device_index or q.dim() != 3:
+        _refuse(f"decode: a cache on device {dev} and q of [heads, tokens, head_dim] expected, got {cache.k.device} and {tuple(q.shape)}")
+    table = _page_table(page_table, dev)
+    n, shape = table.n_seqs, q.shape
+    hq, tokens = shape[:2]
+    q_len = tokens // n if n else 1
+    if tokens != n * q_len or (n and not q_len) or shape[2] != cache.head_dim:
+        _refuse(f"decode: q of [heads, q_len * {n}, {cache.head_dim}] expected, got {tuple(shape)}")
+    rc = lib().upipe_attn_decode(
+        cache.desc, table, _dev(lens, dev, torch.int32, (n,), "lens"), hq, q_len, scale, *_heads(q, dev, shape, "q"),
+        *_heads(o, dev, shape, "o"), None if lse is None else _dev(lse, dev, _F32, (hq, tokens), "lse"),
+        _dev(ws, dev, torch.uint8, ws.shape, "ws"), ws.numel(), _raw_stream(stream, dev))
+    if rc:
+        _check(rc, "decode")
 
 
 # ------------------------------------------------------------------------------------------------

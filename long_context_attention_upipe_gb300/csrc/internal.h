@@ -315,4 +315,48 @@ size_t grad_clip_workspace(int count);
 cudaError_t launch_grad_clip(const GradTensor* t, const int* idx, int count, float max_norm, float* norm, double* part,
                              cudaStream_t st);
 
+// ---------------------------------------------------------------- paged cache of keys and values
+struct KvCache {
+  void *k, *v;              // rows of head_dim elements: bf16, or e4m3 with one scale each
+  float *k_scale, *v_scale;
+  int64_t page_stride, head_stride, token_stride;  // in elements
+  int64_t scale_page_stride, scale_head_stride, scale_token_stride;
+  int n_pages, page_size, n_kv_heads, head_dim, e4m3;
+};
+struct PageTable {
+  const int32_t* pages;  // [n_seqs] rows of max_pages, `stride` apart
+  int64_t stride;
+  int n_seqs, max_pages;
+};
+// Heads of new keys or values (bf16, written by launch_kv_read, read by launch_kv_write).
+struct KvHeads {
+  bf16* p;
+  int64_t head_stride, token_stride;
+};
+struct KvArgs {
+  KvCache c;
+  PageTable t;
+  KvHeads k, v;
+  int64_t tokens;
+  const int32_t *seq, *pos;  // device [tokens]
+};
+cudaError_t launch_kv_write(const KvArgs& a, cudaStream_t st);
+cudaError_t launch_kv_read(const KvArgs& a, cudaStream_t st);
+
+struct DecodeArgs {
+  KvCache c;
+  PageTable t;
+  const int32_t* lens;  // device [n_seqs]
+  int q_len, hq;
+  float scale;
+  const bf16* q;        // [hq][n_seqs * q_len] rows
+  int64_t q_head, q_tok;
+  bf16* o;
+  int64_t o_head, o_tok;
+  float* lse;           // [hq][n_seqs * q_len], or NULL
+  void* ws;
+};
+size_t decode_workspace(const DecodeArgs& a);
+cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t st);
+
 }  // namespace upipe

@@ -117,4 +117,19 @@ static __device__ __noinline__ uint2 quant8_divided(V8 f, float s) {
   return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
 }
 
+// e4m3 codes as fp32 (exact; NaN stays NaN).
+__device__ __forceinline__ float2 e4m3x2(uint16_t q) {
+  return __half22float2(__half2(__nv_cvt_fp8x2_to_halfraw2(q, __NV_E4M3)));
+}
+__device__ __forceinline__ V8 e4m3x8(const uint2& q) {
+  V8 f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 t = e4m3x2((uint16_t)((i < 2 ? q.x : q.y) >> (16 * (i & 1))));
+    f.v[2 * i] = t.x;
+    f.v[2 * i + 1] = t.y;
+  }
+  return f;
+}
+
 }  // namespace upipe
