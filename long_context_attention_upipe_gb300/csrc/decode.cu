@@ -31,12 +31,12 @@
 #include "internal.h"
 #include "kv_cache.cuh"
 #include "quant.cuh"
+#include "tc_common.cuh"
 
 namespace upipe {
 
 namespace {
 
-constexpr int kWarps = 8;
 constexpr int kTileKeys = 16;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.0e38f;  // a reference below all scores, whose difference to them is defined
@@ -51,31 +51,27 @@ struct RowSum {
 template <int D, bool FP8, int NT>
 struct Lay {
   static constexpr int ROWB = D * (FP8 ? 1 : 2);        // bytes of a cached row
-  static constexpr int KCH = ROWB / 64;                 // 16-byte pieces of a key that a lane holds (4 lanes to a key)
-  static constexpr int VB = ROWB / 8;                   // bytes of a value that a lane holds (8 lanes to a value)
-  static constexpr int VCH = VB > 16 ? VB / 16 : 1;     // ... in pieces of 16 (or one of 8)
-  static constexpr int VW = VB > 16 ? 16 : VB;
-  static constexpr int KBYTES = 16 * ROWB;
-  static constexpr int STAGE = 2 * KBYTES + (FP8 ? 128 : 0);  // keys, values, scales of a tile
+  static constexpr int SEG = ROWB > 128 ? 128 : ROWB;   // ... of which a box is so many wide: what a swizzle spans
+  static constexpr int SEGS = ROWB / SEG;
+  static constexpr int KBYTES = kTileKeys * ROWB;
+  static constexpr int STAGE = 2 * KBYTES;              // keys and values of a tile
+  static constexpr int SCALES = FP8 ? 128 : 0;          // their scales
   static constexpr int ROWS = 8 * NT;
   static constexpr int SLOT = ROWS * (D * 4 + (int)sizeof(RowSum));  // a piece
-  static constexpr int PER_WARP = 28800;                // of 227 KB
-  static constexpr int FIT = (PER_WARP - SLOT) / STAGE;
-  static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+  static constexpr int WARPS = 8;
+  static constexpr int FIT = (231 * 1024 / WARPS - SLOT - 128) / (STAGE + SCALES + 8);
+  static constexpr int STAGES = FIT > 6 ? 6 : FIT;
   static constexpr int QUEUE = STAGES * STAGE;
-  static constexpr int WARP = QUEUE + SLOT;
-  static constexpr int BYTES = kWarps * WARP + 256;
+  static constexpr int AT_SCALES = WARPS * QUEUE, AT_SLOTS = AT_SCALES + WARPS * STAGES * SCALES;
+  static constexpr int AT_BARS = AT_SLOTS + WARPS * SLOT, AT_INFO = AT_BARS + WARPS * STAGES * 8;
+  static constexpr int BYTES = AT_INFO + WARPS * 16 + 16 + 1024;  // the queues start on 1024 bytes
   static constexpr int MT = D / 16;                     // tiles of O^T
   static constexpr int KS = D / 16;                     // steps of S^T
-  static_assert(STAGES >= 2 && QUEUE >= SLOT && QUEUE * kWarps >= 2048 * 8, "shared memory");
+  static_assert(STAGES >= 2 && QUEUE >= SLOT && WARPS * QUEUE >= 2048 * 8 && BYTES <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_small(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -83,20 +79,38 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t at) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
-  return v;
+// A tile's box: 16 rows of a page and head, in SEGS halves of 128 bytes where a row is longer.
+template <int SEGS>
+__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar, int row, int head, int page) {
+  if (SEGS == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %2, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(head), "r"(page), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(head), "r"(page), "r"(bar)
+        : "memory");
 }
-__device__ __forceinline__ uint2 lds64(uint32_t at) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
-  return v;
+__device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
 __device__ __forceinline__ float lds32(uint32_t at) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
   return v;
+}
+// Four 8 x 8 matrices of 16-bit elements, a lane's address naming a row of one.
+__device__ __forceinline__ void ldm4(uint32_t (&w)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+}
+__device__ __forceinline__ void ldm4_trans(uint32_t (&w)[4], uint32_t at) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
 }
 
 template <bool FP8>
@@ -115,10 +129,10 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   return d;
 }
 
-__device__ __forceinline__ uint32_t e4m3_to_half2(uint32_t two) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(d) : "h"((uint16_t)two));
-  return d;
+// Four codes as two pairs of fp16.
+__device__ __forceinline__ void e4m3x4(uint32_t four, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(lo), "=r"(hi) : "r"(four));
 }
 __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   uint32_t d;
@@ -211,25 +225,45 @@ __device__ __noinline__ void redo(const DecodeArgs& a, int b, int hk, RowAt at, 
 
 __device__ __forceinline__ float row_lse(float m, float l) { return m * kLn2 + logf(l); }
 
+// Waits, a second at most, for copies that are on their way although a wait for them ran out.
+__device__ __forceinline__ void drain(uint32_t bars, uint32_t in_flight, uint32_t phases) {
+  if (!in_flight) return;
+  const uint64_t t0 = tc::globaltimer();
+  for (int i = 0; i < 8; ++i)
+    while ((in_flight >> i & 1) && !tc::mbar_try_wait_addr(bars + i * 8, phases >> i & 1))
+      if (tc::globaltimer() - t0 > tc::kDrainNs) return;
+}
+
+constexpr int kJoinThreads = 256;
+
 struct DecodeWs {
-  int4* meta;     // [row blocks][CTAs] items of the pieces that the CTA leaves: one that ends an item, one that does not, whether
-                  // the latter begins its item
+  int4* meta;     // [row blocks][CTAs] items of the pieces that the CTA leaves: x of one that ends an item, y of one that does
+                  // not; z whether the latter begins its item, w the CTA in which it ends
   RowSum* sums;   // [row blocks][CTAs][2][rows]
   float* acc;     // [row blocks][CTAs][2][rows][D]
 };
 
 template <int D, bool FP8, int NT>
-__global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant__ DecodeArgs a, const DecodeWs ws) {
+__global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
+    k_decode(const __grid_constant__ DecodeArgs a, const DecodeWs ws, const __grid_constant__ CUtensorMap map_k,
+             const __grid_constant__ CUtensorMap map_v, uint64_t wait_ns) {
   using L = Lay<D, FP8, NT>;
-  extern __shared__ __align__(128) uint8_t smem[];
+  constexpr int kWarps = L::WARPS;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
   const int X = gridDim.x, rb = blockIdx.y;
   const int hkv = a.c.n_kv_heads, g = a.hq / hkv, rows = g * a.q_len, cap = table_keys(a.t, a.c.page_size);
   const int n_seqs = a.t.n_seqs;
-  uint8_t* mine = smem + warp * L::WARP;
-  float* head_acc = reinterpret_cast<float*>(mine + L::QUEUE);  // the piece that ends the item the warp began within
-  float* tail_acc = reinterpret_cast<float*>(mine);             // the piece that is left at the end, over the empty queue
-  int2* info = reinterpret_cast<int2*>(smem + kWarps * L::WARP);  // [warp]: item of the head piece, 2 * item + begins of the tail
+  // pieces of this warp: the one that ends the item that it began within, and the one left at its end, over the empty queue
+  auto head_of = [&](int w) { return reinterpret_cast<float*>(smem + L::AT_SLOTS + w * L::SLOT); };
+  auto tail_of = [&](int w) { return reinterpret_cast<float*>(smem + w * L::QUEUE); };
+  int4* info = reinterpret_cast<int4*>(smem + L::AT_INFO);  // [warp]: item of the head piece, of the tail, tail begins, its last CTA
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::AT_INFO + kWarps * 16);
+  const uint32_t bars = smem_u32(smem + L::AT_BARS) + warp * L::STAGES * 8;
+  if (lane < L::STAGES) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + lane * 8) : "memory");
+  if (threadIdx.x == 0) *abort_flag = 0;
+  tc::fence_mbar_init();
   grid_dep_wait();
   grid_dep_trigger();  // the joining kernel may start when CTAs leave; it reads nothing of this one before it has ended
 
@@ -255,6 +289,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant
     first = t0 + (t1 - t0) * warp / kWarps;
     left = t0 + (t1 - t0) * (warp + 1) / kWarps - first;
   }
+  int64_t next = first + left;  // the tile after the part
   int b0 = 0, hk0 = 0, tile0 = 0;
   if (left > 0) {
     int64_t before = 0;
@@ -278,14 +313,12 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant
     hk0 = (int)min(max(rest / n, (int64_t)0), (int64_t)(hkv - 1));  // within bounds even if lengths change under the call
     tile0 = (int)min(max(rest - hk0 * n, (int64_t)0), n - 1);
   }
-  __syncthreads();  // the queues take the place of the sums
+  fence_async();    // the queues, which the copies fill, take the place of the sums
+  __syncthreads();
 
-  int2 left_over = make_int2(-1, -1);
+  int4 left_over = make_int4(-1, -1, 0, 0);
   if (left > 0) {
-    // ---- places of this lane's pieces of a tile, relative to the tile's first row
-    const int64_t es = FP8 ? 1 : 2, ts = a.c.token_stride * es;
-    const int64_t k_off = r * ts + c * 16, v_off = 2 * c * ts + r * L::VW;
-    const uint32_t queue = smem_u32(mine);
+    const uint32_t queue = smem_u32(smem) + warp * L::QUEUE, scale_queue = smem_u32(smem + L::AT_SCALES) + warp * L::STAGES * L::SCALES + lane * 4;
     const float* scales = FP8 ? (c < 2 ? a.c.k_scale : a.c.v_scale) : nullptr;
     const int s_key = r + 8 * (c & 1);  // the key whose scale this lane brings in: of K for c < 2, else of V
 
@@ -294,39 +327,24 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant
     int ppi = pt * kTileKeys / a.c.page_size, prow = pt * kTileKeys - ppi * a.c.page_size;
     int64_t to_load = left;
     int page = a.t.pages[(int64_t)pb * a.t.stride + ppi];
-    uint32_t missing = 0;  // stages whose page does not exist
+    uint32_t in_flight = 0;  // stages that a copy is on its way to; those of tiles whose page does not exist stay as they are
+    bool ok = true;          // no wait ran out
     auto load = [&](int stage) {
-      const uint32_t at = queue + stage * L::STAGE;
-      const int keys = plen - pt * kTileKeys;  // from 16 on: a whole tile
-      const bool ok = (unsigned)page < (unsigned)a.c.n_pages;
-      missing = ok ? missing & ~(1u << stage) : missing | (1u << stage);
-      const int64_t row = ok ? page * a.c.page_stride + phk * a.c.head_stride + prow * a.c.token_stride : 0;
-      const uint8_t* k = reinterpret_cast<const uint8_t*>(a.c.k) + row * es + (ok ? k_off : 0);
-      const uint8_t* v = reinterpret_cast<const uint8_t*>(a.c.v) + row * es + (ok ? v_off : 0);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {  // keys r and r + 8
-        const bool in = ok && r + 8 * i < keys;
-        const uint8_t* p = in ? k + i * 8 * ts : reinterpret_cast<const uint8_t*>(a.c.k);
-#pragma unroll
-        for (int j = 0; j < L::KCH; ++j) cp16(at + (i * L::KCH + j) * 512 + lane * 16, p + j * 64, in ? 16 : 0);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {  // values 2 c, 2 c + 1, 2 c + 8, 2 c + 9
-        const int key = (i & 1) + 8 * (i >> 1);
-        const bool in = ok && 2 * c + key < keys;
-        const uint8_t* p = in ? v + key * ts : reinterpret_cast<const uint8_t*>(a.c.v);
-#pragma unroll
-        for (int j = 0; j < L::VCH; ++j) {
-          const uint32_t dst = at + L::KBYTES + ((i * L::VCH + j) * 32 + lane) * L::VW;
-          if (L::VW == 16) cp16(dst, p + j * 128, in ? 16 : 0);
-          else cp_small<8>(dst, p, in ? 8 : 0);
+      const bool there = (unsigned)page < (unsigned)a.c.n_pages;
+      if (there) {
+        in_flight |= 1u << stage;
+        if (tc::elect_one()) {
+          const uint32_t at = queue + stage * L::STAGE, bar = bars + stage * 8;
+          expect_tx(bar, L::STAGE);
+          tma_tile<L::SEGS>(at, &map_k, bar, prow, phk, page);
+          tma_tile<L::SEGS>(at + L::KBYTES, &map_v, bar, prow, phk, page);
         }
-      }
-      if (FP8) {
-        const bool in = ok && s_key < keys;
-        const float* p = scales + (in ? page * a.c.scale_page_stride + phk * a.c.scale_head_stride +
-                                            (prow + s_key) * a.c.scale_token_stride : 0);
-        cp_small<4>(at + 2 * L::KBYTES + lane * 4, p, in ? 4 : 0);
+        if (FP8) {
+          const bool in = s_key < plen - pt * kTileKeys;
+          const float* p = scales + (in ? page * a.c.scale_page_stride + phk * a.c.scale_head_stride +
+                                              (prow + s_key) * a.c.scale_token_stride : 0);
+          cp4(scale_queue + stage * L::SCALES, p, in ? 4 : 0);
+        }
       }
       // on to the next tile; its page number is on the way when it is needed
       if (--to_load > 0) {
@@ -353,12 +371,20 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant
 #pragma unroll
     for (int s = 0; s < L::STAGES - 1; ++s) {
       if (to_load > 0) load(s);
-      cp_commit();
+      if (FP8) cp_commit();
     }
 
     // ---- the end that computes
+    // rows of the 8 x 8 matrices that this lane names: keys lane % 8 (+ 8 by bit 3 for K and e4m3's V, bit 4 for bf16's V), 16-byte
+    // pieces of them by the other bit, under the copies' swizzle
+    auto matrix_row = [&](bool key_bit3) {
+      const int key = (lane & 7) + ((key_bit3 ? lane : lane >> 1) & 8), piece = (key_bit3 ? lane >> 4 : lane >> 3) & 1;
+      return key * L::SEG + ((piece ^ (L::SEG == 128 ? key & 7 : (key >> 1) & 3)) << 4);
+    };
+    const uint32_t k_row = matrix_row(true), v_row = L::KBYTES + matrix_row(FP8);
     int cb = b0, chk = hk0, ct = tile0, raw = a.lens[b0], len = min(max(raw, 0), cap), cn = tiles_of(len, cap);
     int stage = 0;
+    uint32_t phases = 0;
     float m[NT][2], l[NT][2], mv[NT][2], acc[NT][L::MT][4], rs[NT][2];
     uint32_t q[NT][L::KS][2];
     int see[NT][2];  // a row sees keys before len + see
@@ -375,23 +401,19 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant
         const bf16* src = a.q + at.head * a.q_head + at.tok * a.q_tok;
         if (!FP8) {
 #pragma unroll
-          for (int j = 0; j < L::KS / 2; ++j) {
-            const uint4 w = R < rows ? *reinterpret_cast<const uint4*>(src + 32 * j + 8 * c) : make_uint4(0, 0, 0, 0);
-            q[nt][2 * j][0] = w.x;
-            q[nt][2 * j][1] = w.y;
-            q[nt][2 * j + 1][0] = w.z;
-            q[nt][2 * j + 1][1] = w.w;
-          }
+          for (int s = 0; s < L::KS; ++s)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) q[nt][s][i] = R < rows ? *reinterpret_cast<const uint32_t*>(src + 16 * s + 8 * i + 2 * c) : 0u;
           rs[nt][0] = rs[nt][1] = a.scale * kLog2e;
         } else {
           // fp16 under a power of two for each row: bf16's 8 bits fit, elements below 2^-14 of the largest lose what fp32 sums
-          // would lose
-          uint4 w[L::KS / 2];
+          // would lose.  A step's 16 elements go to lanes in fours, as the codes of a 16-byte piece do.
+          uint2 w[L::KS];
           uint32_t big = 0;
 #pragma unroll
-          for (int j = 0; j < L::KS / 2; ++j) {  // elements 64 (j / 2) + 16 c + 8 (j % 2) ..
-            w[j] = R < rows ? *reinterpret_cast<const uint4*>(src + 64 * (j >> 1) + 16 * c + 8 * (j & 1)) : make_uint4(0, 0, 0, 0);
-            big = amax2(big, amax2(w[j]));
+          for (int s = 0; s < L::KS; ++s) {
+            w[s] = R < rows ? *reinterpret_cast<const uint2*>(src + 16 * s + 4 * c) : make_uint2(0, 0);
+            big = amax2(big, amax2(w[s].x, w[s].y));
           }
           big = pair_bits(big);
           big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
@@ -399,12 +421,9 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant
           const int ex = min(max((int)(big >> 23) - 127, -126), 126);
           const float down = pow2(-ex), up = pow2(ex) * (a.scale * kLog2e);
 #pragma unroll
-          for (int j = 0; j < L::KS / 2; ++j) {
-            const V8 f = unpack8(w[j]);
-            q[nt][2 * j][0] = pack_half(f.v[0] * down, f.v[1] * down);
-            q[nt][2 * j][1] = pack_half(f.v[2] * down, f.v[3] * down);
-            q[nt][2 * j + 1][0] = pack_half(f.v[4] * down, f.v[5] * down);
-            q[nt][2 * j + 1][1] = pack_half(f.v[6] * down, f.v[7] * down);
+          for (int s = 0; s < L::KS; ++s) {
+            q[nt][s][0] = pack_half(__uint_as_float(w[s].x << 16) * down, __uint_as_float(w[s].x & 0xffff0000u) * down);
+            q[nt][s][1] = pack_half(__uint_as_float(w[s].y << 16) * down, __uint_as_float(w[s].y & 0xffff0000u) * down);
           }
           rs[nt][0] = __shfl_sync(0xffffffffu, up, 8 * c);
           rs[nt][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
@@ -423,11 +442,32 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant
 
       // ---- its tiles
       do {
+        __syncwarp();  // all lanes have read the stage that is loaded next
         const int ahead = stage + L::STAGES - 1;
-        if (to_load > 0) load(ahead >= L::STAGES ? ahead - L::STAGES : ahead);
-        cp_commit();
-        cp_wait<L::STAGES - 1>();
-        const uint32_t at = queue + stage * L::STAGE;
+        if (to_load > 0 && ok) load(ahead >= L::STAGES ? ahead - L::STAGES : ahead);
+        if (FP8) {
+          cp_commit();
+          cp_wait<L::STAGES - 1>();
+        }
+        const uint32_t at = queue + stage * L::STAGE, bit = 1u << stage;
+        bool lost = !(in_flight & bit);  // the page does not exist, or a wait ran out
+        if (!lost && ok) {
+          ok = __all_sync(0xffffffffu, tc::mbar_wait_addr(bars + stage * 8, (phases & bit) != 0, abort_flag, wait_ns));
+          if (ok) {
+            in_flight &= ~bit;
+            phases ^= bit;
+          }
+        }
+        lost |= !ok;
+        const int k0 = ct * kTileKeys;
+        if (len - k0 < kTileKeys) {  // rows behind the sequence's end may hold anything: the values' become zeros
+          for (int i = max(len - k0, 0) * (L::SEG / 16) + lane; i < kTileKeys * (L::SEG / 16); i += 32)
+#pragma unroll
+            for (int sg = 0; sg < L::SEGS; ++sg)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + L::KBYTES + sg * (kTileKeys * L::SEG) + i * 16), "r"(0) : "memory");
+          fence_async();  // a later copy may fill them
+          __syncwarp();
+        }
         float x[NT][4];
         {
           float s2[NT][4];
@@ -436,20 +476,21 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[nt][i] = s2[nt][i] = 0.f;
 #pragma unroll
-          for (int j = 0; j < L::KCH; ++j) {
-            const uint4 k0 = lds128(at + j * 512 + lane * 16), k1 = lds128(at + (L::KCH + j) * 512 + lane * 16);
-            const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w1[4] = {k1.x, k1.y, k1.z, k1.w};
+          for (int j = 0; j < L::ROWB / 32; ++j) {  // two 16-byte pieces: keys 0-7, 8-15 of the first, of the second
+            uint32_t w[4];
+            ldm4(w, (at + j * 32 / L::SEG * (kTileKeys * L::SEG) + k_row) ^ (j * 32 % L::SEG));
+            if (FP8) {
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              if (FP8) {
+              for (int i = 0; i < 2; ++i) {
+                uint32_t a0, a1, a2, a3;
+                e4m3x4(w[2 * i], a0, a2);
+                e4m3x4(w[2 * i + 1], a1, a3);
 #pragma unroll
-                for (int w = 0; w < 4; ++w)
-                  mma<FP8>(w & 1 ? s2[nt] : x[nt], e4m3_to_half2(w0[w]), e4m3_to_half2(w1[w]), e4m3_to_half2(w0[w] >> 16),
-                           e4m3_to_half2(w1[w] >> 16), q[nt][4 * j + w][0], q[nt][4 * j + w][1]);
-              } else {
-                mma<FP8>(x[nt], w0[0], w1[0], w0[1], w1[1], q[nt][2 * j][0], q[nt][2 * j][1]);
-                mma<FP8>(s2[nt], w0[2], w1[2], w0[3], w1[3], q[nt][2 * j + 1][0], q[nt][2 * j + 1][1]);
+                for (int nt = 0; nt < NT; ++nt) mma<FP8>(i ? s2[nt] : x[nt], a0, a1, a2, a3, q[nt][2 * j + i][0], q[nt][2 * j + i][1]);
               }
+            } else {
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma<FP8>(j & 1 ? s2[nt] : x[nt], w[0], w[1], w[2], w[3], q[nt][j][0], q[nt][j][1]);
             }
           }
 #pragma unroll
@@ -461,7 +502,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant
         float y[NT][4];
         float lv[2];
         if (FP8) {
-          const float sc = lds32(at + 2 * L::KBYTES + lane * 4), lg = fast_log2(sc);
+          const float sc = lds32(scale_queue + stage * L::SCALES), lg = fast_log2(sc);
           const float ks[2] = {__shfl_sync(0xffffffffu, sc, lane & 28), __shfl_sync(0xffffffffu, sc, (lane & 28) + 1)};
           lv[0] = __shfl_sync(0xffffffffu, lg, (lane & 28) + 2);
           lv[1] = __shfl_sync(0xffffffffu, lg, (lane & 28) + 3);
@@ -477,16 +518,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant
             x[nt][i] *= rs[nt][i & 1];
             if (FP8) y[nt][i] = x[nt][i] + lv[i >> 1];
           }
-        const int k0 = ct * kTileKeys;
-        if (k0 > len - a.q_len + 1 - kTileKeys || (missing >> stage & 1)) {
-          const float lost = missing >> stage & 1 ? __uint_as_float(0x7fffffffu) : 0.f;
+        if (k0 > len - a.q_len + 1 - kTileKeys || lost) {
+          const float nan = lost ? __uint_as_float(0x7fffffffu) : 0.f;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
               const bool in = k0 + r + 8 * (i >> 1) < len + see[nt][i & 1];
-              x[nt][i] = in ? x[nt][i] + lost : -INFINITY;
-              if (FP8) y[nt][i] = in ? y[nt][i] + lost : -INFINITY;
+              x[nt][i] = in ? x[nt][i] + nan : -INFINITY;
+              if (FP8) y[nt][i] = in ? y[nt][i] + nan : -INFINITY;
             }
         }
         bool raise = false;
@@ -541,43 +581,29 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant
             }
           }
         // ---- O^T += V^T P^T
+        if (FP8) {
 #pragma unroll
-        for (int j = 0; j < L::VCH; ++j) {
-          uint32_t w[4][4];
+          for (int j = 0; j < L::MT / 2; ++j) {  // pieces 2 j, 2 j + 1: pairs of elements by pairs of keys
+            uint32_t w[4];
+            ldm4_trans(w, (at + v_row) ^ (j * 32));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t src = at + L::KBYTES + ((i * L::VCH + j) * 32 + lane) * L::VW;
-            if (L::VW == 16) {
-              const uint4 t = lds128(src);
-              w[i][0] = t.x;
-              w[i][1] = t.y;
-              w[i][2] = t.z;
-              w[i][3] = t.w;
-            } else {
-              const uint2 t = lds64(src);
-              w[i][0] = t.x;
-              w[i][1] = t.y;
+            for (int i = 0; i < 2; ++i) {
+              uint32_t a0, a1, a2, a3;
+              e4m3x4(__byte_perm(w[2 * i], 0, 0x3120), a0, a1);
+              e4m3x4(__byte_perm(w[2 * i + 1], 0, 0x3120), a2, a3);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma<FP8>(acc[nt][2 * j + i], a0, a1, a2, a3, hi[nt][0], hi[nt][1]);
             }
           }
+        } else {
 #pragma unroll
-          for (int u = 0; u < L::VW / 4; ++u) {
-            if (FP8) {
+          for (int mt = 0; mt < L::MT; ++mt) {
+            uint32_t w[4];
+            ldm4_trans(w, (at + mt * 32 / L::SEG * (kTileKeys * L::SEG) + v_row) ^ (mt * 32 % L::SEG));
 #pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                const uint32_t x0 = __byte_perm(w[0][u], w[1][u], half ? 0x7362 : 0x5140);
-                const uint32_t x8 = __byte_perm(w[2][u], w[3][u], half ? 0x7362 : 0x5140);
-                const uint32_t a0 = e4m3_to_half2(x0), a1 = e4m3_to_half2(x0 >> 16), a2 = e4m3_to_half2(x8), a3 = e4m3_to_half2(x8 >> 16);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma<FP8>(acc[nt][2 * u + half], a0, a1, a2, a3, hi[nt][0], hi[nt][1]);
-              }
-            } else {
-              const uint32_t a0 = __byte_perm(w[0][u], w[1][u], 0x5410), a1 = __byte_perm(w[0][u], w[1][u], 0x7632);
-              const uint32_t a2 = __byte_perm(w[2][u], w[3][u], 0x5410), a3 = __byte_perm(w[2][u], w[3][u], 0x7632);
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                mma<FP8>(acc[nt][4 * j + u], a0, a1, a2, a3, hi[nt][0], hi[nt][1]);
-                mma<FP8>(acc[nt][4 * j + u], a0, a1, a2, a3, lo[nt][0], lo[nt][1]);
-              }
+            for (int nt = 0; nt < NT; ++nt) {
+              mma<FP8>(acc[nt][mt], w[0], w[1], w[2], w[3], hi[nt][0], hi[nt][1]);
+              mma<FP8>(acc[nt][mt], w[0], w[1], w[2], w[3], lo[nt][0], lo[nt][1]);
             }
           }
         }
@@ -588,15 +614,23 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant
 
       // ---- the piece ends: whole items are done, others wait in shared memory
       const bool begins = begin == 0, ends = ct == cn, whole = begins && ends;
-      float* slot = ends ? head_acc : tail_acc;
+      float* slot = ends ? head_of(warp) : tail_of(warp);
       RowSum* slot_sums = reinterpret_cast<RowSum*>(slot + L::ROWS * D);
-      if (!ends) cp_wait<0>();  // the queue is empty
       const int item = cb * hkv + chk;
-      if (!whole) (ends ? left_over.x : left_over.y) = ends ? item : 2 * item + begins;
+      if (!ends) {
+        drain(bars, in_flight, phases);
+        if (FP8) cp_wait<0>();
+        left_over.y = item;
+        left_over.z = begins;
+        left_over.w = (int)((max(next + cn - ct, next) * parts + total - 1) / total) - 1;  // the CTA whose part holds its last tile
+      } else if (!whole) {
+        left_over.x = item;
+      }
       __syncwarp();
       uint32_t again = 0;  // rows (8 nt + row) whose o has to be summed once more
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt) {
+        float inv[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           float sum = l[nt][e];
@@ -616,32 +650,50 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant
           for (int i = 0; i < 4; ++i)
             if (bad & (0x11111111u << i)) again |= 1u << (nt * 8 + 2 * i + e);
           if (raw > cap) sum = __uint_as_float(0x7fffffffu);
-          const float inv = 1.f / sum;
+          inv[e] = 1.f / sum;
           if (whole) {
-            if (R < rows) {
-              const bool none = len + see[nt][e] <= 0;
+            if (a.lse && r == 0 && R < rows) {
               const RowAt at = row_at(a, g, cb, chk, R);
-              bf16* o = a.o + at.head * a.o_head + at.tok * a.o_tok;
-#pragma unroll
-              for (int j = 0; j < L::MT / 4; ++j) {
-                uint32_t w[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  w[i] = none ? 0u : pack_bf16(acc[nt][4 * j + i][e] * inv, acc[nt][4 * j + i][e + 2] * inv);
-                *reinterpret_cast<uint4*>(o + (FP8 ? D / 8 * r + 8 * j : 64 * j + 8 * r)) = make_uint4(w[0], w[1], w[2], w[3]);
-              }
-              if (a.lse && r == 0) a.lse[at.head * n_seqs * a.q_len + at.tok] = none ? -INFINITY : row_lse(m[nt][e], sum);
+              a.lse[at.head * n_seqs * a.q_len + at.tok] = len + see[nt][e] <= 0 ? -INFINITY : row_lse(m[nt][e], sum);
             }
           } else {
 #pragma unroll
-            for (int j = 0; j < L::MT / 4; ++j) {
-              float4* dst = reinterpret_cast<float4*>(slot + row * D + (FP8 ? D / 8 * r + 8 * j : 64 * j + 8 * r));
-              dst[0] = make_float4(acc[nt][4 * j][e], acc[nt][4 * j][e + 2], acc[nt][4 * j + 1][e], acc[nt][4 * j + 1][e + 2]);
-              dst[1] = make_float4(acc[nt][4 * j + 2][e], acc[nt][4 * j + 2][e + 2], acc[nt][4 * j + 3][e], acc[nt][4 * j + 3][e + 2]);
+            for (int mt = 0; mt < L::MT; ++mt) {
+              float* dst = slot + row * D + 16 * mt;
+              if (FP8) {
+                *reinterpret_cast<float2*>(dst + 2 * r) = make_float2(acc[nt][mt][e], acc[nt][mt][e + 2]);
+              } else {
+                dst[r] = acc[nt][mt][e];
+                dst[r + 8] = acc[nt][mt][e + 2];
+              }
             }
             if (r == 0) slot_sums[row] = RowSum{m[nt][e], sum};
           }
         }
+        if (whole) {  // a lane gets neighbouring elements of one row: of row r by a transposition, of rows 2 c, 2 c + 1 with e4m3
+#pragma unroll
+          for (int e = 0; e < (FP8 ? 2 : 1); ++e) {
+            const int R = rb * L::ROWS + nt * 8 + (FP8 ? 2 * c + e : r);
+            const RowAt at = row_at(a, g, cb, chk, min(R, rows - 1));
+            const bool none = len - a.q_len + 1 + min(R, rows - 1) / g <= 0;
+            bf16* o = a.o + at.head * a.o_head + at.tok * a.o_tok;
+#pragma unroll
+            for (int mt = 0; mt < L::MT; ++mt) {
+              if (FP8) {
+                const uint32_t w = pack_bf16(acc[nt][mt][e] * inv[e], acc[nt][mt][e + 2] * inv[e]);
+                if (R < rows) *reinterpret_cast<uint32_t*>(o + 16 * mt + 2 * r) = none ? 0u : w;
+              } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  const uint32_t w = transpose8(pack_bf16(acc[nt][mt][2 * i] * inv[0], acc[nt][mt][2 * i + 1] * inv[1]));
+                  if (R < rows) *reinterpret_cast<uint32_t*>(o + 16 * mt + 8 * i + 2 * c) = none ? 0u : w;
+                }
+              }
+            }
+          }
+        }
+      }
+      __syncwarp();
       if (again) {
         constexpr int E = D / 32;
 #pragma unroll
@@ -686,7 +738,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant
         }
       }
     }
-    cp_wait<0>();
+    drain(bars, in_flight, phases);
+    if (FP8) cp_wait<0>();
   }
 
   // ---- the CTA's pieces, in order: runs of one item are joined
@@ -696,13 +749,13 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant
   int p = 0;  // pieces: 2 warp (head), 2 warp + 1 (tail)
   const int64_t place = (int64_t)rb * X + blockIdx.x;
   while (p < 2 * kWarps) {
-    auto item_of = [&](int i) { return i & 1 ? (info[i >> 1].y < 0 ? -1 : info[i >> 1].y >> 1) : info[i >> 1].x; };
+    auto item_of = [&](int i) { return i & 1 ? info[i >> 1].y : info[i >> 1].x; };
     const int item = item_of(p);
     if (item < 0) {
       ++p;
       continue;
     }
-    const bool begins = (p & 1) && (info[p >> 1].y & 1);
+    const bool begins = (p & 1) && info[p >> 1].z;
     int end = p + 1, last = p;
     for (; end < 2 * kWarps; ++end) {
       const int it = item_of(end);
@@ -719,9 +772,8 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant
       const int R = rb * L::ROWS + row;
       constexpr int E = D / 32;
       float top = kLowest;
-      auto sums_of = [&](int i) {
-        return reinterpret_cast<const RowSum*>(smem + (i >> 1) * L::WARP + (i & 1 ? 0 : L::QUEUE) + L::ROWS * D * 4)[row];
-      };
+      auto piece = [&](int i) { return i & 1 ? tail_of(i >> 1) : head_of(i >> 1); };
+      auto sums_of = [&](int i) { return reinterpret_cast<const RowSum*>(piece(i) + L::ROWS * D)[row]; };
       for (int i = p; i <= last; ++i)
         if (item_of(i) == item) top = fmaxf(top, sums_of(i).m);
       float sum = 0.f, o[E] = {};
@@ -730,7 +782,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant
         const RowSum s = sums_of(i);
         const float f = fast_exp2(s.m - top);
         sum += s.l * f;
-        const float* src = reinterpret_cast<const float*>(smem + (i >> 1) * L::WARP + (i & 1 ? 0 : L::QUEUE)) + row * D + lane * E;
+        const float* src = piece(i) + row * D + lane * E;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] += src[e] * f;
       }
@@ -755,6 +807,7 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant
       else {
         meta.y = item;
         meta.z = begins;
+        meta.w = info[last >> 1].w;
       }
     }
     p = end;
@@ -765,17 +818,15 @@ __global__ void __launch_bounds__(32 * kWarps, 1) k_decode(const __grid_constant
 // Joins what an item left in several CTAs, in order; one block for each CTA in which an item begins that goes on, and each row.
 // Sequences without keys get their zeros here.
 template <int D>
-__global__ void __launch_bounds__(128) k_decode_join(const __grid_constant__ DecodeArgs a, const DecodeWs ws, int block_rows) {
-  constexpr int E = 4, LN = D / E, GR = 128 / LN;
-  __shared__ float weight[1024];
+__global__ void __launch_bounds__(kJoinThreads) k_decode_join(const __grid_constant__ DecodeArgs a, const DecodeWs ws, int block_rows) {
+  constexpr int LN = D / 4, GR = kJoinThreads / LN, AHEAD = 8;  // lanes of a row, groups that share the pieces, pieces in flight
   __shared__ float4 part[GR][LN];
-  __shared__ float red[4];
-  __shared__ int stop;
+  __shared__ RowSum part_sums[GR];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, x = blockIdx.x, X = gridDim.x;
   const int hkv = a.c.n_kv_heads, g = a.hq / hkv, R = blockIdx.y, rb = R / block_rows, row = R - rb * block_rows, n_seqs = a.t.n_seqs;
   const int cap = table_keys(a.t, a.c.page_size);
   // lengths were there before the kernel that this one follows began
-  for (int base = (x * 4 + warp) * 32; base < n_seqs; base += X * 128) {
+  for (int base = (x * (kJoinThreads / 32) + warp) * 32; base < n_seqs; base += X * kJoinThreads) {
     const int b = base + lane, len = b < n_seqs ? a.lens[b] : 1;
     unsigned none = __ballot_sync(0xffffffffu, b < n_seqs && tiles_of(len, cap) == 0);
     while (none) {
@@ -791,65 +842,60 @@ __global__ void __launch_bounds__(128) k_decode_join(const __grid_constant__ Dec
     }
   }
   grid_dep_wait();
-  const int4* meta = ws.meta + (int64_t)rb * X;
-  const int4 me = meta[x];
+  const int64_t place = (int64_t)rb * X + x;
+  const int4 me = ws.meta[place];
   if (me.y < 0 || !me.z) return;
-  const int item = me.y;
-  if (tid == 0) stop = -1;
-  __syncthreads();
-  for (int j = x + 1 + tid; j < X; j += 128)
-    if (meta[j].x == item) stop = j;  // one CTA ends it
-  __syncthreads();
-  const int n = stop - x + 1;
-  if (stop < 0 || n > 1024) return;
-  auto slot = [&](int i) { return ((((int64_t)rb * X + x + i) * 2 + (i == n - 1 ? 0 : 1)) * block_rows + row); };
-  float top = kLowest;
-  for (int i = tid; i < n; i += 128) top = fmaxf(top, ws.sums[slot(i)].m);
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  if (lane == 0) red[warp] = top;
-  __syncthreads();
-  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  __syncthreads();
-  float sum = 0.f;
-  for (int i = tid; i < n; i += 128) {
-    const RowSum s = ws.sums[slot(i)];
-    const float f = fast_exp2(s.m - top);
-    weight[i] = f;
-    sum += s.l * f;
-  }
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  if (lane == 0) red[warp] = sum;
-  __syncthreads();
-  sum = red[0] + red[1] + red[2] + red[3];
-  const int grp = tid / LN, d = tid - grp * LN;
+  // pieces 0 .. n - 2 are what CTAs from x on left unfinished, the last is what the item's last CTA began with
+  const int n = min(me.w, X - 1) - x + 1, grp = tid / LN, d = tid - grp * LN;
+  const int b = me.y / hkv, hk = me.y - b * hkv, len = a.lens[b];
+  RowSum run{kLowest, 0.f};
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = grp; i < n; i += GR) {
-    const float4 v = *reinterpret_cast<const float4*>(ws.acc + slot(i) * D + d * E);
-    const float f = weight[i];
-    o.x += v.x * f;
-    o.y += v.y * f;
-    o.z += v.z * f;
-    o.w += v.w * f;
+  for (int i0 = grp; i0 < n; i0 += GR * AHEAD) {
+    RowSum s[AHEAD];
+    float4 v[AHEAD];
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      const int i = i0 + j * GR;
+      const int64_t at = ((place + i) * 2 + (i < n - 1)) * block_rows + row;
+      s[j] = RowSum{kLowest, 0.f};
+      v[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < n) {
+        s[j] = ws.sums[at];
+        v[j] = *reinterpret_cast<const float4*>(ws.acc + at * D + d * 4);
+      }
+    }
+    float top = run.m;
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) top = fmaxf(top, s[j].m);
+    float f = fast_exp2(run.m - top);
+    run = RowSum{top, run.l * f};
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      f = fast_exp2(s[j].m - top);
+      run.l += s[j].l * f;
+      o = make_float4(o.x + v[j].x * f, o.y + v[j].y * f, o.z + v[j].z * f, o.w + v[j].w * f);
+    }
   }
   part[grp][d] = o;
+  if (d == 0) part_sums[grp] = run;
   __syncthreads();
   if (grp) return;
-#pragma unroll
-  for (int i = 1; i < GR; ++i) {
+  const int used = min(n, GR);
+  float top = kLowest, sum = 0.f;
+  for (int i = 0; i < used; ++i) top = fmaxf(top, part_sums[i].m);
+  o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < used; ++i) {
+    const float f = fast_exp2(part_sums[i].m - top);
     const float4 v = part[i][d];
-    o.x += v.x;
-    o.y += v.y;
-    o.z += v.z;
-    o.w += v.w;
+    sum += part_sums[i].l * f;
+    o = make_float4(o.x + v.x * f, o.y + v.y * f, o.z + v.z * f, o.w + v.w * f);
   }
-  const int b = item / hkv, hk = item - b * hkv;
-  const int seen = min(a.lens[b], cap) - a.q_len + 1 + R / g;
+  const int seen = min(len, cap) - a.q_len + 1 + R / g;
   const RowAt at = row_at(a, g, b, hk, R);
   const float inv = 1.f / sum;
   const uint2 w = seen <= 0 ? make_uint2(0, 0) : make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-  *reinterpret_cast<uint2*>(a.o + at.head * a.o_head + at.tok * a.o_tok + d * E) = w;
+  *reinterpret_cast<uint2*>(a.o + at.head * a.o_head + at.tok * a.o_tok + d * 4) = w;
   if (a.lse && d == 0) a.lse[at.head * n_seqs * a.q_len + at.tok] = seen <= 0 ? -INFINITY : row_lse(top, sum);
 }
 
@@ -863,16 +909,30 @@ DecodeShape decode_shape(const DecodeArgs& a) {
   return DecodeShape{rows, blocks, std::max(1, std::min(sm_count(), 1024) / blocks)};
 }
 
+// Tiles of 16 rows of a page and head.  A row longer than 128 bytes is two boxes, side by side in shared memory.
+template <int D, bool FP8, int NT>
+bool tile_map(CUtensorMap* map, const KvCache& c, const void* base) {
+  using L = Lay<D, FP8, NT>;
+  const uint64_t es = FP8 ? 1 : 2;
+  auto stride = [&](int64_t s) { return s ? (uint64_t)s * es : (uint64_t)16; };  // 0: of a single page or head
+  const uint64_t dims[5] = {L::SEG / es, (uint64_t)c.page_size, 2, (uint64_t)c.n_kv_heads, (uint64_t)c.n_pages};
+  const uint64_t strides[4] = {stride(c.token_stride), 128, stride(c.head_stride), stride(c.page_stride)};
+  const uint32_t box[5] = {(uint32_t)(L::SEG / es), kTileKeys, 2, 1, 1};
+  return make_tmap_rows(map, base, !FP8, L::SEGS == 2, dims, strides, box, L::SEG);
+}
+
 template <int D, bool FP8, int NT>
 cudaError_t run(const DecodeArgs& a, const DecodeShape& sh, const DecodeWs& ws, cudaStream_t st) {
   using L = Lay<D, FP8, NT>;
   auto kfn = k_decode<D, FP8, NT>;
+  CUtensorMap mk, mv;
+  if (!tile_map<D, FP8, NT>(&mk, a.c, a.c.k) || !tile_map<D, FP8, NT>(&mv, a.c, a.c.v)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kfn, dim3(sh.ctas, sh.blocks), dim3(32 * kWarps), L::BYTES, st, a, ws);
+  e = launch_pdl(kfn, dim3(sh.ctas, sh.blocks), dim3(32 * L::WARPS), L::BYTES, st, a, ws, mk, mv, wait_limit_ns());
   note_launch();
   if (e != cudaSuccess) return e;
-  e = launch_pdl(k_decode_join<D>, dim3(sh.ctas, a.hq / a.c.n_kv_heads * a.q_len), dim3(128), 0, st, a, ws, sh.rows);
+  e = launch_pdl(k_decode_join<D>, dim3(sh.ctas, a.hq / a.c.n_kv_heads * a.q_len), dim3(kJoinThreads), 0, st, a, ws, sh.rows);
   note_launch();
   return e;
 }

@@ -401,6 +401,9 @@ bool make_tmap_3d_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint6
                        uint32_t box_inner, uint32_t box_rows, uint64_t plane_stride_elems = 0);
 bool make_tmap_2d_bf16(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t row_stride_elems,
                        uint32_t box_inner, uint32_t box_rows);
+// rows of a paged cache, bf16 or 8-bit: see tc_host.cu
+bool make_tmap_rows(CUtensorMap* map, const void* base, bool bf16_rows, bool halves, const uint64_t* dims, const uint64_t* strides,
+                    const uint32_t* box, uint32_t span);
 // 8-bit operand of `rows` rows of `inner` bytes
 bool make_tmap_2d_u8(CUtensorMap* map, const void* base, uint64_t inner, uint64_t rows, uint64_t row_stride_bytes,
                      uint32_t box_inner, uint32_t box_rows);

@@ -89,4 +89,25 @@ bool make_tmap_f32_out(CUtensorMap* map, void* base, int rank, const uint64_t* d
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows of a paged cache: dims {elements, tokens of a page, halves of a row, heads, pages}, the halves left out unless
+// `halves`; strides in bytes of all but the first.  `span`: bytes of the box's rows, 128 or 64, which the swizzle spans.
+bool make_tmap_rows(CUtensorMap* map, const void* base, bool bf16_rows, bool halves, const uint64_t* dims, const uint64_t* strides,
+                    const uint32_t* box, uint32_t span) {
+  auto fn = encode_fn();
+  if (!fn || (span != 64 && span != 128)) return false;
+  cuuint64_t d[5], st[4];
+  cuuint32_t bx[5], es[5] = {1, 1, 1, 1, 1};
+  int rank = 0;
+  for (int i = 0; i < 5; ++i) {
+    if (i == 2 && !halves) continue;
+    d[rank] = dims[i];
+    bx[rank] = box[i];
+    if (i > 0) st[rank - 1] = strides[i - 1];
+    ++rank;
+  }
+  return fn(map, bf16_rows ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), d, st, bx, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, span == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace upipe
