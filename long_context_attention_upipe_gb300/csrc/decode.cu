@@ -169,6 +169,18 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
   return v;
 }
 
+// a * b / c of numbers whose product fits 64 bits; most fit 32, where a division takes a fraction of the time.
+__device__ __forceinline__ int64_t mul_div(int64_t a, int b, int c) {
+  const int64_t p = a * b;
+  return p <= 0xffffffffll ? (int64_t)((uint32_t)p / (uint32_t)c) : p / c;
+}
+
+// The part that holds tile end - 1 where part i ends before tile total * (i + 1) / parts.
+__device__ __forceinline__ int last_part(int64_t end, int64_t total, int parts) {
+  const int64_t p = end * parts + total - 1;
+  return (int)(p <= 0xffffffffll ? (uint32_t)p / (uint32_t)total : p / total) - 1;
+}
+
 // A query row of a key head: row R is head R % g of the group and token R / g of the q_len newest.
 struct RowAt {
   int64_t head, tok;
@@ -270,51 +282,64 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
   // ---- the warp's part of the line of tiles
   int64_t* sums = reinterpret_cast<int64_t*>(smem);
   const int chunks = (n_seqs + 31) / 32;
-  for (int ch = warp; ch < chunks; ch += kWarps) {
-    const int b = ch * 32 + lane;
-    const int64_t s = warp_sum(b < n_seqs ? tiles_of(a.lens[b], cap) : 0);
-    if (lane == 0) sums[ch] = s;
-  }
-  __syncthreads();
-  int64_t total = 0;
-  for (int ch = lane; ch < chunks; ch += 32) total += sums[ch];
+  int lens = lane < n_seqs ? a.lens[lane] : 0;  // of the 32 sequences that the warp is among
+  int64_t in = 0, total = 0;                     // tiles up to a sequence of them, of all
+  if (chunks == 1) {
+    in = warp_scan(tiles_of(lens, cap), lane);
+    total = __shfl_sync(0xffffffffu, in, 31);
+  } else {
+    for (int ch = warp; ch < chunks; ch += kWarps) {
+      const int b = ch * 32 + lane;
+      const int64_t n = warp_sum(b < n_seqs ? tiles_of(a.lens[b], cap) : 0);
+      if (lane == 0) sums[ch] = n;
+    }
+    __syncthreads();
+    for (int ch = lane; ch < chunks; ch += 32) total += sums[ch];
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+    for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  }
   total *= hkv;
   // no CTA gets less than a tile for each warp
-  const int64_t parts = min((int64_t)X, max((total + kWarps - 1) / kWarps, (int64_t)1));
+  const int parts = total < (int64_t)X * kWarps ? max((int)(total + kWarps - 1) / kWarps, 1) : X;
   int64_t first = 0, left = 0;
   if (blockIdx.x < parts) {
-    const int64_t t0 = total * blockIdx.x / parts, t1 = total * (blockIdx.x + 1) / parts;
+    const int64_t t0 = mul_div(total, blockIdx.x, parts), t1 = mul_div(total, blockIdx.x + 1, parts);
     first = t0 + (t1 - t0) * warp / kWarps;
     left = t0 + (t1 - t0) * (warp + 1) / kWarps - first;
   }
-  int64_t next = first + left;  // the tile after the part
+  const int64_t next = first + left;  // the tile after the part
   int b0 = 0, hk0 = 0, tile0 = 0;
   if (left > 0) {
     int64_t before = 0;
-    int ch = 0;
-    for (int base = 0; base < chunks; base += 32) {
-      const int64_t v = base + lane < chunks ? sums[base + lane] : 0, in = warp_scan(v, lane);
-      const unsigned hit = __ballot_sync(0xffffffffu, (before + in) * hkv > first);
-      if (hit) {
-        ch = base + __ffs(hit) - 1;
-        before += __shfl_sync(0xffffffffu, in - v, __ffs(hit) - 1);
-        break;
+    const int64_t seq_first = mul_div(first, 1, hkv);  // the tile's place if there were one head
+    if (chunks > 1) {
+      int ch = 0;
+      for (int base = 0; base < chunks; base += 32) {
+        const int64_t v = base + lane < chunks ? sums[base + lane] : 0, upto = warp_scan(v, lane);
+        const unsigned hit = __ballot_sync(0xffffffffu, before + upto > seq_first);
+        if (hit) {
+          ch = base + __ffs(hit) - 1;
+          before += __shfl_sync(0xffffffffu, upto - v, __ffs(hit) - 1);
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, upto, 31);
       }
-      before += __shfl_sync(0xffffffffu, in, 31);
+      b0 = ch * 32;
+      lens = b0 + lane < n_seqs ? a.lens[b0 + lane] : 0;
+      in = warp_scan(tiles_of(lens, cap), lane);
     }
-    const int b = ch * 32 + lane;
-    const int64_t v = b < n_seqs ? tiles_of(a.lens[b], cap) : 0, in = warp_scan(v, lane);
-    const int at = max(__ffs(__ballot_sync(0xffffffffu, (before + in) * hkv > first)) - 1, 0);
-    before += __shfl_sync(0xffffffffu, in - v, at);
-    b0 = ch * 32 + at;
-    const int64_t n = max(__shfl_sync(0xffffffffu, v, at), (int64_t)1), rest = first - before * hkv;
-    hk0 = (int)min(max(rest / n, (int64_t)0), (int64_t)(hkv - 1));  // within bounds even if lengths change under the call
-    tile0 = (int)min(max(rest - hk0 * n, (int64_t)0), n - 1);
+    const int at = max(__ffs(__ballot_sync(0xffffffffu, before + in > seq_first)) - 1, 0);
+    const int n = max(tiles_of(__shfl_sync(0xffffffffu, lens, at), cap), 1);
+    before += __shfl_sync(0xffffffffu, in, at) - n;
+    b0 = min(b0 + at, n_seqs - 1);
+    const int64_t rest = max(first - before * hkv, (int64_t)0);
+    hk0 = (int)min(mul_div(rest, 1, n), (int64_t)(hkv - 1));  // within bounds even if lengths change under the call
+    tile0 = (int)min(rest - (int64_t)hk0 * n, (int64_t)(n - 1));
   }
-  fence_async();    // the queues, which the copies fill, take the place of the sums
-  __syncthreads();
+  if (chunks > 1) {
+    fence_async();    // the queues, which the copies fill, take the place of the sums
+    __syncthreads();
+  }
 
   int4 left_over = make_int4(-1, -1, 0, 0);
   if (left > 0) {
@@ -322,14 +347,44 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
     const float* scales = FP8 ? (c < 2 ? a.c.k_scale : a.c.v_scale) : nullptr;
     const int s_key = r + 8 * (c & 1);  // the key whose scale this lane brings in: of K for c < 2, else of V
 
-    // ---- the end of the line that loads
-    int pb = b0, phk = hk0, pt = tile0, plen = min(max(a.lens[b0], 0), cap), pn = tiles_of(plen, cap);
-    int ppi = pt * kTileKeys / a.c.page_size, prow = pt * kTileKeys - ppi * a.c.page_size;
+    // ---- the end of the line that loads.  Lengths of 32 sequences and 32 entries of the table lie in the lanes; the
+    // entries that follow are on their way while those are used.
+    const int ps = a.c.page_size;
+    int pb = b0, phk = hk0, pt = tile0, plen = min(max(__shfl_sync(0xffffffffu, lens, b0 & 31), 0), cap), pn = tiles_of(plen, cap);
+    int ppi = pt * kTileKeys / ps, prow = pt * kTileKeys - ppi * ps;
+    int held = (plen + (ps - 1)) / ps;  // pages of the sequence
+    int plens = lens;
     int64_t to_load = left;
-    int page = a.t.pages[(int64_t)pb * a.t.stride + ppi];
+    auto entries = [&](int b, int first_page) {
+      const int i = first_page + lane;
+      return i < a.t.max_pages ? a.t.pages[(int64_t)b * a.t.stride + i] : -1;
+    };
+    // the next sequence with keys, or none
+    auto next_seq = [&](int& b, int& seq_lens) {
+      unsigned some = __ballot_sync(0xffffffffu, seq_lens > 0) & ~((2u << (b & 31)) - 1u);
+      b &= ~31;
+      while (!some) {
+        b += 32;
+        if (b >= n_seqs) return false;
+        seq_lens = b + lane < n_seqs ? a.lens[b + lane] : 0;
+        some = __ballot_sync(0xffffffffu, seq_lens > 0);
+      }
+      b += __ffs(some) - 1;
+      return true;
+    };
+    // entries that follow those of pages ppi / 32 * 32 ..: of the same sequence, again its first ones, or the next sequence's
+    auto following = [&]() {
+      const int batch = ppi & ~31;
+      if (batch + 32 < held) return entries(pb, batch + 32);
+      if (held > 32 && phk + 1 < hkv) return entries(pb, 0);
+      int b = pb, l = plens;
+      return next_seq(b, l) ? entries(b, 0) : -1;
+    };
+    int ids = entries(pb, ppi & ~31), ids_after = following();
     uint32_t in_flight = 0;  // stages that a copy is on its way to; those of tiles whose page does not exist stay as they are
     bool ok = true;          // no wait ran out
     auto load = [&](int stage) {
+      const int page = __shfl_sync(0xffffffffu, ids, ppi & 31);
       const bool there = (unsigned)page < (unsigned)a.c.n_pages;
       if (there) {
         in_flight |= 1u << stage;
@@ -346,26 +401,29 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
           cp4(scale_queue + stage * L::SCALES, p, in ? 4 : 0);
         }
       }
-      // on to the next tile; its page number is on the way when it is needed
-      if (--to_load > 0) {
+      if (--to_load > 0) {  // on to the next tile
+        bool fresh = false;
         prow += kTileKeys;
-        if (prow == a.c.page_size) {
+        if (prow == ps) {
           prow = 0;
-          ++ppi;
+          fresh = (++ppi & 31) == 0;
         }
         if (++pt == pn) {
           pt = ppi = prow = 0;
+          fresh = held > 32;
           if (++phk == hkv) {
             phk = 0;
-            do {
-              ++pb;
-              plen = pb < n_seqs ? min(max(a.lens[pb], 0), cap) : 1;
-            } while (plen == 0);
-            if (pb >= n_seqs) pb = n_seqs - 1;  // only if the lengths changed meanwhile
+            fresh = true;
+            if (!next_seq(pb, plens)) pb = n_seqs - 1;  // only if the lengths changed meanwhile
+            plen = min(max(__shfl_sync(0xffffffffu, plens, pb & 31), 0), cap);
             pn = tiles_of(plen, cap);
+            held = (plen + (ps - 1)) / ps;
           }
         }
-        page = ppi < a.t.max_pages ? a.t.pages[(int64_t)pb * a.t.stride + ppi] : -1;
+        if (fresh) {
+          ids = ids_after;
+          ids_after = following();
+        }
       }
     };
 #pragma unroll
@@ -382,7 +440,7 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
       return key * L::SEG + ((piece ^ (L::SEG == 128 ? key & 7 : (key >> 1) & 3)) << 4);
     };
     const uint32_t k_row = matrix_row(true), v_row = L::KBYTES + matrix_row(FP8);
-    int cb = b0, chk = hk0, ct = tile0, raw = a.lens[b0], len = min(max(raw, 0), cap), cn = tiles_of(len, cap);
+    int cb = b0, chk = hk0, ct = tile0, raw = __shfl_sync(0xffffffffu, lens, b0 & 31), len = min(max(raw, 0), cap), cn = tiles_of(len, cap);
     int stage = 0;
     uint32_t phases = 0;
     float m[NT][2], l[NT][2], mv[NT][2], acc[NT][L::MT][4], rs[NT][2];
@@ -622,7 +680,7 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
         if (FP8) cp_wait<0>();
         left_over.y = item;
         left_over.z = begins;
-        left_over.w = (int)((max(next + cn - ct, next) * parts + total - 1) / total) - 1;  // the CTA whose part holds its last tile
+        left_over.w = last_part(max(next + cn - ct, next), total, parts);  // the CTA whose part holds the item's last tile
       } else if (!whole) {
         left_over.x = item;
       }
@@ -728,12 +786,9 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
         ct = 0;
         if (++chk == hkv) {
           chk = 0;
-          do {
-            ++cb;
-            raw = cb < n_seqs ? a.lens[cb] : 1;
-            len = min(max(raw, 0), cap);
-          } while (len == 0);
-          if (cb >= n_seqs) cb = n_seqs - 1;
+          if (!next_seq(cb, lens)) cb = n_seqs - 1;
+          raw = __shfl_sync(0xffffffffu, lens, cb & 31);
+          len = min(max(raw, 0), cap);
           cn = tiles_of(len, cap);
         }
       }
@@ -742,89 +797,101 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
     if (FP8) cp_wait<0>();
   }
 
-  // ---- the CTA's pieces, in order: runs of one item are joined
+  // ---- the CTA's pieces, in order: lane i of every warp has piece i (2 warp: head, 2 warp + 1: tail), runs of one item are joined,
+  // a row to a warp
   if (lane == 0) info[warp] = left_over;
   __syncthreads();
   int4 meta = make_int4(-1, -1, 0, 0);
-  int p = 0;  // pieces: 2 warp (head), 2 warp + 1 (tail)
   const int64_t place = (int64_t)rb * X + blockIdx.x;
-  while (p < 2 * kWarps) {
-    auto item_of = [&](int i) { return i & 1 ? info[i >> 1].y : info[i >> 1].x; };
-    const int item = item_of(p);
-    if (item < 0) {
-      ++p;
-      continue;
-    }
-    const bool begins = (p & 1) && info[p >> 1].z;
-    int end = p + 1, last = p;
-    for (; end < 2 * kWarps; ++end) {
-      const int it = item_of(end);
-      if (it >= 0 && it != item) break;
-      if (it == item) last = end;
-      if (it == item && !(end & 1)) {
-        ++end;
-        break;
-      }
-    }
-    const bool ends = !(last & 1);
-    const int b = item / hkv, hk = item - b * hkv;
+  static_assert(2 * kWarps <= 32, "a piece to a lane");
+  const int4 mine = lane < 2 * kWarps ? info[lane >> 1] : make_int4(-1, -1, 0, 0);
+  const int my_item = lane & 1 ? mine.y : mine.x;
+  const float* my_piece = lane & 1 ? tail_of(lane >> 1) : head_of(lane >> 1);
+  const unsigned valid = __ballot_sync(0xffffffffu, my_item >= 0), below = valid & ((1u << lane) - 1u);
+  const int prev = __shfl_sync(0xffffffffu, my_item, below ? 31 - __clz(below) : 0);
+  unsigned starts = __ballot_sync(0xffffffffu, my_item >= 0 && (!below || prev != my_item));
+  while (starts) {
+    const int s = __ffs(starts) - 1;
+    starts &= starts - 1;
+    const unsigned run = valid & ~((1u << s) - 1u) & (starts ? (1u << (__ffs(starts) - 1)) - 1u : 0xffffffffu);
+    const int last = 31 - __clz(run), item = __shfl_sync(0xffffffffu, my_item, s);
+    const bool begins = (s & 1) && __shfl_sync(0xffffffffu, mine.z, s), ends = !(last & 1), member = run >> lane & 1;
+    const int end_part = __shfl_sync(0xffffffffu, mine.w, last);
+#pragma unroll 1
     for (int row = warp; row < L::ROWS && rb * L::ROWS + row < rows; row += kWarps) {
-      const int R = rb * L::ROWS + row;
       constexpr int E = D / 32;
-      float top = kLowest;
-      auto piece = [&](int i) { return i & 1 ? tail_of(i >> 1) : head_of(i >> 1); };
-      auto sums_of = [&](int i) { return reinterpret_cast<const RowSum*>(piece(i) + L::ROWS * D)[row]; };
-      for (int i = p; i <= last; ++i)
-        if (item_of(i) == item) top = fmaxf(top, sums_of(i).m);
-      float sum = 0.f, o[E] = {};
-      for (int i = p; i <= last; ++i) {
-        if (item_of(i) != item) continue;
-        const RowSum s = sums_of(i);
-        const float f = fast_exp2(s.m - top);
-        sum += s.l * f;
-        const float* src = piece(i) + row * D + lane * E;
+      RowSum sum{kLowest, 0.f};
+      if (member) sum = reinterpret_cast<const RowSum*>(my_piece + L::ROWS * D)[row];
+      float top = sum.m;
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += src[e] * f;
+      for (int off = kWarps; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      const float f = fast_exp2(sum.m - top);
+      float l = member ? sum.l * f : 0.f, o[E] = {};
+#pragma unroll
+      for (int off = kWarps; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+#pragma unroll 1
+      for (unsigned rest = run; rest;) {  // four pieces at a time
+        const float* src[4];
+        float w[4], v[4][E];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int i = rest ? __ffs(rest) - 1 : -1;
+          rest &= rest - 1;
+          w[j] = __shfl_sync(0xffffffffu, f, i & 31);
+          src[j] = i < 0 ? nullptr : (i & 1 ? tail_of(i >> 1) : head_of(i >> 1)) + row * D + lane * E;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < E; ++e) v[j][e] = src[j] ? src[j][e] : 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] += src[j] ? v[j][e] * w[j] : 0.f;
       }
+      top = __shfl_sync(0xffffffffu, top, 0);  // lanes that hold no piece have not taken part
+      l = __shfl_sync(0xffffffffu, l, 0);
       if (begins && ends) {
-        const int seen = min(a.lens[b], cap) - a.q_len + 1 + R / g;
-        const RowAt at = row_at(a, g, b, hk, R);
+        const int b = item / hkv, R = rb * L::ROWS + row, seen = min(a.lens[b], cap) - a.q_len + 1 + R / g;
+        const RowAt at = row_at(a, g, b, item - b * hkv, R);
         bf16* dst = a.o + at.head * a.o_head + at.tok * a.o_tok + lane * E;
-        const float inv = 1.f / sum;
+        const float inv = 1.f / l;
 #pragma unroll
         for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = seen <= 0 ? 0u : pack_bf16(o[e] * inv, o[e + 1] * inv);
-        if (a.lse && lane == 0) a.lse[at.head * n_seqs * a.q_len + at.tok] = seen <= 0 ? -INFINITY : row_lse(top, sum);
+        if (a.lse && lane == 0) a.lse[at.head * n_seqs * a.q_len + at.tok] = seen <= 0 ? -INFINITY : row_lse(top, l);
       } else {
         const int64_t at = (place * 2 + (ends ? 0 : 1)) * L::ROWS + row;
         float* dst = ws.acc + at * D + lane * E;
 #pragma unroll
         for (int e = 0; e < E; ++e) dst[e] = o[e];
-        if (lane == 0) ws.sums[at] = RowSum{top, sum};
+        if (lane == 0) ws.sums[at] = RowSum{top, l};
       }
     }
-    if (!(begins && ends)) {
-      if (ends) meta.x = item;
-      else {
+    if (!begins || !ends) {
+      if (ends) {
+        meta.x = item;
+      } else {
         meta.y = item;
         meta.z = begins;
-        meta.w = info[last >> 1].w;
+        meta.w = end_part;
       }
     }
-    p = end;
   }
   if (threadIdx.x == 0) ws.meta[place] = meta;
 }
 
 // Joins what an item left in several CTAs, in order; one block for each CTA in which an item begins that goes on, and each row.
 // Sequences without keys get their zeros here.
-template <int D>
+//
+// ROWS 8: a warp to a row, for the short chains of many items (the rest of a block's rows would only be launched to leave);
+// ROWS 1: all warps share a row's pieces, for the long chains of few.
+template <int D, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) k_decode_join(const __grid_constant__ DecodeArgs a, const DecodeWs ws, int block_rows) {
-  constexpr int LN = D / 4, GR = kJoinThreads / LN, AHEAD = 8;  // lanes of a row, groups that share the pieces, pieces in flight
-  __shared__ float4 part[GR][LN];
+  constexpr int LN = D / 4, GR = kJoinThreads / LN / ROWS, AHEAD = ROWS == 1 ? 8 : 4;  // lanes and groups of a row, pieces in flight
+  __shared__ float4 part[ROWS == 1 ? GR : 1][LN];
   __shared__ RowSum part_sums[GR];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, x = blockIdx.x, X = gridDim.x;
-  const int hkv = a.c.n_kv_heads, g = a.hq / hkv, R = blockIdx.y, rb = R / block_rows, row = R - rb * block_rows, n_seqs = a.t.n_seqs;
-  const int cap = table_keys(a.t, a.c.page_size);
+  const int hkv = a.c.n_kv_heads, g = a.hq / hkv, rows = g * a.q_len, n_seqs = a.t.n_seqs, cap = table_keys(a.t, a.c.page_size);
   // lengths were there before the kernel that this one follows began
   for (int base = (x * (kJoinThreads / 32) + warp) * 32; base < n_seqs; base += X * kJoinThreads) {
     const int b = base + lane, len = b < n_seqs ? a.lens[b] : 1;
@@ -832,8 +899,11 @@ __global__ void __launch_bounds__(kJoinThreads) k_decode_join(const __grid_const
     while (none) {
       const int i = __ffs(none) - 1;
       none &= none - 1;
-      const bool lost = __shfl_sync(0xffffffffu, len, i) - a.q_len + 1 + R / g > 0;  // keys, but no table
-      for (int hk = 0; hk < hkv; ++hk) {
+      const int keys = __shfl_sync(0xffffffffu, len, i);
+      for (int j = 0; j < ROWS * hkv; ++j) {
+        const int hk = j / ROWS, R = blockIdx.y * ROWS + j % ROWS;
+        if (R >= rows) continue;
+        const bool lost = keys - a.q_len + 1 + R / g > 0;  // keys, but no table
         const RowAt at = row_at(a, g, base + i, hk, R);
         bf16* o = a.o + at.head * a.o_head + at.tok * a.o_tok;
         if (lane < D / 8) *reinterpret_cast<uint4*>(o + lane * 8) = lost ? make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu) : make_uint4(0, 0, 0, 0);
@@ -841,12 +911,14 @@ __global__ void __launch_bounds__(kJoinThreads) k_decode_join(const __grid_const
       }
     }
   }
+  const int R = blockIdx.y * ROWS + (ROWS == 1 ? 0 : tid / (kJoinThreads / ROWS));
+  const int rb = R / block_rows, row = R - rb * block_rows;  // 8 rows lie in one block of rows
   grid_dep_wait();
   const int64_t place = (int64_t)rb * X + x;
   const int4 me = ws.meta[place];
-  if (me.y < 0 || !me.z) return;
+  if (me.y < 0 || !me.z || R >= rows) return;
   // pieces 0 .. n - 2 are what CTAs from x on left unfinished, the last is what the item's last CTA began with
-  const int n = min(me.w, X - 1) - x + 1, grp = tid / LN, d = tid - grp * LN;
+  const int n = min(me.w, X - 1) - x + 1, grp = tid % (kJoinThreads / ROWS) / LN, d = tid % LN;
   const int b = me.y / hkv, hk = me.y - b * hkv, len = a.lens[b];
   RowSum run{kLowest, 0.f};
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -877,26 +949,39 @@ __global__ void __launch_bounds__(kJoinThreads) k_decode_join(const __grid_const
       o = make_float4(o.x + v[j].x * f, o.y + v[j].y * f, o.z + v[j].z * f, o.w + v[j].w * f);
     }
   }
-  part[grp][d] = o;
-  if (d == 0) part_sums[grp] = run;
-  __syncthreads();
-  if (grp) return;
-  const int used = min(n, GR);
-  float top = kLowest, sum = 0.f;
-  for (int i = 0; i < used; ++i) top = fmaxf(top, part_sums[i].m);
-  o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i = 0; i < used; ++i) {
-    const float f = fast_exp2(part_sums[i].m - top);
-    const float4 v = part[i][d];
-    sum += part_sums[i].l * f;
-    o = make_float4(o.x + v.x * f, o.y + v.y * f, o.z + v.z * f, o.w + v.w * f);
+  if (ROWS == 1) {
+    part[grp][d] = o;
+    if (d == 0) part_sums[grp] = run;
+    __syncthreads();
+    if (grp) return;
+    const int used = min(n, GR);
+    float top = kLowest;
+#pragma unroll
+    for (int i = 0; i < GR; ++i) top = fmaxf(top, i < used ? part_sums[i].m : kLowest);
+    run = RowSum{top, 0.f};
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < GR; ++i) {
+      if (i >= used) break;
+      const float f = fast_exp2(part_sums[i].m - top);
+      const float4 v = part[i][d];
+      run.l += part_sums[i].l * f;
+      o = make_float4(o.x + v.x * f, o.y + v.y * f, o.z + v.z * f, o.w + v.w * f);
+    }
+  } else if (GR == 2) {  // two halves of a warp share a row
+    const float m = __shfl_xor_sync(0xffffffffu, run.m, 16), l = __shfl_xor_sync(0xffffffffu, run.l, 16);
+    const float top = fmaxf(run.m, m), f = fast_exp2(run.m - top), h = fast_exp2(m - top);
+    auto both = [&](float v) { return v * f + __shfl_xor_sync(0xffffffffu, v, 16) * h; };
+    run = RowSum{top, run.l * f + l * h};
+    o = make_float4(both(o.x), both(o.y), both(o.z), both(o.w));
+    if (grp) return;
   }
   const int seen = min(len, cap) - a.q_len + 1 + R / g;
   const RowAt at = row_at(a, g, b, hk, R);
-  const float inv = 1.f / sum;
+  const float inv = 1.f / run.l;
   const uint2 w = seen <= 0 ? make_uint2(0, 0) : make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
   *reinterpret_cast<uint2*>(a.o + at.head * a.o_head + at.tok * a.o_tok + d * 4) = w;
-  if (a.lse && d == 0) a.lse[at.head * n_seqs * a.q_len + at.tok] = seen <= 0 ? -INFINITY : row_lse(top, sum);
+  if (a.lse && d == 0) a.lse[at.head * n_seqs * a.q_len + at.tok] = seen <= 0 ? -INFINITY : row_lse(run.m, run.l);
 }
 
 // Rows of a block, blocks of rows, and CTAs for each of them.
@@ -932,7 +1017,10 @@ cudaError_t run(const DecodeArgs& a, const DecodeShape& sh, const DecodeWs& ws, 
   e = launch_pdl(kfn, dim3(sh.ctas, sh.blocks), dim3(32 * L::WARPS), L::BYTES, st, a, ws, mk, mv, wait_limit_ns());
   note_launch();
   if (e != cudaSuccess) return e;
-  e = launch_pdl(k_decode_join<D>, dim3(sh.ctas, a.hq / a.c.n_kv_heads * a.q_len), dim3(kJoinThreads), 0, st, a, ws, sh.rows);
+  const int rows = a.hq / a.c.n_kv_heads * a.q_len;
+  const bool many = (int64_t)a.t.n_seqs * a.c.n_kv_heads * 8 >= sh.ctas;  // items of 8 CTAs at most, if they are alike
+  e = launch_pdl(many ? k_decode_join<D, 8> : k_decode_join<D, 1>, dim3(sh.ctas, many ? (int)ceil_div(rows, 8) : rows), dim3(kJoinThreads), 0, st, a,
+                 ws, sh.rows);
   note_launch();
   return e;
 }
