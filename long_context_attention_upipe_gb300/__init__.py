@@ -670,30 +670,34 @@ class KVCache:
 
 
 def _page_table(t, dev):
-    if t.get_device() != dev or t.dtype != torch.int32 or t.dim() != 2 or (t.stride(1) != 1 and t.shape[1] > 1):
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or t.get_device() != dev or t.dtype != torch.int32 or (strides[1] != 1 and shape[1] > 1):
         _refuse(f"page_table: int32 [sequences, pages] with contiguous rows on device {dev} expected, got {t.dtype} "
                 f"{tuple(t.shape)} {t.stride()} on {t.device}")
-    n, m = t.shape
-    return PageTable(t.data_ptr(), t.stride(0) if n > 1 else m, n, m)
+    n, m = shape
+    return PageTable(t.data_ptr(), strides[0] if n > 1 else m, n, m)
 
 
 def _heads(t, dev, shape, what):
     """Address, head stride and token stride of bf16 rows [heads, tokens, head_dim]."""
-    if t.get_device() != dev or t.dtype != _BF16 or t.shape != shape or t.stride(2) != 1:
-        _refuse(f"{what}: bf16 {tuple(shape)} with contiguous rows on device {dev} expected, got {t.dtype} {tuple(t.shape)} "
-                f"{t.stride()} on {t.device}")
-    return t.data_ptr(), t.stride(0), t.stride(1)
+    if t.shape != shape or t.get_device() != dev or t.dtype != _BF16:
+        _refuse(f"{what}: bf16 {tuple(shape)} on device {dev} expected, got {t.dtype} {tuple(t.shape)} on {t.device}")
+    hs, ts, es = t.stride()
+    if es != 1:
+        _refuse(f"{what}: contiguous rows expected, got strides {t.stride()}")
+    return t.data_ptr(), hs, ts
 
 
 def _kv_copy(f, where, cache, k, v, seq, pos, page_table, stream):
-    dev = _on(k, "k")
-    if dev != cache.device_index or seq.dim() != 1:
-        _refuse(f"{where}: a cache on device {dev} and seq of [tokens] expected, got {cache.k.device} and {tuple(seq.shape)}")
-    n = seq.shape[0]
-    shape = (cache.n_kv_heads, n, cache.head_dim)
-    rc = f(cache.desc, _page_table(page_table, dev), n, _dev(seq, dev, torch.int32, (n,), "seq"),
-           _dev(pos, dev, torch.int32, (n,), "pos"), *_heads(k, dev, shape, "k"), *_heads(v, dev, shape, "v"),
-           _raw_stream(stream, dev))
+    dev, shape = cache.device_index, seq.shape
+    if dev != torch._C._cuda_getDevice() or len(shape) != 1:
+        _refuse(f"{where}: a cache on the current device and seq of [tokens] expected, got {cache.k.device} and {tuple(shape)}")
+    n, = shape
+    rows = (cache.n_kv_heads, n, cache.head_dim)
+    kp, kh, kt = _heads(k, dev, rows, "k")
+    vp, vh, vt = _heads(v, dev, rows, "v")
+    rc = f(cache.desc, _page_table(page_table, dev), n, _dev(seq, dev, torch.int32, shape, "seq"), _dev(pos, dev, torch.int32, shape, "pos"),
+           kp, kh, kt, vp, vh, vt, _raw_stream(stream, dev))
     if rc:
         _check(rc, where)
 
@@ -722,19 +726,21 @@ def decode(cache: KVCache, q, page_table, lens, o, ws, lse=None, scale=0.0, stre
     [n_q_heads, sequences * q_len, head_dim] of any head and token strides, q_len newest tokens of each sequence in
     order (query t sees the keys before lens[b] - q_len + 1 + t); lens int32 [sequences]; lse, optional, fp32
     [n_q_heads, sequences * q_len]; ws uint8 of decode_workspace_bytes."""
-    dev = _on(q, "q")
-    if dev != cache.device_index or q.dim() != 3:
-        _refuse(f"decode: a cache on device {dev} and q of [heads, tokens, head_dim] expected, got {cache.k.device} and {tuple(q.shape)}")
+    dev, shape = cache.device_index, q.shape
+    if dev != torch._C._cuda_getDevice() or len(shape) != 3:
+        _refuse(f"decode: a cache on the current device and q of [heads, tokens, head_dim] expected, got {cache.k.device} and {tuple(shape)}")
     table = _page_table(page_table, dev)
-    n, shape = table.n_seqs, q.shape
-    hq, tokens = shape[:2]
+    n = table.n_seqs
+    hq, tokens, _ = shape
     q_len = tokens // n if n else 1
-    if tokens != n * q_len or (n and not q_len) or shape[2] != cache.head_dim:
+    if tokens != n * q_len or q_len == 0 or shape[2] != cache.head_dim:
         _refuse(f"decode: q of [heads, q_len * {n}, {cache.head_dim}] expected, got {tuple(shape)}")
+    qp, qh, qt = _heads(q, dev, shape, "q")
+    op, oh, ot = _heads(o, dev, shape, "o")
     rc = lib().upipe_attn_decode(
-        cache.desc, table, _dev(lens, dev, torch.int32, (n,), "lens"), hq, q_len, scale, *_heads(q, dev, shape, "q"),
-        *_heads(o, dev, shape, "o"), None if lse is None else _dev(lse, dev, _F32, (hq, tokens), "lse"),
-        _dev(ws, dev, torch.uint8, ws.shape, "ws"), ws.numel(), _raw_stream(stream, dev))
+        cache.desc, table, _dev(lens, dev, torch.int32, (n,), "lens"), hq, q_len, scale, qp, qh, qt, op, oh, ot,
+        None if lse is None else _dev(lse, dev, _F32, (hq, tokens), "lse"), _dev(ws, dev, torch.uint8, ws.shape, "ws"), ws.numel(),
+        _raw_stream(stream, dev))
     if rc:
         _check(rc, "decode")
 

@@ -59,6 +59,7 @@ struct Lay {
   static constexpr int ROWS = 8 * NT;
   static constexpr int SLOT = ROWS * (D * 4 + (int)sizeof(RowSum));  // a piece
   static constexpr int WARPS = 8;
+  static constexpr int END = FP8 ? 2 : 1;               // tiles' time that an item's end (and the next one's begin) takes
   static constexpr int FIT = (231 * 1024 / WARPS - SLOT - 128) / (STAGE + SCALES + 8);
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
   static constexpr int QUEUE = STAGES * STAGE;
@@ -155,6 +156,13 @@ __host__ __device__ __forceinline__ int table_keys(const PageTable& t, int page_
   return n < INT32_MAX ? (int)n : INT32_MAX;
 }
 __device__ __forceinline__ int tiles_of(int len, int cap) { return (int)(((int64_t)min(max(len, 0), cap) + kTileKeys - 1) / kTileKeys); }
+
+// Length of a sequence's item on the line: its tiles and its end.
+template <int END>
+__device__ __forceinline__ int units_of(int len, int cap) {
+  const int n = tiles_of(len, cap);
+  return n ? n + END : 0;
+}
 
 // Sum over a warp of numbers up to 2^27, which may pass 32 bits.
 __device__ __forceinline__ int64_t warp_sum(int n) {
@@ -285,12 +293,12 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
   int lens = lane < n_seqs ? a.lens[lane] : 0;  // of the 32 sequences that the warp is among
   int64_t in = 0, total = 0;                     // tiles up to a sequence of them, of all
   if (chunks == 1) {
-    in = warp_scan(tiles_of(lens, cap), lane);
+    in = warp_scan(units_of<L::END>(lens, cap), lane);
     total = __shfl_sync(0xffffffffu, in, 31);
   } else {
     for (int ch = warp; ch < chunks; ch += kWarps) {
       const int b = ch * 32 + lane;
-      const int64_t n = warp_sum(b < n_seqs ? tiles_of(a.lens[b], cap) : 0);
+      const int64_t n = warp_sum(b < n_seqs ? units_of<L::END>(a.lens[b], cap) : 0);
       if (lane == 0) sums[ch] = n;
     }
     __syncthreads();
@@ -326,15 +334,39 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
       }
       b0 = ch * 32;
       lens = b0 + lane < n_seqs ? a.lens[b0 + lane] : 0;
-      in = warp_scan(tiles_of(lens, cap), lane);
+      in = warp_scan(units_of<L::END>(lens, cap), lane);
     }
     const int at = max(__ffs(__ballot_sync(0xffffffffu, before + in > seq_first)) - 1, 0);
-    const int n = max(tiles_of(__shfl_sync(0xffffffffu, lens, at), cap), 1);
+    const int n = max(units_of<L::END>(__shfl_sync(0xffffffffu, lens, at), cap), 1);
     before += __shfl_sync(0xffffffffu, in, at) - n;
     b0 = min(b0 + at, n_seqs - 1);
     const int64_t rest = max(first - before * hkv, (int64_t)0);
     hk0 = (int)min(mul_div(rest, 1, n), (int64_t)(hkv - 1));  // within bounds even if lengths change under the call
     tile0 = (int)min(rest - (int64_t)hk0 * n, (int64_t)(n - 1));
+  }
+  // the next sequence with keys, or none; `seq_lens`: the lanes' lengths of b's 32 sequences
+  auto next_seq = [&](int& b, int& seq_lens) {
+    unsigned some = __ballot_sync(0xffffffffu, seq_lens > 0) & ~((2u << (b & 31)) - 1u);
+    b &= ~31;
+    while (!some) {
+      b += 32;
+      if (b >= n_seqs) return false;
+      seq_lens = b + lane < n_seqs ? a.lens[b + lane] : 0;
+      some = __ballot_sync(0xffffffffu, seq_lens > 0);
+    }
+    b += __ffs(some) - 1;
+    return true;
+  };
+  if (left > 0) {
+    const int tiles = tiles_of(__shfl_sync(0xffffffffu, lens, b0 & 31), cap);
+    if (tile0 >= tiles) {  // within an item's end
+      left -= tiles + L::END - tile0;
+      tile0 = 0;
+      if (++hk0 == hkv) {
+        hk0 = 0;
+        if (!next_seq(b0, lens)) left = 0;
+      }
+    }
   }
   if (chunks > 1) {
     fence_async();    // the queues, which the copies fill, take the place of the sums
@@ -358,19 +390,6 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
     auto entries = [&](int b, int first_page) {
       const int i = first_page + lane;
       return i < a.t.max_pages ? a.t.pages[(int64_t)b * a.t.stride + i] : -1;
-    };
-    // the next sequence with keys, or none
-    auto next_seq = [&](int& b, int& seq_lens) {
-      unsigned some = __ballot_sync(0xffffffffu, seq_lens > 0) & ~((2u << (b & 31)) - 1u);
-      b &= ~31;
-      while (!some) {
-        b += 32;
-        if (b >= n_seqs) return false;
-        seq_lens = b + lane < n_seqs ? a.lens[b + lane] : 0;
-        some = __ballot_sync(0xffffffffu, seq_lens > 0);
-      }
-      b += __ffs(some) - 1;
-      return true;
     };
     // entries that follow those of pages ppi / 32 * 32 ..: of the same sequence, again its first ones, or the next sequence's
     auto following = [&]() {
@@ -401,14 +420,15 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
           cp4(scale_queue + stage * L::SCALES, p, in ? 4 : 0);
         }
       }
-      if (--to_load > 0) {  // on to the next tile
+      to_load -= ++pt == pn ? 1 + L::END : 1;
+      if (to_load > 0) {  // on to the next tile
         bool fresh = false;
         prow += kTileKeys;
         if (prow == ps) {
           prow = 0;
           fresh = (++ppi & 31) == 0;
         }
-        if (++pt == pn) {
+        if (pt == pn) {
           pt = ppi = prow = 0;
           fresh = held > 32;
           if (++phk == hkv) {
@@ -497,6 +517,16 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
           for (int i = 0; i < 4; ++i) acc[nt][mt][i] = 0.f;
       }
       const int begin = ct;
+      if (left > cn - ct + L::END) {  // another item follows: its queries come nearer
+        constexpr int LINES = D * 2 / 128;
+        int b = cb, hk = chk + 1, l = lens;
+        if (hk < hkv || (hk = 0, next_seq(b, l))) {
+          const int R = rb * L::ROWS + lane / LINES;
+          const RowAt at = row_at(a, g, b, hk, min(R, rows - 1));
+          const bf16* src = a.q + at.head * a.q_head + at.tok * a.q_tok + lane % LINES * 64;
+          if (lane < L::ROWS * LINES && R < rows) asm volatile("prefetch.global.L1 [%0];" ::"l"(src));
+        }
+      }
 
       // ---- its tiles
       do {
@@ -782,6 +812,7 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
           }
       }
       // ---- on to the next item
+      if (ends) left -= L::END;
       if (left > 0 && ends) {
         ct = 0;
         if (++chk == hkv) {
