@@ -65,7 +65,7 @@ struct Lay {
   static constexpr int QUEUE = STAGES * STAGE;
   static constexpr int AT_SCALES = WARPS * QUEUE, AT_SLOTS = AT_SCALES + WARPS * STAGES * SCALES;
   static constexpr int AT_BARS = AT_SLOTS + WARPS * SLOT, AT_INFO = AT_BARS + WARPS * STAGES * 8;
-  static constexpr int BYTES = AT_INFO + WARPS * 16 + 16 + 1024;  // the queues start on 1024 bytes
+  static constexpr int BYTES = AT_INFO + WARPS * 24 + 16 + 1024;  // the queues start on 1024 bytes
   static constexpr int MT = D / 16;                     // tiles of O^T
   static constexpr int KS = D / 16;                     // steps of S^T
   static_assert(STAGES >= 2 && QUEUE >= SLOT && WARPS * QUEUE >= 2048 * 8 && BYTES <= 227 * 1024, "shared memory");
@@ -103,6 +103,13 @@ __device__ __forceinline__ float lds32(uint32_t at) {
   float v;
   asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
   return v;
+}
+template <int N>
+__device__ __forceinline__ void lds_floats(float* v, uint32_t at) {
+  if (N == 4)
+    asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[N - 2]), "=f"(v[N - 1]) : "r"(at) : "memory");
+  else
+    asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(at) : "memory");
 }
 // Four 8 x 8 matrices of 16-bit elements, a lane's address naming a row of one.
 __device__ __forceinline__ void ldm4(uint32_t (&w)[4], uint32_t at) {
@@ -279,7 +286,8 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
   auto head_of = [&](int w) { return reinterpret_cast<float*>(smem + L::AT_SLOTS + w * L::SLOT); };
   auto tail_of = [&](int w) { return reinterpret_cast<float*>(smem + w * L::QUEUE); };
   int4* info = reinterpret_cast<int4*>(smem + L::AT_INFO);  // [warp]: item of the head piece, of the tail, tail begins, its last CTA
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::AT_INFO + kWarps * 16);
+  int2* info_len = reinterpret_cast<int2*>(info + kWarps);  // ... keys of their sequences
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::AT_INFO + kWarps * 24);
   const uint32_t bars = smem_u32(smem + L::AT_BARS) + warp * L::STAGES * 8;
   if (lane < L::STAGES) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + lane * 8) : "memory");
   if (threadIdx.x == 0) *abort_flag = 0;
@@ -288,13 +296,17 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
   grid_dep_trigger();  // the joining kernel may start when CTAs leave; it reads nothing of this one before it has ended
 
   // ---- the warp's part of the line of tiles
+  // Few sequences: every warp adds all lengths up by itself.  Many: a sum for each 32 of them in shared memory.
   int64_t* sums = reinterpret_cast<int64_t*>(smem);
+  constexpr int FEW = 8;
   const int chunks = (n_seqs + 31) / 32;
-  int lens = lane < n_seqs ? a.lens[lane] : 0;  // of the 32 sequences that the warp is among
-  int64_t in = 0, total = 0;                     // tiles up to a sequence of them, of all
-  if (chunks == 1) {
-    in = warp_scan(units_of<L::END>(lens, cap), lane);
-    total = __shfl_sync(0xffffffffu, in, 31);
+  int few[FEW];
+  int64_t few_sum[FEW], total = 0;
+  if (chunks <= FEW) {
+#pragma unroll
+    for (int i = 0; i < FEW; ++i) few[i] = i * 32 + lane < n_seqs ? a.lens[i * 32 + lane] : 0;
+#pragma unroll
+    for (int i = 0; i < FEW; ++i) total += few_sum[i] = i < chunks ? warp_sum(units_of<L::END>(few[i], cap)) : 0;
   } else {
     for (int ch = warp; ch < chunks; ch += kWarps) {
       const int b = ch * 32 + lane;
@@ -316,11 +328,20 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
     left = t0 + (t1 - t0) * (warp + 1) / kWarps - first;
   }
   const int64_t next = first + left;  // the tile after the part
-  int b0 = 0, hk0 = 0, tile0 = 0;
+  int b0 = 0, hk0 = 0, tile0 = 0, lens = 0;  // lens: of the 32 sequences that b0 is among
   if (left > 0) {
     int64_t before = 0;
     const int64_t seq_first = mul_div(first, 1, hkv);  // the tile's place if there were one head
-    if (chunks > 1) {
+    if (chunks <= FEW) {
+      lens = few[0];
+#pragma unroll
+      for (int i = 1; i < FEW; ++i)
+        if (i < chunks && before + few_sum[i - 1] <= seq_first && b0 == (i - 1) * 32) {
+          before += few_sum[i - 1];
+          b0 = i * 32;
+          lens = few[i];
+        }
+    } else {
       int ch = 0;
       for (int base = 0; base < chunks; base += 32) {
         const int64_t v = base + lane < chunks ? sums[base + lane] : 0, upto = warp_scan(v, lane);
@@ -334,8 +355,8 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
       }
       b0 = ch * 32;
       lens = b0 + lane < n_seqs ? a.lens[b0 + lane] : 0;
-      in = warp_scan(units_of<L::END>(lens, cap), lane);
     }
+    const int64_t in = warp_scan(units_of<L::END>(lens, cap), lane);
     const int at = max(__ffs(__ballot_sync(0xffffffffu, before + in > seq_first)) - 1, 0);
     const int n = max(units_of<L::END>(__shfl_sync(0xffffffffu, lens, at), cap), 1);
     before += __shfl_sync(0xffffffffu, in, at) - n;
@@ -368,23 +389,68 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
       }
     }
   }
-  if (chunks > 1) {
+  if (chunks > FEW) {
     fence_async();    // the queues, which the copies fill, take the place of the sums
     __syncthreads();
   }
 
   int4 left_over = make_int4(-1, -1, 0, 0);
+  int2 left_len = make_int2(0, 0);
   if (left > 0) {
     const uint32_t queue = smem_u32(smem) + warp * L::QUEUE, scale_queue = smem_u32(smem + L::AT_SCALES) + warp * L::STAGES * L::SCALES + lane * 4;
     const float* scales = FP8 ? (c < 2 ? a.c.k_scale : a.c.v_scale) : nullptr;
     const int s_key = r + 8 * (c & 1);  // the key whose scale this lane brings in: of K for c < 2, else of V
+
+    // ---- queries of an item, fetched as they lie and then made fragments
+    float rs[NT][2];
+    uint32_t q[NT][L::KS][2];
+    auto fetch = [&](int b, int hk) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const int R = rb * L::ROWS + nt * 8 + r;
+        const RowAt at = row_at(a, g, b, hk, min(R, rows - 1));
+        const bf16* src = a.q + at.head * a.q_head + at.tok * a.q_tok;
+#pragma unroll
+        for (int s = 0; s < L::KS; ++s) {  // a step's 16 elements; with e4m3 in fours to a lane, as the codes of a 16-byte piece
+          if (FP8) {
+            const uint2 w = R < rows ? *reinterpret_cast<const uint2*>(src + 16 * s + 4 * c) : make_uint2(0, 0);
+            q[nt][s][0] = w.x;
+            q[nt][s][1] = w.y;
+          } else {
+            q[nt][s][0] = R < rows ? *reinterpret_cast<const uint32_t*>(src + 16 * s + 2 * c) : 0u;
+            q[nt][s][1] = R < rows ? *reinterpret_cast<const uint32_t*>(src + 16 * s + 8 + 2 * c) : 0u;
+          }
+        }
+      }
+    };
+    // fp16 under a power of two for each row: bf16's 8 bits fit, elements below 2^-14 of the largest lose what fp32 sums would lose
+    auto convert = [&]() {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        uint32_t big = 0;
+#pragma unroll
+        for (int s = 0; s < L::KS; ++s) big = amax2(big, amax2(q[nt][s][0], q[nt][s][1]));
+        big = pair_bits(big);
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
+        const int ex = min(max((int)(big >> 23) - 127, -126), 126);
+        const float down = pow2(-ex), up = pow2(ex) * (a.scale * kLog2e);
+#pragma unroll
+        for (int s = 0; s < L::KS; ++s)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            q[nt][s][i] = pack_half(__uint_as_float(q[nt][s][i] << 16) * down, __uint_as_float(q[nt][s][i] & 0xffff0000u) * down);
+        rs[nt][0] = __shfl_sync(0xffffffffu, up, 8 * c);
+        rs[nt][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
+      }
+    };
 
     // ---- the end of the line that loads.  Lengths of 32 sequences and 32 entries of the table lie in the lanes; the
     // entries that follow are on their way while those are used.
     const int ps = a.c.page_size;
     int pb = b0, phk = hk0, pt = tile0, plen = min(max(__shfl_sync(0xffffffffu, lens, b0 & 31), 0), cap), pn = tiles_of(plen, cap);
     int ppi = pt * kTileKeys / ps, prow = pt * kTileKeys - ppi * ps;
-    int held = (plen + (ps - 1)) / ps;  // pages of the sequence
+    int held = (int)(((unsigned)plen + (ps - 1)) / ps);  // pages of the sequence
     int plens = lens;
     int64_t to_load = left;
     auto entries = [&](int b, int first_page) {
@@ -400,6 +466,7 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
       return next_seq(b, l) ? entries(b, 0) : -1;
     };
     int ids = entries(pb, ppi & ~31), ids_after = following();
+    fetch(b0, hk0);  // behind the copies it would take microseconds
     uint32_t in_flight = 0;  // stages that a copy is on its way to; those of tiles whose page does not exist stay as they are
     bool ok = true;          // no wait ran out
     auto load = [&](int stage) {
@@ -437,7 +504,7 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
             if (!next_seq(pb, plens)) pb = n_seqs - 1;  // only if the lengths changed meanwhile
             plen = min(max(__shfl_sync(0xffffffffu, plens, pb & 31), 0), cap);
             pn = tiles_of(plen, cap);
-            held = (plen + (ps - 1)) / ps;
+            held = (int)(((unsigned)plen + (ps - 1)) / ps);
           }
         }
         if (fresh) {
@@ -446,7 +513,7 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
         }
       }
     };
-#pragma unroll
+#pragma unroll 1
     for (int s = 0; s < L::STAGES - 1; ++s) {
       if (to_load > 0) load(s);
       if (FP8) cp_commit();
@@ -463,49 +530,16 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
     int cb = b0, chk = hk0, ct = tile0, raw = __shfl_sync(0xffffffffu, lens, b0 & 31), len = min(max(raw, 0), cap), cn = tiles_of(len, cap);
     int stage = 0;
     uint32_t phases = 0;
-    float m[NT][2], l[NT][2], mv[NT][2], acc[NT][L::MT][4], rs[NT][2];
-    uint32_t q[NT][L::KS][2];
+    float m[NT][2], l[NT][2], mv[NT][2], acc[NT][L::MT][4];
     int see[NT][2];  // a row sees keys before len + see
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) see[nt][e] = min((rb * L::ROWS + nt * 8 + 2 * c + e) / g, a.q_len - 1) - a.q_len + 1;
     while (left > 0) {
-      // ---- an item begins: its queries
+      if (FP8) convert();
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const int R = rb * L::ROWS + nt * 8 + r;
-        const RowAt at = row_at(a, g, cb, chk, min(R, rows - 1));
-        const bf16* src = a.q + at.head * a.q_head + at.tok * a.q_tok;
-        if (!FP8) {
-#pragma unroll
-          for (int s = 0; s < L::KS; ++s)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) q[nt][s][i] = R < rows ? *reinterpret_cast<const uint32_t*>(src + 16 * s + 8 * i + 2 * c) : 0u;
-          rs[nt][0] = rs[nt][1] = a.scale * kLog2e;
-        } else {
-          // fp16 under a power of two for each row: bf16's 8 bits fit, elements below 2^-14 of the largest lose what fp32 sums
-          // would lose.  A step's 16 elements go to lanes in fours, as the codes of a 16-byte piece do.
-          uint2 w[L::KS];
-          uint32_t big = 0;
-#pragma unroll
-          for (int s = 0; s < L::KS; ++s) {
-            w[s] = R < rows ? *reinterpret_cast<const uint2*>(src + 16 * s + 4 * c) : make_uint2(0, 0);
-            big = amax2(big, amax2(w[s].x, w[s].y));
-          }
-          big = pair_bits(big);
-          big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
-          big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-          const int ex = min(max((int)(big >> 23) - 127, -126), 126);
-          const float down = pow2(-ex), up = pow2(ex) * (a.scale * kLog2e);
-#pragma unroll
-          for (int s = 0; s < L::KS; ++s) {
-            q[nt][s][0] = pack_half(__uint_as_float(w[s].x << 16) * down, __uint_as_float(w[s].x & 0xffff0000u) * down);
-            q[nt][s][1] = pack_half(__uint_as_float(w[s].y << 16) * down, __uint_as_float(w[s].y & 0xffff0000u) * down);
-          }
-          rs[nt][0] = __shfl_sync(0xffffffffu, up, 8 * c);
-          rs[nt][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
-        }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           m[nt][e] = mv[nt][e] = kLowest;
@@ -603,7 +637,7 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            x[nt][i] *= rs[nt][i & 1];
+            x[nt][i] *= FP8 ? rs[nt][i & 1] : a.scale * kLog2e;
             if (FP8) y[nt][i] = x[nt][i] + lv[i >> 1];
           }
         if (k0 > len - a.q_len + 1 - kTileKeys || lost) {
@@ -709,10 +743,12 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
         drain(bars, in_flight, phases);
         if (FP8) cp_wait<0>();
         left_over.y = item;
+        left_len.y = len;
         left_over.z = begins;
         left_over.w = last_part(max(next + cn - ct, next), total, parts);  // the CTA whose part holds the item's last tile
       } else if (!whole) {
         left_over.x = item;
+        left_len.x = len;
       }
       __syncwarp();
       uint32_t again = 0;  // rows (8 nt + row) whose o has to be summed once more
@@ -822,89 +858,110 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
           len = min(max(raw, 0), cap);
           cn = tiles_of(len, cap);
         }
+        fetch(cb, chk);
       }
     }
     drain(bars, in_flight, phases);
     if (FP8) cp_wait<0>();
   }
 
-  // ---- the CTA's pieces, in order: lane i of every warp has piece i (2 warp: head, 2 warp + 1: tail), runs of one item are joined,
-  // a row to a warp
-  if (lane == 0) info[warp] = left_over;
+  // ---- the CTA's pieces, in order: lane i of every warp has piece i (2 warp: head, 2 warp + 1: tail).  Runs of one item are
+  // joined; the warps share the runs out, and a run's rows among those that have the same one.
+  if (lane == 0) {
+    info[warp] = left_over;
+    info_len[warp] = left_len;
+  }
   __syncthreads();
   int4 meta = make_int4(-1, -1, 0, 0);
   const int64_t place = (int64_t)rb * X + blockIdx.x;
   static_assert(2 * kWarps <= 32, "a piece to a lane");
   const int4 mine = lane < 2 * kWarps ? info[lane >> 1] : make_int4(-1, -1, 0, 0);
+  const int2 my_len = lane < 2 * kWarps ? info_len[lane >> 1] : make_int2(0, 0);
   const int my_item = lane & 1 ? mine.y : mine.x;
-  const float* my_piece = lane & 1 ? tail_of(lane >> 1) : head_of(lane >> 1);
   const unsigned valid = __ballot_sync(0xffffffffu, my_item >= 0), below = valid & ((1u << lane) - 1u);
   const int prev = __shfl_sync(0xffffffffu, my_item, below ? 31 - __clz(below) : 0);
   unsigned starts = __ballot_sync(0xffffffffu, my_item >= 0 && (!below || prev != my_item));
-  while (starts) {
+  const int n_runs = __popc(starts), share = n_runs ? max(kWarps / n_runs, 1) : 1;  // warps to a run
+#pragma unroll 1
+  for (int i = 0; starts; ++i) {
     const int s = __ffs(starts) - 1;
     starts &= starts - 1;
     const unsigned run = valid & ~((1u << s) - 1u) & (starts ? (1u << (__ffs(starts) - 1)) - 1u : 0xffffffffu);
     const int last = 31 - __clz(run), item = __shfl_sync(0xffffffffu, my_item, s);
-    const bool begins = (s & 1) && __shfl_sync(0xffffffffu, mine.z, s), ends = !(last & 1), member = run >> lane & 1;
-    const int end_part = __shfl_sync(0xffffffffu, mine.w, last);
+    const bool begins = (s & 1) && __shfl_sync(0xffffffffu, mine.z, s), ends = !(last & 1);
+    if (!ends) {
+      meta.y = item;
+      meta.z = begins;
+      meta.w = __shfl_sync(0xffffffffu, mine.w, last);
+    } else if (!begins) {
+      meta.x = item;
+    }
+    const int mates = n_runs < kWarps ? share : 1, me = n_runs < kWarps ? warp - i * share : warp - i % kWarps;
+    if (me < 0 || me >= mates) continue;
+    constexpr int E = D / 32, RB = 4;  // elements of a lane, rows at a time
+    const int b = item / hkv, hk = item - b * hkv, len = __shfl_sync(0xffffffffu, lane & 1 ? my_len.y : my_len.x, s);
 #pragma unroll 1
-    for (int row = warp; row < L::ROWS && rb * L::ROWS + row < rows; row += kWarps) {
-      constexpr int E = D / 32;
-      RowSum sum{kLowest, 0.f};
-      if (member) sum = reinterpret_cast<const RowSum*>(my_piece + L::ROWS * D)[row];
-      float top = sum.m;
+    for (int row0 = me * RB; row0 < L::ROWS && rb * L::ROWS + row0 < rows; row0 += mates * RB) {
+      RowSum sum[RB];
+      float o[RB][E];
 #pragma unroll
-      for (int off = kWarps; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-      const float f = fast_exp2(sum.m - top);
-      float l = member ? sum.l * f : 0.f, o[E] = {};
+      for (int k = 0; k < RB; ++k) {
+        sum[k] = RowSum{kLowest, 0.f};
 #pragma unroll
-      for (int off = kWarps; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+        for (int e = 0; e < E; ++e) o[k][e] = 0.f;
+      }
 #pragma unroll 1
-      for (unsigned rest = run; rest;) {  // four pieces at a time
-        const float* src[4];
-        float w[4], v[4][E];
+      for (unsigned rest = run; rest;) {  // two pieces at a time
+        RowSum ps[2][RB];
+        float v[2][RB][E];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int i = rest ? __ffs(rest) - 1 : -1;
+        for (int j = 0; j < 2; ++j) {
+          const bool in = rest;
+          const int p = in ? __ffs(rest) - 1 : s;
           rest &= rest - 1;
-          w[j] = __shfl_sync(0xffffffffu, f, i & 31);
-          src[j] = i < 0 ? nullptr : (i & 1 ? tail_of(i >> 1) : head_of(i >> 1)) + row * D + lane * E;
+          const uint32_t at = smem_u32(smem) + (p & 1 ? (p >> 1) * L::QUEUE : L::AT_SLOTS + (p >> 1) * L::SLOT);
+#pragma unroll
+          for (int k = 0; k < RB; ++k) {
+            lds_floats<2>(reinterpret_cast<float*>(&ps[j][k]), at + L::ROWS * D * 4 + (row0 + k) * (int)sizeof(RowSum));
+            lds_floats<E>(v[j][k], at + ((row0 + k) * D + lane * E) * 4);
+            if (!in) {
+              ps[j][k] = RowSum{kLowest, 0.f};
+#pragma unroll
+              for (int e = 0; e < E; ++e) v[j][k][e] = 0.f;
+            }
+          }
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
+        for (int k = 0; k < RB; ++k) {
+          const float top = fmaxf(fmaxf(ps[0][k].m, ps[1][k].m), sum[k].m);
+          const float f = fast_exp2(sum[k].m - top), f0 = fast_exp2(ps[0][k].m - top), f1 = fast_exp2(ps[1][k].m - top);
+          sum[k] = RowSum{top, sum[k].l * f + ps[0][k].l * f0 + ps[1][k].l * f1};
 #pragma unroll
-          for (int e = 0; e < E; ++e) v[j][e] = src[j] ? src[j][e] : 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[e] += src[j] ? v[j][e] * w[j] : 0.f;
+          for (int e = 0; e < E; ++e) o[k][e] = o[k][e] * f + v[0][k][e] * f0 + v[1][k][e] * f1;
+        }
       }
-      top = __shfl_sync(0xffffffffu, top, 0);  // lanes that hold no piece have not taken part
-      l = __shfl_sync(0xffffffffu, l, 0);
-      if (begins && ends) {
-        const int b = item / hkv, R = rb * L::ROWS + row, seen = min(a.lens[b], cap) - a.q_len + 1 + R / g;
-        const RowAt at = row_at(a, g, b, item - b * hkv, R);
-        bf16* dst = a.o + at.head * a.o_head + at.tok * a.o_tok + lane * E;
-        const float inv = 1.f / l;
 #pragma unroll
-        for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = seen <= 0 ? 0u : pack_bf16(o[e] * inv, o[e + 1] * inv);
-        if (a.lse && lane == 0) a.lse[at.head * n_seqs * a.q_len + at.tok] = seen <= 0 ? -INFINITY : row_lse(top, l);
-      } else {
-        const int64_t at = (place * 2 + (ends ? 0 : 1)) * L::ROWS + row;
-        float* dst = ws.acc + at * D + lane * E;
+      for (int k = 0; k < RB; ++k) {
+        const int row = row0 + k, R = rb * L::ROWS + row;
+        if (R >= rows) break;
+        if (begins && ends) {
+          const bool none = len - a.q_len + 1 + R / g <= 0;
+          const RowAt at = row_at(a, g, b, hk, R);
+          const float inv = 1.f / sum[k].l;
+          uint32_t w[E / 2];
 #pragma unroll
-        for (int e = 0; e < E; ++e) dst[e] = o[e];
-        if (lane == 0) ws.sums[at] = RowSum{top, l};
-      }
-    }
-    if (!begins || !ends) {
-      if (ends) {
-        meta.x = item;
-      } else {
-        meta.y = item;
-        meta.z = begins;
-        meta.w = end_part;
+          for (int e = 0; e < E; e += 2) w[e / 2] = none ? 0u : pack_bf16(o[k][e] * inv, o[k][e + 1] * inv);
+          uint32_t* dst = reinterpret_cast<uint32_t*>(a.o + at.head * a.o_head + at.tok * a.o_tok + lane * E);
+          if (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[E / 2 - 1]);
+          else *dst = w[0];
+          if (a.lse && lane == 0) a.lse[at.head * n_seqs * a.q_len + at.tok] = none ? -INFINITY : row_lse(sum[k].m, sum[k].l);
+        } else {
+          const int64_t at = (place * 2 + (ends ? 0 : 1)) * L::ROWS + row;
+          float* dst = ws.acc + at * D + lane * E;
+          if (E == 4) *reinterpret_cast<float4*>(dst) = make_float4(o[k][0], o[k][1], o[k][E - 2], o[k][E - 1]);
+          else *reinterpret_cast<float2*>(dst) = make_float2(o[k][0], o[k][1]);
+          if (lane == 0) ws.sums[at] = sum[k];
+        }
       }
     }
   }
@@ -918,7 +975,7 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
 // ROWS 1: all warps share a row's pieces, for the long chains of few.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) k_decode_join(const __grid_constant__ DecodeArgs a, const DecodeWs ws, int block_rows) {
-  constexpr int LN = D / 4, GR = kJoinThreads / LN / ROWS, AHEAD = ROWS == 1 ? 8 : 4;  // lanes and groups of a row, pieces in flight
+  constexpr int LN = D / 4, GR = kJoinThreads / LN / ROWS, AHEAD = ROWS == 1 ? 10 : 4;  // lanes and groups of a row, pieces in flight
   __shared__ float4 part[ROWS == 1 ? GR : 1][LN];
   __shared__ RowSum part_sums[GR];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, x = blockIdx.x, X = gridDim.x;
@@ -943,7 +1000,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_decode_join(const __grid_const
     }
   }
   const int R = blockIdx.y * ROWS + (ROWS == 1 ? 0 : tid / (kJoinThreads / ROWS));
-  const int rb = R / block_rows, row = R - rb * block_rows;  // 8 rows lie in one block of rows
+  const int rb = R / block_rows, row = R - rb * block_rows;
   grid_dep_wait();
   const int64_t place = (int64_t)rb * X + x;
   const int4 me = ws.meta[place];

@@ -3,11 +3,12 @@
 //   write  bf16: the row;  e4m3: s = max|x| fp32(1 / 448) (1 below 2^-100), q = e4m3(fp32(x / s)) for each row
 //   read   bf16: the row;  e4m3: bf16(q s)
 //
-// A row belongs to a group of head_dim / 8 neighbouring lanes, 16 bytes of bf16 each, so its maximum is three or four
-// shuffles.  A block takes a chunk of tokens: its threads look up a token's place each, then a group takes one head of keys
-// or values for a run of up to 16 tokens, several rows in flight, and writes the run's scales together.  Runs are as long as
-// the number of tokens allows: a decode step's few tokens spread over blocks, a prompt's rows share their lookups.  Bound by
-// HBM for prompts; a few tokens are bound by the launch.
+// A row belongs to a group of neighbouring lanes: head_dim / 8 with 16 bytes of bf16 each, or, with e4m3, head_dim / 16 with
+// two such pieces half a row apart, since what a row costs beside its elements (the place, the maximum's shuffles, the scale
+// and its reciprocal) then falls to half as many.  A block takes a chunk of tokens: its threads look up a token's place
+// each, then a group takes one head of keys or values for a run of up to 16 tokens, several rows in flight.  Runs are as
+// long as the number of tokens allows: a decode step's few tokens spread over blocks, a prompt's rows share their lookups.
+// Bound by HBM for prompts (and, quantising, by the instructions beside it); a few tokens are bound by the launch.
 #include "internal.h"
 #include "kv_cache.cuh"
 #include "quant.cuh"
@@ -17,7 +18,8 @@ namespace upipe {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kMaxRun = 16, kMaxChunk = kMaxRun * kThreads / 8 / 2;  // tokens of a group, of a block (two rows of one head at least)
+constexpr int kMaxRun = 16;                             // tokens of a group
+constexpr int kMaxChunk = kMaxRun * (kThreads / 4) / 2;  // of a block: two rows of one head, four lanes each
 
 struct KvParams {
   KvCache c;
@@ -33,21 +35,9 @@ struct Place {
   int64_t row, scale;
 };
 
-// The rows of a run, AHEAD at a time: load(j, token, place) and store(j, token, place) see the same places.
-template <int AHEAD, typename Load, typename Store>
-__device__ __forceinline__ void walk(const Place* places, int64_t first, int n, const Load& load, const Store& store) {
-  for (int i = 0; i < n; i += AHEAD) {
-#pragma unroll
-    for (int j = 0; j < AHEAD; ++j)
-      if (i + j < n) load(j, first + i + j, places[i + j]);
-#pragma unroll
-    for (int j = 0; j < AHEAD; ++j)
-      if (i + j < n) store(j, i + j, first + i + j, places[i + j]);
-  }
-}
-
 template <bool WRITE, bool FP8>
 __global__ void __launch_bounds__(kThreads) k_kv_copy(const __grid_constant__ KvParams p) {
+  constexpr int PIECES = FP8 ? 2 : 1, AHEAD = 4;
   __shared__ Place places[kMaxChunk];
   const int chunk = p.run * p.runs;
   const int64_t first = (int64_t)blockIdx.x * chunk;
@@ -61,83 +51,89 @@ __global__ void __launch_bounds__(kThreads) k_kv_copy(const __grid_constant__ Kv
     places[i] = q;
   }
   __syncthreads();
-  const int lanes = p.c.head_dim >> 3, u = threadIdx.x & (lanes - 1), grp = threadIdx.x / lanes;
+  const int lanes = p.c.head_dim / (8 * PIECES), half = p.c.head_dim >> 1, u = threadIdx.x & (lanes - 1), grp = threadIdx.x / lanes;
   const int nh = p.c.n_kv_heads, local = grp / p.runs, r = blockIdx.y * p.rows + local;
   if (local >= p.rows || r >= 2 * nh) return;
   const int start = (grp - local * p.runs) * p.run, len = min(p.run, n - start);
-  if (len <= 0) return;
   const int h = r < nh ? r : r - nh;
   const KvHeads& s = r < nh ? p.k : p.v;
-  bf16* plain = s.p + h * s.head_stride + u * 8;
-  const int64_t ts = s.token_stride, head = h * p.c.head_stride + u * 8, scale_head = h * p.c.scale_head_stride;
-  uint8_t* codes = reinterpret_cast<uint8_t*>(r < nh ? p.c.k : p.c.v);
-  bf16* cached = reinterpret_cast<bf16*>(codes);
-  float* scales = r < nh ? p.c.k_scale : p.c.v_scale;
-  const unsigned group = (lanes == 32 ? 0xffffffffu : (1u << lanes) - 1u) << (threadIdx.x & 31 & ~(lanes - 1));
-  if (WRITE) {
-    constexpr int AHEAD = 4;
-    uint4 x[AHEAD];
-    float my_scale = 1.f;  // of the run's token u
-    walk<AHEAD>(
-        places + start, first + start, len,
-        [&](int j, int64_t tok, const Place& at) {
-          x[j] = at.row >= 0 ? *reinterpret_cast<const uint4*>(plain + tok * ts) : make_uint4(0, 0, 0, 0);
-        },
-        [&](int j, int i, int64_t, const Place& at) {
-          if (!FP8) {
-            if (at.row >= 0) *reinterpret_cast<uint4*>(cached + at.row + head) = x[j];
-            return;
-          }
-          uint32_t m = pair_bits(amax2(x[j]));
-          for (int off = lanes >> 1; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(group, m, off));
-          const float sc = block_scale(m);
-          const Divisor by = divisor(sc);
-          const V8 f = unpack8(x[j]);
-          const uint2 q = by.doubt ? quant8_divided(f, sc) : quant8(f, by);
-          if (at.row >= 0) *reinterpret_cast<uint2*>(codes + at.row + head) = q;
-          if ((i & (lanes - 1)) == u) my_scale = sc;
-          if ((i & (lanes - 1)) == lanes - 1 || i == len - 1) {  // a scale to a lane
-            const int mine = (i & ~(lanes - 1)) + u;
-            if (mine <= i) {
-              const Place to = places[start + mine];
-              if (to.row >= 0) scales[to.scale + scale_head] = my_scale;
-            }
-          }
-        });
-  } else {
-    constexpr int AHEAD = FP8 ? 8 : 4;
-    uint4 x[AHEAD];
+  bf16* plain = s.p + h * s.head_stride + (first + start) * s.token_stride + u * 8;
+  const int64_t head = h * p.c.head_stride + u * 8;
+  uint8_t* codes = reinterpret_cast<uint8_t*>(r < nh ? p.c.k : p.c.v) + head;
+  bf16* cached = reinterpret_cast<bf16*>(r < nh ? p.c.k : p.c.v) + head;
+  float* scales = (r < nh ? p.c.k_scale : p.c.v_scale) + h * p.c.scale_head_stride;
+  const unsigned group = ((1u << lanes) - 1u) << (threadIdx.x & 31 & ~(lanes - 1));
+#pragma unroll 1
+  for (int i = 0; i < len; i += AHEAD, plain += AHEAD * s.token_stride) {
+    Place at[AHEAD];
+    uint4 x[AHEAD][PIECES];
     float sc[AHEAD];
-    walk<AHEAD>(
-        places + start, first + start, len,
-        [&](int j, int64_t, const Place& at) {
-          x[j] = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);  // a row that the cache does not hold is NaN
-          if (at.row < 0) return;
-          if (FP8) {
-            const uint2 q = *reinterpret_cast<const uint2*>(codes + at.row + head);
-            x[j].x = q.x;
-            x[j].y = q.y;
-            sc[j] = scales[at.scale + scale_head];
-          } else {
-            x[j] = *reinterpret_cast<const uint4*>(cached + at.row + head);
-          }
-        },
-        [&](int j, int, int64_t tok, const Place& at) {
-          if (FP8 && at.row >= 0) {
-            V8 f = e4m3x8(make_uint2(x[j].x, x[j].y));
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      at[j] = i + j < len ? places[start + i + j] : Place{-2, 0};
+#pragma unroll
+      for (int k = 0; k < PIECES; ++k) {
+        // a row that is not written counts as zeros; one that the cache does not hold reads as NaN
+        x[j][k] = WRITE ? make_uint4(0, 0, 0, 0) : make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
+        if (at[j].row < 0) continue;
+        if (WRITE) {
+          x[j][k] = *reinterpret_cast<const uint4*>(plain + j * s.token_stride + k * half);
+        } else if (FP8) {
+          const uint2 q = *reinterpret_cast<const uint2*>(codes + at[j].row + k * half);
+          x[j][k].x = q.x;
+          x[j][k].y = q.y;
+        } else {
+          x[j][k] = *reinterpret_cast<const uint4*>(cached + at[j].row);
+        }
+      }
+      if (FP8 && !WRITE && at[j].row >= 0) sc[j] = scales[at[j].scale];
+    }
+    if (WRITE && FP8) {
+      uint32_t m[AHEAD];
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) m[j] = pair_bits(amax2(amax2(x[j][0]), amax2(x[j][PIECES - 1])));
+      for (int off = lanes >> 1; off > 0; off >>= 1)
+#pragma unroll
+        for (int j = 0; j < AHEAD; ++j) m[j] = max(m[j], __shfl_xor_sync(group, m[j], off));
+#pragma unroll
+      for (int j = 0; j < AHEAD; ++j) sc[j] = block_scale(m[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < AHEAD; ++j) {
+      if (at[j].row < (WRITE ? 0 : -1)) continue;
+      const Divisor by = divisor(WRITE && FP8 ? sc[j] : 1.f);
+#pragma unroll
+      for (int k = 0; k < PIECES; ++k) {
+        if (WRITE && FP8) {
+          const V8 f = unpack8(x[j][k]);
+          *reinterpret_cast<uint2*>(codes + at[j].row + k * half) = by.doubt ? quant8_divided(f, sc[j]) : quant8(f, by);
+        } else if (WRITE) {
+          *reinterpret_cast<uint4*>(cached + at[j].row) = x[j][k];
+        } else {
+          if (FP8 && at[j].row >= 0) {
+            V8 f = e4m3x8(make_uint2(x[j][k].x, x[j][k].y));
 #pragma unroll
             for (int e = 0; e < 8; ++e) f.v[e] *= sc[j];
-            x[j] = pack8(f);
+            x[j][k] = pack8(f);
           }
-          if (at.row != -2) *reinterpret_cast<uint4*>(plain + tok * ts) = x[j];
-        });
+          *reinterpret_cast<uint4*>(plain + j * s.token_stride + k * half) = x[j][k];
+        }
+      }
+    }
+    if (WRITE && FP8) {  // four lanes write the four scales
+      static_assert(AHEAD == 4, "a scale to a lane");
+      const float mine = u & 2 ? (u & 1 ? sc[3] : sc[2]) : (u & 1 ? sc[1] : sc[0]);
+      const int64_t row = u & 2 ? (u & 1 ? at[3].row : at[2].row) : (u & 1 ? at[1].row : at[0].row);
+      const int64_t to = u & 2 ? (u & 1 ? at[3].scale : at[2].scale) : (u & 1 ? at[1].scale : at[0].scale);
+      if (u < 4 && row >= 0) scales[to] = mine;
+    }
   }
 }
 
 template <typename K>
 cudaError_t run(K kfn, const KvArgs& a, cudaStream_t st) {
   if (a.tokens <= 0) return cudaSuccess;
-  const int groups = kThreads / (a.c.head_dim >> 3), rows = 2 * a.c.n_kv_heads;
+  const int groups = kThreads * (a.c.e4m3 ? 16 : 8) / a.c.head_dim, rows = 2 * a.c.n_kv_heads;
   KvParams p{a.c, a.t, a.k, a.v, a.seq, a.pos, a.tokens, kMaxRun, 1, std::min(rows, groups)};
   p.runs = groups / p.rows;
   const int64_t by = ceil_div(rows, p.rows);
