@@ -17,7 +17,7 @@ namespace upipe {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kMaxRun = 16;                             // tokens of a group
 constexpr int kMaxChunk = kMaxRun * (kThreads / 4) / 2;  // of a block: two rows of one head, four lanes each
 
@@ -35,8 +35,10 @@ struct Place {
   int64_t row, scale;
 };
 
+// Five blocks to an SM for the quantiser (96 registers; without the bound 102 us instead of 91 at 112K tokens x 8 heads, with
+// six 92); the others are given registers as the compiler likes (read of 1M tokens x 1 head 124 us, 140 at 64 registers).
 template <bool WRITE, bool FP8>
-__global__ void __launch_bounds__(kThreads) k_kv_copy(const __grid_constant__ KvParams p) {
+__global__ void __launch_bounds__(kThreads, WRITE && FP8 ? 5 : 1) k_kv_copy(const __grid_constant__ KvParams p) {
   constexpr int PIECES = FP8 ? 2 : 1, AHEAD = 4;
   __shared__ Place places[kMaxChunk];
   const int chunk = p.run * p.runs;
