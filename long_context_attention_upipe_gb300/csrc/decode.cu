@@ -41,7 +41,7 @@ constexpr int kTileKeys = 16;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.0e38f;  // a reference below all scores, whose difference to them is defined
 constexpr float kSlack = 8.f;        // a score may exceed the reference by this, in powers of two
-constexpr float kSlackV = 5.f, kShiftV = 10.f;  // fp16 weights: the reference stands for 2^10, the largest is below 2^15
+constexpr float kSlackV = 5.f, kShiftV = 10.f;  // fp16 weights: the reference of one lies 10 below the score, the largest is 2^15
 
 // What a row of a piece (or of a joined run of pieces) leaves beside its D sums.
 struct RowSum {
@@ -57,14 +57,15 @@ struct Lay {
   static constexpr int STAGE = 2 * KBYTES;              // keys and values of a tile
   static constexpr int SCALES = FP8 ? 128 : 0;          // their scales
   static constexpr int ROWS = 8 * NT;
-  static constexpr int SLOT = ROWS * (D * 4 + (int)sizeof(RowSum));  // a piece
-  static constexpr int WARPS = 8;
-  static constexpr int END = FP8 ? 2 : 1;               // tiles' time that an item's end (and the next one's begin) takes
-  static constexpr int FIT = (231 * 1024 / WARPS - SLOT - 128) / (STAGE + SCALES + 8);
+  static constexpr int SLOT = ROWS * D * 4;             // sums of a piece's o
+  static constexpr int WARPS = FP8 && NT == 1 ? 16 : 8;
+  static constexpr int END = FP8 ? 4 : 2;               // tiles' time that an item's end (and the next one's begin) takes
+  static constexpr int FIT = ((226 * 1024 - 16) / WARPS - 24 - SLOT - 2 * ROWS * (int)sizeof(RowSum)) / (STAGE + SCALES + 8);
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
   static constexpr int QUEUE = STAGES * STAGE;
   static constexpr int AT_SCALES = WARPS * QUEUE, AT_SLOTS = AT_SCALES + WARPS * STAGES * SCALES;
-  static constexpr int AT_BARS = AT_SLOTS + WARPS * SLOT, AT_INFO = AT_BARS + WARPS * STAGES * 8;
+  static constexpr int AT_SUMS = AT_SLOTS + WARPS * SLOT, AT_BARS = AT_SUMS + WARPS * 2 * ROWS * (int)sizeof(RowSum);
+  static constexpr int AT_INFO = AT_BARS + WARPS * STAGES * 8;
   static constexpr int BYTES = AT_INFO + WARPS * 24 + 16 + 1024;  // the queues start on 1024 bytes
   static constexpr int MT = D / 16;                     // tiles of O^T
   static constexpr int KS = D / 16;                     // steps of S^T
@@ -185,15 +186,16 @@ __device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
 }
 
 // a * b / c of numbers whose product fits 64 bits; most fit 32, where a division takes a fraction of the time.
+__device__ __noinline__ int64_t div64(int64_t p, int64_t c) { return p / c; }
 __device__ __forceinline__ int64_t mul_div(int64_t a, int b, int c) {
   const int64_t p = a * b;
-  return p <= 0xffffffffll ? (int64_t)((uint32_t)p / (uint32_t)c) : p / c;
+  return p <= 0xffffffffll ? (int64_t)((uint32_t)p / (uint32_t)c) : div64(p, c);
 }
 
 // The part that holds tile end - 1 where part i ends before tile total * (i + 1) / parts.
 __device__ __forceinline__ int last_part(int64_t end, int64_t total, int parts) {
   const int64_t p = end * parts + total - 1;
-  return (int)(p <= 0xffffffffll ? (uint32_t)p / (uint32_t)total : p / total) - 1;
+  return (int)(p <= 0xffffffffll ? (int64_t)((uint32_t)p / (uint32_t)total) : div64(p, total)) - 1;
 }
 
 // A query row of a key head: row R is head R % g of the group and token R / g of the q_len newest.
@@ -283,8 +285,9 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
   const int hkv = a.c.n_kv_heads, g = a.hq / hkv, rows = g * a.q_len, cap = table_keys(a.t, a.c.page_size);
   const int n_seqs = a.t.n_seqs;
   // pieces of this warp: the one that ends the item that it began within, and the one left at its end, over the empty queue
-  auto head_of = [&](int w) { return reinterpret_cast<float*>(smem + L::AT_SLOTS + w * L::SLOT); };
-  auto tail_of = [&](int w) { return reinterpret_cast<float*>(smem + w * L::QUEUE); };
+  float* head_slot = reinterpret_cast<float*>(smem + L::AT_SLOTS + warp * L::SLOT);
+  float* tail_slot = reinterpret_cast<float*>(smem + warp * L::QUEUE);
+  RowSum* piece_sums = reinterpret_cast<RowSum*>(smem + L::AT_SUMS);  // [2 warp: head, 2 warp + 1: tail][row]
   int4* info = reinterpret_cast<int4*>(smem + L::AT_INFO);  // [warp]: item of the head piece, of the tail, tail begins, its last CTA
   int2* info_len = reinterpret_cast<int2*>(info + kWarps);  // ... keys of their sequences
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::AT_INFO + kWarps * 24);
@@ -296,18 +299,12 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
   grid_dep_trigger();  // the joining kernel may start when CTAs leave; it reads nothing of this one before it has ended
 
   // ---- the warp's part of the line of tiles
-  // Few sequences: every warp adds all lengths up by itself.  Many: a sum for each 32 of them in shared memory.
-  int64_t* sums = reinterpret_cast<int64_t*>(smem);
-  constexpr int FEW = 8;
+  int lens = lane < n_seqs ? a.lens[lane] : 0;  // of the 32 sequences that b0 is among
+  int b0 = 0;
+  int64_t upto = 0, before = 0, total = 0;  // tiles up to and with a lane's sequence, before the 32, of all
   const int chunks = (n_seqs + 31) / 32;
-  int few[FEW];
-  int64_t few_sum[FEW], total = 0;
-  if (chunks <= FEW) {
-#pragma unroll
-    for (int i = 0; i < FEW; ++i) few[i] = i * 32 + lane < n_seqs ? a.lens[i * 32 + lane] : 0;
-#pragma unroll
-    for (int i = 0; i < FEW; ++i) total += few_sum[i] = i < chunks ? warp_sum(units_of<L::END>(few[i], cap)) : 0;
-  } else {
+  int64_t* sums = reinterpret_cast<int64_t*>(smem);
+  if (chunks > 1) {  // a sum for each 32 sequences
     for (int ch = warp; ch < chunks; ch += kWarps) {
       const int b = ch * 32 + lane;
       const int64_t n = warp_sum(b < n_seqs ? units_of<L::END>(a.lens[b], cap) : 0);
@@ -317,54 +314,13 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
     for (int ch = lane; ch < chunks; ch += 32) total += sums[ch];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
+  } else {
+    upto = warp_scan(units_of<L::END>(lens, cap), lane);
+    total = __shfl_sync(0xffffffffu, upto, 31);
   }
   total *= hkv;
   // no CTA gets less than a tile for each warp
   const int parts = total < (int64_t)X * kWarps ? max((int)(total + kWarps - 1) / kWarps, 1) : X;
-  int64_t first = 0, left = 0;
-  if (blockIdx.x < parts) {
-    const int64_t t0 = mul_div(total, blockIdx.x, parts), t1 = mul_div(total, blockIdx.x + 1, parts);
-    first = t0 + (t1 - t0) * warp / kWarps;
-    left = t0 + (t1 - t0) * (warp + 1) / kWarps - first;
-  }
-  const int64_t next = first + left;  // the tile after the part
-  int b0 = 0, hk0 = 0, tile0 = 0, lens = 0;  // lens: of the 32 sequences that b0 is among
-  if (left > 0) {
-    int64_t before = 0;
-    const int64_t seq_first = mul_div(first, 1, hkv);  // the tile's place if there were one head
-    if (chunks <= FEW) {
-      lens = few[0];
-#pragma unroll
-      for (int i = 1; i < FEW; ++i)
-        if (i < chunks && before + few_sum[i - 1] <= seq_first && b0 == (i - 1) * 32) {
-          before += few_sum[i - 1];
-          b0 = i * 32;
-          lens = few[i];
-        }
-    } else {
-      int ch = 0;
-      for (int base = 0; base < chunks; base += 32) {
-        const int64_t v = base + lane < chunks ? sums[base + lane] : 0, upto = warp_scan(v, lane);
-        const unsigned hit = __ballot_sync(0xffffffffu, before + upto > seq_first);
-        if (hit) {
-          ch = base + __ffs(hit) - 1;
-          before += __shfl_sync(0xffffffffu, upto - v, __ffs(hit) - 1);
-          break;
-        }
-        before += __shfl_sync(0xffffffffu, upto, 31);
-      }
-      b0 = ch * 32;
-      lens = b0 + lane < n_seqs ? a.lens[b0 + lane] : 0;
-    }
-    const int64_t in = warp_scan(units_of<L::END>(lens, cap), lane);
-    const int at = max(__ffs(__ballot_sync(0xffffffffu, before + in > seq_first)) - 1, 0);
-    const int n = max(units_of<L::END>(__shfl_sync(0xffffffffu, lens, at), cap), 1);
-    before += __shfl_sync(0xffffffffu, in, at) - n;
-    b0 = min(b0 + at, n_seqs - 1);
-    const int64_t rest = max(first - before * hkv, (int64_t)0);
-    hk0 = (int)min(mul_div(rest, 1, n), (int64_t)(hkv - 1));  // within bounds even if lengths change under the call
-    tile0 = (int)min(rest - (int64_t)hk0 * n, (int64_t)(n - 1));
-  }
   // the next sequence with keys, or none; `seq_lens`: the lanes' lengths of b's 32 sequences
   auto next_seq = [&](int& b, int& seq_lens) {
     unsigned some = __ballot_sync(0xffffffffu, seq_lens > 0) & ~((2u << (b & 31)) - 1u);
@@ -378,10 +334,39 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
     b += __ffs(some) - 1;
     return true;
   };
+  int64_t first = 0, left = 0;
+  if (blockIdx.x < parts) {
+    const int64_t t0 = mul_div(total, blockIdx.x, parts), t1 = mul_div(total, blockIdx.x + 1, parts);
+    first = t0 + (int64_t)((uint64_t)((t1 - t0) * warp) / kWarps);
+    left = t0 + (int64_t)((uint64_t)((t1 - t0) * (warp + 1)) / kWarps) - first;
+  }
+  const int64_t next = first + left;  // the tile after the part
+  int hk0 = 0, tile0 = 0;
   if (left > 0) {
-    const int tiles = tiles_of(__shfl_sync(0xffffffffu, lens, b0 & 31), cap);
-    if (tile0 >= tiles) {  // within an item's end
-      left -= tiles + L::END - tile0;
+    const int64_t seq_first = mul_div(first, 1, hkv);  // the tile's place if there were one head
+    if (chunks > 1) {
+      for (int base = 0; base < chunks; base += 32) {
+        const int64_t v = base + lane < chunks ? sums[base + lane] : 0, in = warp_scan(v, lane);
+        const unsigned hit = __ballot_sync(0xffffffffu, before + in > seq_first);
+        if (hit) {
+          b0 = (base + __ffs(hit) - 1) * 32;
+          before += __shfl_sync(0xffffffffu, in - v, __ffs(hit) - 1);
+          break;
+        }
+        before += __shfl_sync(0xffffffffu, in, 31);
+      }
+      lens = b0 + lane < n_seqs ? a.lens[b0 + lane] : 0;
+      upto = warp_scan(units_of<L::END>(lens, cap), lane);
+    }
+    const int at = max(__ffs(__ballot_sync(0xffffffffu, before + upto > seq_first)) - 1, 0);
+    const int n = max(units_of<L::END>(__shfl_sync(0xffffffffu, lens, at), cap), 1);
+    before += __shfl_sync(0xffffffffu, upto, at) - n;
+    b0 = min(b0 + at, n_seqs - 1);
+    const int64_t rest = max(first - before * hkv, (int64_t)0);
+    hk0 = (int)min(mul_div(rest, 1, n), (int64_t)(hkv - 1));  // within bounds even if lengths change under the call
+    tile0 = (int)min(rest - (int64_t)hk0 * n, (int64_t)(n - 1));
+    if (tile0 >= n - L::END) {  // within an item's end
+      left -= n - tile0;
       tile0 = 0;
       if (++hk0 == hkv) {
         hk0 = 0;
@@ -389,8 +374,8 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
       }
     }
   }
-  if (chunks > FEW) {
-    fence_async();    // the queues, which the copies fill, take the place of the sums
+  if (chunks > 1) {
+    fence_async();  // the queues, which the copies fill, take the place of the sums
     __syncthreads();
   }
 
@@ -551,17 +536,6 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
           for (int i = 0; i < 4; ++i) acc[nt][mt][i] = 0.f;
       }
       const int begin = ct;
-      if (left > cn - ct + L::END) {  // another item follows: its queries come nearer
-        constexpr int LINES = D * 2 / 128;
-        int b = cb, hk = chk + 1, l = lens;
-        if (hk < hkv || (hk = 0, next_seq(b, l))) {
-          const int R = rb * L::ROWS + lane / LINES;
-          const RowAt at = row_at(a, g, b, hk, min(R, rows - 1));
-          const bf16* src = a.q + at.head * a.q_head + at.tok * a.q_tok + lane % LINES * 64;
-          if (lane < L::ROWS * LINES && R < rows) asm volatile("prefetch.global.L1 [%0];" ::"l"(src));
-        }
-      }
-
       // ---- its tiles
       do {
         __syncwarp();  // all lanes have read the stage that is loaded next
@@ -620,9 +594,9 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[nt][i] += s2[nt][i];
         }
-        // ---- scores in units of log2: x of keys r (0, 1) and r + 8 (2, 3), rows 2 c and 2 c + 1; y weighs values (e4m3)
-        float y[NT][4];
-        float lv[2];
+        // ---- weights.  x: products of keys r (0, 1) and r + 8 (2, 3) with rows 2 c and 2 c + 1, times the key's scale; a score in units
+        // of log2 is x * rs.  d, dv: scores relative to the references, dv with the value's scale in it (e4m3).
+        float d[NT][4], dv[NT][4], lv[2];
         if (FP8) {
           const float sc = lds32(scale_queue + stage * L::SCALES), lg = fast_log2(sc);
           const float ks[2] = {__shfl_sync(0xffffffffu, sc, lane & 28), __shfl_sync(0xffffffffu, sc, (lane & 28) + 1)};
@@ -633,51 +607,59 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[nt][i] *= ks[i >> 1];
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x[nt][i] *= FP8 ? rs[nt][i & 1] : a.scale * kLog2e;
-            if (FP8) y[nt][i] = x[nt][i] + lv[i >> 1];
-          }
-        if (k0 > len - a.q_len + 1 - kTileKeys || lost) {
-          const float nan = lost ? __uint_as_float(0x7fffffffu) : 0.f;
+        const bool some_hidden = k0 > len - a.q_len + 1 - kTileKeys || lost;
+        auto relative = [&]() {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const bool in = k0 + r + 8 * (i >> 1) < len + see[nt][i & 1];
-              x[nt][i] = in ? x[nt][i] + nan : -INFINITY;
-              if (FP8) y[nt][i] = in ? y[nt][i] + nan : -INFINITY;
+              const float by = FP8 ? rs[nt][i & 1] : a.scale * kLog2e;
+              d[nt][i] = __fmaf_rn(x[nt][i], by, -m[nt][i & 1]);
+              if (FP8) dv[nt][i] = __fmaf_rn(x[nt][i], by, lv[i >> 1] - mv[nt][i & 1]);
             }
-        }
-        bool raise = false;
+          if (some_hidden) {
+            const float nan = lost ? __uint_as_float(0x7fffffffu) : 0.f;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            raise |= x[nt][i] > m[nt][i & 1] + kSlack;
-            if (FP8) raise |= y[nt][i] > mv[nt][i & 1] + kSlackV;
+              for (int i = 0; i < 4; ++i) {
+                const bool in = k0 + r + 8 * (i >> 1) < len + see[nt][i & 1];
+                d[nt][i] = in ? d[nt][i] + nan : -INFINITY;
+                if (FP8) dv[nt][i] = in ? dv[nt][i] + nan : -INFINITY;
+              }
           }
-        if (__any_sync(0xffffffffu, raise)) {
+        };
+        relative();
+        float most = d[0][0], most_v = dv[0][0];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          most = fmax3(most, d[nt][0], fmax3(d[nt][1], d[nt][2], d[nt][3]));
+          if (FP8) most_v = fmax3(most_v, dv[nt][0], fmax3(dv[nt][1], dv[nt][2], dv[nt][3]));
+        }
+        if (__any_sync(0xffffffffu, most > kSlack || (FP8 && most_v > kSlackV + kShiftV))) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float top = fmaxf(x[nt][e], x[nt][e + 2]), topv = FP8 ? fmaxf(y[nt][e], y[nt][e + 2]) : 0.f;
+              const float by = FP8 ? rs[nt][e] : a.scale * kLog2e;
+              float top = m[nt][e], top_v = mv[nt][e] + kShiftV;
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float score = d[nt][e + 2 * i] == -INFINITY ? -INFINITY : x[nt][e + 2 * i] * by;
+                top = fmaxf(top, score);
+                if (FP8) top_v = fmaxf(top_v, score + lv[i]);
+              }
 #pragma unroll
               for (int off = 4; off < 32; off <<= 1) {
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                if (FP8) topv = fmaxf(topv, __shfl_xor_sync(0xffffffffu, topv, off));
+                if (FP8) top_v = fmaxf(top_v, __shfl_xor_sync(0xffffffffu, top_v, off));
               }
-              top = fmaxf(top, m[nt][e]);
               float f = fast_exp2(m[nt][e] - top);
               m[nt][e] = top;
               l[nt][e] *= f;
               if (FP8) {
-                topv = fmaxf(topv, mv[nt][e]);
-                f = fast_exp2(mv[nt][e] - topv);
-                mv[nt][e] = topv;
+                f = fast_exp2(mv[nt][e] - (top_v - kShiftV));
+                mv[nt][e] = top_v - kShiftV;
               }
 #pragma unroll
               for (int mt = 0; mt < L::MT; ++mt) {
@@ -685,17 +667,18 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
                 acc[nt][mt][e + 2] *= f;
               }
             }
+          relative();
         }
         uint32_t hi[NT][2], lo[NT][2];  // P^T: rows r, keys 2 c, 2 c + 1 (0) and + 8 (1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float p0 = fast_exp2(x[nt][2 * i] - m[nt][0]), p1 = fast_exp2(x[nt][2 * i + 1] - m[nt][1]);
+            const float p0 = fast_exp2(d[nt][2 * i]), p1 = fast_exp2(d[nt][2 * i + 1]);
             l[nt][0] += p0;
             l[nt][1] += p1;
             if (FP8) {
-              hi[nt][i] = transpose8(pack_half(fast_exp2(y[nt][2 * i] - mv[nt][0] + kShiftV), fast_exp2(y[nt][2 * i + 1] - mv[nt][1] + kShiftV)));
+              hi[nt][i] = transpose8(pack_half(fast_exp2(dv[nt][2 * i]), fast_exp2(dv[nt][2 * i + 1])));
             } else {
               const uint32_t h = pack_bf16(p0, p1);
               hi[nt][i] = transpose8(h);
@@ -736,8 +719,7 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
 
       // ---- the piece ends: whole items are done, others wait in shared memory
       const bool begins = begin == 0, ends = ct == cn, whole = begins && ends;
-      float* slot = ends ? head_of(warp) : tail_of(warp);
-      RowSum* slot_sums = reinterpret_cast<RowSum*>(slot + L::ROWS * D);
+      float* slot = ends ? head_slot : tail_slot;
       const int item = cb * hkv + chk;
       if (!ends) {
         drain(bars, in_flight, phases);
@@ -754,63 +736,60 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
       uint32_t again = 0;  // rows (8 nt + row) whose o has to be summed once more
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float inv[2];
+        float by[2];  // what o's sums are multiplied with
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          float sum = l[nt][e];
+          float sum = l[nt][e], zero = 0.f;
+#pragma unroll
+          for (int mt = 0; mt < L::MT; ++mt) zero = acc[nt][mt][e] * 0.f + (acc[nt][mt][e + 2] * 0.f + zero);  // or NaN
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-          const float back = FP8 ? fast_exp2(mv[nt][e] - m[nt][e] - kShiftV) : 1.f;
           const int row = nt * 8 + 2 * c + e, R = rb * L::ROWS + row;
-          bool fine = true;
+          unsigned bad = __ballot_sync(0xffffffffu, zero != 0.f && fabsf(sum) < INFINITY && R < rows);
+          bad |= bad >> 16;
+          bad |= bad >> 8;
+          bad |= bad >> 4;
 #pragma unroll
-          for (int mt = 0; mt < L::MT; ++mt) {
-            acc[nt][mt][e] *= back;
-            acc[nt][mt][e + 2] *= back;
-            fine = fine && fabsf(acc[nt][mt][e]) < INFINITY && fabsf(acc[nt][mt][e + 2]) < INFINITY;
-          }
-          const unsigned bad = __ballot_sync(0xffffffffu, !fine && fabsf(sum) < INFINITY && R < rows);
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (bad & (0x11111111u << i)) again |= 1u << (nt * 8 + 2 * i + e);
+          for (int i = 0; i < 4; ++i) again |= (bad >> i & 1) << (nt * 8 + 2 * i + e);
           if (raw > cap) sum = __uint_as_float(0x7fffffffu);
-          inv[e] = 1.f / sum;
+          by[e] = FP8 ? fast_exp2(mv[nt][e] - m[nt][e]) : 1.f;
           if (whole) {
+            by[e] /= sum;
             if (a.lse && r == 0 && R < rows) {
               const RowAt at = row_at(a, g, cb, chk, R);
               a.lse[at.head * n_seqs * a.q_len + at.tok] = len + see[nt][e] <= 0 ? -INFINITY : row_lse(m[nt][e], sum);
             }
           } else {
+            float* dst = slot + row * D + (FP8 ? 2 * r : r);
 #pragma unroll
             for (int mt = 0; mt < L::MT; ++mt) {
-              float* dst = slot + row * D + 16 * mt;
               if (FP8) {
-                *reinterpret_cast<float2*>(dst + 2 * r) = make_float2(acc[nt][mt][e], acc[nt][mt][e + 2]);
+                *reinterpret_cast<float2*>(dst + 16 * mt) = make_float2(acc[nt][mt][e] * by[e], acc[nt][mt][e + 2] * by[e]);
               } else {
-                dst[r] = acc[nt][mt][e];
-                dst[r + 8] = acc[nt][mt][e + 2];
+                dst[16 * mt] = acc[nt][mt][e];
+                dst[16 * mt + 8] = acc[nt][mt][e + 2];
               }
             }
-            if (r == 0) slot_sums[row] = RowSum{m[nt][e], sum};
+            if (r == 0) piece_sums[(2 * warp + !ends) * L::ROWS + row] = RowSum{m[nt][e], sum};
           }
         }
         if (whole) {  // a lane gets neighbouring elements of one row: of row r by a transposition, of rows 2 c, 2 c + 1 with e4m3
 #pragma unroll
           for (int e = 0; e < (FP8 ? 2 : 1); ++e) {
-            const int R = rb * L::ROWS + nt * 8 + (FP8 ? 2 * c + e : r);
-            const RowAt at = row_at(a, g, cb, chk, min(R, rows - 1));
-            const bool none = len - a.q_len + 1 + min(R, rows - 1) / g <= 0;
-            bf16* o = a.o + at.head * a.o_head + at.tok * a.o_tok;
+            const int R = rb * L::ROWS + nt * 8 + (FP8 ? 2 * c + e : r), Rin = min(R, rows - 1);
+            const RowAt at = row_at(a, g, cb, chk, Rin);
+            const bool none = len - a.q_len + 1 + Rin / g <= 0;
+            bf16* o = a.o + at.head * a.o_head + at.tok * a.o_tok + (FP8 ? 2 * r : 2 * c);
 #pragma unroll
             for (int mt = 0; mt < L::MT; ++mt) {
               if (FP8) {
-                const uint32_t w = pack_bf16(acc[nt][mt][e] * inv[e], acc[nt][mt][e + 2] * inv[e]);
-                if (R < rows) *reinterpret_cast<uint32_t*>(o + 16 * mt + 2 * r) = none ? 0u : w;
+                const uint32_t w = pack_bf16(acc[nt][mt][e] * by[e], acc[nt][mt][e + 2] * by[e]);
+                if (R < rows) *reinterpret_cast<uint32_t*>(o + 16 * mt) = none ? 0u : w;
               } else {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                  const uint32_t w = transpose8(pack_bf16(acc[nt][mt][2 * i] * inv[0], acc[nt][mt][2 * i + 1] * inv[1]));
-                  if (R < rows) *reinterpret_cast<uint32_t*>(o + 16 * mt + 8 * i + 2 * c) = none ? 0u : w;
+                  const uint32_t w = transpose8(pack_bf16(acc[nt][mt][2 * i] * by[0], acc[nt][mt][2 * i + 1] * by[1]));
+                  if (R < rows) *reinterpret_cast<uint32_t*>(o + 16 * mt + 8 * i) = none ? 0u : w;
                 }
               }
             }
@@ -866,7 +845,7 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
   }
 
   // ---- the CTA's pieces, in order: lane i of every warp has piece i (2 warp: head, 2 warp + 1: tail).  Runs of one item are
-  // joined; the warps share the runs out, and a run's rows among those that have the same one.
+  // joined.
   if (lane == 0) {
     info[warp] = left_over;
     info_len[warp] = left_len;
@@ -881,7 +860,8 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
   const unsigned valid = __ballot_sync(0xffffffffu, my_item >= 0), below = valid & ((1u << lane) - 1u);
   const int prev = __shfl_sync(0xffffffffu, my_item, below ? 31 - __clz(below) : 0);
   unsigned starts = __ballot_sync(0xffffffffu, my_item >= 0 && (!below || prev != my_item));
-  const int n_runs = __popc(starts), share = n_runs ? max(kWarps / n_runs, 1) : 1;  // warps to a run
+  constexpr int RB = NT;  // rows at a time
+  const int groups = (min(L::ROWS, rows - rb * L::ROWS) + RB - 1) / RB;  // units of work of a run: the warps take them in turns
 #pragma unroll 1
   for (int i = 0; starts; ++i) {
     const int s = __ffs(starts) - 1;
@@ -896,12 +876,10 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
     } else if (!begins) {
       meta.x = item;
     }
-    const int mates = n_runs < kWarps ? share : 1, me = n_runs < kWarps ? warp - i * share : warp - i % kWarps;
-    if (me < 0 || me >= mates) continue;
-    constexpr int E = D / 32, RB = 4;  // elements of a lane, rows at a time
+    constexpr int E = D / 32;  // elements of a lane
     const int b = item / hkv, hk = item - b * hkv, len = __shfl_sync(0xffffffffu, lane & 1 ? my_len.y : my_len.x, s);
 #pragma unroll 1
-    for (int row0 = me * RB; row0 < L::ROWS && rb * L::ROWS + row0 < rows; row0 += mates * RB) {
+    for (int row0 = (warp + kWarps - i * groups % kWarps) % kWarps * RB; row0 < groups * RB; row0 += kWarps * RB) {
       RowSum sum[RB];
       float o[RB][E];
 #pragma unroll
@@ -922,7 +900,7 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
           const uint32_t at = smem_u32(smem) + (p & 1 ? (p >> 1) * L::QUEUE : L::AT_SLOTS + (p >> 1) * L::SLOT);
 #pragma unroll
           for (int k = 0; k < RB; ++k) {
-            lds_floats<2>(reinterpret_cast<float*>(&ps[j][k]), at + L::ROWS * D * 4 + (row0 + k) * (int)sizeof(RowSum));
+            ps[j][k] = piece_sums[p * L::ROWS + row0 + k];
             lds_floats<E>(v[j][k], at + ((row0 + k) * D + lane * E) * 4);
             if (!in) {
               ps[j][k] = RowSum{kLowest, 0.f};
@@ -975,7 +953,7 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
 // ROWS 1: all warps share a row's pieces, for the long chains of few.
 template <int D, int ROWS>
 __global__ void __launch_bounds__(kJoinThreads) k_decode_join(const __grid_constant__ DecodeArgs a, const DecodeWs ws, int block_rows) {
-  constexpr int LN = D / 4, GR = kJoinThreads / LN / ROWS, AHEAD = ROWS == 1 ? 10 : 4;  // lanes and groups of a row, pieces in flight
+  constexpr int LN = D / 4, GR = kJoinThreads / LN / ROWS, AHEAD = ROWS == 1 ? 5 : 4;  // lanes and groups of a row, pieces in flight
   __shared__ float4 part[ROWS == 1 ? GR : 1][LN];
   __shared__ RowSum part_sums[GR];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, x = blockIdx.x, X = gridDim.x;
