@@ -670,34 +670,40 @@ class KVCache:
 
 
 def _page_table(t, dev):
-    shape, strides = t.shape, t.stride()
-    if len(shape) != 2 or t.get_device() != dev or t.dtype != torch.int32 or (strides[1] != 1 and shape[1] > 1):
+    shape, (ld, inner) = t.shape, t.stride() if t.dim() == 2 else (0, 0)
+    if inner != 1 and (len(shape) != 2 or shape[1] > 1) or t.dtype != torch.int32 or t.get_device() != dev:
         _refuse(f"page_table: int32 [sequences, pages] with contiguous rows on device {dev} expected, got {t.dtype} "
-                f"{tuple(t.shape)} {t.stride()} on {t.device}")
+                f"{tuple(shape)} {t.stride()} on {t.device}")
     n, m = shape
-    return PageTable(t.data_ptr(), strides[0] if n > 1 else m, n, m)
+    return PageTable(t.data_ptr(), ld if n > 1 else m, n, m)
 
 
 def _heads(t, dev, shape, what):
     """Address, head stride and token stride of bf16 rows [heads, tokens, head_dim]."""
-    if t.shape != shape or t.get_device() != dev or t.dtype != _BF16:
-        _refuse(f"{what}: bf16 {tuple(shape)} on device {dev} expected, got {t.dtype} {tuple(t.shape)} on {t.device}")
-    hs, ts, es = t.stride()
-    if es != 1:
-        _refuse(f"{what}: contiguous rows expected, got strides {t.stride()}")
+    hs, ts, es = t.stride() if t.shape == shape else (0, 0, 0)
+    if es != 1 or t.dtype != _BF16 or t.get_device() != dev:
+        _refuse(f"{what}: bf16 {tuple(shape)} with contiguous rows on device {dev} expected, got {t.dtype} {tuple(t.shape)} "
+                f"{t.stride()} on {t.device}")
     return t.data_ptr(), hs, ts
 
 
+def _ints(t, dev, n, what):
+    """Address of a contiguous vector of n int32."""
+    if t.shape != (n,) or t.dtype != torch.int32 or t.get_device() != dev or not t.is_contiguous():
+        _refuse(f"{what}: contiguous int32 [{n}] on device {dev} expected, got {t.dtype} {tuple(t.shape)} {t.stride()} on {t.device}")
+    return t.data_ptr()
+
+
 def _kv_copy(f, where, cache, k, v, seq, pos, page_table, stream):
-    dev, shape = cache.device_index, seq.shape
-    if dev != torch._C._cuda_getDevice() or len(shape) != 1:
-        _refuse(f"{where}: a cache on the current device and seq of [tokens] expected, got {cache.k.device} and {tuple(shape)}")
-    n, = shape
+    dev = cache.device_index
+    if dev != torch._C._cuda_getDevice() or seq.dim() != 1:
+        _refuse(f"{where}: a cache on the current device and seq of [tokens] expected, got {cache.k.device} and {tuple(seq.shape)}")
+    n = seq.shape[0]
     rows = (cache.n_kv_heads, n, cache.head_dim)
     kp, kh, kt = _heads(k, dev, rows, "k")
     vp, vh, vt = _heads(v, dev, rows, "v")
-    rc = f(cache.desc, _page_table(page_table, dev), n, _dev(seq, dev, torch.int32, shape, "seq"), _dev(pos, dev, torch.int32, shape, "pos"),
-           kp, kh, kt, vp, vh, vt, _raw_stream(stream, dev))
+    rc = f(cache.desc, _page_table(page_table, dev), n, _ints(seq, dev, n, "seq"), _ints(pos, dev, n, "pos"), kp, kh, kt, vp, vh, vt,
+           torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, where)
 
@@ -727,20 +733,23 @@ def decode(cache: KVCache, q, page_table, lens, o, ws, lse=None, scale=0.0, stre
     order (query t sees the keys before lens[b] - q_len + 1 + t); lens int32 [sequences]; lse, optional, fp32
     [n_q_heads, sequences * q_len]; ws uint8 of decode_workspace_bytes."""
     dev, shape = cache.device_index, q.shape
-    if dev != torch._C._cuda_getDevice() or len(shape) != 3:
-        _refuse(f"decode: a cache on the current device and q of [heads, tokens, head_dim] expected, got {cache.k.device} and {tuple(shape)}")
+    if dev != torch._C._cuda_getDevice() or len(shape) != 3 or shape[2] != cache.head_dim:
+        _refuse(f"decode: a cache on the current device and q of [heads, tokens, {cache.head_dim}] expected, got {cache.k.device} and "
+                f"{tuple(shape)}")
     table = _page_table(page_table, dev)
-    n = table.n_seqs
+    n = page_table.shape[0]
     hq, tokens, _ = shape
     q_len = tokens // n if n else 1
-    if tokens != n * q_len or q_len == 0 or shape[2] != cache.head_dim:
+    if tokens != n * q_len or not q_len:
         _refuse(f"decode: q of [heads, q_len * {n}, {cache.head_dim}] expected, got {tuple(shape)}")
     qp, qh, qt = _heads(q, dev, shape, "q")
     op, oh, ot = _heads(o, dev, shape, "o")
-    rc = lib().upipe_attn_decode(
-        cache.desc, table, _dev(lens, dev, torch.int32, (n,), "lens"), hq, q_len, scale, qp, qh, qt, op, oh, ot,
-        None if lse is None else _dev(lse, dev, _F32, (hq, tokens), "lse"), _dev(ws, dev, torch.uint8, ws.shape, "ws"), ws.numel(),
-        _raw_stream(stream, dev))
+    if ws.dtype != torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
+        _refuse(f"decode: ws of contiguous uint8 on device {dev} expected, got {ws.dtype} on {ws.device}")
+    rc = (_lib or lib()).upipe_attn_decode(
+        cache.desc, table, _ints(lens, dev, n, "lens"), hq, q_len, scale, qp, qh, qt, op, oh, ot,
+        None if lse is None else _dev(lse, dev, _F32, (hq, tokens), "lse"), ws.data_ptr(), ws.numel(),
+        torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if rc:
         _check(rc, "decode")
 

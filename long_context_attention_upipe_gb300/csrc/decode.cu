@@ -300,11 +300,12 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
 
   // ---- the warp's part of the line of tiles
   int lens = lane < n_seqs ? a.lens[lane] : 0;  // of the 32 sequences that b0 is among
+  const int lens2 = lane + 32 < n_seqs ? a.lens[lane + 32] : 0;
   int b0 = 0;
-  int64_t upto = 0, before = 0, total = 0;  // tiles up to and with a lane's sequence, before the 32, of all
+  int64_t upto = 0, before = 0, total = 0, first32 = 0;  // tiles up to and with a lane's sequence, before the 32, of all
   const int chunks = (n_seqs + 31) / 32;
   int64_t* sums = reinterpret_cast<int64_t*>(smem);
-  if (chunks > 1) {  // a sum for each 32 sequences
+  if (chunks > 2) {  // a sum for each 32 sequences
     for (int ch = warp; ch < chunks; ch += kWarps) {
       const int b = ch * 32 + lane;
       const int64_t n = warp_sum(b < n_seqs ? units_of<L::END>(a.lens[b], cap) : 0);
@@ -316,7 +317,8 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
     for (int off = 16; off > 0; off >>= 1) total += __shfl_xor_sync(0xffffffffu, total, off);
   } else {
     upto = warp_scan(units_of<L::END>(lens, cap), lane);
-    total = __shfl_sync(0xffffffffu, upto, 31);
+    first32 = __shfl_sync(0xffffffffu, upto, 31);
+    total = first32 + warp_sum(units_of<L::END>(lens2, cap));
   }
   total *= hkv;
   // no CTA gets less than a tile for each warp
@@ -344,7 +346,7 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
   int hk0 = 0, tile0 = 0;
   if (left > 0) {
     const int64_t seq_first = mul_div(first, 1, hkv);  // the tile's place if there were one head
-    if (chunks > 1) {
+    if (chunks > 2) {
       for (int base = 0; base < chunks; base += 32) {
         const int64_t v = base + lane < chunks ? sums[base + lane] : 0, in = warp_scan(v, lane);
         const unsigned hit = __ballot_sync(0xffffffffu, before + in > seq_first);
@@ -356,6 +358,11 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
         before += __shfl_sync(0xffffffffu, in, 31);
       }
       lens = b0 + lane < n_seqs ? a.lens[b0 + lane] : 0;
+      upto = warp_scan(units_of<L::END>(lens, cap), lane);
+    } else if (seq_first >= first32) {
+      b0 = 32;
+      before = first32;
+      lens = lens2;
       upto = warp_scan(units_of<L::END>(lens, cap), lane);
     }
     const int at = max(__ffs(__ballot_sync(0xffffffffu, before + upto > seq_first)) - 1, 0);
@@ -374,7 +381,7 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
       }
     }
   }
-  if (chunks > 1) {
+  if (chunks > 2) {
     fence_async();  // the queues, which the copies fill, take the place of the sums
     __syncthreads();
   }
