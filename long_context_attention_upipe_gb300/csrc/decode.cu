@@ -4,30 +4,42 @@
 //   s_j = scale q . k_j,   lse = log sum_j exp s_j,   o = sum_j exp(s_j - lse) v_j
 // and o = 0, lse = -infinity where no key is seen.
 //
-// The cache is read once, and that bounds the kernel: 4 T g flops for every cached byte pair (g query heads share a
-// key head) are far below the tensor cores' rate.  So the split follows the bytes.  All tiles of 16 keys of all
-// (sequence, key head) items form one line, in order; the CTAs take equal parts of it, and a CTA's eight warps equal
-// parts of that.  A warp runs its tiles through a queue of its own in shared memory: every lane copies exactly the
-// 16-byte pieces that it will read (cp.async), in the order that the matrix instructions want them, so there is no
-// barrier, no bank conflict and no swizzle, and any page, head and token strides cost nothing.
+// The cache is read once, and that bounds the kernel: with g query heads to a key head it takes 2 g T operations for each byte of
+// bf16 (4 g T of e4m3), where the tensor cores have hundreds to spare; a tcgen05 tile of 128 rows would be empty but for g T of
+// them.  So the split follows the bytes.  All tiles of 16 keys of all (sequence, key head) items form one line, in order, with a
+// few tiles' time added at each item's end for what an end costs (without: 99 instead of 91 us for 64 sequences up to 16384
+// keys).  The CTAs, one to an SM, take equal parts of the line, and a CTA's warps equal parts of that, whatever the lengths.
+// A warp runs its tiles through a queue of its own in shared memory: one TMA box each for 16 keys and 16 values of a page, so any
+// page, head and token strides cost nothing and warps wait for nobody but their copies.
 //
-// Per tile, with keys as the 16 rows of the matrix instruction (m16n8k16) and up to 8 (NT = 2: 16) query rows as its
-// columns:   S^T = K Q^T,   P = exp2(S - m),   O^T += V^T P^T.   The order of the head dimension in the first product
-// and of O's rows in the second is free; it is chosen so that a lane's 16 bytes are whole fragments.  Pairs of keys
-// of V are brought together by byte permutations, P^T by one 8 x 8 transposition in registers.
-//   bf16  weights enter as the sum of two bf16 numbers (2^-17), as one they would double the error of o.
-//   e4m3  codes are converted to fp16 (exact), q is scaled by a power of two for each row, and V's scale joins the
-//         weight's exponent, s_j + log2 sv_j, under a maximum of its own; weights are fp16 (2^-11), up to 2^15, which
-//         leaves 2^-35 of the largest.
-// The maximum is a reference that is raised, and the sums rescaled, only when a score exceeds it by a margin: one vote
-// for each tile, no shuffles.  m, l and O are fp32.
+// Per tile, keys are the 16 rows of m16n8k16 and up to 8 (NT = 2: 16) query rows its columns:
+//   S^T = K Q^T,   P = exp2(S - m),   O^T += V^T P^T
+// K's fragments come by ldmatrix, V's by its transposing form, P^T by an 8 x 8 transposition in registers.
+//   bf16  weights enter as the sum of two bf16 numbers (2^-17); a single one would double the error of o.
+//   e4m3  codes are converted to fp16 (exact).  A 16-byte piece of codes gives a lane four neighbouring elements, so the steps of
+//         S^T take the head dimension in that order and the rows of O^T are pairs of elements.  q goes to fp16 under a power of two
+//         for each row, K's scale to the score, and V's scale to the weight's exponent, s_j + log2 sv_j, under a maximum of its own;
+//         weights are fp16 (2^-11) up to 2^15, which leaves 2^-35 of the largest.
+// The maximum is a reference that is raised, and the sums rescaled, only when a score exceeds it by a margin: one vote for each
+// tile, no shuffles.  m, l and O are fp32.
 //
-// A warp's part may begin or end within an item.  The CTA joins such pieces in shared memory in order, and what an item
-// leaves in several CTAs a second kernel joins in order: no atomics, equal calls give equal bits.
+// A warp's part may begin or end within an item.  The CTA joins such pieces in shared memory, in order, and what an item leaves
+// in several CTAs a second kernel joins, in order: no atomics, equal calls give equal bits.
 //
-// A value that is infinite or NaN spoils the products of query rows that do not see it (zero times infinity), and of
-// those that do where a weight's second part is zero.  Then o is not finite although l is, and the piece's o is summed
-// again key by key (redo).
+// A value that is infinite or NaN spoils the products of query rows that do not see it (zero times infinity), and of those that do
+// where a weight's second part is zero.  Then o is not finite although l is, and the piece's o is summed again key by key (redo).
+//
+// Measured (GB300, calls back to back; floor: the cached bytes at the copy rate of 6698 GB/s):
+//   1 sequence of 1048576 keys, 4 / 1 heads, bf16          85.7 us, floor 80.2
+//   1 of 5242880, 8 / 1, e4m3                               206 us, 206.6
+//   64 up to 16384, 32 / 8, e4m3                           86.2 us, 76.0
+//   48 up to 8192, 40 / 8, bf16                            57.7 us, 48.3
+//   16 up to 32768, 4 tokens each, 32 / 8, e4m3            69.7 us, 47.3
+//   256 up to 500, 4 / 2 heads of 64, bf16                 11.3 us, 2.2
+//   1 of 4097, 32 / 8, bf16                                 9.0 us, 2.5
+// One long sequence streams at the copy rate.  What a call adds: 5 us until the first tile lands
+// (lengths, table entries and queries are read one after another), 2 to 4 us for the ends of the last items, 2 to 3 us for the
+// second launch.  With 16 rows the tiles' own chain of instructions bounds e4m3 (5.7 TB/s; 250 registers leave room for 8 warps).
 #include "internal.h"
 #include "kv_cache.cuh"
 #include "quant.cuh"
@@ -48,7 +60,7 @@ struct RowSum {
   float m, l;
 };
 
-template <int D, bool FP8, int NT>
+template <int D, bool FP8, int NT, int W>
 struct Lay {
   static constexpr int ROWB = D * (FP8 ? 1 : 2);        // bytes of a cached row
   static constexpr int SEG = ROWB > 128 ? 128 : ROWB;   // ... of which a box is so many wide: what a swizzle spans
@@ -58,7 +70,7 @@ struct Lay {
   static constexpr int SCALES = FP8 ? 128 : 0;          // their scales
   static constexpr int ROWS = 8 * NT;
   static constexpr int SLOT = ROWS * D * 4;             // sums of a piece's o
-  static constexpr int WARPS = FP8 && NT == 1 ? 16 : 8;
+  static constexpr int WARPS = W;
   static constexpr int END = FP8 ? 4 : 2;               // tiles' time that an item's end (and the next one's begin) takes
   static constexpr int FIT = ((226 * 1024 - 16) / WARPS - 24 - SLOT - 2 * ROWS * (int)sizeof(RowSum)) / (STAGE + SCALES + 8);
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
@@ -270,14 +282,27 @@ struct DecodeWs {
                   // not; z whether the latter begins its item, w the CTA in which it ends
   RowSum* sums;   // [row blocks][CTAs][2][rows]
   float* acc;     // [row blocks][CTAs][2][rows][D]
+  bool solo;      // a CTA to each item: nothing is left for the joining kernel
 };
 
-template <int D, bool FP8, int NT>
-__global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
+// A row of a sequence without tiles: zeros, or NaN where there are keys but no table.  All lanes of a warp.
+template <int D>
+__device__ __forceinline__ void empty_row(const DecodeArgs& a, int g, int b, int hk, int R, int keys) {
+  const int lane = threadIdx.x & 31;
+  const bool lost = keys - a.q_len + 1 + R / g > 0;
+  const RowAt at = row_at(a, g, b, hk, R);
+  bf16* o = a.o + at.head * a.o_head + at.tok * a.o_tok;
+  const uint32_t w = lost ? 0x7fff7fffu : 0u;
+  if (lane < D / 8) *reinterpret_cast<uint4*>(o + lane * 8) = make_uint4(w, w, w, w);
+  if (a.lse && lane == 0) a.lse[at.head * a.t.n_seqs * a.q_len + at.tok] = lost ? __uint_as_float(0x7fffffffu) : -INFINITY;
+}
+
+template <int D, bool FP8, int NT, int W>
+__global__ void __launch_bounds__(32 * W, 1)
     k_decode(const __grid_constant__ DecodeArgs a, const DecodeWs ws, const __grid_constant__ CUtensorMap map_k,
              const __grid_constant__ CUtensorMap map_v, uint64_t wait_ns) {
-  using L = Lay<D, FP8, NT>;
-  constexpr int kWarps = L::WARPS;
+  using L = Lay<D, FP8, NT, W>;
+  constexpr int kWarps = W;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
@@ -299,11 +324,11 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
   grid_dep_trigger();  // the joining kernel may start when CTAs leave; it reads nothing of this one before it has ended
 
   // ---- the warp's part of the line of tiles
-  int lens = lane < n_seqs ? a.lens[lane] : 0;  // of the 32 sequences that b0 is among
+  int b0 = ws.solo ? blockIdx.x / hkv : 0;
+  int lens = (b0 & ~31) + lane < n_seqs ? a.lens[(b0 & ~31) + lane] : 0;  // of the 32 sequences that b0 is among
   const int lens2 = lane + 32 < n_seqs ? a.lens[lane + 32] : 0;
-  int b0 = 0;
   int64_t upto = 0, before = 0, total = 0, first32 = 0;  // tiles up to and with a lane's sequence, before the 32, of all
-  const int chunks = (n_seqs + 31) / 32;
+  const int chunks = ws.solo ? 0 : (n_seqs + 31) / 32;
   int64_t* sums = reinterpret_cast<int64_t*>(smem);
   if (chunks > 2) {  // a sum for each 32 sequences
     for (int ch = warp; ch < chunks; ch += kWarps) {
@@ -344,7 +369,14 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
   }
   const int64_t next = first + left;  // the tile after the part
   int hk0 = 0, tile0 = 0;
-  if (left > 0) {
+  if (ws.solo) {
+    hk0 = blockIdx.x - b0 * hkv;
+    const int keys = __shfl_sync(0xffffffffu, lens, b0 & 31), n = tiles_of(keys, cap);
+    tile0 = n * warp / kWarps;
+    left = n * (warp + 1) / kWarps - tile0;
+    if (n == 0)
+      for (int R = rb * L::ROWS + warp; R < min((rb + 1) * L::ROWS, rows); R += kWarps) empty_row<D>(a, g, b0, hk0, R, keys);
+  } else if (left > 0) {
     const int64_t seq_first = mul_div(first, 1, hkv);  // the tile's place if there were one head
     if (chunks > 2) {
       for (int base = 0; base < chunks; base += 32) {
@@ -950,7 +982,7 @@ __global__ void __launch_bounds__(32 * Lay<D, FP8, NT>::WARPS, 1)
       }
     }
   }
-  if (threadIdx.x == 0) ws.meta[place] = meta;
+  if (threadIdx.x == 0 && !ws.solo) ws.meta[place] = meta;
 }
 
 // Joins what an item left in several CTAs, in order; one block for each CTA in which an item begins that goes on, and each row.
@@ -976,11 +1008,7 @@ __global__ void __launch_bounds__(kJoinThreads) k_decode_join(const __grid_const
       for (int j = 0; j < ROWS * hkv; ++j) {
         const int hk = j / ROWS, R = blockIdx.y * ROWS + j % ROWS;
         if (R >= rows) continue;
-        const bool lost = keys - a.q_len + 1 + R / g > 0;  // keys, but no table
-        const RowAt at = row_at(a, g, base + i, hk, R);
-        bf16* o = a.o + at.head * a.o_head + at.tok * a.o_tok;
-        if (lane < D / 8) *reinterpret_cast<uint4*>(o + lane * 8) = lost ? make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu) : make_uint4(0, 0, 0, 0);
-        if (a.lse && lane == 0) a.lse[at.head * n_seqs * a.q_len + at.tok] = lost ? __uint_as_float(0x7fffffffu) : -INFINITY;
+        empty_row<D>(a, g, base + i, hk, R, keys);
       }
     }
   }
@@ -1057,7 +1085,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_decode_join(const __grid_const
   if (a.lse && d == 0) a.lse[at.head * n_seqs * a.q_len + at.tok] = seen <= 0 ? -INFINITY : row_lse(run.m, run.l);
 }
 
-// Rows of a block, blocks of rows, and CTAs for each of them.
+// Rows of a block, blocks of rows, and CTAs for each of them.  Blocks of 16 where there are more than 8 rows: 69.7 us for 16
+// sequences up to 32768 keys with 16 rows, 95.4 as two blocks of 8 that read the cache twice; 8 rows in a block of 16 take 255 us
+// instead of 206 for 5242880 keys e4m3, and 86.7 instead of 85.7 for 1048576 keys bf16.
 struct DecodeShape {
   int rows, blocks, ctas;
 };
@@ -1068,9 +1098,9 @@ DecodeShape decode_shape(const DecodeArgs& a) {
 }
 
 // Tiles of 16 rows of a page and head.  A row longer than 128 bytes is two boxes, side by side in shared memory.
-template <int D, bool FP8, int NT>
+template <int D, bool FP8>
 bool tile_map(CUtensorMap* map, const KvCache& c, const void* base) {
-  using L = Lay<D, FP8, NT>;
+  using L = Lay<D, FP8, 1, 8>;
   const uint64_t es = FP8 ? 1 : 2;
   auto stride = [&](int64_t s) { return s ? (uint64_t)s * es : (uint64_t)16; };  // 0: of a single page or head
   const uint64_t dims[5] = {L::SEG / es, (uint64_t)c.page_size, 2, (uint64_t)c.n_kv_heads, (uint64_t)c.n_pages};
@@ -1079,19 +1109,26 @@ bool tile_map(CUtensorMap* map, const KvCache& c, const void* base) {
   return make_tmap_rows(map, base, !FP8, L::SEGS == 2, dims, strides, box, L::SEG);
 }
 
-template <int D, bool FP8, int NT>
-cudaError_t run(const DecodeArgs& a, const DecodeShape& sh, const DecodeWs& ws, cudaStream_t st) {
-  using L = Lay<D, FP8, NT>;
-  auto kfn = k_decode<D, FP8, NT>;
+template <int D, bool FP8, int NT, int W>
+cudaError_t run(const DecodeArgs& a, const DecodeShape& sh, DecodeWs ws, cudaStream_t st) {
+  using L = Lay<D, FP8, NT, W>;
+  auto kfn = k_decode<D, FP8, NT, W>;
   CUtensorMap mk, mv;
-  if (!tile_map<D, FP8, NT>(&mk, a.c, a.c.k) || !tile_map<D, FP8, NT>(&mv, a.c, a.c.v)) return cudaErrorInvalidValue;
+  if (!tile_map<D, FP8>(&mk, a.c, a.c.k) || !tile_map<D, FP8>(&mv, a.c, a.c.v)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kfn, dim3(sh.ctas, sh.blocks), dim3(32 * L::WARPS), L::BYTES, st, a, ws, mk, mv, wait_limit_ns());
+  // Few short sequences: a CTA to each item, and one launch, where the line of tiles takes two.  With the longest sequence that
+  // the table has room for, 8 key heads bf16: 256 keys 8.6 against 11.3 us a call (6.1 against 7.9 on the device), 1024 keys
+  // 10.1 against 11.3, 2048 keys 14.7 against 11.1; e4m3, 512 keys 10.1 against 11.4, 1024 keys 12.7 against 11.7.
+  const int64_t items = (int64_t)a.t.n_seqs * a.c.n_kv_heads;
+  ws.solo = items <= sh.ctas && table_keys(a.t, a.c.page_size) <= (FP8 ? 512 : 1024);
+  e = launch_pdl(kfn, dim3(ws.solo ? (unsigned)items : sh.ctas, sh.blocks), dim3(32 * W), L::BYTES, st, a, ws, mk, mv, wait_limit_ns());
   note_launch();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || ws.solo) return e;
   const int rows = a.hq / a.c.n_kv_heads * a.q_len;
-  const bool many = (int64_t)a.t.n_seqs * a.c.n_kv_heads * 8 >= sh.ctas;  // items of 8 CTAs at most, if they are alike
+  // A joining block for 8 rows where items are of 8 CTAs at most, if they are alike (16 sequences of 8 heads, 16 rows: 69.7 us, 72.6 with
+  // a block to a row), a block to a row where they are longer (one item of 152 CTAs: 206 us, 227 with a warp to a row).
+  const bool many = items * 8 >= sh.ctas;
   e = launch_pdl(many ? k_decode_join<D, 8> : k_decode_join<D, 1>, dim3(sh.ctas, many ? (int)ceil_div(rows, 8) : rows), dim3(kJoinThreads), 0, st, a,
                  ws, sh.rows);
   note_launch();
@@ -1100,7 +1137,16 @@ cudaError_t run(const DecodeArgs& a, const DecodeShape& sh, const DecodeWs& ws, 
 
 template <int D, bool FP8>
 cudaError_t run_rows(const DecodeArgs& a, const DecodeShape& sh, const DecodeWs& ws, cudaStream_t st) {
-  return sh.rows == 8 ? run<D, FP8, 1>(a, sh, ws, st) : run<D, FP8, 2>(a, sh, ws, st);
+  if (sh.rows == 16) return run<D, FP8, 2, 8>(a, sh, ws, st);
+  if constexpr (FP8) {
+    // Converting codes takes instructions, which 16 warps overlap better; fewer warps leave fewer pieces to join where there is
+    // little to read.  One sequence of 8 key heads: 4096 keys 9.7 us with 8 warps, 11.4 with 16; 131072 keys 50.7 and 51.6;
+    // 262144 keys 91.5 and 89.3; 5242880 keys of one head 216 and 209.
+    constexpr int kFewTiles = 600;  // to a CTA, if all sequences were as long as the table allows
+    const int64_t tiles = (int64_t)a.t.n_seqs * a.c.n_kv_heads * ceil_div(table_keys(a.t, a.c.page_size), kTileKeys);
+    if (tiles > (int64_t)sh.ctas * kFewTiles) return run<D, FP8, 1, 16>(a, sh, ws, st);
+  }
+  return run<D, FP8, 1, 8>(a, sh, ws, st);
 }
 
 }  // namespace
