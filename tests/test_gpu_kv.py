@@ -589,3 +589,162 @@ def test_generation_step_by_step(kind):
     tol = float(vr.double().abs().max()) * (4 * BF + math.expm1(2 * ds) + 2.0 ** -12)
     assert float((o[:, new].double() - oc[:, new].double()).abs().max()) <= tol
     assert float((lse[:, new] - lc[:, new]).abs().max()) <= ds + 2.0 ** -12 * (1 + float(lse[:, new].abs().max()))
+
+
+# ------------------------------------------------------------------------------------------------
+# every way through the decode kernels: tables with room for far more keys than there are (the division of work goes by the
+# device's lengths, the choice of kernels by the table's room), batches around 32 and 64 sequences, very many sequences
+# ------------------------------------------------------------------------------------------------
+
+def widened(table, columns, g):
+    """The table with `columns` more entries of garbage in every row."""
+    junk = torch.randint(-2 ** 31, 2 ** 31 - 1, (table.shape[0], columns), generator=g, device="cuda").int()
+    return torch.cat([table, junk], 1)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dh,hq,hkv,q_len", [(64, 4, 2, 1), (128, 8, 1, 1), (128, 24, 3, 1), (128, 6, 3, 4), (64, 40, 2, 1), (64, 16, 4, 3)])
+@pytest.mark.parametrize("columns", [100, 100000])
+def test_decode_in_wide_tables(kind, dh, hq, hkv, q_len, columns):
+    lens = [0, 1, 15, 16, 17, 40, 0, 127, 128, 129, 700, 2, 333]
+    c, table, q = setup(kind, lens, hq, hkv, dh, 16, q_len)
+    check_decode(c, q, widened(table, columns, gen(1)), lens, q_len=q_len)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n", [31, 32, 33, 63, 64, 65, 97, 256, 257])
+def test_decode_batches(kind, n):
+    g = torch.Generator()
+    g.manual_seed(n)
+    lens = [int(x) if x < 150 else 0 for x in torch.randint(0, 200, (n,), generator=g)]
+    c, table, q = setup_many(kind, lens, 8, 2, 64, 16)
+    check_decode(c, q, table, lens)
+    check_decode(c, q, widened(table, 3000, gen(2)), lens)
+
+
+def test_decode_65536_sequences():
+    """Each of one key: o is its value, lse its score; every other sequence empty."""
+    n, pages = 65536, 37
+    c = make_cache("bf16", pages=pages, hkv=1, size=16, dh=64, fill=gen(9))
+    b = torch.arange(n, device="cuda")
+    table = (b % pages).int()[:, None].contiguous()
+    lens = (b % 2).int()
+    q = randn(gen(10), 2, n, 64).bfloat16()
+    o, lse = run_decode(c, q, table, lens)
+    assert bool((o[:, ::2] == 0).all()) and bool((lse[:, ::2] == -math.inf).all())
+    rows = (b % pages)[1::2]
+    assert torch.equal(o[:, 1::2], c.v[rows, 0, 0][None].expand(2, -1, -1))
+    s = (q[:, 1::2].double() * c.k[rows, 0, 0].double()).sum(-1) / 8
+    mass = (q[:, 1::2].double() * c.k[rows, 0, 0].double()).abs().sum(-1) / 8
+    # (2 D + 8) roundings of the products' sum, 4 of the score in units of log2 and back, the logarithm's of l = 1
+    assert bool(((lse[:, 1::2].double() - s).abs() <= mass * (2 * 64 + 8) * U + s.abs() * 8 * U + 2.0 ** -20).all())
+    with pytest.raises(up.UpipeError):
+        run_decode(c, torch.zeros(2, n + 1, 64, dtype=torch.bfloat16, device="cuda"), torch.zeros(n + 1, 1, dtype=torch.int32, device="cuda"),
+                   [0] * (n + 1), ws=torch.empty(1 << 24, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_decode_whose_waits_run_out_gives_nan_or_the_right_values(kind):
+    lens = [3000, 40, 900]
+    c, table, q = setup(kind, lens, 8, 2, 128, 64)
+    want, wl = run_decode(c, q, table, lens)
+    try:
+        up.set_wait_limit_ns(1)
+        for _ in range(20):
+            o, lse = run_decode(c, q, table, lens)
+            torch.cuda.synchronize()
+            lost = o.isnan().any(-1)
+            assert torch.equal(o.isnan().all(-1), lost) and torch.equal(lse.isnan(), lost)
+            assert torch.equal(o[~lost], want[~lost]) and torch.equal(lse[~lost], wl[~lost])
+    finally:
+        up.set_wait_limit_ns(0)
+    o, lse = run_decode(c, q, table, lens)
+    assert torch.equal(o, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_write_and_decode_captured_and_replayed(kind):
+    """A decode step as a graph: new tokens, positions, lengths and table are the device's."""
+    hq, hkv, dh, n = 8, 2, 128, 5
+    g = gen(33)
+    lens = [30, 0, 63, 100, 16]
+    c, table, q = setup(kind, [n + 8 for n in lens], hq, hkv, dh, 16)
+    k, v = heads(g, "head", hkv, n, dh), heads(g, "token", hkv, n, dh)
+    seq, pos = torch.arange(n, device="cuda").int(), torch.zeros(n, dtype=torch.int32, device="cuda")
+    ln = torch.zeros(n, dtype=torch.int32, device="cuda")
+    ws = torch.full((up.decode_workspace_bytes(c, n, hq),), 0xff, dtype=torch.uint8, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(hq, n, device="cuda")
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        up.kv_write(c, k, v, seq, pos, table)
+        up.decode(c, q, table, ln, o, ws, lse=lse)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        up.kv_write(c, k, v, seq, pos, table)
+        up.decode(c, q, table, ln, o, ws, lse=lse)
+    for step in range(4):
+        now = [x + step + 1 if b != 1 or step > 1 else 0 for b, x in enumerate(lens)]
+        k.copy_(heads(g, "head", hkv, n, dh))
+        v.copy_(heads(g, "token", hkv, n, dh))
+        pos.copy_(torch.tensor([x - 1 for x in now], dtype=torch.int32))
+        seq.copy_(torch.tensor([b if x > 0 else -1 for b, x in enumerate(now)], dtype=torch.int32))
+        ln.copy_(torch.tensor(now, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        for b, x in enumerate(now):
+            if x:
+                rows = cached(c, "k", table, b, x)[:, -1]
+                assert kind == "e4m3" or torch.equal(rows, k[:, b].double())
+        want, wl = check_decode(c, q, table, now)
+        assert torch.equal(o, want) and torch.equal(lse, wl)
+
+
+def test_entry_points_on_a_stream_of_their_own():
+    c, table, q = setup("e4m3", [200, 300], 8, 2, 128, 64)
+    want, wl = run_decode(c, q, table, [200, 300])
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    pos, seq = torch.arange(200, device="cuda").int(), torch.zeros(200, dtype=torch.int32, device="cuda")
+    k, v = torch.empty(2, 200, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(2, 200, 128, dtype=torch.bfloat16, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty(8, 2, device="cuda")
+    ws = torch.empty(up.decode_workspace_bytes(c, 2, 8), dtype=torch.uint8, device="cuda")
+    ln = torch.tensor([200, 300], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    up.kv_read(c, seq, pos, table, k, v, stream=st)
+    up.kv_write(c, k, v, seq, pos, table, stream=st)       # what was read is written back: the same codes, scales within a rounding
+    up.kv_read(c, seq, pos, table, k, v, stream=st)
+    up.decode(c, q, table, ln, o, ws, lse=lse, stream=st)
+    st.synchronize()
+    assert torch.equal(o[:, 1], want[:, 1]) and torch.equal(lse[:, 1], wl[:, 1])
+    ref = cached(c, "k", table, 0, 200)
+    assert bool(((k.double() - ref).abs() <= ref.abs() * BF + 2.0 ** -133).all())
+
+
+def test_binding_refuses_on_the_gpu():
+    c, table, q = setup("bf16", [20, 30], 8, 2, 128, 16)
+    o, ws = torch.empty_like(q), torch.empty(up.decode_workspace_bytes(c, 2, 8), dtype=torch.uint8, device="cuda")
+    ln = torch.tensor([20, 30], dtype=torch.int32, device="cuda")
+    k = torch.zeros(2, 3, 128, dtype=torch.bfloat16, device="cuda")
+    i = torch.zeros(3, dtype=torch.int32, device="cuda")
+    n = up.launch_count()
+    for call in (lambda: up.decode(c, q.float(), table, ln, o, ws), lambda: up.decode(c, q, table.long(), ln, o, ws),
+                 lambda: up.decode(c, q, table, ln.long(), o, ws), lambda: up.decode(c, q, table, ln[:1], o, ws),
+                 lambda: up.decode(c, q[:, :1], table, ln, o[:, :1], ws), lambda: up.decode(c, q, table, ln, o[:4], ws),
+                 lambda: up.decode(c, q[..., :64], table, ln, o[..., :64], ws), lambda: up.decode(c, q, table[0], ln, o, ws),
+                 lambda: up.decode(c, q, table.t(), ln, o, ws), lambda: up.decode(c, q, table, ln.cpu(), o, ws),
+                 lambda: up.decode(c, q, table, ln, o, ws.int()), lambda: up.decode(c, q, table, ln, o, ws, lse=torch.empty(2, 8, device="cuda")),
+                 lambda: up.decode(c, q[0], table, ln, o[0], ws), lambda: up.decode(c, q.transpose(1, 2), table, ln, o, ws),
+                 lambda: up.kv_write(c, k[:1], k, i, i, table), lambda: up.kv_write(c, k, k.float(), i, i, table),
+                 lambda: up.kv_write(c, k, k, i[:2], i, table), lambda: up.kv_write(c, k, k, i.long(), i, table),
+                 lambda: up.kv_write(c, k, k, i, i, table.cpu()), lambda: up.kv_write(c, k, k, i[None], i, table),
+                 lambda: up.kv_read(c, i, i, table, k, k.cpu()), lambda: up.KVCache(c.k, c.v.transpose(1, 2)),
+                 lambda: up.KVCache(c.k, c.v, torch.zeros(1, device="cuda"), None), lambda: up.KVCache(c.k.transpose(2, 3), c.v.transpose(2, 3))):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: up.decode(c, q, table, ln, q, ws), lambda: up.decode(c, q, table, ln, o, ws[:16]), lambda: up.kv_read(c, i, i, table, k, k),
+                 lambda: up.decode(c, q, table, ln, o, ws, scale=math.nan), lambda: up.kv_write(c, c.k[0, :, :3], k, i, i, table)):
+        with pytest.raises(up.UpipeError):
+            call()
+    assert up.launch_count() == n
