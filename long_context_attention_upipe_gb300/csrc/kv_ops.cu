@@ -27,6 +27,7 @@ bool pool_rows(PoolRows& r, const void* base, int64_t pages, int64_t heads, int6
   for (int i = 0; i < 3; ++i) {
     if (r.s[i] < 0 || r.s[i] > kMaxSpan / 16 / r.n[i]) return false;
     r.s[i] *= elem;
+    if (r.s[i] >= (int64_t)1 << 40) return false;  // what a TMA map takes
   }
   for (int i = 0; i < 2; ++i)  // sort three by falling stride
     for (int j = 0; j < 2 - i; ++j)

@@ -207,6 +207,24 @@ def test_write_keeps_nan_infinity_and_zero_in_their_rows(dh):
     assert bool(vo.isfinite().all())
 
 
+def test_write_codes_of_every_pair_of_significands():
+    """Rows whose largest magnitude and elements take every bf16 significand: the codes are those of the exact quotient."""
+    top = torch.arange(128, 256, device="cuda").float()
+    x = torch.arange(128, 256, device="cuda").float()
+    for shift in (0, 1, 2, 5, 8, 12, 16):
+        for size in (2.0 ** -7, 2.0 ** 40, 2.0 ** 70, 2.0 ** -90):
+            rows = torch.minimum(x[None] / 2 ** shift, top[:, None]).repeat(1, 1)
+            rows[:, 0] = top
+            rows = (rows * size * torch.where(torch.arange(128, device="cuda") % 2 == 1, -1, 1)).bfloat16()
+            c = make_cache("e4m3", pages=8, hkv=1, size=16, dh=128)
+            pos, table = torch.arange(128, device="cuda").int(), torch.arange(8, device="cuda").int()[None].contiguous()
+            up.kv_write(c, rows[None], rows[None], torch.zeros_like(pos), pos, table)
+            s = rows.float().abs().amax(1) * torch.tensor(1 / 448, dtype=torch.float32, device="cuda")
+            want = (rows.double() / s.double()[:, None]).float().to(torch.float8_e4m3fn)
+            assert torch.equal(bits(c.k).view(128, 128), bits(want)) and torch.equal(bits(c.v), bits(c.k))
+            assert torch.equal(c.k_scale.view(-1), s) and torch.equal(c.v_scale, c.k_scale)
+
+
 def test_no_tokens():
     c = make_cache("bf16")
     e, i = torch.empty(2, 0, 128, dtype=torch.bfloat16, device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda")

@@ -163,3 +163,16 @@ def test_binding_refuses():
                  lambda: up.KVCache(k.to(torch.float8_e4m3fn), k.to(torch.float8_e4m3fn))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_codes_of_bf16_rows_do_not_hang_on_the_quotients_last_bits():
+    """For every bf16 magnitude over a scale that a bf16 magnitude gives: the quotient lowered and raised by 2^-42 of itself (the
+    kernel's is within 2^-43) rounds to the same code, by way of fp32 as the definition has it."""
+    top = torch.arange(128, 256, dtype=torch.float32)
+    scale = top * torch.tensor(1.0 / 448.0, dtype=torch.float32)
+    x = torch.arange(128, 256, dtype=torch.float64)
+    for shift in range(24):                              # below that every code is zero
+        q = (x / 2.0 ** shift)[None, :] / scale.double()[:, None]
+        q = torch.where((x / 2.0 ** shift)[None, :] <= top.double()[:, None], q, torch.zeros_like(q))
+        low, high = ((q * (1 + d)).float().to(torch.float8_e4m3fn).view(torch.uint8) for d in (-2.0 ** -42, 2.0 ** -42))
+        assert torch.equal(low, high)
