@@ -612,7 +612,7 @@ upipe_status_t upipe_attn_no_alloc_device_status(int32_t* code, void* stream);
  * pages point to a profiler to find where memory and time go: podcast summary, chapter
  * "PyTorch profiler").  While enabled, every kernel launch of upipe_attn_fwd / upipe_attn_bwd
  * (and their offloaded forms), upipe_mlp_fwd / upipe_mlp_bwd and the ring steps (not of the operators around
- * the two blocks) is
+ * the two blocks, nor of the paged cache's) is
  * bracketed by two CUDA events on the call's stream and logged with its kind and shape; do not
  * enable it while a stream is being captured into a CUDA graph.  Process-wide; off by default.
  *   kind      UPIPE_K_* below
@@ -664,7 +664,7 @@ upipe_status_t upipe_attn_set_dkdv_window(int32_t items);
 /* Limit of every bounded device-side wait of the library's kernels, in nanoseconds (0 restores the
  * default of 4 s; at most 60 s).  Each kernel receives the value in effect when it is launched.
  * When a wait runs out, the kernel raises UPIPE_ERR_DEVICE_TIMEOUT in the error word of its
- * workspace or table (the operators around the two blocks, which have none, leave NaN) and returns instead of
+ * workspace or table (the operators around the two blocks and upipe_attn_decode, which have none, leave NaN) and returns instead of
  * hanging.  A diagnostic with no counterpart on the
  * pages: shorter limits are for testing the timeout path with upipe_attn_wait_probe. */
 upipe_status_t upipe_attn_set_wait_limit_ns(uint64_t ns);

@@ -671,7 +671,7 @@ class KVCache:
 
 def _page_table(t, dev):
     shape, (ld, inner) = t.shape, t.stride() if t.dim() == 2 else (0, 0)
-    if inner != 1 and (len(shape) != 2 or shape[1] > 1) or t.dtype != torch.int32 or t.get_device() != dev:
+    if inner != 1 and (len(shape) != 2 or shape[1] > 1) or t.dtype is not torch.int32 or t.get_device() != dev:
         _refuse(f"page_table: int32 [sequences, pages] with contiguous rows on device {dev} expected, got {t.dtype} "
                 f"{tuple(shape)} {t.stride()} on {t.device}")
     n, m = shape
@@ -681,7 +681,7 @@ def _page_table(t, dev):
 def _heads(t, dev, shape, what):
     """Address, head stride and token stride of bf16 rows [heads, tokens, head_dim]."""
     hs, ts, es = t.stride() if t.shape == shape else (0, 0, 0)
-    if es != 1 or t.dtype != _BF16 or t.get_device() != dev:
+    if es != 1 or t.dtype is not _BF16 or t.get_device() != dev:
         _refuse(f"{what}: bf16 {tuple(shape)} with contiguous rows on device {dev} expected, got {t.dtype} {tuple(t.shape)} "
                 f"{t.stride()} on {t.device}")
     return t.data_ptr(), hs, ts
@@ -689,7 +689,7 @@ def _heads(t, dev, shape, what):
 
 def _ints(t, dev, n, what):
     """Address of a contiguous vector of n int32."""
-    if t.shape != (n,) or t.dtype != torch.int32 or t.get_device() != dev or not t.is_contiguous():
+    if t.shape != (n,) or t.dtype is not torch.int32 or t.get_device() != dev or not t.is_contiguous():
         _refuse(f"{what}: contiguous int32 [{n}] on device {dev} expected, got {t.dtype} {tuple(t.shape)} {t.stride()} on {t.device}")
     return t.data_ptr()
 
@@ -733,21 +733,21 @@ def decode(cache: KVCache, q, page_table, lens, o, ws, lse=None, scale=0.0, stre
     order (query t sees the keys before lens[b] - q_len + 1 + t); lens int32 [sequences]; lse, optional, fp32
     [n_q_heads, sequences * q_len]; ws uint8 of decode_workspace_bytes."""
     dev, shape = cache.device_index, q.shape
-    if dev != torch._C._cuda_getDevice() or len(shape) != 3 or shape[2] != cache.head_dim:
-        _refuse(f"decode: a cache on the current device and q of [heads, tokens, {cache.head_dim}] expected, got {cache.k.device} and "
-                f"{tuple(shape)}")
     table = _page_table(page_table, dev)
-    n = page_table.shape[0]
-    hq, tokens, _ = shape
+    n = table.n_seqs
+    hq, tokens, dh = shape if len(shape) == 3 else (0, 0, 0)
     q_len = tokens // n if n else 1
-    if tokens != n * q_len or not q_len:
-        _refuse(f"decode: q of [heads, q_len * {n}, {cache.head_dim}] expected, got {tuple(shape)}")
-    qp, qh, qt = _heads(q, dev, shape, "q")
-    op, oh, ot = _heads(o, dev, shape, "o")
-    if ws.dtype != torch.uint8 or ws.get_device() != dev or not ws.is_contiguous():
-        _refuse(f"decode: ws of contiguous uint8 on device {dev} expected, got {ws.dtype} on {ws.device}")
+    if dh != cache.head_dim or tokens != n * q_len or not q_len or o.shape != shape:
+        _refuse(f"decode: q and o of [heads, q_len * {n}, {cache.head_dim}] expected, got {tuple(shape)} and {tuple(o.shape)}")
+    qh, qt, qe = q.stride()
+    oh, ot, oe = o.stride()
+    if (dev != torch._C._cuda_getDevice() or q.get_device() != dev or o.get_device() != dev or ws.get_device() != dev or qe != 1 or oe != 1
+            or q.dtype is not _BF16 or o.dtype is not _BF16 or ws.dtype is not torch.uint8 or not ws.is_contiguous()):
+        _refuse(f"decode: q and o of bf16 with contiguous rows and a contiguous ws of uint8, on the cache's device, which is the current one, "
+                f"expected, got {q.dtype} {q.stride()} on {q.device}, {o.dtype} {o.stride()} on {o.device}, {ws.dtype} on {ws.device}, "
+                f"a cache on {cache.k.device}")
     rc = (_lib or lib()).upipe_attn_decode(
-        cache.desc, table, _ints(lens, dev, n, "lens"), hq, q_len, scale, qp, qh, qt, op, oh, ot,
+        cache.desc, table, _ints(lens, dev, n, "lens"), hq, q_len, scale, q.data_ptr(), qh, qt, o.data_ptr(), oh, ot,
         None if lse is None else _dev(lse, dev, _F32, (hq, tokens), "lse"), ws.data_ptr(), ws.numel(),
         torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if rc:

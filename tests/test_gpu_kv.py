@@ -766,3 +766,30 @@ def test_binding_refuses_on_the_gpu():
         with pytest.raises(up.UpipeError):
             call()
     assert up.launch_count() == n
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_decode_of_the_longest_sequence(kind):
+    """2^31 - 1 keys: one page of 2^20 tokens under every entry of the table.
+
+    A lane's part of l is a chain of some 2 x 2^27 / (152 x 8) additions, each within 2^-24 of the sum so far, O's sums chains of half
+    as many that may truncate (2^-23); W / |o| is small here, so the tolerance is in units of W."""
+    size, dh, n = 1 << 20, 64, 2 ** 31 - 1
+    g = gen(77)
+    c = make_cache(kind, pages=1, hkv=1, size=size, dh=dh, fill=g)
+    table = torch.zeros(1, 2048, dtype=torch.int32, device="cuda")
+    q = randn(g, 2, 1, dh).bfloat16()
+    o, lse = run_decode(c, q, table, [n])
+    k, v = cached(c, "k", table, 0, size)[0], cached(c, "v", table, 0, size)[0]
+    s = q[:, 0].double() @ k.t() / 8
+    top = s.amax(1, keepdim=True)
+    w = torch.exp(s - top)
+    total = 2048 * w.sum(1) - w[:, -1]
+    want = (2048 * (w @ v) - w[:, -1:] * v[-1:]) / total[:, None]
+    size_ = (2048 * (w @ v.abs())) / total[:, None]
+    chain = 2 * 2 ** 27 / (152 * 8) * 2.0 ** -24
+    assert bool(((o[:, 0].double() - want).abs() <= want.abs() * BF + size_ * 2 * chain).all())
+    assert bool(((lse[:, 0].double() - top[:, 0] - torch.log(total)).abs() <= chain + 2.0 ** -16).all())
+    # one key more than the table holds, and the table's last key
+    o, lse = run_decode(c, q, table[:, :2047], [2047 * size + 1])
+    assert bool(o.isnan().all()) and bool(lse.isnan().all())
