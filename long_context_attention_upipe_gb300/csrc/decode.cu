@@ -40,6 +40,8 @@
 // One long sequence streams at the copy rate.  What a call adds: 5 us until the first tile lands
 // (lengths, table entries and queries are read one after another), 2 to 4 us for the ends of the last items, 2 to 3 us for the
 // second launch.  With 16 rows the tiles' own chain of instructions bounds e4m3 (5.7 TB/s; 250 registers leave room for 8 warps).
+#include <type_traits>
+
 #include "internal.h"
 #include "kv_cache.cuh"
 #include "quant.cuh"
@@ -72,20 +74,20 @@ struct Lay {
   static constexpr int SLOT = ROWS * D * 4;             // sums of a piece's o
   static constexpr int WARPS = W;
   static constexpr int END = FP8 ? 4 : 2;               // tiles' time that an item's end (and the next one's begin) takes
-  static constexpr int FIT = ((226 * 1024 - 16) / WARPS - 24 - SLOT - 2 * ROWS * (int)sizeof(RowSum)) / (STAGE + SCALES + 8);
+  static constexpr int FIT = ((226 * 1024 - 16) / WARPS - 40 - SLOT - 2 * ROWS * (int)sizeof(RowSum)) / (STAGE + SCALES + 8);
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
   static constexpr int QUEUE = STAGES * STAGE;
   static constexpr int AT_SCALES = WARPS * QUEUE, AT_SLOTS = AT_SCALES + WARPS * STAGES * SCALES;
   static constexpr int AT_SUMS = AT_SLOTS + WARPS * SLOT, AT_BARS = AT_SUMS + WARPS * 2 * ROWS * (int)sizeof(RowSum);
   static constexpr int AT_INFO = AT_BARS + WARPS * STAGES * 8;
-  static constexpr int BYTES = AT_INFO + WARPS * 24 + 16 + 1024;  // the queues start on 1024 bytes
+  static constexpr int BYTES = AT_INFO + WARPS * 40 + 16 + 1024;  // the queues start on 1024 bytes
   static constexpr int MT = D / 16;                     // tiles of O^T
   static constexpr int KS = D / 16;                     // steps of S^T
   static_assert(STAGES >= 2 && QUEUE >= SLOT && WARPS * QUEUE >= 2048 * 8 && BYTES <= 227 * 1024, "shared memory");
 };
 
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -125,13 +127,23 @@ __device__ __forceinline__ void lds_floats(float* v, uint32_t at) {
     asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(at) : "memory");
 }
 // Four 8 x 8 matrices of 16-bit elements, a lane's address naming a row of one.
+template <int AT>
 __device__ __forceinline__ void ldm4(uint32_t (&w)[4], uint32_t at) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4 + %5];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at), "n"(AT) : "memory");
 }
+template <int AT>
 __device__ __forceinline__ void ldm4_trans(uint32_t (&w)[4], uint32_t at) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at) : "memory");
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4 + %5];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(at), "n"(AT) : "memory");
+}
+// f(0), f(1) .. f(N - 1), the argument known at compile time.
+template <int N, int I = 0, typename F>
+__device__ __forceinline__ void each(const F& f) {
+  if constexpr (I < N) {
+    f(std::integral_constant<int, I>());
+    each<N, I + 1>(f);
+  }
 }
 
 template <bool FP8>
@@ -204,6 +216,11 @@ __device__ __forceinline__ int64_t mul_div(int64_t a, int b, int c) {
   return p <= 0xffffffffll ? (int64_t)((uint32_t)p / (uint32_t)c) : div64(p, c);
 }
 
+// Parts that a line of `total` tiles is cut into: no CTA gets less than a tile for each warp.
+__device__ __forceinline__ int parts_of(int64_t total, int ctas, int warps) {
+  return total < (int64_t)ctas * warps ? max((int)(total + warps - 1) / warps, 1) : ctas;
+}
+
 // The part that holds tile end - 1 where part i ends before tile total * (i + 1) / parts.
 __device__ __forceinline__ int last_part(int64_t end, int64_t total, int parts) {
   const int64_t p = end * parts + total - 1;
@@ -266,13 +283,18 @@ __device__ __noinline__ void redo(const DecodeArgs& a, int b, int hk, RowAt at, 
 
 __device__ __forceinline__ float row_lse(float m, float l) { return m * kLn2 + logf(l); }
 
-// Waits, a second at most, for copies that are on their way although a wait for them ran out.
-__device__ __forceinline__ void drain(uint32_t bars, uint32_t in_flight, uint32_t phases) {
-  if (!in_flight) return;
+// Waits, a second at most, for the `n` copies from `stage` on that are on their way although a wait for one ran out.
+__device__ __forceinline__ void drain(uint32_t bars, int stages, int stage, uint32_t parity, int n) {
+  if (n == 0) return;
   const uint64_t t0 = tc::globaltimer();
-  for (int i = 0; i < 8; ++i)
-    while ((in_flight >> i & 1) && !tc::mbar_try_wait_addr(bars + i * 8, phases >> i & 1))
+  for (; n > 0; --n) {
+    while (!tc::mbar_try_wait_addr(bars + stage * 8, parity))
       if (tc::globaltimer() - t0 > tc::kDrainNs) return;
+    if (++stage == stages) {
+      stage = 0;
+      parity ^= 1;
+    }
+  }
 }
 
 constexpr int kJoinThreads = 256;
@@ -282,6 +304,7 @@ struct DecodeWs {
                   // not; z whether the latter begins its item, w the CTA in which it ends
   RowSum* sums;   // [row blocks][CTAs][2][rows]
   float* acc;     // [row blocks][CTAs][2][rows][D]
+  int64_t scale_step;  // from a row's scale to the one 16 rows on
   bool solo;      // a CTA to each item: nothing is left for the joining kernel
 };
 
@@ -315,7 +338,7 @@ __global__ void __launch_bounds__(32 * W, 1)
   RowSum* piece_sums = reinterpret_cast<RowSum*>(smem + L::AT_SUMS);  // [2 warp: head, 2 warp + 1: tail][row]
   int4* info = reinterpret_cast<int4*>(smem + L::AT_INFO);  // [warp]: item of the head piece, of the tail, tail begins, its last CTA
   int2* info_len = reinterpret_cast<int2*>(info + kWarps);  // ... keys of their sequences
-  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::AT_INFO + kWarps * 24);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::AT_INFO + kWarps * 40);
   const uint32_t bars = smem_u32(smem + L::AT_BARS) + warp * L::STAGES * 8;
   if (lane < L::STAGES) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + lane * 8) : "memory");
   if (threadIdx.x == 0) *abort_flag = 0;
@@ -346,8 +369,7 @@ __global__ void __launch_bounds__(32 * W, 1)
     total = first32 + warp_sum(units_of<L::END>(lens2, cap));
   }
   total *= hkv;
-  // no CTA gets less than a tile for each warp
-  const int parts = total < (int64_t)X * kWarps ? max((int)(total + kWarps - 1) / kWarps, 1) : X;
+  const int parts = parts_of(total, X, kWarps);
   // the next sequence with keys, or none; `seq_lens`: the lanes' lengths of b's 32 sequences
   auto next_seq = [&](int& b, int& seq_lens) {
     unsigned some = __ballot_sync(0xffffffffu, seq_lens > 0) & ~((2u << (b & 31)) - 1u);
@@ -367,7 +389,12 @@ __global__ void __launch_bounds__(32 * W, 1)
     first = t0 + (int64_t)((uint64_t)((t1 - t0) * warp) / kWarps);
     left = t0 + (int64_t)((uint64_t)((t1 - t0) * (warp + 1)) / kWarps) - first;
   }
-  const int64_t next = first + left;  // the tile after the part
+  // the tile after the part, and all tiles: read again when the part ends
+  volatile int64_t* part_end = reinterpret_cast<volatile int64_t*>(smem + L::AT_INFO + kWarps * 24) + 2 * warp;
+  if (lane == 0) {
+    part_end[0] = first + left;
+    part_end[1] = total;
+  }
   int hk0 = 0, tile0 = 0;
   if (ws.solo) {
     hk0 = blockIdx.x - b0 * hkv;
@@ -476,7 +503,8 @@ __global__ void __launch_bounds__(32 * W, 1)
     int ppi = pt * kTileKeys / ps, prow = pt * kTileKeys - ppi * ps;
     int held = (int)(((unsigned)plen + (ps - 1)) / ps);  // pages of the sequence
     int plens = lens;
-    int64_t to_load = left;
+    int load_left = (int)min(left, (int64_t)(pn - pt));  // tiles of this item that are still to be loaded
+    int64_t to_load = left - load_left;                  // and what follows it
     auto entries = [&](int b, int first_page) {
       const int i = first_page + lane;
       return i < a.t.max_pages ? a.t.pages[(int64_t)b * a.t.stride + i] : -1;
@@ -491,55 +519,68 @@ __global__ void __launch_bounds__(32 * W, 1)
     };
     int ids = entries(pb, ppi & ~31), ids_after = following();
     fetch(b0, hk0);  // behind the copies it would take microseconds
-    uint32_t in_flight = 0;  // stages that a copy is on its way to; those of tiles whose page does not exist stay as they are
-    bool ok = true;          // no wait ran out
+    int page = __shfl_sync(0xffffffffu, ids, ppi & 31);
+    const float* scale = scales;  // this lane's of the next tile
+    auto scale_row = [&]() {
+      if (FP8)
+        scale = scales + ((unsigned)page < (unsigned)a.c.n_pages ? page * a.c.scale_page_stride + phk * a.c.scale_head_stride +
+                                                                       (prow + s_key) * a.c.scale_token_stride : 0);
+    };
+    scale_row();
+    uint32_t missing = 0;  // stages of tiles whose page does not exist
+    int in_flight = 0;     // copies that have not been waited for
+    bool ok = true;        // no wait ran out; else
+    int lost_at = 0;       // 2 * the stage of the first that did, + its parity
     auto load = [&](int stage) {
-      const int page = __shfl_sync(0xffffffffu, ids, ppi & 31);
-      const bool there = (unsigned)page < (unsigned)a.c.n_pages;
-      if (there) {
-        in_flight |= 1u << stage;
+      const uint32_t bar = bars + stage * 8;
+      missing &= ~(1u << stage);
+      ++in_flight;
+      if ((unsigned)page < (unsigned)a.c.n_pages) {
         if (tc::elect_one()) {
-          const uint32_t at = queue + stage * L::STAGE, bar = bars + stage * 8;
+          const uint32_t at = queue + stage * L::STAGE;
           expect_tx(bar, L::STAGE);
           tma_tile<L::SEGS>(at, &map_k, bar, prow, phk, page);
           tma_tile<L::SEGS>(at + L::KBYTES, &map_v, bar, prow, phk, page);
         }
-        if (FP8) {
-          const bool in = s_key < plen - pt * kTileKeys;
-          const float* p = scales + (in ? page * a.c.scale_page_stride + phk * a.c.scale_head_stride +
-                                              (prow + s_key) * a.c.scale_token_stride : 0);
-          cp4(scale_queue + stage * L::SCALES, p, in ? 4 : 0);
-        }
+        if (FP8) cp4(scale_queue + stage * L::SCALES, scale);  // those behind the sequence's end are not used
+      } else {
+        if (lane == 0) tc::mbar_arrive_addr(bar);
+        missing |= 1u << stage;
       }
-      to_load -= ++pt == pn ? 1 + L::END : 1;
-      if (to_load > 0) {  // on to the next tile
-        bool fresh = false;
-        prow += kTileKeys;
-        if (prow == ps) {
-          prow = 0;
-          fresh = (++ppi & 31) == 0;
+      // on to the next tile
+      prow += kTileKeys;
+      if (FP8) scale += ws.scale_step;
+      if (--load_left > 0 && prow < ps) return;
+      bool fresh = false;
+      if (load_left > 0) {  // the next page
+        prow = 0;
+        fresh = (++ppi & 31) == 0;
+      } else {  // the next item
+        if (to_load > 0) to_load -= L::END;
+        if (to_load <= 0) return;
+        ppi = prow = 0;
+        fresh = held > 32;
+        if (++phk == hkv) {
+          phk = 0;
+          fresh = true;
+          if (!next_seq(pb, plens)) pb = n_seqs - 1;  // only if the lengths changed meanwhile
+          plen = min(max(__shfl_sync(0xffffffffu, plens, pb & 31), 0), cap);
+          pn = tiles_of(plen, cap);
+          held = (int)(((unsigned)plen + (ps - 1)) / ps);
         }
-        if (pt == pn) {
-          pt = ppi = prow = 0;
-          fresh = held > 32;
-          if (++phk == hkv) {
-            phk = 0;
-            fresh = true;
-            if (!next_seq(pb, plens)) pb = n_seqs - 1;  // only if the lengths changed meanwhile
-            plen = min(max(__shfl_sync(0xffffffffu, plens, pb & 31), 0), cap);
-            pn = tiles_of(plen, cap);
-            held = (int)(((unsigned)plen + (ps - 1)) / ps);
-          }
-        }
-        if (fresh) {
-          ids = ids_after;
-          ids_after = following();
-        }
+        load_left = (int)min(to_load, (int64_t)max(pn, 1));
+        to_load -= load_left;
       }
+      if (fresh) {
+        ids = ids_after;
+        ids_after = following();
+      }
+      page = __shfl_sync(0xffffffffu, ids, ppi & 31);
+      scale_row();
     };
 #pragma unroll 1
     for (int s = 0; s < L::STAGES - 1; ++s) {
-      if (to_load > 0) load(s);
+      if (load_left > 0) load(s);
       if (FP8) cp_commit();
     }
 
@@ -550,10 +591,16 @@ __global__ void __launch_bounds__(32 * W, 1)
       const int key = (lane & 7) + ((key_bit3 ? lane : lane >> 1) & 8), piece = (key_bit3 ? lane >> 4 : lane >> 3) & 1;
       return key * L::SEG + ((piece ^ (L::SEG == 128 ? key & 7 : (key >> 1) & 3)) << 4);
     };
-    const uint32_t k_row = matrix_row(true), v_row = L::KBYTES + matrix_row(FP8);
+    constexpr int STEPS = L::SEG / 32;  // pairs of 16-byte pieces of a box's row
+    uint32_t k_row[STEPS], v_row[STEPS];
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      k_row[i] = matrix_row(true) ^ (32 * i);
+      v_row[i] = matrix_row(FP8) ^ (32 * i);
+    }
     int cb = b0, chk = hk0, ct = tile0, raw = __shfl_sync(0xffffffffu, lens, b0 & 31), len = min(max(raw, 0), cap), cn = tiles_of(len, cap);
     int stage = 0;
-    uint32_t phases = 0;
+    uint32_t parity = 0;
     float m[NT][2], l[NT][2], mv[NT][2], acc[NT][L::MT][4];
     int see[NT][2];  // a row sees keys before len + see
 #pragma unroll
@@ -575,28 +622,27 @@ __global__ void __launch_bounds__(32 * W, 1)
           for (int i = 0; i < 4; ++i) acc[nt][mt][i] = 0.f;
       }
       const int begin = ct;
+      const int all_seen = max(len - a.q_len + 1, 0) / kTileKeys;    // tiles before this are seen by every row
+      const int partial = len % kTileKeys ? cn - 1 : -1;             // a tile that the sequence ends in
+      int tiles = (int)min(left, (int64_t)max(cn - ct, 1));
+      left -= tiles;
       // ---- its tiles
       do {
         __syncwarp();  // all lanes have read the stage that is loaded next
-        const int ahead = stage + L::STAGES - 1;
-        if (to_load > 0 && ok) load(ahead >= L::STAGES ? ahead - L::STAGES : ahead);
+        if (load_left > 0 && ok) load(stage == 0 ? L::STAGES - 1 : stage - 1);
         if (FP8) {
           cp_commit();
           cp_wait<L::STAGES - 1>();
         }
-        const uint32_t at = queue + stage * L::STAGE, bit = 1u << stage;
-        bool lost = !(in_flight & bit);  // the page does not exist, or a wait ran out
-        if (!lost && ok) {
-          ok = __all_sync(0xffffffffu, tc::mbar_wait_addr(bars + stage * 8, (phases & bit) != 0, abort_flag, wait_ns));
-          if (ok) {
-            in_flight &= ~bit;
-            phases ^= bit;
-          }
+        const uint32_t at = queue + stage * L::STAGE;
+        if (ok) {
+          ok = __all_sync(0xffffffffu, tc::mbar_wait_addr(bars + stage * 8, parity, abort_flag, wait_ns));
+          if (ok) --in_flight;
+          else lost_at = 2 * stage + parity;
         }
-        lost |= !ok;
-        const int k0 = ct * kTileKeys;
-        if (len - k0 < kTileKeys) {  // rows behind the sequence's end may hold anything: the values' become zeros
-          for (int i = max(len - k0, 0) * (L::SEG / 16) + lane; i < kTileKeys * (L::SEG / 16); i += 32)
+        const bool lost = !ok || (missing >> stage & 1);  // a wait ran out, or the page does not exist
+        if (ct == partial) {  // rows behind the sequence's end may hold anything: the values' become zeros
+          for (int i = len % kTileKeys * (L::SEG / 16) + lane; i < kTileKeys * (L::SEG / 16); i += 32)
 #pragma unroll
             for (int sg = 0; sg < L::SEGS; ++sg)
               asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(at + L::KBYTES + sg * (kTileKeys * L::SEG) + i * 16), "r"(0) : "memory");
@@ -610,11 +656,14 @@ __global__ void __launch_bounds__(32 * W, 1)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[nt][i] = s2[nt][i] = 0.f;
+          uint32_t from[STEPS];
 #pragma unroll
-          for (int j = 0; j < L::ROWB / 32; ++j) {  // two 16-byte pieces: keys 0-7, 8-15 of the first, of the second
+          for (int i = 0; i < STEPS; ++i) from[i] = at + k_row[i];
+          each<L::ROWB / 32>([&](auto jc) {  // two 16-byte pieces: keys 0-7, 8-15 of the first, of the second
+            constexpr int j = decltype(jc)::value;
             uint32_t w[4];
-            ldm4(w, (at + j * 32 / L::SEG * (kTileKeys * L::SEG) + k_row) ^ (j * 32 % L::SEG));
-            if (FP8) {
+            ldm4<j / STEPS * (kTileKeys * L::SEG)>(w, from[j % STEPS]);
+            if constexpr (FP8) {
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
                 uint32_t a0, a1, a2, a3;
@@ -627,7 +676,7 @@ __global__ void __launch_bounds__(32 * W, 1)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma<FP8>(j & 1 ? s2[nt] : x[nt], w[0], w[1], w[2], w[3], q[nt][j][0], q[nt][j][1]);
             }
-          }
+          });
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -646,7 +695,7 @@ __global__ void __launch_bounds__(32 * W, 1)
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[nt][i] *= ks[i >> 1];
         }
-        const bool some_hidden = k0 > len - a.q_len + 1 - kTileKeys || lost;
+        const bool some_hidden = ct >= all_seen || lost;
         auto relative = [&]() {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
@@ -662,7 +711,7 @@ __global__ void __launch_bounds__(32 * W, 1)
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
-                const bool in = k0 + r + 8 * (i >> 1) < len + see[nt][i & 1];
+                const bool in = ct * kTileKeys + r + 8 * (i >> 1) < len + see[nt][i & 1];
                 d[nt][i] = in ? d[nt][i] + nan : -INFINITY;
                 if (FP8) dv[nt][i] = in ? dv[nt][i] + nan : -INFINITY;
               }
@@ -725,11 +774,14 @@ __global__ void __launch_bounds__(32 * W, 1)
             }
           }
         // ---- O^T += V^T P^T
-        if (FP8) {
+        uint32_t from[STEPS];
 #pragma unroll
-          for (int j = 0; j < L::MT / 2; ++j) {  // pieces 2 j, 2 j + 1: pairs of elements by pairs of keys
+        for (int i = 0; i < STEPS; ++i) from[i] = at + v_row[i];
+        if constexpr (FP8) {
+          each<L::MT / 2>([&](auto jc) {  // pieces 2 j, 2 j + 1: pairs of elements by pairs of keys
+            constexpr int j = decltype(jc)::value;
             uint32_t w[4];
-            ldm4_trans(w, (at + v_row) ^ (j * 32));
+            ldm4_trans<L::KBYTES>(w, from[j]);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               uint32_t a0, a1, a2, a3;
@@ -738,35 +790,41 @@ __global__ void __launch_bounds__(32 * W, 1)
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) mma<FP8>(acc[nt][2 * j + i], a0, a1, a2, a3, hi[nt][0], hi[nt][1]);
             }
-          }
+          });
         } else {
-#pragma unroll
-          for (int mt = 0; mt < L::MT; ++mt) {
+          each<L::MT>([&](auto mc) {
+            constexpr int mt = decltype(mc)::value;
             uint32_t w[4];
-            ldm4_trans(w, (at + mt * 32 / L::SEG * (kTileKeys * L::SEG) + v_row) ^ (mt * 32 % L::SEG));
+            ldm4_trans<L::KBYTES + mt / STEPS * (kTileKeys * L::SEG)>(w, from[mt % STEPS]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
               mma<FP8>(acc[nt][mt], w[0], w[1], w[2], w[3], hi[nt][0], hi[nt][1]);
               mma<FP8>(acc[nt][mt], w[0], w[1], w[2], w[3], lo[nt][0], lo[nt][1]);
             }
-          }
+          });
         }
-        if (++stage == L::STAGES) stage = 0;
-        --left;
+        if (++stage == L::STAGES) {
+          stage = 0;
+          parity ^= 1;
+        }
         ++ct;
-      } while (left > 0 && ct < cn);
+      } while (--tiles > 0);
 
       // ---- the piece ends: whole items are done, others wait in shared memory
       const bool begins = begin == 0, ends = ct == cn, whole = begins && ends;
       float* slot = ends ? head_slot : tail_slot;
       const int item = cb * hkv + chk;
       if (!ends) {
-        drain(bars, in_flight, phases);
+        drain(bars, L::STAGES, lost_at >> 1, lost_at & 1, in_flight);
+        in_flight = 0;
         if (FP8) cp_wait<0>();
         left_over.y = item;
         left_len.y = len;
         left_over.z = begins;
-        left_over.w = last_part(max(next + cn - ct, next), total, parts);  // the CTA whose part holds the item's last tile
+        __syncwarp();
+        const int64_t next = part_end[0], all = part_end[1];
+        // the CTA whose part holds the item's last tile
+        left_over.w = last_part(max(next + cn - ct, next), all, parts_of(all, X, kWarps));
       } else if (!whole) {
         left_over.x = item;
         left_len.x = len;
@@ -879,7 +937,7 @@ __global__ void __launch_bounds__(32 * W, 1)
         fetch(cb, chk);
       }
     }
-    drain(bars, in_flight, phases);
+    drain(bars, L::STAGES, lost_at >> 1, lost_at & 1, in_flight);
     if (FP8) cp_wait<0>();
   }
 
@@ -1168,6 +1226,7 @@ cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t st) {
   ws.sums = reinterpret_cast<RowSum*>(p);
   p += places * 2 * sh.rows * sizeof(RowSum);
   ws.meta = reinterpret_cast<int4*>(p);
+  ws.scale_step = kTileKeys * a.c.scale_token_stride;
   if (a.c.head_dim == 128) return a.c.e4m3 ? run_rows<128, true>(a, sh, ws, st) : run_rows<128, false>(a, sh, ws, st);
   return a.c.e4m3 ? run_rows<64, true>(a, sh, ws, st) : run_rows<64, false>(a, sh, ws, st);
 }
