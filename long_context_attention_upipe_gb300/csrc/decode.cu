@@ -7,7 +7,7 @@
 // The cache is read once, and that bounds the kernel: with g query heads to a key head it takes 2 g T operations for each byte of
 // bf16 (4 g T of e4m3), where the tensor cores have hundreds to spare; a tcgen05 tile of 128 rows would be empty but for g T of
 // them.  So the split follows the bytes.  All tiles of 16 keys of all (sequence, key head) items form one line, in order, with a
-// few tiles' time added at each item's end for what an end costs (without: 99 instead of 91 us for 64 sequences up to 16384
+// few tiles' time added at each item's end for what an end costs (without: 94 instead of 88.6 us for 64 sequences up to 16384
 // keys).  The CTAs, one to an SM, take equal parts of the line, and a CTA's warps equal parts of that, whatever the lengths.
 // A warp runs its tiles through a queue of its own in shared memory: one TMA box each for 16 keys and 16 values of a page, so any
 // page, head and token strides cost nothing and warps wait for nobody but their copies.
@@ -30,16 +30,16 @@
 // where a weight's second part is zero.  Then o is not finite although l is, and the piece's o is summed again key by key (redo).
 //
 // Measured (GB300, calls back to back; floor: the cached bytes at the copy rate of 6698 GB/s):
-//   1 sequence of 1048576 keys, 4 / 1 heads, bf16          85.7 us, floor 80.2
-//   1 of 5242880, 8 / 1, e4m3                               206 us, 206.6
-//   64 up to 16384, 32 / 8, e4m3                           86.2 us, 76.0
-//   48 up to 8192, 40 / 8, bf16                            57.7 us, 48.3
-//   16 up to 32768, 4 tokens each, 32 / 8, e4m3            69.7 us, 47.3
-//   256 up to 500, 4 / 2 heads of 64, bf16                 11.3 us, 2.2
-//   1 of 4097, 32 / 8, bf16                                 9.0 us, 2.5
-// One long sequence streams at the copy rate.  What a call adds: 5 us until the first tile lands
-// (lengths, table entries and queries are read one after another), 2 to 4 us for the ends of the last items, 2 to 3 us for the
-// second launch.  With 16 rows the tiles' own chain of instructions bounds e4m3 (5.7 TB/s; 250 registers leave room for 8 warps).
+//   1 sequence of 1048576 keys, 4 / 1 heads, bf16            86 us, floor 80.2
+//   1 of 5242880, 8 / 1, e4m3                           206 - 214 us, 206.6 (as fast as the box's memory)
+//   64 up to 16384, 32 / 8, e4m3                             88 us, 76.0
+//   48 up to 8192, 40 / 8, bf16                              58 us, 48.3
+//   16 up to 32768, 4 tokens each, 32 / 8, e4m3              64 us, 47.3
+//   256 up to 500, 4 / 2 heads of 64, bf16                 11.4 us, 2.2
+//   1 of 4097, 32 / 8, bf16                                 9.1 us, 2.5
+// One long sequence streams at the copy rate.  What a call adds: 5 us until the first tile lands (lengths, table entries and
+// queries are read one after another), 2 to 4 us for the ends of the last items, 2 to 3 us for the second launch.  With 16 rows
+// of an e4m3 cache the tiles' own chain of instructions shows as well: 255 registers leave room for 8 warps.
 #include <type_traits>
 
 #include "internal.h"
@@ -1143,9 +1143,9 @@ __global__ void __launch_bounds__(kJoinThreads) k_decode_join(const __grid_const
   if (a.lse && d == 0) a.lse[at.head * n_seqs * a.q_len + at.tok] = seen <= 0 ? -INFINITY : row_lse(run.m, run.l);
 }
 
-// Rows of a block, blocks of rows, and CTAs for each of them.  Blocks of 16 where there are more than 8 rows: 69.7 us for 16
-// sequences up to 32768 keys with 16 rows, 95.4 as two blocks of 8 that read the cache twice; 8 rows in a block of 16 take 255 us
-// instead of 206 for 5242880 keys e4m3, and 86.7 instead of 85.7 for 1048576 keys bf16.
+// Rows of a block, blocks of rows, and CTAs for each of them.  Blocks of 16 where there are more than 8 rows: 63.8 us for 16
+// sequences up to 32768 keys with 16 rows, 85.6 as two blocks of 8 that read the cache twice; 8 rows in a block of 16 take 224 us
+// instead of 214 for 5242880 keys e4m3, and 87.5 instead of 85.9 for 1048576 keys bf16.
 struct DecodeShape {
   int rows, blocks, ctas;
 };
@@ -1184,8 +1184,8 @@ cudaError_t run(const DecodeArgs& a, const DecodeShape& sh, DecodeWs ws, cudaStr
   note_launch();
   if (e != cudaSuccess || ws.solo) return e;
   const int rows = a.hq / a.c.n_kv_heads * a.q_len;
-  // A joining block for 8 rows where items are of 8 CTAs at most, if they are alike (16 sequences of 8 heads, 16 rows: 69.7 us, 72.6 with
-  // a block to a row), a block to a row where they are longer (one item of 152 CTAs: 206 us, 227 with a warp to a row).
+  // A joining block for 8 rows where items are of 8 CTAs at most, if they are alike (16 sequences of 8 heads, 16 rows: 63.8 us, 66.5 with
+  // a block to a row), a block to a row where they are longer (one item of 152 CTAs: 214 us, 235 with a warp to a row).
   const bool many = items * 8 >= sh.ctas;
   e = launch_pdl(many ? k_decode_join<D, 8> : k_decode_join<D, 1>, dim3(sh.ctas, many ? (int)ceil_div(rows, 8) : rows), dim3(kJoinThreads), 0, st, a,
                  ws, sh.rows);
@@ -1198,9 +1198,9 @@ cudaError_t run_rows(const DecodeArgs& a, const DecodeShape& sh, const DecodeWs&
   if (sh.rows == 16) return run<D, FP8, 2, 8>(a, sh, ws, st);
   if constexpr (FP8) {
     // Converting codes takes instructions, which 16 warps overlap better; fewer warps leave fewer pieces to join where there is
-    // little to read.  One sequence of 8 key heads: 4096 keys 9.7 us with 8 warps, 11.4 with 16; 131072 keys 50.7 and 51.6;
-    // 262144 keys 91.5 and 89.3; 5242880 keys of one head 216 and 209.
-    constexpr int kFewTiles = 600;  // to a CTA, if all sequences were as long as the table allows
+    // little to read.  One sequence of 8 key heads: 4096 keys 9.3 us with 8 warps, 11.6 with 16; 262144 keys 92.7 and 93.3;
+    // 524288 keys 176.7 and 172.7; 5242880 keys of one head 221 and 217.
+    constexpr int kFewTiles = 1200;  // to a CTA, if all sequences were as long as the table allows
     const int64_t tiles = (int64_t)a.t.n_seqs * a.c.n_kv_heads * ceil_div(table_keys(a.t, a.c.page_size), kTileKeys);
     if (tiles > (int64_t)sh.ctas * kFewTiles) return run<D, FP8, 1, 16>(a, sh, ws, st);
   }
