@@ -25,6 +25,7 @@
 //
 // A warp's part may begin or end within an item.  The CTA joins such pieces in shared memory, in order, and what an item leaves
 // in several CTAs a second kernel joins, in order: no atomics, equal calls give equal bits.
+// (More than 16 rows of a long bf16 cache: decode_wide.cu.)
 //
 // A value that is infinite or NaN spoils the products of query rows that do not see it (zero times infinity), and of those that do
 // where a weight's second part is zero.  Then o is not finite although l is, and the piece's o is summed again key by key (redo).
@@ -42,25 +43,11 @@
 // of an e4m3 cache the tiles' own chain of instructions shows as well: 255 registers leave room for 8 warps.
 #include <type_traits>
 
-#include "internal.h"
-#include "kv_cache.cuh"
-#include "quant.cuh"
-#include "tc_common.cuh"
+#include "decode.cuh"
 
 namespace upipe {
 
 namespace {
-
-constexpr int kTileKeys = 16;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kLowest = -3.0e38f;  // a reference below all scores, whose difference to them is defined
-constexpr float kSlack = 8.f;        // a score may exceed the reference by this, in powers of two
-constexpr float kSlackV = 5.f, kShiftV = 10.f;  // fp16 weights: the reference of one lies 10 below the score, the largest is 2^15
-
-// What a row of a piece (or of a joined run of pieces) leaves beside its D sums.
-struct RowSum {
-  float m, l;
-};
 
 template <int D, bool FP8, int NT, int W>
 struct Lay {
@@ -85,34 +72,6 @@ struct Lay {
   static constexpr int KS = D / 16;                     // steps of S^T
   static_assert(STAGES >= 2 && QUEUE >= SLOT && WARPS * QUEUE >= 2048 * 8 && BYTES <= 227 * 1024, "shared memory");
 };
-
-__device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// A tile's box: 16 rows of a page and head, in SEGS halves of 128 bytes where a row is longer.
-template <int SEGS>
-__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, uint32_t bar, int row, int head, int page) {
-  if (SEGS == 2)
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %2, %4, %5}], [%6];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(head), "r"(page), "r"(bar)
-        : "memory");
-  else
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(head), "r"(page), "r"(bar)
-        : "memory");
-}
-__device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ float lds32(uint32_t at) {
   float v;
@@ -162,127 +121,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
   return d;
 }
 
-// Four codes as two pairs of fp16.
-__device__ __forceinline__ void e4m3x4(uint32_t four, uint32_t& lo, uint32_t& hi) {
-  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
-      : "=r"(lo), "=r"(hi) : "r"(four));
-}
-__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
-  uint32_t d;
-  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
-  return d;
-}
-
-__device__ __forceinline__ float fast_log2(float x) {
-  float y;
-  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-// 2^e for -126 <= e <= 127.
-__device__ __forceinline__ float pow2(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }
-
-// Keys that the table can hold, and tiles of a sequence of `len` keys.
-__host__ __device__ __forceinline__ int table_keys(const PageTable& t, int page_size) {
-  const int64_t n = (int64_t)t.max_pages * page_size;
-  return n < INT32_MAX ? (int)n : INT32_MAX;
-}
-__device__ __forceinline__ int tiles_of(int len, int cap) { return (int)(((int64_t)min(max(len, 0), cap) + kTileKeys - 1) / kTileKeys); }
-
-// Length of a sequence's item on the line: its tiles and its end.
-template <int END>
-__device__ __forceinline__ int units_of(int len, int cap) {
-  const int n = tiles_of(len, cap);
-  return n ? n + END : 0;
-}
-
-// Sum over a warp of numbers up to 2^27, which may pass 32 bits.
-__device__ __forceinline__ int64_t warp_sum(int n) {
-  return ((int64_t)__reduce_add_sync(0xffffffffu, (unsigned)n >> 16) << 16) + __reduce_add_sync(0xffffffffu, (unsigned)n & 0xffffu);
-}
-__device__ __forceinline__ int64_t warp_scan(int64_t v, int lane) {
-#pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int64_t o = __shfl_up_sync(0xffffffffu, v, off);
-    if (lane >= off) v += o;
-  }
-  return v;
-}
-
-// a * b / c of numbers whose product fits 64 bits; most fit 32, where a division takes a fraction of the time.
-__device__ __noinline__ int64_t div64(int64_t p, int64_t c) { return p / c; }
-__device__ __forceinline__ int64_t mul_div(int64_t a, int b, int c) {
-  const int64_t p = a * b;
-  return p <= 0xffffffffll ? (int64_t)((uint32_t)p / (uint32_t)c) : div64(p, c);
-}
-
-// Parts that a line of `total` tiles is cut into: no CTA gets less than a tile for each warp.
-__device__ __forceinline__ int parts_of(int64_t total, int ctas, int warps) {
-  return total < (int64_t)ctas * warps ? max((int)(total + warps - 1) / warps, 1) : ctas;
-}
-
-// The part that holds tile end - 1 where part i ends before tile total * (i + 1) / parts.
-__device__ __forceinline__ int last_part(int64_t end, int64_t total, int parts) {
-  const int64_t p = end * parts + total - 1;
-  return (int)(p <= 0xffffffffll ? (int64_t)((uint32_t)p / (uint32_t)total) : div64(p, total)) - 1;
-}
-
-// A query row of a key head: row R is head R % g of the group and token R / g of the q_len newest.
-struct RowAt {
-  int64_t head, tok;
-};
-__device__ __forceinline__ RowAt row_at(const DecodeArgs& a, int g, int b, int hk, int R) {
-  const int t = R / g;
-  return RowAt{hk * g + (R - t * g), (int64_t)b * a.q_len + t};
-}
-
-// Elements e0 .. e0 + E of a cached row, times its scale.
-template <int E, bool FP8>
-__device__ __forceinline__ void load_row(const void* base, int64_t row, int e0, float scale, float (&x)[E]) {
-#pragma unroll
-  for (int i = 0; i < E; i += 2) {
-    float2 f;
-    if (FP8) {
-      f = e4m3x2(*reinterpret_cast<const uint16_t*>(reinterpret_cast<const uint8_t*>(base) + row + e0 + i));
-      f.x *= scale;
-      f.y *= scale;
-    } else {
-      f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(reinterpret_cast<const bf16*>(base) + row + e0 + i));
-    }
-    x[i] = f.x;
-    x[i + 1] = f.y;
-  }
-}
-
-// The sums of one query row over the keys [k0, k1) that it sees, key by key, relative to the reference m: a lane gets
-// elements lane * D / 32 .. of o.
-template <int D, bool FP8>
-__device__ __noinline__ void redo(const DecodeArgs& a, int b, int hk, RowAt at, int k0, int k1, float m, float* out) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  float q[E], acc[E] = {};
-  load_row<E, false>(a.q, at.head * a.q_head + at.tok * a.q_tok, lane * E, 1.f, q);
-  for (int j = k0; j < k1; ++j) {
-    const KvPlace p = kv_place(a.c, a.t, b, j);
-    if (p.page < 0) continue;  // its l is NaN
-    const int64_t row = kv_row(a.c, p, hk), sc = FP8 ? kv_scale(a.c, p, hk) : 0;
-    float k[E], v[E], s = 0.f;
-    load_row<E, FP8>(a.c.k, row, lane * E, FP8 ? a.c.k_scale[sc] : 1.f, k);
-    load_row<E, FP8>(a.c.v, row, lane * E, FP8 ? a.c.v_scale[sc] : 1.f, v);
-#pragma unroll
-    for (int e = 0; e < E; ++e) s += q[e] * k[e];
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    const float w = exp2f(s * (a.scale * kLog2e) - m);
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] += w * v[e];
-  }
-#pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = acc[e];
-}
-
-__device__ __forceinline__ float row_lse(float m, float l) { return m * kLn2 + logf(l); }
-
 // Waits, a second at most, for the `n` copies from `stage` on that are on their way although a wait for one ran out.
 __device__ __forceinline__ void drain(uint32_t bars, int stages, int stage, uint32_t parity, int n) {
   if (n == 0) return;
@@ -298,27 +136,6 @@ __device__ __forceinline__ void drain(uint32_t bars, int stages, int stage, uint
 }
 
 constexpr int kJoinThreads = 256;
-
-struct DecodeWs {
-  int4* meta;     // [row blocks][CTAs] items of the pieces that the CTA leaves: x of one that ends an item, y of one that does
-                  // not; z whether the latter begins its item, w the CTA in which it ends
-  RowSum* sums;   // [row blocks][CTAs][2][rows]
-  float* acc;     // [row blocks][CTAs][2][rows][D]
-  int64_t scale_step;  // from a row's scale to the one 16 rows on
-  bool solo;      // a CTA to each item: nothing is left for the joining kernel
-};
-
-// A row of a sequence without tiles: zeros, or NaN where there are keys but no table.  All lanes of a warp.
-template <int D>
-__device__ __forceinline__ void empty_row(const DecodeArgs& a, int g, int b, int hk, int R, int keys) {
-  const int lane = threadIdx.x & 31;
-  const bool lost = keys - a.q_len + 1 + R / g > 0;
-  const RowAt at = row_at(a, g, b, hk, R);
-  bf16* o = a.o + at.head * a.o_head + at.tok * a.o_tok;
-  const uint32_t w = lost ? 0x7fff7fffu : 0u;
-  if (lane < D / 8) *reinterpret_cast<uint4*>(o + lane * 8) = make_uint4(w, w, w, w);
-  if (a.lse && lane == 0) a.lse[at.head * a.t.n_seqs * a.q_len + at.tok] = lost ? __uint_as_float(0x7fffffffu) : -INFINITY;
-}
 
 template <int D, bool FP8, int NT, int W>
 __global__ void __launch_bounds__(32 * W, 1)
@@ -539,8 +356,8 @@ __global__ void __launch_bounds__(32 * W, 1)
         if (tc::elect_one()) {
           const uint32_t at = queue + stage * L::STAGE;
           expect_tx(bar, L::STAGE);
-          tma_tile<L::SEGS>(at, &map_k, bar, prow, phk, page);
-          tma_tile<L::SEGS>(at + L::KBYTES, &map_v, bar, prow, phk, page);
+          tma_tile<L::SEGS>(at, &map_k, bar, prow, 0, phk, page);
+          tma_tile<L::SEGS>(at + L::KBYTES, &map_v, bar, prow, 0, phk, page);
         }
         if (FP8) cp4(scale_queue + stage * L::SCALES, scale);  // those behind the sequence's end are not used
       } else {
@@ -1143,28 +960,34 @@ __global__ void __launch_bounds__(kJoinThreads) k_decode_join(const __grid_const
   if (a.lse && d == 0) a.lse[at.head * n_seqs * a.q_len + at.tok] = seen <= 0 ? -INFINITY : row_lse(run.m, run.l);
 }
 
-// Rows of a block, blocks of rows, and CTAs for each of them.  Blocks of 16 where there are more than 8 rows: 63.8 us for 16
-// sequences up to 32768 keys with 16 rows, 85.6 as two blocks of 8 that read the cache twice; 8 rows in a block of 16 take 224 us
-// instead of 214 for 5242880 keys e4m3, and 87.5 instead of 85.9 for 1048576 keys bf16.
-struct DecodeShape {
-  int rows, blocks, ctas;
-};
-DecodeShape decode_shape(const DecodeArgs& a) {
+// Blocks of 16 rows where there are more than 8: 63.8 us for 16 sequences up to 32768 keys with 16 rows, 85.6 as two blocks of 8 that
+// read the cache twice; 8 rows in a block of 16 take 224 us instead of 214 for 5242880 keys e4m3, and 87.5 instead of 85.9 for 1048576
+// keys bf16.
+DecodeShape narrow_shape(const DecodeArgs& a) {
   const int all = a.hq / a.c.n_kv_heads * a.q_len;
   const int rows = all <= 8 ? 8 : 16, blocks = (int)ceil_div(all, rows);
   return DecodeShape{rows, blocks, std::max(1, std::min(sm_count(), 1024) / blocks)};
 }
 
-// Tiles of 16 rows of a page and head.  A row longer than 128 bytes is two boxes, side by side in shared memory.
-template <int D, bool FP8>
-bool tile_map(CUtensorMap* map, const KvCache& c, const void* base) {
-  using L = Lay<D, FP8, 1, 8>;
-  const uint64_t es = FP8 ? 1 : 2;
-  auto stride = [&](int64_t s) { return s ? (uint64_t)s * es : (uint64_t)16; };  // 0: of a single page or head
-  const uint64_t dims[5] = {L::SEG / es, (uint64_t)c.page_size, 2, (uint64_t)c.n_kv_heads, (uint64_t)c.n_pages};
-  const uint64_t strides[4] = {stride(c.token_stride), 128, stride(c.head_stride), stride(c.page_stride)};
-  const uint32_t box[5] = {(uint32_t)(L::SEG / es), kTileKeys, 2, 1, 1};
-  return make_tmap_rows(map, base, !FP8, L::SEGS == 2, dims, strides, box, L::SEG);
+// More rows of a bf16 cache may go to decode_wide.cu.  Rows of 64 elements, half the bytes of a tile, from 33 on: one sequence of 128000
+// keys, 8 key heads, 69.2 us as blocks of 16 and 77.4 as one of 32 with 32 rows, 96.0 and 89.7 with 40.
+bool may_be_wide(const DecodeArgs& a) { return !a.c.e4m3 && a.hq / a.c.n_kv_heads * a.q_len > (a.c.head_dim == 128 ? 16 : 32); }
+DecodeShape wide_shape(const DecodeArgs& a) {
+  const int all = a.hq / a.c.n_kv_heads * a.q_len;
+  const int rows = all <= 32 ? 32 : 64, blocks = (int)ceil_div(all, rows);
+  return DecodeShape{rows, blocks, std::max(1, std::min(sm_count(), 1024) / blocks)};
+}
+
+template <int D>
+cudaError_t join(const DecodeArgs& a, const DecodeShape& sh, const DecodeWs& ws, cudaStream_t st) {
+  const int rows = a.hq / a.c.n_kv_heads * a.q_len;
+  // A joining block for 8 rows where items are of 8 CTAs at most, if they are alike (16 sequences of 8 heads, 16 rows: 63.8 us, 66.5 with
+  // a block to a row), a block to a row where they are longer (one item of 152 CTAs: 214 us, 235 with a warp to a row).
+  const bool many = (int64_t)a.t.n_seqs * a.c.n_kv_heads * 8 >= sh.ctas;
+  const cudaError_t e = launch_pdl(many ? k_decode_join<D, 8> : k_decode_join<D, 1>, dim3(sh.ctas, many ? (int)ceil_div(rows, 8) : rows),
+                                   dim3(kJoinThreads), 0, st, a, ws, sh.rows);
+  note_launch();
+  return e;
 }
 
 template <int D, bool FP8, int NT, int W>
@@ -1172,7 +995,7 @@ cudaError_t run(const DecodeArgs& a, const DecodeShape& sh, DecodeWs ws, cudaStr
   using L = Lay<D, FP8, NT, W>;
   auto kfn = k_decode<D, FP8, NT, W>;
   CUtensorMap mk, mv;
-  if (!tile_map<D, FP8>(&mk, a.c, a.c.k) || !tile_map<D, FP8>(&mv, a.c, a.c.v)) return cudaErrorInvalidValue;
+  if (!tile_map<D, FP8>(&mk, a.c, a.c.k, kTileKeys, 2) || !tile_map<D, FP8>(&mv, a.c, a.c.v, kTileKeys, 2)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
   if (e != cudaSuccess) return e;
   // Few short sequences: a CTA to each item, and one launch, where the line of tiles takes two.  With the longest sequence that
@@ -1183,14 +1006,7 @@ cudaError_t run(const DecodeArgs& a, const DecodeShape& sh, DecodeWs ws, cudaStr
   e = launch_pdl(kfn, dim3(ws.solo ? (unsigned)items : sh.ctas, sh.blocks), dim3(32 * W), L::BYTES, st, a, ws, mk, mv, wait_limit_ns());
   note_launch();
   if (e != cudaSuccess || ws.solo) return e;
-  const int rows = a.hq / a.c.n_kv_heads * a.q_len;
-  // A joining block for 8 rows where items are of 8 CTAs at most, if they are alike (16 sequences of 8 heads, 16 rows: 63.8 us, 66.5 with
-  // a block to a row), a block to a row where they are longer (one item of 152 CTAs: 214 us, 235 with a warp to a row).
-  const bool many = items * 8 >= sh.ctas;
-  e = launch_pdl(many ? k_decode_join<D, 8> : k_decode_join<D, 1>, dim3(sh.ctas, many ? (int)ceil_div(rows, 8) : rows), dim3(kJoinThreads), 0, st, a,
-                 ws, sh.rows);
-  note_launch();
-  return e;
+  return join<D>(a, sh, ws, st);
 }
 
 template <int D, bool FP8>
@@ -1210,23 +1026,38 @@ cudaError_t run_rows(const DecodeArgs& a, const DecodeShape& sh, const DecodeWs&
 }  // namespace
 
 size_t decode_workspace(const DecodeArgs& a) {
-  const DecodeShape sh = decode_shape(a);
-  const size_t places = (size_t)sh.ctas * sh.blocks;
-  return places * (sizeof(int4) + 2 * sh.rows * (sizeof(RowSum) + sizeof(float) * a.c.head_dim));
+  auto bytes = [&](const DecodeShape& sh) {
+    return (size_t)sh.ctas * sh.blocks * (sizeof(int4) + 2 * sh.rows * (sizeof(RowSum) + sizeof(float) * a.c.head_dim));
+  };
+  return may_be_wide(a) ? std::max(bytes(narrow_shape(a)), bytes(wide_shape(a))) : bytes(narrow_shape(a));
 }
 
 cudaError_t launch_decode(const DecodeArgs& a, cudaStream_t st) {
   if (a.t.n_seqs <= 0) return cudaSuccess;
-  const DecodeShape sh = decode_shape(a);
+  // Tiles of 128 keys cost more to begin and to end, and pay where a CTA has enough of them, if all sequences were as long as the table
+  // allows.  bf16, 8 key heads of 128, us as blocks of 16 rows and as one of 32 or 64: one sequence of 16000 keys (7 tiles to a CTA) 22.4
+  // and 23.2 with 24 rows, 31.4 and 32.9 with 64; 64000 keys (26 tiles) 66.6 and 52.9, 86.7 and 63.1; 16 sequences up to 1000 keys
+  // (7) 16.9 and 21.2, up to 4000 (27) 30.2 and 26.8, up to 16000 64.2 and 48.7, with 64 rows 88.4 and 55.3.  (64 up to 1000, 27
+  // tiles but 8 to an item, lose: 36 and 45 with 64 rows of 64 elements.)
+  constexpr int kManyTiles = 24;
+  const int64_t tiles = (int64_t)a.t.n_seqs * a.c.n_kv_heads * ceil_div(table_keys(a.t, a.c.page_size), 128);
+  const bool wide = may_be_wide(a) && tiles >= (int64_t)wide_shape(a).ctas * kManyTiles;
+  const DecodeShape sh = wide ? wide_shape(a) : narrow_shape(a);
   const size_t places = (size_t)sh.ctas * sh.blocks;
   uint8_t* p = reinterpret_cast<uint8_t*>(a.ws);
-  DecodeWs ws;
+  DecodeWs ws{};
   ws.acc = reinterpret_cast<float*>(p);
   p += places * 2 * sh.rows * sizeof(float) * a.c.head_dim;
   ws.sums = reinterpret_cast<RowSum*>(p);
   p += places * 2 * sh.rows * sizeof(RowSum);
   ws.meta = reinterpret_cast<int4*>(p);
   ws.scale_step = kTileKeys * a.c.scale_token_stride;
+  if (wide) {
+    const cudaError_t e = launch_decode_wide(a, sh, ws, st);
+    note_launch();
+    if (e != cudaSuccess) return e;
+    return a.c.head_dim == 128 ? join<128>(a, sh, ws, st) : join<64>(a, sh, ws, st);
+  }
   if (a.c.head_dim == 128) return a.c.e4m3 ? run_rows<128, true>(a, sh, ws, st) : run_rows<128, false>(a, sh, ws, st);
   return a.c.e4m3 ? run_rows<64, true>(a, sh, ws, st) : run_rows<64, false>(a, sh, ws, st);
 }
