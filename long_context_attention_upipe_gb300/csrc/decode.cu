@@ -25,6 +25,7 @@
 //
 // A warp's part may begin or end within an item.  The CTA joins such pieces in shared memory, in order, and what an item leaves
 // in several CTAs a second kernel joins, in order: no atomics, equal calls give equal bits.
+// Few short sequences have a cluster of CTAs to each item instead, which join their sums through each other's shared memory: one launch.
 // (More than 16 rows of a long bf16 cache: decode_wide.cu.)
 //
 // A value that is infinite or NaN spoils the products of query rows that do not see it (zero times infinity), and of those that do
@@ -70,7 +71,7 @@ struct Lay {
   static constexpr int BYTES = AT_INFO + WARPS * 40 + 16 + 1024;  // the queues start on 1024 bytes
   static constexpr int MT = D / 16;                     // tiles of O^T
   static constexpr int KS = D / 16;                     // steps of S^T
-  static_assert(STAGES >= 2 && QUEUE >= SLOT && WARPS * QUEUE >= 2048 * 8 && BYTES <= 227 * 1024, "shared memory");
+  static_assert(STAGES >= 2 && QUEUE >= 2 * SLOT && WARPS * QUEUE >= 2048 * 8 && BYTES <= 227 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ float lds32(uint32_t at) {
@@ -84,6 +85,14 @@ __device__ __forceinline__ void lds_floats(float* v, uint32_t at) {
     asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[N - 2]), "=f"(v[N - 1]) : "r"(at) : "memory");
   else
     asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(at) : "memory");
+}
+// From the shared memory of another CTA of the cluster.
+template <int N>
+__device__ __forceinline__ void ld_cluster(float* v, uint32_t at) {
+  if (N == 4)
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v[0]), "=f"(v[1]), "=f"(v[N - 2]), "=f"(v[N - 1]) : "r"(at) : "memory");
+  else
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(at) : "memory");
 }
 // Four 8 x 8 matrices of 16-bit elements, a lane's address naming a row of one.
 template <int AT>
@@ -143,6 +152,7 @@ __global__ void __launch_bounds__(32 * W, 1)
              const __grid_constant__ CUtensorMap map_v, uint64_t wait_ns) {
   using L = Lay<D, FP8, NT, W>;
   constexpr int kWarps = W;
+  const int share = W == 8 ? ws.share : 0;  // 16 warps: always the line
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
@@ -164,11 +174,12 @@ __global__ void __launch_bounds__(32 * W, 1)
   grid_dep_trigger();  // the joining kernel may start when CTAs leave; it reads nothing of this one before it has ended
 
   // ---- the warp's part of the line of tiles
-  int b0 = ws.solo ? blockIdx.x / hkv : 0;
+  const int own = share ? blockIdx.x / share : 0, rank = share ? blockIdx.x - own * share : 0;  // item, and which of its CTAs
+  int b0 = own / hkv;
   int lens = (b0 & ~31) + lane < n_seqs ? a.lens[(b0 & ~31) + lane] : 0;  // of the 32 sequences that b0 is among
   const int lens2 = lane + 32 < n_seqs ? a.lens[lane + 32] : 0;
   int64_t upto = 0, before = 0, total = 0, first32 = 0;  // tiles up to and with a lane's sequence, before the 32, of all
-  const int chunks = ws.solo ? 0 : (n_seqs + 31) / 32;
+  const int chunks = share ? 0 : (n_seqs + 31) / 32;
   int64_t* sums = reinterpret_cast<int64_t*>(smem);
   if (chunks > 2) {  // a sum for each 32 sequences
     for (int ch = warp; ch < chunks; ch += kWarps) {
@@ -213,12 +224,12 @@ __global__ void __launch_bounds__(32 * W, 1)
     part_end[1] = total;
   }
   int hk0 = 0, tile0 = 0;
-  if (ws.solo) {
-    hk0 = blockIdx.x - b0 * hkv;
-    const int keys = __shfl_sync(0xffffffffu, lens, b0 & 31), n = tiles_of(keys, cap);
-    tile0 = n * warp / kWarps;
-    left = n * (warp + 1) / kWarps - tile0;
-    if (n == 0)
+  if (share) {
+    hk0 = own - b0 * hkv;
+    const int keys = __shfl_sync(0xffffffffu, lens, b0 & 31), n = tiles_of(keys, cap), of = max(share, 1) * kWarps, me = rank * kWarps + warp;
+    tile0 = n * me / of;
+    left = n * (me + 1) / of - tile0;
+    if (n == 0 && rank == 0)
       for (int R = rb * L::ROWS + warp; R < min((rb + 1) * L::ROWS, rows); R += kWarps) empty_row<D>(a, g, b0, hk0, R, keys);
   } else if (left > 0) {
     const int64_t seq_first = mul_div(first, 1, hkv);  // the tile's place if there were one head
@@ -775,6 +786,9 @@ __global__ void __launch_bounds__(32 * W, 1)
   const int prev = __shfl_sync(0xffffffffu, my_item, below ? 31 - __clz(below) : 0);
   unsigned starts = __ballot_sync(0xffffffffu, my_item >= 0 && (!below || prev != my_item));
   constexpr int RB = NT;  // rows at a time
+  // with several CTAs to an item: what this one leaves, beside the pieces
+  float* cta_o = reinterpret_cast<float*>(smem + L::SLOT);
+  RowSum* cta_sums = reinterpret_cast<RowSum*>(smem + L::QUEUE + L::SLOT);
   const int groups = (min(L::ROWS, rows - rb * L::ROWS) + RB - 1) / RB;  // units of work of a run: the warps take them in turns
 #pragma unroll 1
   for (int i = 0; starts; ++i) {
@@ -847,6 +861,11 @@ __global__ void __launch_bounds__(32 * W, 1)
           if (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[E / 2 - 1]);
           else *dst = w[0];
           if (a.lse && lane == 0) a.lse[at.head * n_seqs * a.q_len + at.tok] = none ? -INFINITY : row_lse(sum[k].m, sum[k].l);
+        } else if (share) {
+          float* dst = cta_o + row * D + lane * E;
+#pragma unroll
+          for (int e = 0; e < E; ++e) dst[e] = o[k][e];
+          if (lane == 0) cta_sums[row] = sum[k];
         } else {
           const int64_t at = (place * 2 + (ends ? 0 : 1)) * L::ROWS + row;
           float* dst = ws.acc + at * D + lane * E;
@@ -857,7 +876,50 @@ __global__ void __launch_bounds__(32 * W, 1)
       }
     }
   }
-  if (threadIdx.x == 0 && !ws.solo) ws.meta[place] = meta;
+  if (!share) {
+    if (threadIdx.x == 0) ws.meta[place] = meta;
+  } else if (share > 1) {  // the item's CTAs are a cluster: each joins some of the rows, in order
+    constexpr int E = D / 32;
+    if (valid == 0 || (meta.x < 0 && meta.y < 0))  // nothing left: no tiles, or all of them and the rows are written
+      for (int row = threadIdx.x; row < L::ROWS; row += 32 * kWarps) cta_sums[row] = RowSum{kLowest, -1.f};
+    tc::cluster_sync();
+#pragma unroll 1
+    for (int row = warp * share + rank; row < min(L::ROWS, rows - rb * L::ROWS); row += kWarps * share) {
+      RowSum sum{kLowest, 0.f};
+      float o[E] = {};
+      bool some = false;
+#pragma unroll 1
+      for (int i = 0; i < share; i += 2) {  // two at a time
+        RowSum part[2];
+        float v[2][E];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          ld_cluster<2>(reinterpret_cast<float*>(&part[j]), tc::mapa_cluster(smem_u32(cta_sums + row), i + j));
+          ld_cluster<E>(v[j], tc::mapa_cluster(smem_u32(cta_o + row * D + lane * E), i + j));
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          if (part[j].l == -1.f) continue;
+          some = true;
+          const float top = fmaxf(sum.m, part[j].m), f = fast_exp2(sum.m - top), f1 = fast_exp2(part[j].m - top);
+          sum = RowSum{top, sum.l * f + part[j].l * f1};
+#pragma unroll
+          for (int e = 0; e < E; ++e) o[e] = o[e] * f + v[j][e] * f1;
+        }
+      }
+      if (some) {
+        const int R = rb * L::ROWS + row, keys = min(__shfl_sync(0xffffffffu, lens, b0 & 31), cap);
+        const bool none = keys - a.q_len + 1 + R / g <= 0;
+        const RowAt at = row_at(a, g, b0, own - b0 * hkv, R);
+        const float inv = 1.f / sum.l;
+        bf16* dst = a.o + at.head * a.o_head + at.tok * a.o_tok + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(dst + e) = none ? 0u : pack_bf16(o[e] * inv, o[e + 1] * inv);
+        if (a.lse && lane == 0) a.lse[at.head * n_seqs * a.q_len + at.tok] = none ? -INFINITY : row_lse(sum.m, sum.l);
+      }
+    }
+    tc::cluster_sync();  // the others have read this one's sums
+  }
 }
 
 // Joins what an item left in several CTAs, in order; one block for each CTA in which an item begins that goes on, and each row.
@@ -998,14 +1060,25 @@ cudaError_t run(const DecodeArgs& a, const DecodeShape& sh, DecodeWs ws, cudaStr
   if (!tile_map<D, FP8>(&mk, a.c, a.c.k, kTileKeys, 2) || !tile_map<D, FP8>(&mv, a.c, a.c.v, kTileKeys, 2)) return cudaErrorInvalidValue;
   cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
   if (e != cudaSuccess) return e;
-  // Few short sequences: a CTA to each item, and one launch, where the line of tiles takes two.  With the longest sequence that
-  // the table has room for, 8 key heads bf16: 256 keys 8.6 against 11.3 us a call (6.1 against 7.9 on the device), 1024 keys
-  // 10.1 against 11.3, 2048 keys 14.7 against 11.1; e4m3, 512 keys 10.1 against 11.4, 1024 keys 12.7 against 11.7.
+  // Few short sequences: a CTA or a cluster of CTAs to each item, and one launch, where the line of tiles takes two.  One CTA up to 512 keys
+  // of the longest sequence that the table has room for (320 keys 6.6 us on the device, 7.1 as a cluster of 2), then as many as get 256
+  // keys each, if the items are few enough.  us on the device and a call, bf16, 8 key heads, on the line, with one CTA and in clusters: 1000
+  // keys 7.9 and 11.3, 9.2 and 9.8, 7.6 and 8.2; 2000 keys 8.7 and 10.2 on the line, 8.2 and 9.1 in clusters of 8 (e4m3 9.2 and 10.2, 8.7
+  // and 9.5; 16 rows 13.0 and 13.5, 10.9 and 11.7); with 512 keys to a CTA, 4000 of one head, the line is as fast (9.6 and 10.3, 9.6
+  // and 10.5).  Clusters of 8 find room for 12 items at once (8.8 us; 9.2 in clusters of 4), not for 16 (12.7 instead of 8.6 us).
   const int64_t items = (int64_t)a.t.n_seqs * a.c.n_kv_heads;
-  ws.solo = items <= sh.ctas && table_keys(a.t, a.c.page_size) <= (FP8 ? 512 : 1024);
-  e = launch_pdl(kfn, dim3(ws.solo ? (unsigned)items : sh.ctas, sh.blocks), dim3(32 * W), L::BYTES, st, a, ws, mk, mv, wait_limit_ns());
+  const int keys = table_keys(a.t, a.c.page_size);
+  int share = 1;
+  while (share < 8 && keys > (share == 1 ? 512 : 256 * share) && items * sh.blocks * 2 * share <= (share == 4 ? 96 : 128)) share *= 2;
+  ws.share = W == 8 && items <= sh.ctas && keys <= share * (FP8 || share > 1 ? 512 : 1024) ? share : 0;
+  if (ws.share) {
+    e = launch_pdl_cluster(kfn, dim3((unsigned)items * ws.share, sh.blocks), dim3(32 * W), L::BYTES, st, ws.share, a, ws, mk, mv, wait_limit_ns());
+    note_launch();
+    return e;
+  }
+  e = launch_pdl(kfn, dim3(sh.ctas, sh.blocks), dim3(32 * W), L::BYTES, st, a, ws, mk, mv, wait_limit_ns());
   note_launch();
-  if (e != cudaSuccess || ws.solo) return e;
+  if (e != cudaSuccess) return e;
   return join<D>(a, sh, ws, st);
 }
 

@@ -21,7 +21,7 @@ struct DecodeWs {
   float* acc;     // [row blocks][CTAs][2][rows][D]
   int64_t scale_step;  // from a row's scale to the one 16 rows on
   int box_rows;   // rows of a copy: what divides a page and a tile of 128 keys (more than 16 rows)
-  bool solo;      // a CTA to each item: nothing is left for the joining kernel
+  int share;      // 0, or the CTAs that each item has, a cluster: nothing is left for the joining kernel
 };
 
 // Rows of a block, blocks of rows, and CTAs for each of them.
