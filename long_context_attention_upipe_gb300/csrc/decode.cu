@@ -152,7 +152,8 @@ __global__ void __launch_bounds__(32 * W, 1)
              const __grid_constant__ CUtensorMap map_v, uint64_t wait_ns) {
   using L = Lay<D, FP8, NT, W>;
   constexpr int kWarps = W;
-  const int share = W == 8 ? ws.share : 0;  // 16 warps: always the line
+  const int share = W == 8 ? max(ws.share, 0) : 0;        // CTAs of an item; 16 warps: always the line
+  const bool whole_items = W == 8 && ws.share < 0;        // ... or parts of the line that begin and end with items
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
@@ -212,59 +213,80 @@ __global__ void __launch_bounds__(32 * W, 1)
     return true;
   };
   int64_t first = 0, left = 0;
-  if (blockIdx.x < parts) {
-    const int64_t t0 = mul_div(total, blockIdx.x, parts), t1 = mul_div(total, blockIdx.x + 1, parts);
-    first = t0 + (int64_t)((uint64_t)((t1 - t0) * warp) / kWarps);
-    left = t0 + (int64_t)((uint64_t)((t1 - t0) * (warp + 1)) / kWarps) - first;
-  }
   // the tile after the part, and all tiles: read again when the part ends
   volatile int64_t* part_end = reinterpret_cast<volatile int64_t*>(smem + L::AT_INFO + kWarps * 24) + 2 * warp;
-  if (lane == 0) {
-    part_end[0] = first + left;
-    part_end[1] = total;
-  }
   int hk0 = 0, tile0 = 0;
   if (share) {
     hk0 = own - b0 * hkv;
     const int keys = __shfl_sync(0xffffffffu, lens, b0 & 31), n = tiles_of(keys, cap), of = max(share, 1) * kWarps, me = rank * kWarps + warp;
     tile0 = n * me / of;
     left = n * (me + 1) / of - tile0;
-    if (n == 0 && rank == 0)
-      for (int R = rb * L::ROWS + warp; R < min((rb + 1) * L::ROWS, rows); R += kWarps) empty_row<D>(a, g, b0, hk0, R, keys);
-  } else if (left > 0) {
-    const int64_t seq_first = mul_div(first, 1, hkv);  // the tile's place if there were one head
-    if (chunks > 2) {
-      for (int base = 0; base < chunks; base += 32) {
-        const int64_t v = base + lane < chunks ? sums[base + lane] : 0, in = warp_scan(v, lane);
-        const unsigned hit = __ballot_sync(0xffffffffu, before + in > seq_first);
-        if (hit) {
-          b0 = (base + __ffs(hit) - 1) * 32;
-          before += __shfl_sync(0xffffffffu, in - v, __ffs(hit) - 1);
-          break;
+    if (n == 0 && rank == 0 && warp == 0) empty_rows<D>(a, g, b0, hk0, hk0 + 1, rb * L::ROWS, min((rb + 1) * L::ROWS, rows), keys);
+  } else if (blockIdx.x < parts) {
+    int64_t t0 = mul_div(total, blockIdx.x, parts), t1 = mul_div(total, blockIdx.x + 1, parts);
+    const int lens1 = lens;
+    const int64_t upto1 = upto;
+#pragma unroll 1
+    for (int round = whole_items ? 0 : 1; round < 2; ++round) {
+      int64_t at_line;
+      if (round == 0) {
+        at_line = warp == 0 ? t0 : t1;  // of which the next begin of an item is wanted
+      } else {
+        first = t0 + (int64_t)((uint64_t)((t1 - t0) * warp) / kWarps);
+        left = t0 + (int64_t)((uint64_t)((t1 - t0) * (warp + 1)) / kWarps) - first;
+        at_line = first;
+        if (left <= 0) break;
+        if (lane == 0) {
+          part_end[0] = first + left;
+          part_end[1] = total;
         }
-        before += __shfl_sync(0xffffffffu, in, 31);
       }
-      lens = b0 + lane < n_seqs ? a.lens[b0 + lane] : 0;
-      upto = warp_scan(units_of<L::END>(lens, cap), lane);
-    } else if (seq_first >= first32) {
-      b0 = 32;
-      before = first32;
-      lens = lens2;
-      upto = warp_scan(units_of<L::END>(lens, cap), lane);
-    }
-    const int at = max(__ffs(__ballot_sync(0xffffffffu, before + upto > seq_first)) - 1, 0);
-    const int n = max(units_of<L::END>(__shfl_sync(0xffffffffu, lens, at), cap), 1);
-    before += __shfl_sync(0xffffffffu, upto, at) - n;
-    b0 = min(b0 + at, n_seqs - 1);
-    const int64_t rest = max(first - before * hkv, (int64_t)0);
-    hk0 = (int)min(mul_div(rest, 1, n), (int64_t)(hkv - 1));  // within bounds even if lengths change under the call
-    tile0 = (int)min(rest - (int64_t)hk0 * n, (int64_t)(n - 1));
-    if (tile0 >= n - L::END) {  // within an item's end
-      left -= n - tile0;
-      tile0 = 0;
-      if (++hk0 == hkv) {
-        hk0 = 0;
-        if (!next_seq(b0, lens)) left = 0;
+      const int64_t seq_first = mul_div(at_line, 1, hkv);  // the tile's place if there were one head
+      before = 0;
+      b0 = 0;
+      if (chunks > 2) {
+        for (int base = 0; base < chunks; base += 32) {
+          const int64_t v = base + lane < chunks ? sums[base + lane] : 0, in = warp_scan(v, lane);
+          const unsigned hit = __ballot_sync(0xffffffffu, before + in > seq_first);
+          if (hit) {
+            b0 = (base + __ffs(hit) - 1) * 32;
+            before += __shfl_sync(0xffffffffu, in - v, __ffs(hit) - 1);
+            break;
+          }
+          before += __shfl_sync(0xffffffffu, in, 31);
+        }
+        lens = b0 + lane < n_seqs ? a.lens[b0 + lane] : 0;
+        upto = warp_scan(units_of<L::END>(lens, cap), lane);
+      } else if (seq_first >= first32) {
+        b0 = 32;
+        before = first32;
+        lens = lens2;
+        upto = warp_scan(units_of<L::END>(lens, cap), lane);
+      } else {
+        lens = lens1;
+        upto = upto1;
+      }
+      const int at = max(__ffs(__ballot_sync(0xffffffffu, before + upto > seq_first)) - 1, 0);
+      const int n = max(units_of<L::END>(__shfl_sync(0xffffffffu, lens, at), cap), 1);
+      before += __shfl_sync(0xffffffffu, upto, at) - n;
+      b0 = min(b0 + at, n_seqs - 1);
+      const int64_t rest = max(at_line - before * hkv, (int64_t)0);
+      hk0 = (int)min(mul_div(rest, 1, n), (int64_t)(hkv - 1));  // within bounds even if lengths change under the call
+      tile0 = (int)min(rest - (int64_t)hk0 * n, (int64_t)(n - 1));
+      if (round == 0) {
+        int64_t* ends = reinterpret_cast<int64_t*>(smem + L::AT_INFO);
+        if (lane == 0 && warp < 2) ends[warp] = at_line >= total ? total : tile0 ? at_line - tile0 + n : at_line;
+        __syncthreads();
+        t0 = ends[0];
+        t1 = ends[1];
+        __syncthreads();
+      } else if (tile0 >= n - L::END) {  // within an item's end
+        left -= n - tile0;
+        tile0 = 0;
+        if (++hk0 == hkv) {
+          hk0 = 0;
+          if (!next_seq(b0, lens)) left = 0;
+        }
       }
     }
   }
@@ -876,7 +898,9 @@ __global__ void __launch_bounds__(32 * W, 1)
       }
     }
   }
-  if (!share) {
+  if (whole_items) {  // no other kernel writes the rows of empty sequences
+    empty_sequences<D>(a, g, cap, blockIdx.x * kWarps + warp, X * kWarps, rb * L::ROWS, min((rb + 1) * L::ROWS, rows));
+  } else if (!share) {
     if (threadIdx.x == 0) ws.meta[place] = meta;
   } else if (share > 1) {  // the item's CTAs are a cluster: each joins some of the rows, in order
     constexpr int E = D / 32;
@@ -932,23 +956,10 @@ __global__ void __launch_bounds__(kJoinThreads) k_decode_join(const __grid_const
   constexpr int LN = D / 4, GR = kJoinThreads / LN / ROWS, AHEAD = ROWS == 1 ? 5 : 4;  // lanes and groups of a row, pieces in flight
   __shared__ float4 part[ROWS == 1 ? GR : 1][LN];
   __shared__ RowSum part_sums[GR];
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, x = blockIdx.x, X = gridDim.x;
+  const int tid = threadIdx.x, warp = tid >> 5, x = blockIdx.x, X = gridDim.x;
   const int hkv = a.c.n_kv_heads, g = a.hq / hkv, rows = g * a.q_len, n_seqs = a.t.n_seqs, cap = table_keys(a.t, a.c.page_size);
   // lengths were there before the kernel that this one follows began
-  for (int base = (x * (kJoinThreads / 32) + warp) * 32; base < n_seqs; base += X * kJoinThreads) {
-    const int b = base + lane, len = b < n_seqs ? a.lens[b] : 1;
-    unsigned none = __ballot_sync(0xffffffffu, b < n_seqs && tiles_of(len, cap) == 0);
-    while (none) {
-      const int i = __ffs(none) - 1;
-      none &= none - 1;
-      const int keys = __shfl_sync(0xffffffffu, len, i);
-      for (int j = 0; j < ROWS * hkv; ++j) {
-        const int hk = j / ROWS, R = blockIdx.y * ROWS + j % ROWS;
-        if (R >= rows) continue;
-        empty_row<D>(a, g, base + i, hk, R, keys);
-      }
-    }
-  }
+  empty_sequences<D>(a, g, cap, x * (kJoinThreads / 32) + warp, X * (kJoinThreads / 32), blockIdx.y * ROWS, min((int)(blockIdx.y + 1) * ROWS, rows));
   const int R = blockIdx.y * ROWS + (ROWS == 1 ? 0 : tid / (kJoinThreads / ROWS));
   const int rb = R / block_rows, row = R - rb * block_rows;
   grid_dep_wait();
@@ -1071,8 +1082,12 @@ cudaError_t run(const DecodeArgs& a, const DecodeShape& sh, DecodeWs ws, cudaStr
   int share = 1;
   while (share < 8 && keys > (share == 1 ? 512 : 256 * share) && items * sh.blocks * 2 * share <= (share == 4 ? 96 : 128)) share *= 2;
   ws.share = W == 8 && items <= sh.ctas && keys <= share * (FP8 || share > 1 ? 512 : 1024) ? share : 0;
+  // Up to four times as many short items as CTAs: parts of the line that begin and end with items, and one launch.  bf16, keys of the longest
+  // sequence: 64 sequences of 4 key heads up to 300 keys 8.6 us a call (10.3 with a second launch), 256 of 2 heads of 64 up to 500
+  // 11.0 (12.0); but 64 of 8 heads up to 1000, e4m3, 15.0 (14.2), 200 of 8 heads up to 500 20.4 (19.3).
+  if (!ws.share && W == 8 && items <= 4 * (int64_t)sh.ctas && keys <= 512) ws.share = -1;
   if (ws.share) {
-    e = launch_pdl_cluster(kfn, dim3((unsigned)items * ws.share, sh.blocks), dim3(32 * W), L::BYTES, st, ws.share, a, ws, mk, mv, wait_limit_ns());
+    e = launch_pdl_cluster(kfn, dim3(ws.share > 0 ? (unsigned)items * ws.share : sh.ctas, sh.blocks), dim3(32 * W), L::BYTES, st, std::max(ws.share, 1), a, ws, mk, mv, wait_limit_ns());
     note_launch();
     return e;
   }

@@ -21,7 +21,8 @@ struct DecodeWs {
   float* acc;     // [row blocks][CTAs][2][rows][D]
   int64_t scale_step;  // from a row's scale to the one 16 rows on
   int box_rows;   // rows of a copy: what divides a page and a tile of 128 keys (more than 16 rows)
-  int share;      // 0, or the CTAs that each item has, a cluster: nothing is left for the joining kernel
+  int share;      // 0; or the CTAs that each item has, a cluster; or -1: parts of the line that begin and end with items (nothing is left for the
+                  // joining kernel)
 };
 
 // Rows of a block, blocks of rows, and CTAs for each of them.
@@ -189,16 +190,35 @@ __device__ __noinline__ void redo(const DecodeArgs& a, int b, int hk, RowAt at, 
 
 __device__ __forceinline__ float row_lse(float m, float l) { return m * kLn2 + logf(l); }
 
-// A row of a sequence without tiles: zeros, or NaN where there are keys but no table.  All lanes of a warp.
+// Rows R0 .. R1 of key heads h0 .. h1 of a sequence without tiles: zeros, or NaN where there are keys but no table.  All lanes of a
+// warp, D / 8 to a row.
 template <int D>
-__device__ __forceinline__ void empty_row(const DecodeArgs& a, int g, int b, int hk, int R, int keys) {
+__device__ __forceinline__ void empty_rows(const DecodeArgs& a, int g, int b, int h0, int h1, int R0, int R1, int keys) {
+  constexpr int LANES = D / 8;
+  const int lane = threadIdx.x & 31, n = R1 - R0;
+  for (int i = lane / LANES; i < (h1 - h0) * n; i += 32 / LANES) {
+    const int h = i / n, R = R0 + i - h * n;
+    const bool lost = keys - a.q_len + 1 + R / g > 0;
+    const RowAt at = row_at(a, g, b, h0 + h, R);
+    const uint32_t w = lost ? 0x7fff7fffu : 0u;
+    *reinterpret_cast<uint4*>(a.o + at.head * a.o_head + at.tok * a.o_tok + lane % LANES * 8) = make_uint4(w, w, w, w);
+    if (a.lse && lane % LANES == 0) a.lse[at.head * a.t.n_seqs * a.q_len + at.tok] = lost ? __uint_as_float(0x7fffffffu) : -INFINITY;
+  }
+}
+// ... of the sequences that have none, a warp of the grid to a sequence (to each of the grid's `warps`th).
+template <int D>
+__device__ __forceinline__ void empty_sequences(const DecodeArgs& a, int g, int cap, int warp, int warps, int R0, int R1) {
   const int lane = threadIdx.x & 31;
-  const bool lost = keys - a.q_len + 1 + R / g > 0;
-  const RowAt at = row_at(a, g, b, hk, R);
-  bf16* o = a.o + at.head * a.o_head + at.tok * a.o_tok;
-  const uint32_t w = lost ? 0x7fff7fffu : 0u;
-  if (lane < D / 8) *reinterpret_cast<uint4*>(o + lane * 8) = make_uint4(w, w, w, w);
-  if (a.lse && lane == 0) a.lse[at.head * a.t.n_seqs * a.q_len + at.tok] = lost ? __uint_as_float(0x7fffffffu) : -INFINITY;
+  for (int64_t b0 = warp; b0 < a.t.n_seqs; b0 += (int64_t)32 * warps) {
+    const int64_t b = b0 + (int64_t)lane * warps;
+    const int len = b < a.t.n_seqs ? a.lens[b] : 1;
+    unsigned none = __ballot_sync(0xffffffffu, b < a.t.n_seqs && tiles_of(len, cap) == 0);
+    while (none) {
+      const int i = __ffs(none) - 1;
+      none &= none - 1;
+      empty_rows<D>(a, g, (int)(b0 + (int64_t)i * warps), 0, a.c.n_kv_heads, R0, R1, __shfl_sync(0xffffffffu, len, i));
+    }
+  }
 }
 
 // Boxes of box_rows rows of a page and head, rows of SEGS halves of SEG bytes, of which a box has `halves`, side by side in shared memory.

@@ -1,5 +1,6 @@
-"""Decode of few short sequences: one CTA, or a cluster of 2, 4 or 8, to a sequence and key head, by the keys that the table has room for,
-against plain 64-bit arithmetic (the tolerances of the other decode tests)."""
+"""Decode of short sequences: few of them with one CTA, or a cluster of 2, 4 or 8, to a sequence and key head, more as parts of the line that
+begin and end with items, by the keys that the table has room for; against plain 64-bit arithmetic (the tolerances of the other decode
+tests)."""
 import pytest
 import torch
 
@@ -155,3 +156,57 @@ def test_clusters_beside_other_work():
     torch.cuda.synchronize()
     for (o, lse, _), (wo, wl) in zip(out, want):
         assert torch.equal(o, wo) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("seqs,hkv", [(153, 1), (160, 2), (100, 3), (304, 2), (608, 1), (609, 1)])
+@pytest.mark.parametrize("some", ["none", "one", "last", "few", "many"])
+def test_more_items_than_ctas(kind, seqs, hkv, some):
+    """Up to 512 keys each; most sequences empty or not."""
+    keys = {"none": [], "one": [(77, 300)], "last": [(seqs - 1, 512)], "few": [(i, 1 + i * 5 % 512) for i in range(3, seqs, 29)],
+            "many": [(i, i * 7 % 130) for i in range(seqs) if i % 6]}[some]
+    lens = [-1] * seqs
+    for i, n in keys:
+        lens[i] = n
+    c, table, q = setup(kind, lens, 4 * hkv, hkv, 64, 32)
+    check_decode(c, q, widened(table, 16 - table.shape[1], gen(1)), lens)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_more_items_than_ctas_replayed_with_other_lengths(kind):
+    seqs = 200
+    c, table, q = setup(kind, [64] * seqs, 24, 1, 128, 64)
+    ln, o, lse = torch.zeros(seqs, dtype=torch.int32, device="cuda"), torch.empty_like(q), torch.empty(24, seqs, device="cuda")
+    ws = torch.full((up.decode_workspace_bytes(c, seqs, 24),), 0xff, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        up.decode(c, q, table, ln, o, ws, lse=lse)
+        up.decode(c, q, table, ln, o, ws, lse=lse)
+    for step in range(4):
+        lens = [(i * (step + 3)) % 65 for i in range(seqs)] if step else [0] * seqs
+        ln.copy_(torch.tensor(lens, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        want, wl = check_decode(c, q, table, lens)
+        assert torch.equal(o, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("columns", [1, 3, 40])
+def test_lengths_past_the_table_and_no_table(columns):
+    """65 keys and a table of fewer, for few and for many items and for the line: NaN; the others as they were."""
+    for seqs in (3, 200, 700):
+        c, table, q = setup("bf16", [16] * seqs, 8, 2, 64, 16)
+        table = widened(table, columns - 1, gen(2))
+        lens = [16 if i % 3 else columns * 16 + 1 for i in range(seqs)]
+        o, lse = run_decode(c, q, table, lens)
+        lost = torch.arange(seqs, device="cuda") % 3 == 0
+        assert bool(o[:, lost].isnan().all()) and bool(lse[:, lost].isnan().all()) and bool(o[:, ~lost].isfinite().all())
+        o, lse = run_decode(c, q, table[:, :0], [0 if i % 3 else 5 for i in range(seqs)])
+        assert bool(o[:, lost].isnan().all()) and bool((o[:, ~lost] == 0).all()) and bool((lse[:, ~lost] == -float("inf")).all())
+
+
+def test_many_empty_sequences_among_long_ones():
+    lens = [0 if i % 8 else 1200 + i for i in range(150)]
+    c, table, q = setup("bf16", lens, 40, 8, 128, 64, 2)
+    check_decode(c, q, table, lens, q_len=2)
