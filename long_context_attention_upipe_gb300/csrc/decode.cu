@@ -146,14 +146,15 @@ __device__ __forceinline__ void drain(uint32_t bars, int stages, int stage, uint
 
 constexpr int kJoinThreads = 256;
 
-template <int D, bool FP8, int NT, int W>
+// LINE: parts of the line, the last of whose items may go on in the next CTA; else items have CTAs of their own (ws.share).
+template <int D, bool FP8, int NT, int W, bool LINE>
 __global__ void __launch_bounds__(32 * W, 1)
     k_decode(const __grid_constant__ DecodeArgs a, const DecodeWs ws, const __grid_constant__ CUtensorMap map_k,
              const __grid_constant__ CUtensorMap map_v, uint64_t wait_ns) {
   using L = Lay<D, FP8, NT, W>;
   constexpr int kWarps = W;
-  const int share = W == 8 ? max(ws.share, 0) : 0;        // CTAs of an item; 16 warps: always the line
-  const bool whole_items = W == 8 && ws.share < 0;        // ... or parts of the line that begin and end with items
+  const int share = LINE ? 0 : max(ws.share, 0);        // CTAs of an item
+  const bool whole_items = !LINE && ws.share < 0;       // ... or parts of the line that begin and end with items
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
@@ -224,26 +225,9 @@ __global__ void __launch_bounds__(32 * W, 1)
     if (n == 0 && rank == 0 && warp == 0) empty_rows<D>(a, g, b0, hk0, hk0 + 1, rb * L::ROWS, min((rb + 1) * L::ROWS, rows), keys);
   } else if (blockIdx.x < parts) {
     int64_t t0 = mul_div(total, blockIdx.x, parts), t1 = mul_div(total, blockIdx.x + 1, parts);
-    const int lens1 = lens;
-    const int64_t upto1 = upto;
-#pragma unroll 1
-    for (int round = whole_items ? 0 : 1; round < 2; ++round) {
-      int64_t at_line;
-      if (round == 0) {
-        at_line = warp == 0 ? t0 : t1;  // of which the next begin of an item is wanted
-      } else {
-        first = t0 + (int64_t)((uint64_t)((t1 - t0) * warp) / kWarps);
-        left = t0 + (int64_t)((uint64_t)((t1 - t0) * (warp + 1)) / kWarps) - first;
-        at_line = first;
-        if (left <= 0) break;
-        if (lane == 0) {
-          part_end[0] = first + left;
-          part_end[1] = total;
-        }
-      }
-      const int64_t seq_first = mul_div(at_line, 1, hkv);  // the tile's place if there were one head
-      before = 0;
-      b0 = 0;
+    // the item that a place on the line lies in, and the tile; the item's length
+    auto find = [&](int64_t place) {
+      const int64_t seq_first = mul_div(place, 1, hkv);  // the tile's place if there were one head
       if (chunks > 2) {
         for (int base = 0; base < chunks; base += 32) {
           const int64_t v = base + lane < chunks ? sums[base + lane] : 0, in = warp_scan(v, lane);
@@ -262,25 +246,40 @@ __global__ void __launch_bounds__(32 * W, 1)
         before = first32;
         lens = lens2;
         upto = warp_scan(units_of<L::END>(lens, cap), lane);
-      } else {
-        lens = lens1;
-        upto = upto1;
       }
       const int at = max(__ffs(__ballot_sync(0xffffffffu, before + upto > seq_first)) - 1, 0);
       const int n = max(units_of<L::END>(__shfl_sync(0xffffffffu, lens, at), cap), 1);
       before += __shfl_sync(0xffffffffu, upto, at) - n;
       b0 = min(b0 + at, n_seqs - 1);
-      const int64_t rest = max(at_line - before * hkv, (int64_t)0);
+      const int64_t rest = max(place - before * hkv, (int64_t)0);
       hk0 = (int)min(mul_div(rest, 1, n), (int64_t)(hkv - 1));  // within bounds even if lengths change under the call
       tile0 = (int)min(rest - (int64_t)hk0 * n, (int64_t)(n - 1));
-      if (round == 0) {
-        int64_t* ends = reinterpret_cast<int64_t*>(smem + L::AT_INFO);
-        if (lane == 0 && warp < 2) ends[warp] = at_line >= total ? total : tile0 ? at_line - tile0 + n : at_line;
-        __syncthreads();
-        t0 = ends[0];
-        t1 = ends[1];
-        __syncthreads();
-      } else if (tile0 >= n - L::END) {  // within an item's end
+      return n;
+    };
+    if (whole_items) {  // on to the next begin of an item: warp 0 of the part's begin, the others of its end
+      const int lens0 = lens;
+      const int64_t upto0 = upto, place = warp == 0 ? t0 : t1;
+      const int n = find(place);
+      int64_t* bounds = reinterpret_cast<int64_t*>(smem + L::AT_INFO);
+      if (lane == 0 && warp < 2) bounds[warp] = place >= total ? total : tile0 ? place - tile0 + n : place;
+      __syncthreads();
+      t0 = bounds[0];
+      t1 = bounds[1];
+      __syncthreads();
+      lens = lens0;
+      upto = upto0;
+      before = 0;
+      b0 = 0;
+    }
+    first = t0 + (int64_t)((uint64_t)((t1 - t0) * warp) / kWarps);
+    left = t0 + (int64_t)((uint64_t)((t1 - t0) * (warp + 1)) / kWarps) - first;
+    if (lane == 0) {
+      part_end[0] = first + left;
+      part_end[1] = total;
+    }
+    if (left > 0) {
+      const int n = find(first);
+      if (tile0 >= n - L::END) {  // within an item's end
         left -= n - tile0;
         tile0 = 0;
         if (++hk0 == hkv) {
@@ -1066,31 +1065,38 @@ cudaError_t join(const DecodeArgs& a, const DecodeShape& sh, const DecodeWs& ws,
 template <int D, bool FP8, int NT, int W>
 cudaError_t run(const DecodeArgs& a, const DecodeShape& sh, DecodeWs ws, cudaStream_t st) {
   using L = Lay<D, FP8, NT, W>;
-  auto kfn = k_decode<D, FP8, NT, W>;
   CUtensorMap mk, mv;
   if (!tile_map<D, FP8>(&mk, a.c, a.c.k, kTileKeys, 2) || !tile_map<D, FP8>(&mv, a.c, a.c.v, kTileKeys, 2)) return cudaErrorInvalidValue;
-  cudaError_t e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
-  if (e != cudaSuccess) return e;
-  // Few short sequences: a CTA or a cluster of CTAs to each item, and one launch, where the line of tiles takes two.  One CTA up to 512 keys
-  // of the longest sequence that the table has room for (320 keys 6.6 us on the device, 7.1 as a cluster of 2), then as many as get 256
-  // keys each, if the items are few enough.  us on the device and a call, bf16, 8 key heads, on the line, with one CTA and in clusters: 1000
-  // keys 7.9 and 11.3, 9.2 and 9.8, 7.6 and 8.2; 2000 keys 8.7 and 10.2 on the line, 8.2 and 9.1 in clusters of 8 (e4m3 9.2 and 10.2, 8.7
-  // and 9.5; 16 rows 13.0 and 13.5, 10.9 and 11.7); with 512 keys to a CTA, 4000 of one head, the line is as fast (9.6 and 10.3, 9.6
-  // and 10.5).  Clusters of 8 find room for 12 items at once (8.8 us; 9.2 in clusters of 4), not for 16 (12.7 instead of 8.6 us).
-  const int64_t items = (int64_t)a.t.n_seqs * a.c.n_kv_heads;
-  const int keys = table_keys(a.t, a.c.page_size);
-  int share = 1;
-  while (share < 8 && keys > (share == 1 ? 512 : 256 * share) && items * sh.blocks * 2 * share <= (share == 4 ? 96 : 128)) share *= 2;
-  ws.share = W == 8 && items <= sh.ctas && keys <= share * (FP8 || share > 1 ? 512 : 1024) ? share : 0;
-  // Up to four times as many short items as CTAs: parts of the line that begin and end with items, and one launch.  bf16, keys of the longest
-  // sequence: 64 sequences of 4 key heads up to 300 keys 8.6 us a call (10.3 with a second launch), 256 of 2 heads of 64 up to 500
-  // 11.0 (12.0); but 64 of 8 heads up to 1000, e4m3, 15.0 (14.2), 200 of 8 heads up to 500 20.4 (19.3).
-  if (!ws.share && W == 8 && items <= 4 * (int64_t)sh.ctas && keys <= 512) ws.share = -1;
-  if (ws.share) {
-    e = launch_pdl_cluster(kfn, dim3(ws.share > 0 ? (unsigned)items * ws.share : sh.ctas, sh.blocks), dim3(32 * W), L::BYTES, st, std::max(ws.share, 1), a, ws, mk, mv, wait_limit_ns());
-    note_launch();
-    return e;
+  cudaError_t e;
+  if constexpr (W == 8) {  // 16 warps are for far more keys
+    // Few short sequences: a CTA or a cluster of CTAs to each item, and one launch, where the line of tiles takes two.  One CTA up to 512 keys
+    // of the longest sequence that the table has room for (320 keys 6.6 us on the device, 7.1 as a cluster of 2), then as many as get 256
+    // keys each, if the items are few enough.  us on the device and a call, bf16, 8 key heads, on the line, with one CTA and in clusters: 1000
+    // keys 7.9 and 11.3, 9.2 and 9.8, 7.6 and 8.2; 2000 keys 8.7 and 10.2 on the line, 8.2 and 9.1 in clusters of 8 (e4m3 9.2 and 10.2, 8.7
+    // and 9.5; 16 rows 13.0 and 13.5, 10.9 and 11.7); with 512 keys to a CTA, 4000 of one head, the line is as fast (9.6 and 10.3, 9.6
+    // and 10.5).  Clusters of 8 find room for 12 items at once (8.8 us; 9.2 in clusters of 4), not for 16 (12.7 instead of 8.6 us).
+    const int64_t items = (int64_t)a.t.n_seqs * a.c.n_kv_heads;
+    const int keys = table_keys(a.t, a.c.page_size);
+    int share = 1;
+    while (share < 8 && keys > (share == 1 ? 512 : 256 * share) && items * sh.blocks * 2 * share <= (share == 4 ? 96 : 128)) share *= 2;
+    ws.share = items <= sh.ctas && keys <= share * (FP8 || share > 1 ? 512 : 1024) ? share : 0;
+    // Up to four times as many short items as CTAs: parts of the line that begin and end with items, and one launch.  bf16, keys of the longest
+    // sequence: 64 sequences of 4 key heads up to 300 keys 8.6 us a call (10.3 with a second launch), 256 of 2 heads of 64 up to 500
+    // 11.0 (12.0); but 64 of 8 heads up to 1000, e4m3, 15.0 (14.2), 200 of 8 heads up to 500 20.4 (19.3).
+    if (!ws.share && items <= 4 * (int64_t)sh.ctas && keys <= 512) ws.share = -1;
+    if (ws.share) {
+      auto kfn = k_decode<D, FP8, NT, W, false>;
+      e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+      if (e != cudaSuccess) return e;
+      e = launch_pdl_cluster(kfn, dim3(ws.share > 0 ? (unsigned)items * ws.share : sh.ctas, sh.blocks), dim3(32 * W), L::BYTES, st,
+                             std::max(ws.share, 1), a, ws, mk, mv, wait_limit_ns());
+      note_launch();
+      return e;
+    }
   }
+  auto kfn = k_decode<D, FP8, NT, W, true>;
+  e = cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+  if (e != cudaSuccess) return e;
   e = launch_pdl(kfn, dim3(sh.ctas, sh.blocks), dim3(32 * W), L::BYTES, st, a, ws, mk, mv, wait_limit_ns());
   note_launch();
   if (e != cudaSuccess) return e;
