@@ -25,7 +25,9 @@
 //
 // A warp's part may begin or end within an item.  The CTA joins such pieces in shared memory, in order, and what an item leaves
 // in several CTAs a second kernel joins, in order: no atomics, equal calls give equal bits.
-// Few short sequences have a cluster of CTAs to each item instead, which join their sums through each other's shared memory: one launch.
+// Few short sequences have a cluster of CTAs to each item instead, which join their sums through each other's shared memory, and somewhat
+// more get parts that begin and end with items: one launch.  Rows of empty sequences are written by all warps of the last launch, a
+// sequence to each (200 sequences of 8 heads, one in eight empty: 14 us; with 32 sequences to a warp 58).
 // (More than 16 rows of a long bf16 cache: decode_wide.cu.)
 //
 // A value that is infinite or NaN spoils the products of query rows that do not see it (zero times infinity), and of those that do
@@ -33,12 +35,12 @@
 //
 // Measured (GB300, calls back to back; floor: the cached bytes at the copy rate of 6698 GB/s):
 //   1 sequence of 1048576 keys, 4 / 1 heads, bf16            86 us, floor 80.2
-//   1 of 5242880, 8 / 1, e4m3                           206 - 214 us, 206.6 (as fast as the box's memory)
+//   1 of 5242880, 8 / 1, e4m3                           206 - 218 us, 206.6 (as fast as the box's memory)
 //   64 up to 16384, 32 / 8, e4m3                             88 us, 76.0
 //   48 up to 8192, 40 / 8, bf16                              58 us, 48.3
 //   16 up to 32768, 4 tokens each, 32 / 8, e4m3              64 us, 47.3
-//   256 up to 500, 4 / 2 heads of 64, bf16                 11.4 us, 2.2
-//   1 of 4097, 32 / 8, bf16                                 9.1 us, 2.5
+//   256 up to 500, 4 / 2 heads of 64, bf16                 10.4 us, 2.2
+//   1 of 4097, 32 / 8, bf16                                 9.2 us, 2.5
 // One long sequence streams at the copy rate.  What a call adds: 5 us until the first tile lands (lengths, table entries and
 // queries are read one after another), 2 to 4 us for the ends of the last items, 2 to 3 us for the second launch.  With 16 rows
 // of an e4m3 cache the tiles' own chain of instructions shows as well: 255 registers leave room for 8 warps.
