@@ -240,8 +240,9 @@ __global__ void __launch_bounds__(Wide<D, RP>::THREADS, 1)
   const int box_rows = ws.box_rows, boxes_col = kKeys / box_rows, my_box = lane % boxes_col, my_col = lane / boxes_col;
   const bool mine = lane < boxes_col * SEGS;
   auto entry = [&](const Line& w, int key) {
+    if (w.left <= 0) return -1;  // the tile may be the one after the longest sequence's last
     key += w.tile * kKeys;
-    return w.left > 0 && key < w.len && key / ps < a.t.max_pages ? a.t.pages[(int64_t)w.b * a.t.stride + key / ps] : -1;
+    return key < w.len && key / ps < a.t.max_pages ? a.t.pages[(int64_t)w.b * a.t.stride + key / ps] : -1;
   };
   auto bring = [&](const CUtensorMap* map, uint32_t u, int page, int hk, int row) {
     const uint32_t slot = u % RING;
@@ -411,7 +412,8 @@ __global__ void __launch_bounds__(Wide<D, RP>::THREADS, 1)
         ok = ok && wait(s_full + (t & 1) * 8, t >> 1 & 1);
         tc::fence_after_sync();
         if (!ok) nan = __uint_as_float(0x7fffffffu);
-        const bool some_hidden = k0 + kKeys > all_seen || __any_sync(0xffffffffu, nan != 0.f);
+        // (k0 + kKeys may pass 32 bits in the last tile of the longest sequence)
+        const bool some_hidden = k0 > all_seen - kKeys || __any_sync(0xffffffffu, nan != 0.f);
         const int unseen = k0 + key - len;  // less than a row's `see`: seen
         // scores in units of log2, less the references; until none exceeds them by too much
         float d[RH];
@@ -474,7 +476,7 @@ __global__ void __launch_bounds__(Wide<D, RP>::THREADS, 1)
         __syncwarp();
         if (lane == 0) tc::mbar_arrive_addr(s_empty + (t & 1) * 8);
         ok = ok && wait(p_empty, (t & 1) ^ 1);  // the weights of the tile before have been used
-        if (side_of == 0 && k0 + kKeys > len) {  // rows behind the sequence's end may hold anything: the values' become zeros
+        if (side_of == 0 && k0 > len - kKeys) {  // rows behind the sequence's end may hold anything: the values' become zeros
           const uint32_t u = 2 * t + 1, slot = u % RING;
           ok = ok && wait(full + slot * 8, u / RING & 1);
           if (ok && k0 + key >= len)
