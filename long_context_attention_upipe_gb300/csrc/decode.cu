@@ -18,8 +18,9 @@
 //   bf16  weights enter as the sum of two bf16 numbers (2^-17); a single one would double the error of o.
 //   e4m3  codes are converted to fp16 (exact).  A 16-byte piece of codes gives a lane four neighbouring elements, so the steps of
 //         S^T take the head dimension in that order and the rows of O^T are pairs of elements.  q goes to fp16 under a power of two
-//         for each row, K's scale to the score, and V's scale to the weight's exponent, s_j + log2 sv_j, under a maximum of its own;
-//         weights are fp16 (2^-11) up to 2^15, which leaves 2^-35 of the largest.
+//         for each row (exact, but for rows whose elements are further apart than 2^32: redo), K's scale to the score, and V's scale to
+//         the weight's exponent, s_j + log2 sv_j, under a maximum of its own; weights are fp16 (2^-11) up to 2^15, which leaves 2^-35 of
+//         the largest.
 // The maximum is a reference that is raised, and the sums rescaled, only when a score exceeds it by a margin: one vote for each
 // tile, no shuffles.  m, l and O are fp32.
 //
@@ -32,6 +33,7 @@
 //
 // A value that is infinite or NaN spoils the products of query rows that do not see it (zero times infinity), and of those that do
 // where a weight's second part is zero.  Then o is not finite although l is, and the piece's o is summed again key by key (redo).
+// So are the scores, l and o of a query row that fp16 does not hold.
 //
 // Measured (GB300, calls back to back; floor: the cached bytes at the copy rate of 6698 GB/s):
 //   1 sequence of 1048576 keys, 4 / 1 heads, bf16            86 us, floor 80.2
@@ -64,13 +66,13 @@ struct Lay {
   static constexpr int SLOT = ROWS * D * 4;             // sums of a piece's o
   static constexpr int WARPS = W;
   static constexpr int END = FP8 ? 4 : 2;               // tiles' time that an item's end (and the next one's begin) takes
-  static constexpr int FIT = ((226 * 1024 - 16) / WARPS - 40 - SLOT - 2 * ROWS * (int)sizeof(RowSum)) / (STAGE + SCALES + 8);
+  static constexpr int FIT = ((226 * 1024 - 16) / WARPS - 44 - SLOT - 2 * ROWS * (int)sizeof(RowSum)) / (STAGE + SCALES + 8);
   static constexpr int STAGES = FIT > 6 ? 6 : FIT;
   static constexpr int QUEUE = STAGES * STAGE;
   static constexpr int AT_SCALES = WARPS * QUEUE, AT_SLOTS = AT_SCALES + WARPS * STAGES * SCALES;
   static constexpr int AT_SUMS = AT_SLOTS + WARPS * SLOT, AT_BARS = AT_SUMS + WARPS * 2 * ROWS * (int)sizeof(RowSum);
   static constexpr int AT_INFO = AT_BARS + WARPS * STAGES * 8;
-  static constexpr int BYTES = AT_INFO + WARPS * 40 + 16 + 1024;  // the queues start on 1024 bytes
+  static constexpr int BYTES = AT_INFO + WARPS * 44 + 16 + 1024;  // the queues start on 1024 bytes
   static constexpr int MT = D / 16;                     // tiles of O^T
   static constexpr int KS = D / 16;                     // steps of S^T
   static_assert(STAGES >= 2 && QUEUE >= 2 * SLOT && WARPS * QUEUE >= 2048 * 8 && BYTES <= 227 * 1024, "shared memory");
@@ -170,6 +172,7 @@ __global__ void __launch_bounds__(32 * W, 1)
   int4* info = reinterpret_cast<int4*>(smem + L::AT_INFO);  // [warp]: item of the head piece, of the tail, tail begins, its last CTA
   int2* info_len = reinterpret_cast<int2*>(info + kWarps);  // ... keys of their sequences
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::AT_INFO + kWarps * 40);
+  volatile uint32_t* far_rows = reinterpret_cast<volatile uint32_t*>(smem + L::AT_INFO + kWarps * 40 + 16) + warp;  // of the item: see `convert`
   const uint32_t bars = smem_u32(smem + L::AT_BARS) + warp * L::STAGES * 8;
   if (lane < L::STAGES) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + lane * 8) : "memory");
   if (threadIdx.x == 0) *abort_flag = 0;
@@ -325,18 +328,30 @@ __global__ void __launch_bounds__(32 * W, 1)
         }
       }
     };
-    // fp16 under a power of two for each row: bf16's 8 bits fit, elements below 2^-14 of the largest lose what fp32 sums would lose
+    // fp16 under a power of two for each row, the largest element in [2^15, 2^16): bf16's 8 bits fit exactly down to 2^-17.  Rows with
+    // elements below that are remembered, and their sums made key by key in the end.  (With the largest in [1, 2) rows that span more than
+    // 2^17 would need that, and some models' queries have a few elements that large.)
     auto convert = [&]() {
+      uint32_t far = 0;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        uint32_t big = 0;
+        uint32_t big = 0, small = 0x7fff7fffu;  // of pairs: the smallest magnitude but zero, as the signed number magnitude - 0x8001
 #pragma unroll
-        for (int s = 0; s < L::KS; ++s) big = amax2(big, amax2(q[nt][s][0], q[nt][s][1]));
+        for (int s = 0; s < L::KS; ++s) {
+          big = amax2(big, amax2(q[nt][s][0], q[nt][s][1]));
+          small = min_s16x2(small, min_s16x2((q[nt][s][0] | 0x80008000u) - 0x00010001u, (q[nt][s][1] | 0x80008000u) - 0x00010001u));
+        }
         big = pair_bits(big);
+        small = min_s16x2(small, small >> 16 | small << 16);
         big = max(big, __shfl_xor_sync(0xffffffffu, big, 1));
+        small = min_s16x2(small, __shfl_xor_sync(0xffffffffu, small, 1));
         big = max(big, __shfl_xor_sync(0xffffffffu, big, 2));
-        const int ex = min(max((int)(big >> 23) - 127, -126), 126);
-        const float down = pow2(-ex), up = pow2(ex) * (a.scale * kLog2e);
+        small = min_s16x2(small, __shfl_xor_sync(0xffffffffu, small, 2));
+        const int ex = min(max((int)(big >> 23) - 127, -111), 127);
+        const float down = pow2(kQueryTop - ex), up = pow2(ex) * (a.scale * kLog2e);  // 2^-15 goes to the key's scale
+        const int least = max((int)((small + 1) >> 7 & 0xff), 1) - 127;  // exponent (all zeros: the lowest)
+        const unsigned lost = __ballot_sync(0xffffffffu, c == 0 && big < 0x7f800000u && small != 0x7fff7fffu && least + kQueryTop - ex < -17);
+        for (unsigned rest = lost; rest; rest &= rest - 1) far |= 1u << (nt * 8 + (__ffs(rest) - 1) / 4);
 #pragma unroll
         for (int s = 0; s < L::KS; ++s)
 #pragma unroll
@@ -345,6 +360,7 @@ __global__ void __launch_bounds__(32 * W, 1)
         rs[nt][0] = __shfl_sync(0xffffffffu, up, 8 * c);
         rs[nt][1] = __shfl_sync(0xffffffffu, up, 8 * c + 4);
       }
+      if (lane == 0) *far_rows = far;
     };
 
     // ---- the end of the line that loads.  Lengths of 32 sequences and 32 entries of the table lie in the lanes; the
@@ -537,8 +553,9 @@ __global__ void __launch_bounds__(32 * W, 1)
         // of log2 is x * rs.  d, dv: scores relative to the references, dv with the value's scale in it (e4m3).
         float d[NT][4], dv[NT][4], lv[2];
         if (FP8) {
-          const float sc = lds32(scale_queue + stage * L::SCALES), lg = fast_log2(sc);
-          const float ks[2] = {__shfl_sync(0xffffffffu, sc, lane & 28), __shfl_sync(0xffffffffu, sc, (lane & 28) + 1)};
+          // (scales that kv_write makes are above 2^-109: exact)
+          const float sc = lds32(scale_queue + stage * L::SCALES), lg = fast_log2(sc), sk = sc * pow2(-kQueryTop);
+          const float ks[2] = {__shfl_sync(0xffffffffu, sk, lane & 28), __shfl_sync(0xffffffffu, sk, (lane & 28) + 1)};
           lv[0] = __shfl_sync(0xffffffffu, lg, (lane & 28) + 2);
           lv[1] = __shfl_sync(0xffffffffu, lg, (lane & 28) + 3);
 #pragma unroll
@@ -681,7 +698,8 @@ __global__ void __launch_bounds__(32 * W, 1)
         left_len.x = len;
       }
       __syncwarp();
-      uint32_t again = 0;  // rows (8 nt + row) whose o has to be summed once more
+      const uint32_t far = FP8 ? *far_rows : 0;
+      uint32_t again = far;  // rows (8 nt + row) whose o has to be summed once more; of some l too
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float by[2];  // what o's sums are multiplied with
@@ -759,18 +777,21 @@ __global__ void __launch_bounds__(32 * W, 1)
             float part = i & 1 ? l[nt][1] : l[nt][0];
 #pragma unroll
             for (int off = 4; off < 32; off <<= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
-            const float inv = 1.f / __shfl_sync(0xffffffffu, part, i >> 1);
+            const bool scores = FP8 && far >> row & 1;
             float out[E];
-            redo<D, FP8>(a, cb, chk, at, begin * kTileKeys, end, ref, out);
+            const RowSum sum = redo<D, FP8>(a, cb, chk, at, begin * kTileKeys, end, RowSum{ref, __shfl_sync(0xffffffffu, part, i >> 1)}, scores, out);
+            const float inv = 1.f / sum.l;
             __syncwarp();
             if (whole) {
               bf16* o = a.o + at.head * a.o_head + at.tok * a.o_tok + lane * E;
 #pragma unroll
               for (int e = 0; e < E; e += 2)
                 if (raw <= cap && end > 0) *reinterpret_cast<uint32_t*>(o + e) = pack_bf16(out[e] * inv, out[e + 1] * inv);
+              if (scores && a.lse && lane == 0 && raw <= cap && end > 0) a.lse[at.head * n_seqs * a.q_len + at.tok] = row_lse(sum.m, sum.l);
             } else {
 #pragma unroll
               for (int e = 0; e < E; ++e) slot[row * D + lane * E + e] = out[e];
+              if (scores && lane == 0 && raw <= cap) piece_sums[(2 * warp + !ends) * L::ROWS + row] = sum;
             }
           }
       }

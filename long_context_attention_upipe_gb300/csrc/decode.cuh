@@ -37,6 +37,7 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.0e38f;  // a reference below all scores, whose difference to them is defined
 constexpr float kSlack = 8.f;        // a score may exceed the reference by this, in powers of two
 constexpr float kSlackV = 5.f, kShiftV = 10.f;  // fp16 weights: the reference of one lies 10 below the score, the largest is 2^15
+constexpr int kQueryTop = 15;        // fp16 queries: a row's largest element is in [2^15, 2^16)
 
 __device__ __forceinline__ void cp4(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
@@ -77,6 +78,11 @@ __device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
   return d;
 }
 
+__device__ __forceinline__ uint32_t min_s16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("min.s16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 __device__ __forceinline__ float fast_log2(float x) {
   float y;
   asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -161,17 +167,21 @@ __device__ __forceinline__ void load_row(const void* base, int64_t row, int e0, 
   }
 }
 
-// The sums of one query row over the keys [k0, k1) that it sees, key by key, relative to the reference m: a lane gets
-// elements lane * D / 32 .. of o.
+// The sums of one query row over the keys [k0, k1) that it sees, key by key, relative to the reference sum.m: a lane gets elements
+// lane * D / 32 .. of o.  With `scores` the reference and l are found anew as well.
 template <int D, bool FP8>
-__device__ __noinline__ void redo(const DecodeArgs& a, int b, int hk, RowAt at, int k0, int k1, float m, float* out) {
+__device__ __noinline__ RowSum redo(const DecodeArgs& a, int b, int hk, RowAt at, int k0, int k1, RowSum sum, bool scores, float* out) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
   float q[E], acc[E] = {};
   load_row<E, false>(a.q, at.head * a.q_head + at.tok * a.q_tok, lane * E, 1.f, q);
+  if (scores) sum = RowSum{kLowest, 0.f};
   for (int j = k0; j < k1; ++j) {
     const KvPlace p = kv_place(a.c, a.t, b, j);
-    if (p.page < 0) continue;  // its l is NaN
+    if (p.page < 0) {  // else l is NaN already
+      if (scores) sum.l = __uint_as_float(0x7fffffffu);
+      continue;
+    }
     const int64_t row = kv_row(a.c, p, hk), sc = FP8 ? kv_scale(a.c, p, hk) : 0;
     float k[E], v[E], s = 0.f;
     load_row<E, FP8>(a.c.k, row, lane * E, FP8 ? a.c.k_scale[sc] : 1.f, k);
@@ -180,12 +190,23 @@ __device__ __noinline__ void redo(const DecodeArgs& a, int b, int hk, RowAt at, 
     for (int e = 0; e < E; ++e) s += q[e] * k[e];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    const float w = exp2f(s * (a.scale * kLog2e) - m);
+    s *= a.scale * kLog2e;
+    if (scores) {
+      if (s > sum.m) {
+        const float f = exp2f(sum.m - s);
+        sum = RowSum{s, sum.l * f};
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= f;
+      }
+      sum.l += exp2f(s - sum.m);
+    }
+    const float w = exp2f(s - sum.m);
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] += w * v[e];
   }
 #pragma unroll
   for (int e = 0; e < E; ++e) out[e] = acc[e];
+  return sum;
 }
 
 __device__ __forceinline__ float row_lse(float m, float l) { return m * kLn2 + logf(l); }

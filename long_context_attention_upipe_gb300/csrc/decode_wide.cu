@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(Wide<D, RP>::THREADS, 1)
           const int r = col + j, R = rb * RP + r, end = (int)min((int64_t)(begin + tiles) * kKeys, (int64_t)(len + t_see[r]));
           const RowAt row = row_at(a, g, b, hk, R);
           float out[E];
-          redo<D, false>(a, b, hk, row, begin * kKeys, end, t_m[r], out);
+          redo<D, false>(a, b, hk, row, begin * kKeys, end, RowSum{t_m[r], 0.f}, false, out);
           __syncwarp();
           if (whole) {
             const float inv = 1.f / t_sum[r];
