@@ -19,8 +19,8 @@
 //   e4m3  codes are converted to fp16 (exact).  A 16-byte piece of codes gives a lane four neighbouring elements, so the steps of
 //         S^T take the head dimension in that order and the rows of O^T are pairs of elements.  q goes to fp16 under a power of two
 //         for each row (exact, but for rows whose elements are further apart than 2^32: redo), K's scale to the score, and V's scale to
-//         the weight's exponent, s_j + log2 sv_j, under a maximum of its own; weights are fp16 (2^-11) up to 2^15, which leaves 2^-35 of
-//         the largest.
+//         the weight's exponent, s_j - m + log2 sv_j, under a maximum of its own; weights are fp16 (2^-11) up to 2^15, which leaves
+//         2^-35 of the largest.
 // The maximum is a reference that is raised, and the sums rescaled, only when a score exceeds it by a margin: one vote for each
 // tile, no shuffles.  m, l and O are fp32.
 //
@@ -468,7 +468,7 @@ __global__ void __launch_bounds__(32 * W, 1)
     int cb = b0, chk = hk0, ct = tile0, raw = __shfl_sync(0xffffffffu, lens, b0 & 31), len = min(max(raw, 0), cap), cn = tiles_of(len, cap);
     int stage = 0;
     uint32_t parity = 0;
-    float m[NT][2], l[NT][2], mv[NT][2], acc[NT][L::MT][4];
+    float m[NT][2], l[NT][2], mv[NT][2], acc[NT][L::MT][4];  // mv: the reference of the weights with values' scales in them, less m
     int see[NT][2];  // a row sees keys before len + see
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -480,8 +480,8 @@ __global__ void __launch_bounds__(32 * W, 1)
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          m[nt][e] = mv[nt][e] = kLowest;
-          l[nt][e] = 0.f;
+          m[nt][e] = kLowest;
+          mv[nt][e] = l[nt][e] = 0.f;
         }
 #pragma unroll
         for (int mt = 0; mt < L::MT; ++mt)
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(32 * W, 1)
             for (int i = 0; i < 4; ++i) {
               const float by = FP8 ? rs[nt][i & 1] : a.scale * kLog2e;
               d[nt][i] = __fmaf_rn(x[nt][i], by, -m[nt][i & 1]);
-              if (FP8) dv[nt][i] = __fmaf_rn(x[nt][i], by, lv[i >> 1] - mv[nt][i & 1]);
+              if (FP8) dv[nt][i] = d[nt][i] + (lv[i >> 1] - mv[nt][i & 1]);
             }
           if (some_hidden) {
             const float nan = lost ? __uint_as_float(0x7fffffffu) : 0.f;
@@ -598,23 +598,25 @@ __global__ void __launch_bounds__(32 * W, 1)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float by = FP8 ? rs[nt][e] : a.scale * kLog2e;
-              float top = m[nt][e], top_v = mv[nt][e] + kShiftV;
+              float top = m[nt][e], score[2];
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                const float score = d[nt][e + 2 * i] == -INFINITY ? -INFINITY : x[nt][e + 2 * i] * by;
-                top = fmaxf(top, score);
-                if (FP8) top_v = fmaxf(top_v, score + lv[i]);
+                score[i] = d[nt][e + 2 * i] == -INFINITY ? -INFINITY : x[nt][e + 2 * i] * by;
+                top = fmaxf(top, score[i]);
               }
 #pragma unroll
-              for (int off = 4; off < 32; off <<= 1) {
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-                if (FP8) top_v = fmaxf(top_v, __shfl_xor_sync(0xffffffffu, top_v, off));
-              }
-              float f = fast_exp2(m[nt][e] - top);
+              for (int off = 4; off < 32; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+              const float step = m[nt][e] - top;
               m[nt][e] = top;
+              float f = fast_exp2(step);
               l[nt][e] *= f;
               if (FP8) {
-                f = fast_exp2(mv[nt][e] - (top_v - kShiftV));
+                float top_v = mv[nt][e] + kShiftV + step;  // less the new m, so that a large score takes no bits of it
+#pragma unroll
+                for (int i = 0; i < 2; ++i) top_v = fmaxf(top_v, score[i] - top + lv[i]);
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) top_v = fmaxf(top_v, __shfl_xor_sync(0xffffffffu, top_v, off));
+                f = fast_exp2(step + mv[nt][e] - (top_v - kShiftV));
                 mv[nt][e] = top_v - kShiftV;
               }
 #pragma unroll
@@ -718,7 +720,7 @@ __global__ void __launch_bounds__(32 * W, 1)
 #pragma unroll
           for (int i = 0; i < 4; ++i) again |= (bad >> i & 1) << (nt * 8 + 2 * i + e);
           if (raw > cap) sum = __uint_as_float(0x7fffffffu);
-          by[e] = FP8 ? fast_exp2(mv[nt][e] - m[nt][e]) : 1.f;
+          by[e] = FP8 ? fast_exp2(mv[nt][e]) : 1.f;
           if (whole) {
             by[e] /= sum;
             if (a.lse && r == 0 && R < rows) {
