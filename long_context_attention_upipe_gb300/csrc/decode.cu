@@ -32,8 +32,8 @@
 // (More than 16 rows of a long bf16 cache: decode_wide.cu.)
 //
 // A value that is infinite or NaN spoils the products of query rows that do not see it (zero times infinity), and of those that do
-// where a weight's second part is zero.  Then o is not finite although l is, and the piece's o is summed again key by key (redo).
-// So are the scores, l and o of a query row that fp16 does not hold.
+// where a weight's second part is zero.  Then o is not finite although l is, and the piece is made again key by key (redo), as
+// is that of a query row that fp16 does not hold.
 //
 // Measured (GB300, calls back to back; floor: the cached bytes at the copy rate of 6698 GB/s):
 //   1 sequence of 1048576 keys, 4 / 1 heads, bf16            86 us, floor 80.2
@@ -569,8 +569,8 @@ __global__ void __launch_bounds__(32 * W, 1)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              const float by = FP8 ? rs[nt][i & 1] : a.scale * kLog2e;
-              d[nt][i] = __fmaf_rn(x[nt][i], by, -m[nt][i & 1]);
+              // (two roundings: equal keys have equal scores, and the largest of a row is 0 however large it is)
+              d[nt][i] = __fsub_rn(__fmul_rn(x[nt][i], FP8 ? rs[nt][i & 1] : a.scale * kLog2e), m[nt][i & 1]);
               if (FP8) dv[nt][i] = d[nt][i] + (lv[i >> 1] - mv[nt][i & 1]);
             }
           if (some_hidden) {
@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(32 * W, 1)
               float top = m[nt][e], score[2];
 #pragma unroll
               for (int i = 0; i < 2; ++i) {
-                score[i] = d[nt][e + 2 * i] == -INFINITY ? -INFINITY : x[nt][e + 2 * i] * by;
+                score[i] = d[nt][e + 2 * i] == -INFINITY ? -INFINITY : __fmul_rn(x[nt][e + 2 * i], by);
                 top = fmaxf(top, score[i]);
               }
 #pragma unroll
@@ -700,8 +700,7 @@ __global__ void __launch_bounds__(32 * W, 1)
         left_len.x = len;
       }
       __syncwarp();
-      const uint32_t far = FP8 ? *far_rows : 0;
-      uint32_t again = far;  // rows (8 nt + row) whose o has to be summed once more; of some l too
+      uint32_t again = FP8 ? *far_rows : 0;  // rows (8 nt + row) whose sums have to be made once more
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float by[2];  // what o's sums are multiplied with
@@ -775,25 +774,20 @@ __global__ void __launch_bounds__(32 * W, 1)
             const int row = nt * 8 + i, R = rb * L::ROWS + row;
             const RowAt at = row_at(a, g, cb, chk, R);
             const int end = (int)min((int64_t)ct * kTileKeys, (int64_t)(len - a.q_len + 1 + R / g));
-            const float ref = __shfl_sync(0xffffffffu, i & 1 ? m[nt][1] : m[nt][0], i >> 1);
-            float part = i & 1 ? l[nt][1] : l[nt][0];
-#pragma unroll
-            for (int off = 4; off < 32; off <<= 1) part += __shfl_xor_sync(0xffffffffu, part, off);
-            const bool scores = FP8 && far >> row & 1;
             float out[E];
-            const RowSum sum = redo<D, FP8>(a, cb, chk, at, begin * kTileKeys, end, RowSum{ref, __shfl_sync(0xffffffffu, part, i >> 1)}, scores, out);
-            const float inv = 1.f / sum.l;
+            const RowSum sum = redo<D, FP8>(a, cb, chk, at, begin * kTileKeys, end, out);
             __syncwarp();
-            if (whole) {
-              bf16* o = a.o + at.head * a.o_head + at.tok * a.o_tok + lane * E;
-#pragma unroll
-              for (int e = 0; e < E; e += 2)
-                if (raw <= cap && end > 0) *reinterpret_cast<uint32_t*>(o + e) = pack_bf16(out[e] * inv, out[e + 1] * inv);
-              if (scores && a.lse && lane == 0 && raw <= cap && end > 0) a.lse[at.head * n_seqs * a.q_len + at.tok] = row_lse(sum.m, sum.l);
-            } else {
+            if (raw > cap) continue;  // NaN
+            if (!whole) {
 #pragma unroll
               for (int e = 0; e < E; ++e) slot[row * D + lane * E + e] = out[e];
-              if (scores && lane == 0 && raw <= cap) piece_sums[(2 * warp + !ends) * L::ROWS + row] = sum;
+              if (lane == 0) piece_sums[(2 * warp + !ends) * L::ROWS + row] = sum;
+            } else if (end > 0) {
+              bf16* o = a.o + at.head * a.o_head + at.tok * a.o_tok + lane * E;
+              const float inv = 1.f / sum.l;
+#pragma unroll
+              for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(o + e) = pack_bf16(out[e] * inv, out[e + 1] * inv);
+              if (a.lse && lane == 0) a.lse[at.head * n_seqs * a.q_len + at.tok] = row_lse(sum.m, sum.l);
             }
           }
       }

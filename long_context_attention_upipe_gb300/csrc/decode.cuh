@@ -167,19 +167,19 @@ __device__ __forceinline__ void load_row(const void* base, int64_t row, int e0, 
   }
 }
 
-// The sums of one query row over the keys [k0, k1) that it sees, key by key, relative to the reference sum.m: a lane gets elements
-// lane * D / 32 .. of o.  With `scores` the reference and l are found anew as well.
+// Reference, l and o of one query row over the keys [k0, k1) that it sees, key by key: a lane gets elements lane * D / 32 .. of o.  (All
+// three, since o would not fit the l of scores that were added up in another order, if these are large.)
 template <int D, bool FP8>
-__device__ __noinline__ RowSum redo(const DecodeArgs& a, int b, int hk, RowAt at, int k0, int k1, RowSum sum, bool scores, float* out) {
+__device__ __noinline__ RowSum redo(const DecodeArgs& a, int b, int hk, RowAt at, int k0, int k1, float* out) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
+  RowSum sum{kLowest, 0.f};
   float q[E], acc[E] = {};
   load_row<E, false>(a.q, at.head * a.q_head + at.tok * a.q_tok, lane * E, 1.f, q);
-  if (scores) sum = RowSum{kLowest, 0.f};
   for (int j = k0; j < k1; ++j) {
     const KvPlace p = kv_place(a.c, a.t, b, j);
-    if (p.page < 0) {  // else l is NaN already
-      if (scores) sum.l = __uint_as_float(0x7fffffffu);
+    if (p.page < 0) {
+      sum.l = __uint_as_float(0x7fffffffu);
       continue;
     }
     const int64_t row = kv_row(a.c, p, hk), sc = FP8 ? kv_scale(a.c, p, hk) : 0;
@@ -190,17 +190,15 @@ __device__ __noinline__ RowSum redo(const DecodeArgs& a, int b, int hk, RowAt at
     for (int e = 0; e < E; ++e) s += q[e] * k[e];
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    s *= a.scale * kLog2e;
-    if (scores) {
-      if (s > sum.m) {
-        const float f = exp2f(sum.m - s);
-        sum = RowSum{s, sum.l * f};
+    s = __fmul_rn(s, a.scale * kLog2e);
+    if (s > sum.m) {
+      const float f = exp2f(sum.m - s);
+      sum = RowSum{s, sum.l * f};
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] *= f;
-      }
-      sum.l += exp2f(s - sum.m);
+      for (int e = 0; e < E; ++e) acc[e] *= f;
     }
     const float w = exp2f(s - sum.m);
+    sum.l += w;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] += w * v[e];
   }

@@ -425,10 +425,10 @@ __global__ void __launch_bounds__(Wide<D, RP>::THREADS, 1)
 #pragma unroll
           for (int j = 0; j < RH; j += 4) {
             const float4 m = *reinterpret_cast<const float4*>(t_m + col + j);
-            d[j] = __fmaf_rn(__uint_as_float(x[j]), cs, -m.x);
-            d[j + 1] = __fmaf_rn(__uint_as_float(x[j + 1]), cs, -m.y);
-            d[j + 2] = __fmaf_rn(__uint_as_float(x[j + 2]), cs, -m.z);
-            d[j + 3] = __fmaf_rn(__uint_as_float(x[j + 3]), cs, -m.w);
+            d[j] = __fsub_rn(__fmul_rn(__uint_as_float(x[j]), cs), m.x);  // two roundings, as in decode.cu
+            d[j + 1] = __fsub_rn(__fmul_rn(__uint_as_float(x[j + 1]), cs), m.y);
+            d[j + 2] = __fsub_rn(__fmul_rn(__uint_as_float(x[j + 2]), cs), m.z);
+            d[j + 3] = __fsub_rn(__fmul_rn(__uint_as_float(x[j + 3]), cs), m.w);
             most = fmax3(fmax3(most, d[j], d[j + 1]), d[j + 2], d[j + 3]);
           }
           if (some_hidden) {
@@ -445,7 +445,7 @@ __global__ void __launch_bounds__(Wide<D, RP>::THREADS, 1)
             tmem_ld4(s_at + j, *reinterpret_cast<uint32_t(*)[4]>(x));
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float top = warp_top(unseen < t_see[col + j + k] ? __uint_as_float(x[k]) * cs : -INFINITY);
+              const float top = warp_top(unseen < t_see[col + j + k] ? __fmul_rn(__uint_as_float(x[k]), cs) : -INFINITY);
               if (lane == 0) t_top[quarter * RP + col + j + k] = top;
             }
           }
@@ -571,7 +571,7 @@ __global__ void __launch_bounds__(Wide<D, RP>::THREADS, 1)
       tc::fence_before_sync();
       tc::named_bar_sync(2, L::SOFTMAX);
       const uint32_t redone = again[side_of];
-      if (redone) {  // rows whose o has to be summed once more
+      if (redone) {  // rows whose sums have to be made once more
         constexpr int E = D / 32;
 #pragma unroll 1
         for (int j = quarter; j < RH; j += 4) {
@@ -579,17 +579,19 @@ __global__ void __launch_bounds__(Wide<D, RP>::THREADS, 1)
           const int r = col + j, R = rb * RP + r, end = (int)min((int64_t)(begin + tiles) * kKeys, (int64_t)(len + t_see[r]));
           const RowAt row = row_at(a, g, b, hk, R);
           float out[E];
-          redo<D, false>(a, b, hk, row, begin * kKeys, end, RowSum{t_m[r], 0.f}, false, out);
+          const RowSum sum = redo<D, false>(a, b, hk, row, begin * kKeys, end, out);
           __syncwarp();
-          if (whole) {
-            const float inv = 1.f / t_sum[r];
-            bf16* o = a.o + row.head * a.o_head + row.tok * a.o_tok + lane * E;
-#pragma unroll
-            for (int e = 0; e < E; e += 2)
-              if (w.raw <= cap && end > 0) *reinterpret_cast<uint32_t*>(o + e) = pack_bf16(out[e] * inv, out[e + 1] * inv);
-          } else {
+          if (w.raw > cap) continue;  // NaN
+          if (!whole) {
 #pragma unroll
             for (int e = 0; e < E; ++e) ws.acc[(left_at + r) * D + lane * E + e] = out[e];
+            if (lane == 0) ws.sums[left_at + r] = sum;
+          } else if (end > 0) {
+            bf16* o = a.o + row.head * a.o_head + row.tok * a.o_tok + lane * E;
+            const float inv = 1.f / sum.l;
+#pragma unroll
+            for (int e = 0; e < E; e += 2) *reinterpret_cast<uint32_t*>(o + e) = pack_bf16(out[e] * inv, out[e + 1] * inv);
+            if (a.lse && lane == 0) a.lse[row.head * n_seqs * a.q_len + row.tok] = row_lse(sum.m, sum.l);
           }
         }
       }

@@ -88,3 +88,64 @@ def test_value_scales_beside_large_scores(power, form):
     """An e4m3 value's scale is part of its weight's exponent, and no bit of it is lost to the score."""
     check("e4m3", form, power)
     check("e4m3", form, power, 20)
+
+
+@pytest.mark.parametrize("kind,form", [(k, f) for k in ("bf16", "e4m3") for f in FORMS if k == "bf16" or f[:4] != "wide"])
+@pytest.mark.parametrize("power", [8, 24, 30, 60, 100])
+def test_finite_scores_of_any_size(power, kind, form):
+    check(kind, form, power)
+
+
+@pytest.mark.parametrize("kind,form", [(k, f) for k in ("bf16", "e4m3") for f in FORMS if k == "bf16" or f[:4] != "wide"])
+@pytest.mark.parametrize("power", [8, 14, 20, 40, 100])
+def test_equal_keys_weigh_alike(power, kind, form):
+    """Every key is there twice, in the other half of the sequence: o is the mean of two values, to its own rounding and the weights'."""
+    lens, hq, hkv, dh, size, q_len, more = FORMS[form]
+    lens = [n // 2 * 2 for n in lens]
+    g = gen(len(lens) * 5 + dh + power)
+    pages = sum(-(-n // size) for n in lens) + 1
+    c = make_cache(kind, "heads", pages, hkv, size, dh, None)
+    table = table_of(g, lens, size, pages)
+    q = torch.zeros(hq, len(lens), dh, dtype=torch.bfloat16, device="cuda")
+    which = torch.zeros(hq, len(lens), dtype=torch.long, device="cuda")
+    for b, n in enumerate(lens):
+        if n:
+            k, v = randn(g, hkv, n // 2, dh).bfloat16(), randn(g, hkv, n, dh).bfloat16()
+            pos = torch.arange(n, device="cuda").int()
+            up.kv_write(c, torch.cat([k, k], 1), v, torch.full_like(pos, b), pos, table)
+            for h in range(hq):
+                which[h, b] = j = (h * 131 + 17) % (n // 2)
+                q[h, b] = (cached(c, "k", table, b, n)[h // (hq // hkv), j] * 2.0 ** power).bfloat16()
+    if more:
+        table = widened(table, more, gen(1))
+    o, _ = run_decode(c, q, table, lens)
+    r = 2.0 ** -10 if kind == "e4m3" else 2.0 ** -16
+    for b, n in enumerate(lens):
+        if not n:
+            continue
+        x = q[:, b].double().view(hkv, -1, dh)
+        s = (x @ cached(c, "k", table, b, n).transpose(1, 2))[..., : n // 2] * dh ** -0.5
+        j = which[:, b].view(hkv, -1, 1)
+        assert bool((s.gather(2, j) - s.scatter(2, j, -math.inf).amax(-1, keepdim=True) > 60).all())
+        v = cached(c, "v", table, b, n)
+        one, two = (v.gather(1, (j + i).expand(-1, -1, dh)) for i in (0, n // 2))
+        ref, mass = (one + two) / 2, (one.abs() + two.abs()) / 2
+        err = (o[:, b].double().view(ref.shape) - ref).abs()
+        assert bool((err <= ref.abs() * BF + mass * (r + 2.0 ** -18) + 2.0 ** -20).all()), f"sequence {b}: {float(err.max())}"
+
+
+@pytest.mark.parametrize("kind,form", [("bf16", "cta"), ("e4m3", "line"), ("bf16", "line"), ("bf16", "wide32"), ("bf16", "wide64")])
+@pytest.mark.parametrize("power", [14, 24, 60])
+def test_values_that_are_not_finite_beside_large_scores(power, kind, form):
+    """A key without weight has an infinite value: the elements beside it are those of the key that has all of it."""
+    lens, hq, hkv, dh, size, q_len, _ = FORMS[form]
+    c, table, q, which = one_key_each(kind, form, power)
+    clean, lse = run_decode(c, q, table, lens, q_len=q_len)
+    page = int(table[0, 1]) if lens[0] > size else int(table[2, 1])
+    b = 0 if lens[0] > size else 2
+    (c.v.view(torch.uint8) if kind == "e4m3" else c.v)[page, :, 3, 9] = 0x7f if kind == "e4m3" else math.inf
+    o, lse2 = run_decode(c, q, table, lens, q_len=q_len)
+    rest = torch.arange(dh, device="cuda") != 9
+    mine = slice(b * q_len, b * q_len + q_len)
+    assert bool(((o - clean)[:, mine, rest].abs() <= clean[:, mine, rest].abs() * 2.0 ** -7 + 2.0 ** -130).all())
+    assert bool(((lse2 - lse)[:, mine].abs() <= lse[:, mine].abs() * (2 * dh + 16) * 16 * U).all())
