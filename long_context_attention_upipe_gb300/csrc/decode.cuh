@@ -217,7 +217,7 @@ __device__ __forceinline__ void empty_rows(const DecodeArgs& a, int g, int b, in
   const int lane = threadIdx.x & 31, n = R1 - R0;
   for (int i = lane / LANES; i < (h1 - h0) * n; i += 32 / LANES) {
     const int h = i / n, R = R0 + i - h * n;
-    const bool lost = keys - a.q_len + 1 + R / g > 0;
+    const bool lost = max(keys, 0) - a.q_len + 1 + R / g > 0;  // (the lowest lengths less q_len pass 32 bits)
     const RowAt at = row_at(a, g, b, h0 + h, R);
     const uint32_t w = lost ? 0x7fff7fffu : 0u;
     *reinterpret_cast<uint4*>(a.o + at.head * a.o_head + at.tok * a.o_tok + lane % LANES * 8) = make_uint4(w, w, w, w);
