@@ -51,16 +51,19 @@ bool pool_disjoint(const PoolRows& r) {
   return true;
 }
 
-// Two tensors of the same shape and strides: whether they share bytes, but for one lying in the gaps of the other.
+// Two tensors of the same shape and strides, rows of either disjoint: whether they share bytes when the second lies `d` bytes behind
+// the first.  A row of each meet if some difference of their indices, |i| < n at each level, leaves less than a row of d; what the levels
+// below span leaves two differences to look at.
+bool meet_at(const PoolRows& r, int level, int64_t d) {
+  if (level == 3) return d > -r.row && d < r.row;
+  if (r.n[level] <= 1) return meet_at(r, level + 1, d);
+  const int64_t s = r.s[level], q = d >= 0 ? d / s : -((s - 1 - d) / s);  // floor
+  for (int64_t i = q; i <= q + 1; ++i)
+    if (i > -r.n[level] && i < r.n[level] && meet_at(r, level + 1, d - i * s)) return true;
+  return false;
+}
 bool pools_meet(const PoolRows& a, const PoolRows& b) {
-  if (!overlaps(a.base, a.span(), b.base, b.span())) return false;
-  const int64_t d = reinterpret_cast<intptr_t>(b.base) - reinterpret_cast<intptr_t>(a.base);
-  for (int i = 0; i < 3; ++i) {
-    if (a.n[i] <= 1) continue;
-    const int64_t in = inner_span(a, i), off = ((d % a.s[i]) + a.s[i]) % a.s[i];
-    if (off >= in && off + in <= a.s[i]) return false;
-  }
-  return true;
+  return meet_at(a, 0, reinterpret_cast<intptr_t>(b.base) - reinterpret_cast<intptr_t>(a.base));
 }
 
 struct CacheSpans {
@@ -85,7 +88,7 @@ upipe_status_t check_cache(const upipe_kv_cache_t* c, KvCache& out, CacheSpans& 
                      c->scale_head_stride, c->scale_token_stride, 4, 4))
         return UPIPE_ERR_INVALID_ARG;
   for (int i = 0; i < (c->dtype ? 4 : 2); i += 2)
-    if (!pool_disjoint(r[i]) || pools_meet(r[i], r[i + 1])) return UPIPE_ERR_INVALID_ARG;
+    if (!pool_disjoint(r[i]) || pools_meet(r[i], r[i + 1])) return UPIPE_ERR_INVALID_ARG;  // (strides are above zero then)
   for (int i = 0; i < 3; ++i)
     if (r[0].s[i] % 16) return UPIPE_ERR_UNSUPPORTED;
   if (!aligned16(c->k) || !aligned16(c->v) || !aligned16(c->k_scale) || !aligned16(c->v_scale)) return UPIPE_ERR_ALIGNMENT;
