@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(32 * W, 1)
   if (lane < L::STAGES) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + lane * 8) : "memory");
   if (threadIdx.x == 0) *abort_flag = 0;
   tc::fence_mbar_init();
+  __syncthreads();  // the flag may hold anything before, and another lane than that which prepared a barrier may use it
   grid_dep_wait();
   grid_dep_trigger();  // the joining kernel may start when CTAs leave; it reads nothing of this one before it has ended
 
