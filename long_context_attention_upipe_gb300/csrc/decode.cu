@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(32 * W, 1)
     return true;
   };
   int64_t first = 0, left = 0;
-  // the tile after the part, and all tiles: read again when the part ends
+  // the tile after the part, and all tiles (LINE): read again when the part ends
   volatile int64_t* part_end = reinterpret_cast<volatile int64_t*>(smem + L::AT_INFO + kWarps * 24) + 2 * warp;
   int hk0 = 0, tile0 = 0;
   if (share) {
@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(32 * W, 1)
     }
     first = t0 + (int64_t)((uint64_t)((t1 - t0) * warp) / kWarps);
     left = t0 + (int64_t)((uint64_t)((t1 - t0) * (warp + 1)) / kWarps) - first;
-    if (lane == 0) {
+    if (LINE && lane == 0) {
       part_end[0] = first + left;
       part_end[1] = total;
     }
@@ -693,9 +693,10 @@ __global__ void __launch_bounds__(32 * W, 1)
         left_len.y = len;
         left_over.z = begins;
         __syncwarp();
-        const int64_t next = part_end[0], all = part_end[1];
-        // the CTA whose part holds the item's last tile
-        left_over.w = last_part(max(next + cn - ct, next), all, parts_of(all, X, kWarps));
+        if constexpr (LINE) {  // the CTA whose part holds the item's last tile
+          const int64_t next = part_end[0], all = part_end[1];
+          left_over.w = last_part(max(next + cn - ct, next), all, parts_of(all, X, kWarps));
+        }
       } else if (!whole) {
         left_over.x = item;
         left_len.x = len;
