@@ -666,7 +666,9 @@ upipe_status_t upipe_attn_set_dkdv_window(int32_t items);
  * When a wait runs out, the kernel raises UPIPE_ERR_DEVICE_TIMEOUT in the error word of its
  * workspace or table (the operators around the two blocks and upipe_attn_decode, which have none, leave NaN) and returns instead of
  * hanging.  A diagnostic with no counterpart on the
- * pages: shorter limits are for testing the timeout path with upipe_attn_wait_probe. */
+ * pages: shorter limits are for testing the timeout path with upipe_attn_wait_probe; and below 64 ns
+ * upipe_attn_decode lets a wait for one of the first tiles of each of its queues run out (limit 1: for the first one,
+ * 2: the second, ..), whether it has come or not. */
 upipe_status_t upipe_attn_set_wait_limit_ns(uint64_t ns);
 
 /* Runs the library's bounded wait on a barrier that nothing completes (arrive = 0) or on one it

@@ -135,12 +135,12 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
 }
 
 // Waits, a second at most, for the `n` copies from `stage` on that are on their way although a wait for one ran out.
-__device__ __forceinline__ void drain(uint32_t bars, int stages, int stage, uint32_t parity, int n) {
+__device__ __forceinline__ void drain(uint32_t bars, int stages, int stage, uint32_t parity, int n, uint64_t ns) {
   if (n == 0) return;
   const uint64_t t0 = tc::globaltimer();
   for (; n > 0; --n) {
     while (!tc::mbar_try_wait_addr(bars + stage * 8, parity))
-      if (tc::globaltimer() - t0 > tc::kDrainNs) return;
+      if (tc::globaltimer() - t0 > ns) return;
     if (++stage == stages) {
       stage = 0;
       parity ^= 1;
@@ -174,7 +174,8 @@ __global__ void __launch_bounds__(32 * W, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::AT_INFO + kWarps * 40);
   volatile uint32_t* far_rows = reinterpret_cast<volatile uint32_t*>(smem + L::AT_INFO + kWarps * 40 + 16) + warp;  // of the item: see `convert`
   const uint32_t bars = smem_u32(smem + L::AT_BARS) + warp * L::STAGES * 8;
-  if (lane < L::STAGES) asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bars + lane * 8) : "memory");
+  if (lane < L::STAGES)
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bars + lane * 8), "r"(arrivals(lane, L::STAGES, wait_ns)) : "memory");
   if (threadIdx.x == 0) *abort_flag = 0;
   tc::fence_mbar_init();
   __syncthreads();  // the flag may hold anything before, and another lane than that which prepared a barrier may use it
@@ -686,7 +687,7 @@ __global__ void __launch_bounds__(32 * W, 1)
       float* slot = ends ? head_slot : tail_slot;
       const int item = cb * hkv + chk;
       if (!ends) {
-        drain(bars, L::STAGES, lost_at >> 1, lost_at & 1, in_flight);
+        drain(bars, L::STAGES, lost_at >> 1, lost_at & 1, in_flight, drain_ns(wait_ns));
         in_flight = 0;
         if (FP8) cp_wait<0>();
         left_over.y = item;
@@ -807,7 +808,7 @@ __global__ void __launch_bounds__(32 * W, 1)
         fetch(cb, chk);
       }
     }
-    drain(bars, L::STAGES, lost_at >> 1, lost_at & 1, in_flight);
+    drain(bars, L::STAGES, lost_at >> 1, lost_at & 1, in_flight, drain_ns(wait_ns));
     if (FP8) cp_wait<0>();
   }
 

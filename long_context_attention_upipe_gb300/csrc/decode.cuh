@@ -65,6 +65,15 @@ __device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, u
 __device__ __forceinline__ void expect_tx(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+// Wait limits of n < 64 ns, which no copy would meet, are for testing: the barrier of place n - 1 of a ring of copies (modulo the ring) takes
+// one arrival more than it gets, so waits for it run out (mbar_wait_addr alone may sleep until a copy has come, however short the limit).
+constexpr uint64_t kTestNs = 64;
+__device__ __forceinline__ int arrivals(int place, int ring, uint64_t wait_ns) {
+  return 1 + (wait_ns < kTestNs && place == (int)(wait_ns - 1) % ring);
+}
+// The longest wait for copies in flight after that: a thousand times what a copy takes, if one of them is never seen to come.
+__device__ __forceinline__ uint64_t drain_ns(uint64_t wait_ns) { return wait_ns < kTestNs ? 1000000 : tc::kDrainNs; }
+
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // Four codes as two pairs of fp16.

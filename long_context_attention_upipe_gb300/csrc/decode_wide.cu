@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(Wide<D, RP>::THREADS, 1)
     auto init = [](uint32_t bar, int n, uint32_t count) {
       for (int i = 0; i < n; ++i) asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar + 8 * i), "r"(count) : "memory");
     };
-    init(full, RING, 1);
+    for (int i = 0; i < RING; ++i) init(full + 8 * i, 1, arrivals(i, RING, wait_ns));
     init(empty, RING, 1);
     init(s_full, 2, 1);
     init(s_empty, 2, L::SOFTMAX / 32);
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(Wide<D, RP>::THREADS, 1)
     const uint64_t t0 = tc::globaltimer();
     for (uint32_t u = end > RING ? end - RING : end & 1; u < end; u += 2)
       while (!tc::mbar_try_wait_addr(full + u % RING * 8, u / RING & 1))
-        if (tc::globaltimer() - t0 > tc::kDrainNs) return;
+        if (tc::globaltimer() - t0 > drain_ns(wait_ns)) return;
   };
   if (warp == 0) {
     Line w = at;

@@ -46,12 +46,55 @@ def test_a_call_after_one_that_gave_up(kind, form):
     want, wl = run_decode(c, q, table, ln, q_len=q_len)
     ws = torch.full((up.decode_workspace_bytes(c, table.shape[0], q.shape[0], q_len),), 0xff, dtype=torch.uint8, device="cuda")
     lost, good = (torch.full_like(q, 55.0) for _ in range(2))
-    for _ in range(10):
+    for limit in (1, 2, 3, 5):
         lse = torch.empty(q.shape[:2], device="cuda")
         good.fill_(55.0)
-        up.set_wait_limit_ns(1)
+        up.set_wait_limit_ns(limit)
         up.decode(c, q, table, ln, lost, ws)
         up.set_wait_limit_ns(0)
         up.decode(c, q, table, ln, good, ws, lse=lse)
         torch.cuda.synchronize()
         assert torch.equal(good, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("kind,form", CASES)
+def test_waits_run_out(kind, form):
+    """Limits below 64 ns: a wait for the first tile of every queue runs out (1), or for a later one.  A row is all NaN, or what it is with the usual
+    limit."""
+    c, table, q, ln, q_len = case(kind, form)
+    want, wl = run_decode(c, q, table, ln, q_len=q_len)
+    seen = ~((want == 0).all(-1) & (wl == -float("inf")))
+    for limit in (1, 2, 3, 4, 5, 6, 63):
+        up.set_wait_limit_ns(limit)
+        o, lse = run_decode(c, q, table, ln, q_len=q_len)
+        up.set_wait_limit_ns(0)
+        torch.cuda.synchronize()
+        lost = o.isnan().any(-1)
+        assert torch.equal(o.isnan().all(-1), lost) and torch.equal(lse.isnan(), lost) and not bool((lost & ~seen).any())
+        assert torch.equal(o[~lost], want[~lost]) and torch.equal(lse[~lost], wl[~lost])
+        if limit == 1:
+            assert torch.equal(lost, seen)
+    o, lse = run_decode(c, q, table, ln, q_len=q_len)
+    assert torch.equal(o, want) and torch.equal(lse, wl)
+
+
+@pytest.mark.parametrize("kind,form", [("bf16", "line"), ("bf16", "clusters"), ("bf16", "wide64")])
+def test_calls_that_gave_up_in_a_graph(kind, form):
+    """The limit is the one at the capture: every replay gives up, and the call behind it in the same workspace does not."""
+    c, table, q, ln, q_len = case(kind, form)
+    want, wl = run_decode(c, q, table, ln, q_len=q_len)
+    ws = torch.full((up.decode_workspace_bytes(c, table.shape[0], q.shape[0], q_len),), 0xff, dtype=torch.uint8, device="cuda")
+    lost, good, lse = torch.empty_like(q), torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        up.set_wait_limit_ns(1)
+        up.decode(c, q, table, ln, lost, ws)
+        up.set_wait_limit_ns(0)
+        up.decode(c, q, table, ln, good, ws, lse=lse)
+    for _ in range(5):
+        lost.zero_()
+        good.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(good, want) and torch.equal(lse, wl) and bool(lost.isnan().all(-1)[wl > -float("inf")].all())
