@@ -528,7 +528,7 @@ upipe_status_t upipe_attn_grad_clip(const upipe_grad_tensor_t* tensors, int32_t 
  *              order of strides (in elements, whole 16 bytes), the same for both; the two may interleave
  *   k_scale, v_scale  device fp32 with e4m3, else NULL: one scale for each row (a row reads code * scale),
  *              through strides of their own
- *   page_size  a multiple of 16;  n_kv_heads  at most 1024;  head_dim  64 or 128
+ *   page_size  a multiple of 16, at most 2^20;  n_kv_heads  at most 1024;  head_dim  64 or 128;  n_pages  below 2^31
  * Strides of a single page or head do not count.  Rows do not overlap, nor do the tensors
  * (UPIPE_ERR_INVALID_ARG). */
 typedef struct {
@@ -574,8 +574,12 @@ upipe_status_t upipe_attn_kv_read(const upipe_kv_cache_t* cache, const upipe_pag
 /* Attention of the q_len newest tokens of every sequence over its cached keys (theirs among them: write first).
  * Query t of sequence b sees the keys j < lens[b] - q_len + 1 + t:
  *   s_j = scale q . k_j,  lse = log sum_j exp s_j,  o = sum_j exp(s_j - lse) v_j
- * fp32 sums, o rounded once; a row that sees no key gets o = 0 and lse = -infinity (an empty sequence, or fewer
- * keys than q_len).  What a query does not see does not reach it, infinities and NaN included.
+ * fp32 scores, maxima and sums; o rounded once.  A weight exp(s_j - max s) meets v_j as two bf16 numbers (2^-16 of it) with a bf16
+ * cache; with e4m3 its product with the value's scale is one fp16 number (2^-11 of it, or 2^-35 of the row's largest such product where
+ * that is more), and the sums are of products of these with codes.  Queries and keys are exact in both.  Where the weighted sum of |v|,
+ * not divided by that of the weights yet, passes fp32's range, o is not finite.
+ * A row that sees no key gets o = 0 and lse = -infinity (an empty sequence, or fewer keys than q_len).  What a query does not see
+ * does not reach it, infinities and NaN included.
  *   lens    device int32 [n_seqs]; the result depends on the device's values alone, so a captured call may be
  *           replayed with other lengths, tables and pages.  Negative lengths count as 0.  Where a page number that
  *           is needed lies outside the cache, or a length past the table, the rows that depend on it are NaN.
@@ -583,8 +587,10 @@ upipe_status_t upipe_attn_kv_read(const upipe_kv_cache_t* cache, const upipe_pag
  *   q, o    device bf16, [n_q_heads][n_seqs * q_len] rows, a sequence's tokens in order, through their strides (in
  *           elements, multiples of 8); o (written) may lie beside q in one tensor, but not over it
  *   lse     NULL, or device fp32 [n_q_heads][n_seqs * q_len] (written)
- *   ws      device workspace of upipe_attn_decode_workspace_size bytes
- * The order of all sums depends on sizes and lengths alone: equal calls give equal bits. */
+ *   ws      device workspace of upipe_attn_decode_workspace_size bytes, of one call at a time
+ * The order of all sums depends on sizes and lengths alone: equal calls give equal bits.  Which kernel runs, and thereby that
+ * order, goes by the keys that the table has room for (max_pages): short sequences take less time in a table that is as wide as they
+ * are long. */
 upipe_status_t upipe_attn_decode_workspace_size(const upipe_kv_cache_t* cache, int32_t n_seqs, int32_t n_q_heads, int32_t q_len,
                                                 size_t* bytes);
 upipe_status_t upipe_attn_decode(const upipe_kv_cache_t* cache, const upipe_page_table_t* table, const int32_t* lens,

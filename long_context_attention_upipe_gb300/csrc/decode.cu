@@ -10,7 +10,9 @@
 // few tiles' time added at each item's end for what an end costs (without: 94 instead of 88.6 us for 64 sequences up to 16384
 // keys).  The CTAs, one to an SM, take equal parts of the line, and a CTA's warps equal parts of that, whatever the lengths.
 // A warp runs its tiles through a queue of its own in shared memory: one TMA box each for 16 keys and 16 values of a page, so any
-// page, head and token strides cost nothing and warps wait for nobody but their copies.
+// page, head and token strides cost no instructions, and warps wait for nobody but their copies.  (Memory does care: rows that lie token
+// by token, 8 heads of 256 bytes, take 60 instead of 58 us for 48 sequences up to 8192 keys in bf16; of 128 bytes, with their scales
+// token by token too, 127 instead of 88 for 64 up to 16384 in e4m3, 118 with scales head by head.)
 //
 // Per tile, keys are the 16 rows of m16n8k16 and up to 8 (NT = 2: 16) query rows its columns:
 //   S^T = K Q^T,   P = exp2(S - m),   O^T += V^T P^T
@@ -36,13 +38,15 @@
 // is that of a query row that fp16 does not hold.
 //
 // Measured (GB300, calls back to back; floor: the cached bytes at the copy rate of 6698 GB/s):
-//   1 sequence of 1048576 keys, 4 / 1 heads, bf16            86 us, floor 80.2
-//   1 of 5242880, 8 / 1, e4m3                           206 - 218 us, 206.6 (as fast as the box's memory)
+//   1 sequence of 1048576 keys, 4 / 1 heads, bf16       86 - 88 us, floor 80.2
+//   1 of 5242880, 8 / 1, e4m3                           206 - 222 us, 206.6 (as fast as the box's memory)
 //   64 up to 16384, 32 / 8, e4m3                             88 us, 76.0
 //   48 up to 8192, 40 / 8, bf16                              58 us, 48.3
 //   16 up to 32768, 4 tokens each, 32 / 8, e4m3              64 us, 47.3
 //   256 up to 500, 4 / 2 heads of 64, bf16                 10.4 us, 2.2
-//   1 of 4097, 32 / 8, bf16                                 9.2 us, 2.5
+//   1 of 4097, 32 / 8, bf16                           9.2 - 9.6 us, 2.5
+// (With tables as wide as the longest sequence is long: kernels are chosen by the table's room, and 1000 keys of 8 heads take 8.7 instead
+// of 7.2 us, 256 sequences up to 500 11.2 instead of 10.4, in a table for 131072.)
 // One long sequence streams at the copy rate.  What a call adds: 5 us until the first tile lands (lengths, table entries and
 // queries are read one after another), 2 to 4 us for the ends of the last items, 2 to 3 us for the second launch.  With 16 rows
 // of an e4m3 cache the tiles' own chain of instructions shows as well: 255 registers leave room for 8 warps.
@@ -1096,7 +1100,8 @@ cudaError_t run(const DecodeArgs& a, const DecodeShape& sh, DecodeWs ws, cudaStr
     // keys each, if the items are few enough.  us on the device and a call, bf16, 8 key heads, on the line, with one CTA and in clusters: 1000
     // keys 7.9 and 11.3, 9.2 and 9.8, 7.6 and 8.2; 2000 keys 8.7 and 10.2 on the line, 8.2 and 9.1 in clusters of 8 (e4m3 9.2 and 10.2, 8.7
     // and 9.5; 16 rows 13.0 and 13.5, 10.9 and 11.7); with 512 keys to a CTA, 4000 of one head, the line is as fast (9.6 and 10.3, 9.6
-    // and 10.5).  Clusters of 8 find room for 12 items at once (8.8 us; 9.2 in clusters of 4), not for 16 (12.7 instead of 8.6 us).
+    // and 10.5).  Clusters of 8 find room for 12 items at once (8.8 us; 9.2 in clusters of 4), not for 16 (12.7 instead of 8.6 us): as
+    // this GPU's 152 SMs are grouped.
     const int64_t items = (int64_t)a.t.n_seqs * a.c.n_kv_heads;
     const int keys = table_keys(a.t, a.c.page_size);
     int share = 1;

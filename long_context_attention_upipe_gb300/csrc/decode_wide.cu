@@ -10,7 +10,8 @@
 // raised only when a score passes it by 2^16; the threads vote on that once a tile.  Weights are two bf16 numbers (2^-17), two products.
 //
 // Warps: 0 brings keys and 3 values, in boxes of 16 to 128 rows of a page; 1 issues the products; 2 brings queries; the others make
-// weights.  S is double, so the next tile's product runs under this one's weights; P and O are not (shared memory is full).
+// weights.  S is double, so the next tile's product runs under this one's weights; P and O are not
+// (with rows of 128 elements shared memory is full; with 64 a second P would fit, and has not been tried).
 //
 // Bound by HBM where few items end: a CTA's share of it brings a tile's 64 KB in 2800 clocks, and a tile's chain with 64 rows (product 600
 // clocks, weights 2100, product 980, overlapped but for P) takes 3200.  An item's end costs four tiles' time (kEnd 1: 60.7 instead of
