@@ -134,3 +134,16 @@ def test_queries_of_any_size_as_a_whole(power):
     against = max(-90, min(110, -power))
     up.kv_write(c, (randn(g, hkv, n, dh) * 2.0 ** against).bfloat16(), randn(g, hkv, n, dh).bfloat16(), torch.zeros_like(pos), pos, table)
     check_decode(c, (randn(g, 8, 1, dh).double() * 2.0 ** power).bfloat16(), table, [n])
+
+
+@pytest.mark.parametrize("power", [-140, -126, -118, -112, -60, 60, 100, 108])
+@pytest.mark.parametrize("hq,q_len", [(8, 1), (8, 4)])
+def test_scales_that_no_write_makes(power, hq, q_len):
+    """Scales of keys down to subnormal numbers and up to 2^108, of a cache that was filled some other way; queries of the opposite size."""
+    g = gen(6)
+    n, hkv, dh = 200, 2, 128
+    c = make_cache("e4m3", pages=14, hkv=hkv, size=16, dh=dh, fill=g)
+    table = table_of(g, [n], 16, 14)
+    c.k_scale.copy_((0.5 + torch.rand(c.k_scale.shape, generator=g, device="cuda")).double() * 2.0 ** power)
+    q = randn(g, hq, q_len, dh).double() * 2.0 ** (min(122, -power) - 7)
+    check_decode(c, q.bfloat16(), table, [n], q_len=q_len)
