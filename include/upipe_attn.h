@@ -576,9 +576,9 @@ upipe_status_t upipe_attn_kv_read(const upipe_kv_cache_t* cache, const upipe_pag
  *   s_j = scale q . k_j,  lse = log sum_j exp s_j,  o = sum_j exp(s_j - lse) v_j
  * fp32 scores, maxima and sums; o rounded once.  A weight exp(s_j - max s) meets v_j as two bf16 numbers (2^-16 of it) with a bf16
  * cache; with e4m3 its product with the value's scale is one fp16 number (2^-11 of it, or 2^-35 of the row's largest such product where
- * that is more), and the sums are of products of these with codes.  Queries and keys enter exactly (with e4m3, keys of scales from
- * 2^-111 on: kv_write makes none below 2^-109).  Where the weighted sum of |v|,
- * not divided by that of the weights yet, passes fp32's range, o is not finite.
+ * that is more), and the sums are of products of these with codes.  Queries and keys enter exactly; with e4m3, elements of a query below
+ * 2^-32 of its largest do where they could move a score by more than 2^-20, and keys do whose scales are from 2^-111 on (kv_write makes
+ * none below 2^-109).  Where the weighted sum of |v|, not divided by that of the weights yet, passes fp32's range, o is not finite.
  * A row that sees no key gets o = 0 and lse = -infinity (an empty sequence, or fewer keys than q_len).  What a query does not see
  * does not reach it, infinities and NaN included.
  *   lens    device int32 [n_seqs]; the result depends on the device's values alone, so a captured call may be

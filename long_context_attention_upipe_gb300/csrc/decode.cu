@@ -20,9 +20,9 @@
 //   bf16  weights enter as the sum of two bf16 numbers (2^-17); a single one would double the error of o.
 //   e4m3  codes are converted to fp16 (exact).  A 16-byte piece of codes gives a lane four neighbouring elements, so the steps of
 //         S^T take the head dimension in that order and the rows of O^T are pairs of elements.  q goes to fp16 under a power of two
-//         for each row (exact, but for rows whose elements are further apart than 2^32: redo), K's scale to the score, and V's scale to
-//         the weight's exponent, s_j - m + log2 sv_j, under a maximum of its own; weights are fp16 (2^-11) up to 2^15, which leaves
-//         2^-35 of the largest.
+//         for each row (exact, but for elements below 2^-32 of the largest: redo, if they can move a score), K's scale to the score, and
+//         V's scale to the weight's exponent, s_j - m + log2 sv_j, under a maximum of its own; weights are fp16 (2^-11) up to 2^15, which
+//         leaves 2^-35 of the largest.
 // The maximum is a reference that is raised, and the sums rescaled, only when a score exceeds it by a margin: one vote for each
 // tile, no shuffles.  m, l and O are fp32.
 //
@@ -35,7 +35,8 @@
 //
 // A value that is infinite or NaN spoils the products of query rows that do not see it (zero times infinity), and of those that do
 // where a weight's second part is zero.  Then o is not finite although l is, and the piece is made again key by key (redo), as
-// is that of a query row that fp16 does not hold.
+// is that of a query row that fp16 does not hold.  (Which takes 40 times as long: 3.6 ms for 64 sequences up to 16384 keys, each query
+// with an element that towers 2^40 over the others; to make sure that dead channels need none of it takes 108 us instead of 90.)
 //
 // Measured (GB300, calls back to back; floor: the cached bytes at the copy rate of 6698 GB/s):
 //   1 sequence of 1048576 keys, 4 / 1 heads, bf16       86 - 88 us, floor 80.2
@@ -335,8 +336,7 @@ __global__ void __launch_bounds__(32 * W, 1)
       }
     };
     // fp16 under a power of two for each row, the largest element in [2^15, 2^16): bf16's 8 bits fit exactly down to 2^-17.  Rows with
-    // elements below that are remembered, and their sums made key by key in the end.  (With the largest in [1, 2) rows that span more than
-    // 2^17 would need that, and some models' queries have a few elements that large.)
+    // elements below that are remembered, and their sums made key by key in the end if it can matter.
     auto convert = [&]() {
       uint32_t far = 0;
 #pragma unroll
@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(32 * W, 1)
         left_len.x = len;
       }
       __syncwarp();
-      uint32_t again = FP8 ? *far_rows : 0;  // rows (8 nt + row) whose sums have to be made once more
+      uint32_t again = 0;  // rows (8 nt + row) whose sums have to be made once more
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float by[2];  // what o's sums are multiplied with
@@ -772,6 +772,20 @@ __global__ void __launch_bounds__(32 * W, 1)
         }
       }
       __syncwarp();
+      uint32_t far = FP8 ? *far_rows : 0;
+      if (far) {
+        // What fp16 leaves of such a row's small elements is within 2^-25, so a score in units of log2 within D 2^-25 448 times its two scales.
+        // Below 2^-20 no weight shows it: channels that are dead, not one that towers over the others, and nothing has to be made anew.
+        const float most = most_key_scale(a, cb, chk, begin * kTileKeys, (int)min((int64_t)ct * kTileKeys, (int64_t)len)) * pow2(-kQueryTop);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            unsigned fine = __ballot_sync(0xffffffffu, r == 0 && fabsf(rs[nt][e]) * most * (D * 448.f * pow2(-25)) < pow2(-20));
+            for (; fine; fine &= fine - 1) far &= ~(1u << (nt * 8 + 2 * (__ffs(fine) - 1) + e));
+          }
+        again |= far;
+      }
       if (again) {
         constexpr int E = D / 32;
 #pragma unroll

@@ -216,6 +216,19 @@ __device__ __noinline__ RowSum redo(const DecodeArgs& a, int b, int hk, RowAt at
   return sum;
 }
 
+// The largest scale of a sequence's keys [k0, k1).
+__device__ __noinline__ float most_key_scale(const DecodeArgs& a, int b, int hk, int k0, int k1) {
+  float most = 0.f;
+#pragma unroll 4
+  for (int64_t j = k0 + (int)(threadIdx.x & 31); j < k1; j += 32) {  // (may pass 32 bits behind the longest sequence's end)
+    const KvPlace p = kv_place(a.c, a.t, b, (int)j);
+    if (p.page >= 0) most = fmaxf(most, fabsf(a.c.k_scale[kv_scale(a.c, p, hk)]));
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, off));
+  return most;
+}
+
 __device__ __forceinline__ float row_lse(float m, float l) { return m * kLn2 + logf(l); }
 
 // Rows R0 .. R1 of key heads h0 .. h1 of a sequence without tiles: zeros, or NaN where there are keys but no table.  All lanes of a

@@ -1,5 +1,5 @@
-"""Decode of the longest sequence with more than 16 query rows to a key head: 2^31 - 1 keys, whose last tile of 128 ends where 32-bit
-positions do, against plain 64-bit arithmetic."""
+"""Decode of the longest sequence: with more than 16 query rows to a key head 2^31 - 1 keys, whose last tile of 128 ends where 32-bit positions do,
+against plain 64-bit arithmetic; with an e4m3 cache, queries whose small elements have to be looked after."""
 import math
 
 import pytest
@@ -55,3 +55,19 @@ def test_masks_of_the_longest_sequence(dh, hq, q_len, short):
         assert bool(((o[:, t].double() - ref).abs() <= ref.abs() * BF + mass * (2.0 ** -10 + links * U)).all())
         assert bool(((lse[:, t].double() - want).abs() <= 2.0 ** -10 + links / 16 * U).all())
         assert bool((ref > 99).all()) if t == q_len - 1 else bool((ref < 20).all())
+
+
+def test_dead_channels_of_the_longest_sequence():
+    """A query with an element next to nothing: the scales of all keys up to 2^31 - 1 are looked at, and the result is that without the element."""
+    size, dh = 1 << 20, 64
+    g = gen(78)
+    c = make_cache("e4m3", pages=1, hkv=1, size=size, dh=dh, fill=g)
+    table = torch.zeros(1, 2048, dtype=torch.int32, device="cuda")
+    q = randn(g, 2, 1, dh).bfloat16()
+    q[..., 9] = 0
+    want, wl = run_decode(c, q, table, [2 ** 31 - 1])
+    q[..., 9] = 1e-30
+    o, lse = run_decode(c, q, table, [2 ** 31 - 1])
+    assert bool(o.isfinite().all())
+    # below fp16's smallest number, so the products are the same
+    assert torch.equal(o, want) and torch.equal(lse, wl)

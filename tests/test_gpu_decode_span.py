@@ -147,3 +147,52 @@ def test_scales_that_no_write_makes(power, hq, q_len):
     c.k_scale.copy_((0.5 + torch.rand(c.k_scale.shape, generator=g, device="cuda")).double() * 2.0 ** power)
     q = randn(g, hq, q_len, dh).double() * 2.0 ** (min(122, -power) - 7)
     check_decode(c, q.bfloat16(), table, [n], q_len=q_len)
+
+
+@pytest.mark.parametrize("form", range(len(FORMS)))
+@pytest.mark.parametrize("power", [-40, -90, -133])
+def test_dead_channels(power, form):
+    """Some elements of most queries are next to nothing, beside ordinary ones: no score shows it."""
+    lens, hq, hkv, dh, size, q_len, more = FORMS[form]
+    c, table, q = setup("e4m3", lens, hq, hkv, dh, size, q_len)
+    dead = (torch.arange(dh, device="cuda") % 5 == 2) & (torch.arange(hq, device="cuda")[:, None, None] % 4 != 1)
+    q = torch.where(dead, (q.double() * 2.0 ** power).bfloat16(), q)
+    if more:
+        table = widened(table, more, gen(1))
+    check_decode(c, q, table, lens, q_len=q_len)
+
+
+@pytest.mark.parametrize("what", ["v", "missing"])
+def test_dead_channels_beside_other_trouble(what):
+    """A row that needs nothing made anew for its small elements may need it for a value that is not finite."""
+    lens = [1000, 90]
+    c, table, q = setup("e4m3", lens, 8, 2, 128, 16)
+    q[..., 5] = 1e-30
+    clean, lse = check_decode(c, q, table, lens)
+    if what == "v":
+        c.v.view(torch.uint8)[int(table[0, 20]), :, 3, 9] = 0x7f
+        rest = torch.arange(128, device="cuda") != 9
+        o, e = run_decode(c, q, table, lens)
+        assert bool(o[:, 0, 9].isnan().all()) and bool(e.isfinite().all())
+        assert bool(((o - clean)[:, 0, rest].abs() <= clean[:, 0, rest].abs() * 2.0 ** -7 + 2.0 ** -9).all())
+    else:
+        table = table.clone()
+        table[0, 20] = -1
+        o, e = run_decode(c, q, table, lens)
+        assert bool(o[:, 0].isnan().all()) and bool(e[:, 0].isnan().all())
+    assert torch.equal(o[:, 1], clean[:, 1]) and torch.equal(e[:, 1], lse[:, 1])
+
+
+@pytest.mark.parametrize("keys", [1.0, 2.0 ** 8, 2.0 ** 14, 2.0 ** 30])
+def test_small_elements_that_matter_by_the_size_of_the_keys(keys):
+    """Elements 2^-34 of a row's largest, which meets zeros: the score grows with the keys, and its loss would."""
+    g = gen(9)
+    n, hkv, dh = 300, 1, 128
+    c = make_cache("e4m3", pages=20, hkv=hkv, size=16, dh=dh)
+    table, pos = table_of(g, [n], 16, 20), torch.arange(n, device="cuda").int()
+    k = keys * randn(g, hkv, n, dh)
+    k[..., 0] = 0
+    up.kv_write(c, k.bfloat16(), randn(g, hkv, n, dh).bfloat16(), torch.zeros_like(pos), pos, table)
+    q = 4 * randn(g, 8, 1, dh) / keys
+    q[..., 0] = 2.0 ** 36 / keys
+    check_decode(c, q.bfloat16(), table, [n])
