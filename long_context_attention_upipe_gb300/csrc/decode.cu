@@ -43,14 +43,14 @@
 //   1 of 5242880, 8 / 1, e4m3                           206 - 222 us, 206.6 (as fast as the box's memory)
 //   64 up to 16384, 32 / 8, e4m3                             88 us, 76.0
 //   48 up to 8192, 40 / 8, bf16                              58 us, 48.3
-//   16 up to 32768, 4 tokens each, 32 / 8, e4m3              64 us, 47.3
+//   16 up to 32768, 4 tokens each, 32 / 8, e4m3         64 - 65 us, 47.3
 //   256 up to 500, 4 / 2 heads of 64, bf16                 10.4 us, 2.2
 //   1 of 4097, 32 / 8, bf16                           9.2 - 9.6 us, 2.5
 // (With tables as wide as the longest sequence is long: kernels are chosen by the table's room, and 1000 keys of 8 heads take 8.7 instead
 // of 7.2 us, 256 sequences up to 500 11.2 instead of 10.4, in a table for 131072.)
 // One long sequence streams at the copy rate.  What a call adds: 5 us until the first tile lands (lengths, table entries and
 // queries are read one after another), 2 to 4 us for the ends of the last items, 2 to 3 us for the second launch.  With 16 rows
-// of an e4m3 cache the tiles' own chain of instructions shows as well: 255 registers leave room for 8 warps.
+// of an e4m3 cache the tiles' own chain of instructions shows as well: 254 registers leave room for 8 warps.
 #include <type_traits>
 
 #include "decode.cuh"
